@@ -1,12 +1,14 @@
 """GB300 (sm_103a) GatedDeltaNet verify + commit for MTP speculative decoding.
 
 The compute lives in ``libgdnspec.so`` (C ABI, ``include/gdnspec.h``);
-``gdn`` is its ctypes binding, ``inputs`` the seeded synthetic workloads and
-``build`` compiles the library in-tree.  The binding is imported lazily so
-that ``inputs`` and ``build`` work before the library exists.
+``gdn`` is its ctypes binding, ``hybrid`` the binding of the operators a
+Qwen3.5-style hybrid's step needs beside those layers (``include/gdnhybrid.h``),
+``inputs`` the seeded synthetic workloads and ``build`` compiles the library
+in-tree.  The bindings are imported lazily so that ``inputs`` and ``build`` work
+before the library exists.
 """
 
-__all__ = ["gdn", "inputs", "build"]
+__all__ = ["gdn", "hybrid", "inputs", "build"]
 
 
 def __getattr__(name):
@@ -16,4 +18,9 @@ def __getattr__(name):
         from . import gdn
 
         return getattr(gdn, name)
+    if name in ("gdn_page_map", "gdn_kv_append", "gdn_paged_attention", "gdn_sample_accept", "make_page_map_args",
+                "make_kv_append_args", "make_paged_attention_args", "make_sample_accept_args", "paged_attention_work_bytes"):
+        from . import hybrid
+
+        return getattr(hybrid, name)
     raise AttributeError(name)

@@ -1,0 +1,313 @@
+// What the paged-attention kernels share: the call's parameters, the division
+// of its work over blocks, and the join of partial results.
+//
+// Rows.  For one request and kv head, the G = H_q / H_kv query heads of the n
+//   new tokens are one matrix of n*G rows (row r: token r / G, head r % G), cut
+//   into tiles of kRows rows; K and V are cut into blocks of kKeys positions.
+//   A tile needs the blocks up to its last row's position:
+//     c(m) = floor((ctx + floor((last row of m) / G)) / kKeys) + 1.
+// Division.  All (request, kv head, tile, key block) units of a call form one
+//   line; block i takes units [i*per, (i+1)*per).  Every block so has the same
+//   number of key blocks however ragged the lengths are: a long context is
+//   split over many blocks, many short ones share a block.  The line's length
+//   needs only sums of c(m), which a floor-sum gives without a loop over tiles,
+//   so each block finds its own part in a scan over the requests, with no
+//   planning launch before it.
+// Join.  A tile whose units lie in several blocks is split: its first block
+//   writes a head partial (slot 1) and a note of how many blocks follow, each
+//   of those writes a tail partial (slot 0): the running maximum, sum and
+//   unnormalised output in 32 bits.  combine_kernel adds them up in block
+//   order, so the result does not depend on timing.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "gdnhybrid.h"
+
+namespace gdnattn {
+
+constexpr unsigned kFull = 0xffffffffu;
+
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+struct Params {
+  int B, R, H_kv, G, d;
+  int page_size, n_pages, table_stride, n_q_rows;
+  int64_t max_tokens;  // max_pages * page_size
+  float scale_log2;    // scale * log2(e): scores are kept in the exponent of 2
+  const void* q;
+  int64_t q_row, q_head;
+  const void *k, *v;
+  int64_t k_page, k_head, k_token, v_page, v_head, v_token;
+  const int32_t *table, *ctx_len, *n_rows, *row_start;
+  void* o;
+  int64_t o_row, o_head;
+  int4* notes;      // [blocks] {blocks that follow (0: none), b, h, m} of a split tile's first block
+  float* partials;  // [blocks][2 slots][kRows][d + 2]: outputs, then the rows' maxima and sums
+  int32_t* status;
+  int n_blocks;     // blocks of the attention launch
+};
+
+struct Request {
+  int ctx, n, row0;
+};
+
+// request b's lengths; n = 0 where it takes no part
+__device__ __forceinline__ Request request(const Params& p, int b, int* why = nullptr) {
+  Request r;
+  r.ctx = p.ctx_len[b];
+  r.n = p.n_rows[b];
+  r.row0 = p.row_start ? p.row_start[b] : b * p.R;
+  int bad = 0;
+  if (r.n < 0 || (p.R > 0 && r.n > p.R)) bad |= GDN_STATUS_BAD_NROWS;
+  if (r.n > 0 && (r.ctx < 0 || (int64_t)r.ctx + r.n > p.max_tokens || r.row0 < 0 || (int64_t)r.row0 + r.n > p.n_q_rows))
+    bad |= GDN_STATUS_BAD_LENGTH;
+  if (bad) r.n = 0;
+  if (why) *why |= bad;
+  return r;
+}
+
+// sum over i in [0, n) of floor((a*i + b) / m), by the Euclidean descent on (m, a)
+__device__ inline long long floor_sum(long long n, long long m, long long a, long long b) {
+  long long s = 0;
+  while (n > 0) {
+    if (a >= m) {
+      s += n * (n - 1) / 2 * (a / m);
+      a %= m;
+    }
+    if (b >= m) {
+      s += n * (b / m);
+      b %= m;
+    }
+    const long long y = a * n + b;
+    if (y < m) break;
+    n = y / m;
+    b = y % m;
+    const long long t = m;
+    m = a;
+    a = t;
+  }
+  return s;
+}
+
+template <int kRows, int kKeys>
+struct Tiles {
+  __device__ static int count(const Params& p, const Request& r) { return ((long long)r.n * p.G + kRows - 1) / kRows; }
+  __device__ static int blocks(const Params& p, const Request& r, int m) {
+    const long long last = min((long long)(m + 1) * kRows, (long long)r.n * p.G) - 1;
+    return (int)((r.ctx + last / p.G) / kKeys) + 1;
+  }
+  // key blocks of the tiles before m
+  __device__ static long long before(const Params& p, const Request& r, int m) {
+    if (m == 0) return 0;
+    return m + floor_sum(m, (long long)p.G * kKeys, kRows, (long long)p.G * r.ctx + kRows - 1);
+  }
+  // key blocks of one kv head of the request
+  __device__ static long long sum(const Params& p, const Request& r) {
+    if (r.n <= 0) return 0;
+    const int M = count(p, r);
+    return before(p, r, M - 1) + blocks(p, r, M - 1);
+  }
+};
+
+// one block's walk over its units, tile by tile
+template <int kRows, int kKeys>
+struct Walk {
+  using T = Tiles<kRows, kKeys>;
+  Request req;
+  int b, h, m, tiles, left;  // left: units still to do
+  int kb0, kb1, blocks;      // this segment's key blocks, and how many the whole tile has
+
+  __device__ void segment() {
+    blocks = T::blocks(*p, req, m);
+    kb1 = min(blocks, kb0 + left);
+  }
+  __device__ bool done() const { return left <= 0; }
+  __device__ void next() {
+    left -= kb1 - kb0;
+    if (left <= 0) return;
+    kb0 = 0;
+    if (++m == tiles) {
+      m = 0;
+      if (++h == p->H_kv) {
+        h = 0;
+        do {
+          req = request(*p, ++b);
+        } while (req.n <= 0);
+        tiles = T::count(*p, req);
+      }
+    }
+    segment();
+  }
+  const Params* p;
+};
+
+struct Start {
+  long long off;  // units from the request's first to the block's first
+  long long total;
+  int b;
+  int per;
+};
+
+// Every thread of the block calls this; all get the block's first unit.  scan:
+// kThreads/32 words of shared memory.
+template <int kRows, int kKeys, int kThreads>
+__device__ void find_start(const Params& p, int min_units, long long* scan, Start* out) {
+  using T = Tiles<kRows, kKeys>;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int each = (p.B + kThreads - 1) / kThreads;
+  const int b0 = threadIdx.x * each, b1 = min(p.B, b0 + each);
+  long long mine = 0;
+  int why = 0;
+  for (int b = b0; b < b1; ++b) mine += p.H_kv * T::sum(p, request(p, b, &why));
+  if (why && blockIdx.x == 0 && p.status) atomicOr(p.status, why);
+  long long inc = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long v = __shfl_up_sync(kFull, inc, off);
+    if (lane >= off) inc += v;
+  }
+  if (lane == 31) scan[warp] = inc;
+  __syncthreads();
+  long long before = 0, total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += scan[w];
+    total += scan[w];
+  }
+  const long long at = before + inc - mine;
+  const long long per = max((total + p.n_blocks - 1) / p.n_blocks, (long long)min_units);
+  const long long first = per * blockIdx.x;
+  if (threadIdx.x == 0) {
+    out->total = total;
+    out->per = (int)min(per, (long long)INT32_MAX);
+  }
+  if (first >= at && first < at + mine) {  // one thread at most
+    long long off = first - at;
+    int b = b0;
+    for (;; ++b) {
+      const long long c = p.H_kv * T::sum(p, request(p, b));
+      if (off < c) break;
+      off -= c;
+    }
+    out->b = b;
+    out->off = off;
+  }
+  __syncthreads();
+}
+
+template <int kRows, int kKeys>
+__device__ bool begin(Walk<kRows, kKeys>& w, const Params& p, const Start& s) {
+  using T = Tiles<kRows, kKeys>;
+  w.p = &p;
+  const long long first = (long long)s.per * blockIdx.x;
+  w.left = (int)max(0ll, min((long long)s.per, s.total - first));
+  if (w.left <= 0) return false;
+  w.b = s.b;
+  w.req = request(p, s.b);
+  w.tiles = T::count(p, w.req);
+  const long long S = T::sum(p, w.req);
+  long long off = s.off;
+  w.h = (int)(off / S);
+  off -= w.h * S;
+  int lo = 0, hi = w.tiles;  // before(lo) <= off < before(hi)
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (T::before(p, w.req, mid) <= off) lo = mid;
+    else hi = mid;
+  }
+  w.m = lo;
+  w.kb0 = (int)(off - T::before(p, w.req, lo));
+  w.segment();
+  return true;
+}
+
+// the blocks that follow this one in a tile it begins and does not finish
+template <int kRows, int kKeys>
+__device__ __forceinline__ int followers(const Walk<kRows, kKeys>& w, const Start& s) {
+  const int rest = w.blocks - w.kb1;
+  return (rest + s.per - 1) / s.per;
+}
+
+__device__ __forceinline__ float* partial(const Params& p, int block, int slot, int rows) {
+  return p.partials + (size_t)(block * 2 + slot) * rows * (p.d + 2);
+}
+
+// one warp per row: joins the partials of the split tile that block
+// blockIdx.x begins, in block order
+template <typename T, int kD, int kRows>
+__global__ void __launch_bounds__(128) combine_kernel(const Params p) {
+  pdl_wait();
+  pdl_trigger();
+  const int4 note = p.notes[blockIdx.x];
+  const int parts = note.x + 1;
+  if (parts <= 1) return;
+  const Request req = request(p, note.y);
+  const int row = blockIdx.y * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int at = note.w * kRows + row;
+  if ((long long)at >= (long long)req.n * p.G) return;
+  auto part = [&](int i) { return partial(p, blockIdx.x + i, i == 0, kRows); };
+  auto stats = [&](int i) { return reinterpret_cast<const float2*>(part(i) + (size_t)kRows * kD)[row]; };
+  float top = -INFINITY;
+  for (int i = lane; i < parts; i += 32) top = fmaxf(top, stats(i).x);
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
+  if (top == -INFINITY) top = 0.f;
+  constexpr int kPer = kD / 32;
+  float acc[kPer] = {};
+  float sum = 0.f;
+  for (int i0 = 0; i0 < parts; i0 += 32) {
+    float w = 0.f, l = 0.f;
+    if (i0 + lane < parts) {
+      const float2 s = stats(i0 + lane);
+      w = exp2f(s.x - top);
+      l = s.y * w;
+    }
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) l += __shfl_xor_sync(kFull, l, off);
+    sum += l;
+    const int n = min(32, parts - i0);
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float wi = __shfl_sync(kFull, w, i);
+      const float* src = part(i0 + i) + (size_t)row * kD;
+#pragma unroll
+      for (int c = 0; c < kPer / 2; ++c) {
+        const float2 x = reinterpret_cast<const float2*>(src)[c * 32 + lane];
+        acc[2 * c] += wi * x.x;
+        acc[2 * c + 1] += wi * x.y;
+      }
+    }
+  }
+  const float inv = 1.f / sum;
+  const int token = at / p.G, head = note.z * p.G + at % p.G;
+  T* dst = static_cast<T*>(p.o) + (req.row0 + token) * p.o_row + head * p.o_head;
+#pragma unroll
+  for (int c = 0; c < kPer / 2; ++c) {
+    const int col = (c * 32 + lane) * 2;
+    if constexpr (sizeof(T) == 2) {
+      *reinterpret_cast<__nv_bfloat162*>(dst + col) = __floats2bfloat162_rn(acc[2 * c] * inv, acc[2 * c + 1] * inv);
+    } else {
+      *reinterpret_cast<float2*>(dst + col) = make_float2(acc[2 * c] * inv, acc[2 * c + 1] * inv);
+    }
+  }
+}
+
+template <typename Kernel, typename... Args>
+int launch(Kernel kernel, dim3 grid, dim3 block, size_t smem, cudaStream_t st, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) return GDN_ERR_LAUNCH;
+  return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+}
+
+}  // namespace gdnattn

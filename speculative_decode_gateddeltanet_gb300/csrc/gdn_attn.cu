@@ -1,0 +1,296 @@
+// Attention of a request's new tokens over its pages: argument checks, the
+// launch, and the kernel on the CUDA cores.
+//
+// simt_kernel: one pass over K and V with the running maximum and sum of the
+//   softmax, 32-bit arithmetic throughout.  A block of four warps holds 32 rows
+//   (token, query head) of one kv head and walks blocks of 32 keys staged in
+//   shared memory.  Scores: a lane is a key, a warp's eight rows in registers;
+//   the row of K it reads is padded by four words so that the 16-byte reads of
+//   a quarter warp fall into different banks, q is broadcast.  Output: a lane
+//   owns d/32 columns of the eight rows.  Bound by the 32-bit multiply-add rate
+//   when a kv head has many rows, by HBM when it has few.
+#include "attn_common.cuh"
+
+namespace gdnattn {
+
+constexpr int kSimtRows = 32, kSimtKeys = 32, kSimtThreads = 128;
+constexpr int kSimtMinUnits = 4;  // a block does 128 keys at least: below that the join costs more than the split saves
+
+template <typename T>
+__device__ __forceinline__ float4 load4(const T* p) {
+  if constexpr (sizeof(T) == 4) {
+    return *reinterpret_cast<const float4*>(p);
+  } else {
+    const uint2 w = *reinterpret_cast<const uint2*>(p);
+    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                       __uint_as_float(w.y & 0xffff0000u));
+  }
+}
+
+template <int kD>
+constexpr int simt_smem() {
+  return (kSimtRows * kD + kSimtKeys * (kD + 4) + kSimtKeys * kD + kSimtRows * kSimtKeys) * (int)sizeof(float);
+}
+
+template <typename T, int kD>
+__global__ void __launch_bounds__(kSimtThreads) simt_kernel(const Params p) {
+  constexpr int kR = kSimtRows, kN = kSimtKeys, kWarpRows = kR / 4, kCols = kD / 32, kChunks = kD / 4;
+  extern __shared__ float4 smem4[];
+  float* const qs = reinterpret_cast<float*>(smem4);  // [kR][kD]
+  float* const ks = qs + kR * kD;                     // [kN][kD + 4]
+  float* const vs = ks + kN * (kD + 4);               // [kN][kD]
+  float* const ps = vs + kN * kD;                     // [kR][kN]
+  __shared__ long long scan[kSimtThreads / 32];
+  __shared__ Start start;
+  __shared__ int64_t k_at[kN], v_at[kN];  // element offsets of the block's keys; -1: no key
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  find_start<kR, kN, kSimtThreads>(p, kSimtMinUnits, scan, &start);
+  const Start s = start;
+  int4 note = {0, 0, 0, 0};
+  Walk<kR, kN> w;
+  if (begin(w, p, s)) {
+    for (; !w.done(); w.next()) {
+      const int rows = (int)min((long long)kR, (long long)w.req.n * p.G - (long long)w.m * kR);
+      __syncthreads();
+      for (int i = tid; i < kR * kChunks; i += kSimtThreads) {
+        const int r = i / kChunks, c = i % kChunks, at = w.m * kR + r;
+        float4 x = {0.f, 0.f, 0.f, 0.f};
+        if (r < rows)
+          x = load4(static_cast<const T*>(p.q) + (w.req.row0 + at / p.G) * p.q_row + (w.h * p.G + at % p.G) * p.q_head + 4 * c);
+        reinterpret_cast<float4*>(qs)[i] = x;
+      }
+      float top[kWarpRows], sum[kWarpRows], acc[kWarpRows][kCols];
+      int last[kWarpRows];  // the last position a row sees
+#pragma unroll
+      for (int r = 0; r < kWarpRows; ++r) {
+        top[r] = -INFINITY;
+        sum[r] = 0.f;
+        last[r] = w.req.ctx + (w.m * kR + warp * kWarpRows + r) / p.G;
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) acc[r][c] = 0.f;
+      }
+      const int len = w.req.ctx + w.req.n;
+      for (int kb = w.kb0; kb < w.kb1; ++kb) {
+        __syncthreads();
+        if (tid < kN) {
+          const int j = kb * kN + tid;
+          k_at[tid] = v_at[tid] = -1;
+          if (j < len) {
+            const int i = j / p.page_size, token = j - i * p.page_size;
+            const int page = p.table[(size_t)w.b * p.table_stride + i];
+            if ((unsigned)page < (unsigned)p.n_pages) {
+              k_at[tid] = page * p.k_page + w.h * p.k_head + token * p.k_token;
+              v_at[tid] = page * p.v_page + w.h * p.v_head + token * p.v_token;
+            } else if (p.status) {
+              atomicOr(p.status, GDN_STATUS_BAD_PAGE);
+            }
+          }
+        }
+        __syncthreads();
+#pragma unroll 4
+        for (int i = tid; i < kN * kChunks; i += kSimtThreads) {
+          const int j = i / kChunks, c = i % kChunks;
+          float4 kx = {0.f, 0.f, 0.f, 0.f}, vx = kx;
+          if (k_at[j] >= 0) {
+            kx = load4(static_cast<const T*>(p.k) + k_at[j] + 4 * c);
+            vx = load4(static_cast<const T*>(p.v) + v_at[j] + 4 * c);
+          }
+          *reinterpret_cast<float4*>(ks + j * (kD + 4) + 4 * c) = kx;
+          *reinterpret_cast<float4*>(vs + j * kD + 4 * c) = vx;
+        }
+        __syncthreads();
+        float sc[kWarpRows] = {};
+#pragma unroll 4
+        for (int c = 0; c < kChunks; ++c) {
+          const float4 kx = *reinterpret_cast<const float4*>(ks + lane * (kD + 4) + 4 * c);
+#pragma unroll
+          for (int r = 0; r < kWarpRows; ++r) {
+            const float4 qx = *reinterpret_cast<const float4*>(qs + (warp * kWarpRows + r) * kD + 4 * c);
+            sc[r] = fmaf(qx.x, kx.x, sc[r]);
+            sc[r] = fmaf(qx.y, kx.y, sc[r]);
+            sc[r] = fmaf(qx.z, kx.z, sc[r]);
+            sc[r] = fmaf(qx.w, kx.w, sc[r]);
+          }
+        }
+        const int j = kb * kN + lane;
+#pragma unroll
+        for (int r = 0; r < kWarpRows; ++r) {
+          const float x = j <= last[r] ? sc[r] * p.scale_log2 : -INFINITY;
+          float m = x;
+#pragma unroll
+          for (int off = 16; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, off));
+          m = fmaxf(m, top[r]);
+          const float base = m == -INFINITY ? 0.f : m;  // no key yet: exp2(-inf - 0) = 0
+          const float shrink = exp2f(top[r] - base), e = exp2f(x - base);
+          top[r] = m;
+          sum[r] = sum[r] * shrink + e;  // this lane's share
+#pragma unroll
+          for (int c = 0; c < kCols; ++c) acc[r][c] *= shrink;
+          ps[(warp * kWarpRows + r) * kN + lane] = e;
+        }
+        __syncwarp();
+#pragma unroll 2
+        for (int j4 = 0; j4 < kN; j4 += 4) {
+          float vx[4][kCols];
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int c = 0; c < kCols / 2; ++c) {
+              const float2 x = *reinterpret_cast<const float2*>(vs + (j4 + u) * kD + (c * 32 + lane) * 2);
+              vx[u][2 * c] = x.x;
+              vx[u][2 * c + 1] = x.y;
+            }
+#pragma unroll
+          for (int r = 0; r < kWarpRows; ++r) {
+            const float4 e = *reinterpret_cast<const float4*>(ps + (warp * kWarpRows + r) * kN + j4);
+            const float es[4] = {e.x, e.y, e.z, e.w};
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+              for (int c = 0; c < kCols; ++c) acc[r][c] = fmaf(es[u], vx[u][c], acc[r][c]);
+          }
+        }
+        __syncwarp();
+      }
+      const bool whole = w.kb0 == 0 && w.kb1 == w.blocks;
+      const int slot = w.kb0 == 0 ? 1 : 0;
+      if (!whole && slot == 1) note = {followers(w, s), w.b, w.h, w.m};
+      float* const out = partial(p, blockIdx.x, slot, kR);
+#pragma unroll
+      for (int r = 0; r < kWarpRows; ++r) {
+        float l = sum[r];
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) l += __shfl_xor_sync(kFull, l, off);
+        const int row = warp * kWarpRows + r, at = w.m * kR + row;
+        if (row >= rows) continue;
+        if (whole) {
+          const float inv = 1.f / l;
+          T* dst = static_cast<T*>(p.o) + (w.req.row0 + at / p.G) * p.o_row + (w.h * p.G + at % p.G) * p.o_head;
+#pragma unroll
+          for (int c = 0; c < kCols / 2; ++c) {
+            const int col = (c * 32 + lane) * 2;
+            const float x = acc[r][2 * c] * inv, y = acc[r][2 * c + 1] * inv;
+            if constexpr (sizeof(T) == 2) *reinterpret_cast<__nv_bfloat162*>(dst + col) = __floats2bfloat162_rn(x, y);
+            else *reinterpret_cast<float2*>(dst + col) = make_float2(x, y);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < kCols / 2; ++c)
+            *reinterpret_cast<float2*>(out + row * kD + (c * 32 + lane) * 2) = make_float2(acc[r][2 * c], acc[r][2 * c + 1]);
+          if (lane == 0) reinterpret_cast<float2*>(out + kR * kD)[row] = make_float2(top[r], l);
+        }
+      }
+    }
+  }
+  if (tid == 0) p.notes[blockIdx.x] = note;
+}
+
+// blocks of the launch: a fixed number per d and type (as many as 152 SMs hold
+// at once), so that the work buffer's size depends on neither lengths nor device
+constexpr int kSms = 152;
+constexpr int simt_blocks(int d) { return kSms * (d == 256 ? 2 : 4); }
+
+size_t work_bytes(int d, int) {
+  const size_t blocks = simt_blocks(d);
+  return blocks * sizeof(int4) + blocks * 2 * kSimtRows * (d + 2) * sizeof(float);
+}
+
+template <typename T, int kD>
+int run_simt(Params& p, cudaStream_t st) {
+  constexpr int smem = simt_smem<kD>();
+  if (smem > 48 * 1024 &&
+      cudaFuncSetAttribute(simt_kernel<T, kD>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return GDN_ERR_LAUNCH;
+  p.n_blocks = simt_blocks(kD);
+  const int rc = launch(simt_kernel<T, kD>, dim3(p.n_blocks), dim3(kSimtThreads), smem, st, p);
+  if (rc != GDN_OK) return rc;
+  return launch(combine_kernel<T, kD, kSimtRows>, dim3(p.n_blocks, kSimtRows / 4), dim3(128), 0, st, p);
+}
+
+template <typename T>
+int run_simt(Params& p, cudaStream_t st) {
+  return p.d == 64 ? run_simt<T, 64>(p, st) : p.d == 128 ? run_simt<T, 128>(p, st) : run_simt<T, 256>(p, st);
+}
+
+int check_sizes(const gdn_paged_attn_args* a) {
+  if (!a) return GDN_ERR_INVALID_ARG;
+  if (a->B < 0 || a->R < 0 || a->H_kv < 1 || a->H_q < 1 || a->page_size < 1 || a->n_pages < 1 || a->max_pages < 0 ||
+      a->table_stride < a->max_pages || a->n_q_rows < 0)
+    return GDN_ERR_INVALID_ARG;
+  if (a->in_dtype != GDN_DTYPE_BF16 && a->in_dtype != GDN_DTYPE_F32) return GDN_ERR_UNSUPPORTED;
+  if ((a->d != 64 && a->d != 128 && a->d != 256) || a->H_q % a->H_kv != 0 || a->H_q / a->H_kv > 128 ||
+      (int64_t)a->n_pages * a->page_size > INT32_MAX || (int64_t)a->B * a->R > INT32_MAX)
+    return GDN_ERR_UNSUPPORTED;
+  if (a->in_dtype == GDN_DTYPE_BF16 && (a->page_size % 16 != 0 || a->page_size > 1024)) return GDN_ERR_UNSUPPORTED;
+  return GDN_OK;
+}
+
+int check(const gdn_paged_attn_args* a) {
+  const int rc = check_sizes(a);
+  if (rc != GDN_OK) return rc;
+  if (!(a->scale - a->scale == 0.f)) return GDN_ERR_INVALID_ARG;  // not finite
+  if (a->B == 0 || a->n_q_rows == 0) return GDN_OK;
+  if (!a->q || !a->k_cache || !a->v_cache || !a->block_table || !a->ctx_len || !a->n_rows || !a->o || !a->work)
+    return GDN_ERR_INVALID_ARG;
+  if (a->R == 0 && !a->row_start) return GDN_ERR_INVALID_ARG;
+  const int size = a->in_dtype == GDN_DTYPE_BF16 ? 2 : 4;
+  const int64_t strides[] = {a->q_row_stride, a->q_head_stride, a->k_page_stride, a->k_head_stride, a->k_token_stride,
+                             a->v_page_stride, a->v_head_stride, a->v_token_stride, a->o_row_stride, a->o_head_stride};
+  for (int64_t s : strides)
+    if (s * size % 16 != 0) return GDN_ERR_MISALIGNED;
+  auto al = [](const void* ptr, uintptr_t n) { return reinterpret_cast<uintptr_t>(ptr) % n == 0; };
+  if (!al(a->q, 16) || !al(a->k_cache, 16) || !al(a->v_cache, 16) || !al(a->o, 16) || !al(a->work, 16) ||
+      !al(a->block_table, 4) || !al(a->ctx_len, 4) || !al(a->n_rows, 4) || !al(a->row_start, 4) || !al(a->status, 4))
+    return GDN_ERR_MISALIGNED;
+  return GDN_OK;
+}
+
+}  // namespace gdnattn
+
+using namespace gdnattn;
+
+extern "C" GDN_API size_t gdn_paged_attention_work_bytes(const gdn_paged_attn_args* args) {
+  return check_sizes(args) == GDN_OK ? work_bytes(args->d, args->in_dtype) : 0;
+}
+
+extern "C" GDN_API int gdn_paged_attention(const gdn_paged_attn_args* a, void* stream) {
+  const int rc = check(a);
+  if (rc != GDN_OK || a->B == 0 || a->n_q_rows == 0) return rc;
+  Params p;
+  p.B = a->B;
+  p.R = a->R;
+  p.H_kv = a->H_kv;
+  p.G = a->H_q / a->H_kv;
+  p.d = a->d;
+  p.page_size = a->page_size;
+  p.n_pages = a->n_pages;
+  p.table_stride = a->table_stride;
+  p.n_q_rows = a->n_q_rows;
+  p.max_tokens = (int64_t)a->max_pages * a->page_size;
+  p.scale_log2 = (float)((double)a->scale * 1.4426950408889634);
+  p.q = a->q;
+  p.q_row = a->q_row_stride;
+  p.q_head = a->q_head_stride;
+  p.k = a->k_cache;
+  p.k_page = a->k_page_stride;
+  p.k_head = a->k_head_stride;
+  p.k_token = a->k_token_stride;
+  p.v = a->v_cache;
+  p.v_page = a->v_page_stride;
+  p.v_head = a->v_head_stride;
+  p.v_token = a->v_token_stride;
+  p.table = a->block_table;
+  p.ctx_len = a->ctx_len;
+  p.n_rows = a->n_rows;
+  p.row_start = a->row_start;
+  p.o = a->o;
+  p.o_row = a->o_row_stride;
+  p.o_head = a->o_head_stride;
+  p.status = a->status;
+  p.notes = static_cast<int4*>(a->work);
+  p.partials = reinterpret_cast<float*>(p.notes + simt_blocks(p.d));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return a->in_dtype == GDN_DTYPE_BF16 ? run_simt<__nv_bfloat16>(p, st) : run_simt<float>(p, st);
+}

@@ -13,8 +13,9 @@ from pathlib import Path
 
 PKG = Path(__file__).resolve().parent
 ROOT = PKG.parent
-SOURCES = [PKG / "csrc" / f"{name}.cu" for name in ("gdn_spec", "gdn_accept", "gdn_pages", "gdn_attn", "gdn_sample")]
-HEADERS = [ROOT / "include" / "gdnspec.h", ROOT / "include" / "gdnhybrid.h", PKG / "csrc" / "attn_common.cuh"]
+SOURCES = [PKG / "csrc" / f"{name}.cu" for name in ("gdn_spec", "gdn_accept", "gdn_pages", "gdn_attn", "gdn_attn_tc", "gdn_sample")]
+HEADERS = [ROOT / "include" / "gdnspec.h", ROOT / "include" / "gdnhybrid.h", PKG / "csrc" / "attn_common.cuh",
+           PKG / "csrc" / "attn_tc.h"]
 LIB = PKG / "_lib" / "libgdnspec.so"
 # test-only variant: the verify/commit kernels with GDN_TEST_HOOKS (a state copy
 # that can be declared and never issued) and a 2 ms staging-wait limit, for the

@@ -234,6 +234,8 @@ __device__ __forceinline__ float* partial(const Params& p, int block, int slot, 
   return p.partials + (size_t)(block * 2 + slot) * rows * (p.d + 2);
 }
 
+constexpr int kCombineRows = 32;  // rows that the combine blocks of one split tile take at a time
+
 // one warp per row: joins the partials of the split tile that block
 // blockIdx.x begins, in block order
 template <typename T, int kD, int kRows>
@@ -244,52 +246,54 @@ __global__ void __launch_bounds__(128) combine_kernel(const Params p) {
   const int parts = note.x + 1;
   if (parts <= 1) return;
   const Request req = request(p, note.y);
-  const int row = blockIdx.y * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int at = note.w * kRows + row;
-  if ((long long)at >= (long long)req.n * p.G) return;
+  const int lane = threadIdx.x & 31;
+  const int rows = (int)min((long long)kRows, (long long)req.n * p.G - (long long)note.w * kRows);
   auto part = [&](int i) { return partial(p, blockIdx.x + i, i == 0, kRows); };
-  auto stats = [&](int i) { return reinterpret_cast<const float2*>(part(i) + (size_t)kRows * kD)[row]; };
-  float top = -INFINITY;
-  for (int i = lane; i < parts; i += 32) top = fmaxf(top, stats(i).x);
-#pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
-  if (top == -INFINITY) top = 0.f;
-  constexpr int kPer = kD / 32;
-  float acc[kPer] = {};
-  float sum = 0.f;
-  for (int i0 = 0; i0 < parts; i0 += 32) {
-    float w = 0.f, l = 0.f;
-    if (i0 + lane < parts) {
-      const float2 s = stats(i0 + lane);
-      w = exp2f(s.x - top);
-      l = s.y * w;
-    }
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) l += __shfl_xor_sync(kFull, l, off);
-    sum += l;
-    const int n = min(32, parts - i0);
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const float wi = __shfl_sync(kFull, w, i);
-      const float* src = part(i0 + i) + (size_t)row * kD;
-#pragma unroll
-      for (int c = 0; c < kPer / 2; ++c) {
-        const float2 x = reinterpret_cast<const float2*>(src)[c * 32 + lane];
-        acc[2 * c] += wi * x.x;
-        acc[2 * c + 1] += wi * x.y;
+  for (int row = blockIdx.y * 4 + (threadIdx.x >> 5); row < rows; row += kCombineRows) {
+    auto stats = [&](int i) { return reinterpret_cast<const float2*>(part(i) + (size_t)kRows * kD)[row]; };
+    float top = -INFINITY;
+    for (int i = lane; i < parts; i += 32) top = fmaxf(top, stats(i).x);
+  #pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
+    if (top == -INFINITY) top = 0.f;
+    constexpr int kPer = kD / 32;
+    float acc[kPer] = {};
+    float sum = 0.f;
+    for (int i0 = 0; i0 < parts; i0 += 32) {
+      float w = 0.f, l = 0.f;
+      if (i0 + lane < parts) {
+        const float2 s = stats(i0 + lane);
+        w = exp2f(s.x - top);
+        l = s.y * w;
+      }
+  #pragma unroll
+      for (int off = 16; off >= 1; off >>= 1) l += __shfl_xor_sync(kFull, l, off);
+      sum += l;
+      const int n = min(32, parts - i0);
+  #pragma unroll 4
+      for (int i = 0; i < n; ++i) {
+        const float wi = __shfl_sync(kFull, w, i);
+        const float* src = part(i0 + i) + (size_t)row * kD;
+  #pragma unroll
+        for (int c = 0; c < kPer / 2; ++c) {
+          const float2 x = reinterpret_cast<const float2*>(src)[c * 32 + lane];
+          acc[2 * c] += wi * x.x;
+          acc[2 * c + 1] += wi * x.y;
+        }
       }
     }
-  }
-  const float inv = 1.f / sum;
-  const int token = at / p.G, head = note.z * p.G + at % p.G;
-  T* dst = static_cast<T*>(p.o) + (req.row0 + token) * p.o_row + head * p.o_head;
-#pragma unroll
-  for (int c = 0; c < kPer / 2; ++c) {
-    const int col = (c * 32 + lane) * 2;
-    if constexpr (sizeof(T) == 2) {
-      *reinterpret_cast<__nv_bfloat162*>(dst + col) = __floats2bfloat162_rn(acc[2 * c] * inv, acc[2 * c + 1] * inv);
-    } else {
-      *reinterpret_cast<float2*>(dst + col) = make_float2(acc[2 * c] * inv, acc[2 * c + 1] * inv);
+    const float inv = 1.f / sum;
+    const int at = note.w * kRows + row;
+    const int token = at / p.G, head = note.z * p.G + at % p.G;
+    T* dst = static_cast<T*>(p.o) + (int64_t)(req.row0 + token) * p.o_row + head * p.o_head;
+  #pragma unroll
+    for (int c = 0; c < kPer / 2; ++c) {
+      const int col = (c * 32 + lane) * 2;
+      if constexpr (sizeof(T) == 2) {
+        *reinterpret_cast<__nv_bfloat162*>(dst + col) = __floats2bfloat162_rn(acc[2 * c] * inv, acc[2 * c + 1] * inv);
+      } else {
+        *reinterpret_cast<float2*>(dst + col) = make_float2(acc[2 * c] * inv, acc[2 * c + 1] * inv);
+      }
     }
   }
 }

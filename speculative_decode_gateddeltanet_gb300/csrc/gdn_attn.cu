@@ -1,5 +1,5 @@
 // Attention of a request's new tokens over its pages: argument checks, the
-// launch, and the kernel on the CUDA cores.
+// launch, and the 32-bit kernel, on the CUDA cores.
 //
 // simt_kernel: one pass over K and V with the running maximum and sum of the
 //   softmax, 32-bit arithmetic throughout.  A block of four warps holds 32 rows
@@ -10,29 +10,21 @@
 //   owns d/32 columns of the eight rows.  Bound by the 32-bit multiply-add rate
 //   when a kv head has many rows, by HBM when it has few.
 #include "attn_common.cuh"
+#include "attn_tc.h"
 
 namespace gdnattn {
 
 constexpr int kSimtRows = 32, kSimtKeys = 32, kSimtThreads = 128;
 constexpr int kSimtMinUnits = 4;  // a block does 128 keys at least: below that the join costs more than the split saves
 
-template <typename T>
-__device__ __forceinline__ float4 load4(const T* p) {
-  if constexpr (sizeof(T) == 4) {
-    return *reinterpret_cast<const float4*>(p);
-  } else {
-    const uint2 w = *reinterpret_cast<const uint2*>(p);
-    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
-                       __uint_as_float(w.y & 0xffff0000u));
-  }
-}
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 
 template <int kD>
 constexpr int simt_smem() {
   return (kSimtRows * kD + kSimtKeys * (kD + 4) + kSimtKeys * kD + kSimtRows * kSimtKeys) * (int)sizeof(float);
 }
 
-template <typename T, int kD>
+template <int kD>
 __global__ void __launch_bounds__(kSimtThreads) simt_kernel(const Params p) {
   constexpr int kR = kSimtRows, kN = kSimtKeys, kWarpRows = kR / 4, kCols = kD / 32, kChunks = kD / 4;
   extern __shared__ float4 smem4[];
@@ -58,7 +50,7 @@ __global__ void __launch_bounds__(kSimtThreads) simt_kernel(const Params p) {
         const int r = i / kChunks, c = i % kChunks, at = w.m * kR + r;
         float4 x = {0.f, 0.f, 0.f, 0.f};
         if (r < rows)
-          x = load4(static_cast<const T*>(p.q) + (w.req.row0 + at / p.G) * p.q_row + (w.h * p.G + at % p.G) * p.q_head + 4 * c);
+          x = load4(static_cast<const float*>(p.q) + (w.req.row0 + at / p.G) * p.q_row + (w.h * p.G + at % p.G) * p.q_head + 4 * c);
         reinterpret_cast<float4*>(qs)[i] = x;
       }
       float top[kWarpRows], sum[kWarpRows], acc[kWarpRows][kCols];
@@ -94,8 +86,8 @@ __global__ void __launch_bounds__(kSimtThreads) simt_kernel(const Params p) {
           const int j = i / kChunks, c = i % kChunks;
           float4 kx = {0.f, 0.f, 0.f, 0.f}, vx = kx;
           if (k_at[j] >= 0) {
-            kx = load4(static_cast<const T*>(p.k) + k_at[j] + 4 * c);
-            vx = load4(static_cast<const T*>(p.v) + v_at[j] + 4 * c);
+            kx = load4(static_cast<const float*>(p.k) + k_at[j] + 4 * c);
+            vx = load4(static_cast<const float*>(p.v) + v_at[j] + 4 * c);
           }
           *reinterpret_cast<float4*>(ks + j * (kD + 4) + 4 * c) = kx;
           *reinterpret_cast<float4*>(vs + j * kD + 4 * c) = vx;
@@ -167,13 +159,12 @@ __global__ void __launch_bounds__(kSimtThreads) simt_kernel(const Params p) {
         if (row >= rows) continue;
         if (whole) {
           const float inv = 1.f / l;
-          T* dst = static_cast<T*>(p.o) + (w.req.row0 + at / p.G) * p.o_row + (w.h * p.G + at % p.G) * p.o_head;
+          float* dst = static_cast<float*>(p.o) + (w.req.row0 + at / p.G) * p.o_row + (w.h * p.G + at % p.G) * p.o_head;
 #pragma unroll
           for (int c = 0; c < kCols / 2; ++c) {
             const int col = (c * 32 + lane) * 2;
             const float x = acc[r][2 * c] * inv, y = acc[r][2 * c + 1] * inv;
-            if constexpr (sizeof(T) == 2) *reinterpret_cast<__nv_bfloat162*>(dst + col) = __floats2bfloat162_rn(x, y);
-            else *reinterpret_cast<float2*>(dst + col) = make_float2(x, y);
+            *reinterpret_cast<float2*>(dst + col) = make_float2(x, y);
           }
         } else {
 #pragma unroll
@@ -192,26 +183,27 @@ __global__ void __launch_bounds__(kSimtThreads) simt_kernel(const Params p) {
 constexpr int kSms = 152;
 constexpr int simt_blocks(int d) { return kSms * (d == 256 ? 2 : 4); }
 
-size_t work_bytes(int d, int) {
-  const size_t blocks = simt_blocks(d);
-  return blocks * sizeof(int4) + blocks * 2 * kSimtRows * (d + 2) * sizeof(float);
+int blocks_of(int d, int dtype) { return dtype == GDN_DTYPE_BF16 ? tc_blocks() : simt_blocks(d); }
+
+size_t work_bytes(int d, int dtype) {
+  const size_t blocks = blocks_of(d, dtype), rows = dtype == GDN_DTYPE_BF16 ? tc_rows() : kSimtRows;
+  return blocks * sizeof(int4) + blocks * 2 * rows * (d + 2) * sizeof(float);
 }
 
-template <typename T, int kD>
+template <int kD>
 int run_simt(Params& p, cudaStream_t st) {
   constexpr int smem = simt_smem<kD>();
   if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(simt_kernel<T, kD>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+      cudaFuncSetAttribute(simt_kernel<kD>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return GDN_ERR_LAUNCH;
   p.n_blocks = simt_blocks(kD);
-  const int rc = launch(simt_kernel<T, kD>, dim3(p.n_blocks), dim3(kSimtThreads), smem, st, p);
+  const int rc = launch(simt_kernel<kD>, dim3(p.n_blocks), dim3(kSimtThreads), smem, st, p);
   if (rc != GDN_OK) return rc;
-  return launch(combine_kernel<T, kD, kSimtRows>, dim3(p.n_blocks, kSimtRows / 4), dim3(128), 0, st, p);
+  return launch(combine_kernel<float, kD, kSimtRows>, dim3(p.n_blocks, kCombineRows / 4), dim3(128), 0, st, p);
 }
 
-template <typename T>
 int run_simt(Params& p, cudaStream_t st) {
-  return p.d == 64 ? run_simt<T, 64>(p, st) : p.d == 128 ? run_simt<T, 128>(p, st) : run_simt<T, 256>(p, st);
+  return p.d == 64 ? run_simt<64>(p, st) : p.d == 128 ? run_simt<128>(p, st) : run_simt<256>(p, st);
 }
 
 int check_sizes(const gdn_paged_attn_args* a) {
@@ -290,7 +282,7 @@ extern "C" GDN_API int gdn_paged_attention(const gdn_paged_attn_args* a, void* s
   p.o_head = a->o_head_stride;
   p.status = a->status;
   p.notes = static_cast<int4*>(a->work);
-  p.partials = reinterpret_cast<float*>(p.notes + simt_blocks(p.d));
+  p.partials = reinterpret_cast<float*>(p.notes + blocks_of(p.d, a->in_dtype));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return a->in_dtype == GDN_DTYPE_BF16 ? run_simt<__nv_bfloat16>(p, st) : run_simt<float>(p, st);
+  return a->in_dtype == GDN_DTYPE_BF16 ? run_tc(p, st) : run_simt(p, st);
 }

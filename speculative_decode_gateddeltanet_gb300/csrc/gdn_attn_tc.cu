@@ -1,0 +1,579 @@
+// Paged attention in bf16 on the 5th-generation tensor cores.
+//
+// One block per SM walks its share of (tile of 128 rows, key block) units.  A
+// tile's rows are the query heads of one kv head over its tokens, so K and V
+// are read once for the whole group.  Per key block j:
+//   S = Q K^T       tcgen05.mma, Q and K from shared memory, S (32-bit) in TMEM
+//   P = 2^(s - m)   one thread per row: running maximum m, running sum, P to
+//                   TMEM as bf16 over S's columns
+//   O += P V        tcgen05.mma, P from TMEM, V from shared memory, O in TMEM
+// S has two buffers: the tensor cores form S of block j+1 while the softmax
+// works on block j, so the two overlap and the longer of them sets the pace.
+//
+// Roles (256 threads): warps 0-3 softmax and output, warp 4 issues the MMAs,
+// warp 5 the TMA copies of K and V, warps 6-7 stage Q and clear the V rows
+// behind a request's last token.
+//
+// A page is copied in boxes of 64 columns by a power of two of tokens that
+// divides the page, straight into the 128-byte-swizzled layout the MMA reads;
+// pools of any strides are the tensor map's affair.  V is used as it lies (its
+// columns are the MMA's N), so nothing is transposed.
+//
+// The running maximum is raised only when it would grow by more than 2^8:
+// until then P stays below 2^8 and its sum is exact enough in 32 bits, and O
+// (in TMEM) need not be rescaled.  P is rounded to bf16 for the second product
+// (2^-9 of each weight); sums stay in 32 bits.
+//
+// Every wait is bounded by time; when one runs out the block flags it, sets
+// GDN_STATUS_TIMEOUT, waits (bounded) for its own copies and products in
+// flight, frees its TMEM and ends.
+#include <cuda.h>
+
+#include <mutex>
+
+#include "attn_common.cuh"
+#include "attn_tc.h"
+
+namespace gdnattn {
+
+constexpr int kTcRows = 128;
+constexpr int kTcThreads = 256;
+constexpr int kTcBlocks = 152;  // one block per SM of a GB300
+constexpr int kTcMinUnits = 1;
+constexpr unsigned long long kWaitNs = 2000000000ull;
+
+template <int kD>
+struct Shape {
+  static constexpr int kKeys = kD == 256 ? 64 : 128;
+  static constexpr int kChunks = kD / 64;                 // 128-byte column chunks of a row
+  static constexpr int kQBytes = kTcRows * kD * 2;
+  static constexpr int kTileBytes = kKeys * kD * 2;       // a K or V tile
+  static constexpr int kK = kD == 64 ? 6 : 3;             // K tiles in flight
+  static constexpr int kV = kD == 64 ? 6 : kD == 128 ? 3 : 2;
+  static constexpr int kSmem = 1024 + kQBytes + (kK + kV) * kTileBytes;
+};
+static_assert(Shape<128>::kSmem <= 230 * 1024 && Shape<256>::kSmem <= 230 * 1024 && Shape<64>::kSmem <= 230 * 1024);
+
+// ---- PTX -------------------------------------------------------------------
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ void bar_init(uint32_t bar, int count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok;
+}
+__device__ __forceinline__ unsigned long long now_ns() {
+  unsigned long long t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+
+// false when the wait ran out or another role gave up
+__device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, volatile int* gave_up) {
+  const unsigned long long end = now_ns() + kWaitNs;
+  while (!bar_try(bar, parity)) {
+    if (*gave_up) return false;
+    if (now_ns() > end) {
+      *gave_up = 1;
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
+  if (bar_try(bar, parity)) return true;
+  return bar_wait_slow(bar, parity, gave_up);
+}
+
+// the same for a whole warp: all lanes go on, or none
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
+  return __all_sync(kFull, bar_wait(bar, parity, gave_up));
+}
+
+__device__ __forceinline__ void tma_box(const CUtensorMap* map, uint32_t dst, uint32_t bar, int col, int token, int head, int page) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(map), "r"(col), "r"(token), "r"(head), "r"(page), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+
+#define GDN_R4(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3])
+#define GDN_W4(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3])
+// 32 columns of this thread's TMEM lane
+__device__ __forceinline__ void tmem_load(uint32_t (&r)[32], uint32_t at) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : GDN_R4(r, 0), GDN_R4(r, 4), GDN_R4(r, 8), GDN_R4(r, 12), GDN_R4(r, 16), GDN_R4(r, 20), GDN_R4(r, 24), GDN_R4(r, 28)
+      : "r"(at));
+}
+__device__ __forceinline__ void tmem_store(uint32_t at, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(at),
+      GDN_W4(r, 0), GDN_W4(r, 4), GDN_W4(r, 8), GDN_W4(r, 12), GDN_W4(r, 16), GDN_W4(r, 20), GDN_W4(r, 24), GDN_W4(r, 28)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// shared-memory operand descriptor, 128-byte swizzle: start address, the two
+// strides in 16-byte units, version 1
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead, uint32_t stride) {
+  return (uint64_t)((addr >> 4) & 0x3fff) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(stride >> 4) << 32 | 1ull << 46 | 2ull << 61;
+}
+// bf16 x bf16 -> 32-bit, M = 128; transpose_b: B's N is its contiguous dimension
+__host__ __device__ constexpr uint32_t instruction(int n, bool transpose_b) {
+  return 1u << 4 | 1u << 7 | 1u << 10 | (transpose_b ? 1u << 16 : 0) | (uint32_t)(n >> 3) << 17 | (uint32_t)(kTcRows >> 4) << 24;
+}
+
+struct TcParams {
+  Params p;
+  int box;          // tokens per TMA box: a power of two that divides the page and kKeys
+  uint32_t q_flip;  // sign bits to flip in q: a negative scale is taken into q, exactly
+};
+
+template <int kD>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    tc_kernel(const TcParams t, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
+  using S = Shape<kD>;
+  constexpr int kKeys = S::kKeys, kChunks = S::kChunks;
+  const Params& p = t.p;
+  extern __shared__ uint8_t raw[];
+  __shared__ __align__(8) uint64_t bars[2 * S::kK + 2 * S::kV + 11];
+  __shared__ long long scan[kTcThreads / 32];
+  __shared__ Start start;
+  __shared__ uint32_t tmem_base;
+  __shared__ int gave_up;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
+  const uint32_t q_s = base, k_s = q_s + S::kQBytes, v_s = k_s + S::kK * S::kTileBytes;
+  const uint32_t b0 = smem_addr(bars);
+  auto k_full = [&](int i) { return b0 + 8 * i; };
+  auto k_empty = [&](int i) { return b0 + 8 * (S::kK + i); };
+  auto v_full = [&](int i) { return b0 + 8 * (2 * S::kK + i); };
+  auto v_empty = [&](int i) { return b0 + 8 * (2 * S::kK + S::kV + i); };
+  constexpr int kRest = 2 * S::kK + 2 * S::kV;
+  auto s_full = [&](int i) { return b0 + 8 * (kRest + i); };    // S of a block is in TMEM
+  auto p_ready = [&](int i) { return b0 + 8 * (kRest + 2 + i); };  // its P is
+  const uint32_t pv_done = b0 + 8 * (kRest + 4), q_full = b0 + 8 * (kRest + 5), q_empty = b0 + 8 * (kRest + 6),
+                 o_free = b0 + 8 * (kRest + 7), drained = b0 + 8 * (kRest + 10);
+  // the Q warps may clear for the next segment before the MMA warp asks for this one's: two in turn
+  auto v_clear = [&](int i) { return b0 + 8 * (kRest + 8 + (i & 1)); };
+  if (tid == 0) {
+    gave_up = 0;
+    for (int i = 0; i < S::kK; ++i) {
+      bar_init(k_full(i), 1);
+      bar_init(k_empty(i), 1);
+    }
+    for (int i = 0; i < S::kV; ++i) {
+      bar_init(v_full(i), 1);
+      bar_init(v_empty(i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      bar_init(s_full(i), 1);
+      bar_init(p_ready(i), 128);
+    }
+    bar_init(pv_done, 1);
+    bar_init(q_full, 64);
+    bar_init(q_empty, 1);
+    bar_init(o_free, 128);
+    bar_init(v_clear(0), 64);
+    bar_init(v_clear(1), 64);
+    bar_init(drained, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 4) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&tmem_base)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_wait();
+  pdl_trigger();
+  const uint32_t tmem = tmem_base;
+  find_start<kTcRows, kKeys, kTcThreads>(p, kTcMinUnits, scan, &start);
+  const Start s = start;
+  constexpr uint32_t kOCol = 2 * kKeys;  // TMEM columns: two S buffers, then O
+  int4 note = {0, 0, 0, 0};
+  Walk<kTcRows, kKeys> w;
+  const bool any = begin(w, p, s);
+  bool ok = true;
+  int k_sent = 0, v_sent = 0;  // tiles whose copies were issued
+
+  if (any && warp < 4) {
+    // ---- softmax and output: one thread per row
+    const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
+    int it = 0, seen = 0;
+    // O holds the products of blocks up to i.  A parity tells the current phase of pv_done from the one before it
+    // only, so its phases are waited for one by one, each once.
+    auto products = [&](int i) {
+      for (; seen <= i; ++seen)
+        if (!warp_wait(pv_done, seen & 1, &gave_up)) return false;
+      return true;
+    };
+    for (; ok && !w.done(); w.next()) {
+      const int rows = (int)min((long long)kTcRows, (long long)w.req.n * p.G - (long long)w.m * kTcRows);
+      const bool active = warp * 32 < rows;  // a warp with no row only keeps step
+      const int at = w.m * kTcRows + tid;
+      const int last = tid < rows ? w.req.ctx + at / p.G : -1;
+      float top = -INFINITY, sum = 0.f;
+      for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
+        const int buf = it & 1;
+        if (!(ok = warp_wait(s_full(buf), (it >> 1) & 1, &gave_up))) break;
+        if (!(ok = products(it - 2))) break;
+        if (active) {
+          tc_fence_after();
+          uint32_t x[kKeys / 32][32];
+#pragma unroll
+          for (int c = 0; c < kKeys / 32; ++c) tmem_load(x[c], lanes + buf * kKeys + c * 32);
+          tmem_wait_load();
+          const int edge = last - kb * kKeys;  // columns up to edge are seen
+          if (edge < kKeys - 1) {
+#pragma unroll
+            for (int c = 0; c < kKeys / 32; ++c)
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (c * 32 + i > edge) x[c][i] = 0xff800000u;
+          }
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int c = 0; c < kKeys / 32; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(x[c][i]));
+          const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.scale_log2;
+          const bool raise = mx > top + 8.f;  // also the first time: top is -inf
+          if (__any_sync(kFull, raise)) {
+            const float m = raise ? mx : top;
+            const float shrink = raise ? ex2(top - mx) : 1.f;
+            sum *= shrink;
+            top = m;
+            if (kb > w.kb0) {
+              if (!(ok = products(it - 1))) break;
+              tc_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < kD / 32; ++c) {
+                uint32_t o[32];
+                tmem_load(o, lanes + kOCol + c * 32);
+                tmem_wait_load();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * shrink);
+                tmem_store(lanes + kOCol + c * 32, o);
+              }
+              tmem_wait_store();
+            }
+          }
+          const float sub = top == -INFINITY ? 0.f : top;
+          float s4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < kKeys / 32; c += 2) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float e0 = ex2(fmaf(__uint_as_float(x[c + i / 16][(2 * i) & 31]), p.scale_log2, -sub));
+              const float e1 = ex2(fmaf(__uint_as_float(x[c + i / 16][(2 * i + 1) & 31]), p.scale_log2, -sub));
+              s4[(2 * i) & 3] += e0;
+              s4[(2 * i + 1) & 3] += e1;
+              pk[i] = pack_bf16(e0, e1);
+            }
+            tmem_store(lanes + buf * kKeys + c * 16, pk);
+          }
+          sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+          tmem_wait_store();
+          tc_fence_before();
+        }
+        bar_arrive(p_ready(buf));
+      }
+      if (!ok || !(ok = products(it - 1))) break;
+      const bool whole = w.kb0 == 0 && w.kb1 == w.blocks;
+      const int slot = w.kb0 == 0 ? 1 : 0;
+      if (!whole && slot == 1) note = {followers(w, s), w.b, w.h, w.m};
+      if (active) {
+        tc_fence_after();
+        float* const out = partial(p, blockIdx.x, slot, kTcRows);
+        const float inv = 1.f / sum;
+        __nv_bfloat16* const dst = static_cast<__nv_bfloat16*>(p.o) + (int64_t)(w.req.row0 + at / p.G) * p.o_row +
+                                   (int64_t)(w.h * p.G + at % p.G) * p.o_head;
+#pragma unroll 1
+        for (int c = 0; c < kD / 32; ++c) {
+          uint32_t o[32];
+          tmem_load(o, lanes + kOCol + c * 32);
+          tmem_wait_load();
+          if (tid < rows) {
+            if (whole) {
+              uint32_t pk[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) pk[i] = pack_bf16(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                reinterpret_cast<uint4*>(dst + c * 32)[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                reinterpret_cast<uint4*>(out + tid * kD + c * 32)[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            }
+          }
+        }
+        if (!whole && tid < rows) reinterpret_cast<float2*>(out + kTcRows * kD)[tid] = make_float2(top, sum);
+        tc_fence_before();
+      }
+      bar_arrive(o_free);
+    }
+  } else if (any && warp == 4) {
+    // ---- the MMAs, issued by one thread
+    if (lane == 0) {
+      constexpr uint32_t kQk = instruction(kKeys, false), kPv = instruction(kD, true);
+      int it = 0, seg = 0;
+      int cuts = 0;
+      for (; ok && !w.done(); w.next(), ++seg) {
+        if (!(ok = bar_wait(q_full, seg & 1, &gave_up))) break;
+        const int len = w.req.ctx + w.req.n;
+        for (int kb = w.kb0; kb <= w.kb1; ++kb) {
+          if (kb < w.kb1) {
+            const int i = it + kb - w.kb0, st = i % S::kK, buf = i & 1;
+            if (!(ok = bar_wait(k_full(st), (i / S::kK) & 1, &gave_up))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < kD / 16; ++k) {
+              const uint32_t q_at = q_s + (k / 4) * (kTcRows * 128) + (k % 4) * 32;
+              const uint32_t k_at = k_s + st * S::kTileBytes + (k / 4) * (kKeys * 128) + (k % 4) * 32;
+              mma_ss(tmem + buf * kKeys, operand(q_at, 16, 1024), operand(k_at, 16, 1024), kQk, k > 0);
+            }
+            tc_commit(k_empty(st));
+            tc_commit(s_full(buf));
+            if (kb == w.kb1 - 1) tc_commit(q_empty);
+          }
+          if (kb > w.kb0) {
+            const int i = it + kb - 1 - w.kb0, buf = i & 1, st = i % S::kV;
+            const bool first = kb - 1 == w.kb0, cut = kb * kKeys > len;  // block kb - 1 reaches behind the last token
+            ok = bar_wait(p_ready(buf), (i >> 1) & 1, &gave_up) && bar_wait(v_full(st), (i / S::kV) & 1, &gave_up);
+            if (ok && first && seg > 0) ok = bar_wait(o_free, (seg - 1) & 1, &gave_up);
+            if (ok && cut) {
+              ok = bar_wait(v_clear(cuts), (cuts >> 1) & 1, &gave_up);
+              ++cuts;
+            }
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < kKeys / 16; ++k)
+              mma_ts(tmem + kOCol, tmem + buf * kKeys + k * 8, operand(v_s + st * S::kTileBytes + k * 2048, kKeys * 128, 1024),
+                     kPv, !(first && k == 0));
+            tc_commit(v_empty(st));
+            tc_commit(pv_done);
+          }
+        }
+        it += w.kb1 - w.kb0;
+      }
+    }
+    __syncwarp();
+  } else if (any && warp == 5) {
+    // ---- K and V tiles by TMA: lane (box, chunk) copies its box of 64 columns
+    const int n_box = kKeys / t.box, box = lane / kChunks, chunk = lane % kChunks;
+    const uint32_t at = (uint32_t)chunk * (kKeys * 128) + (uint32_t)box * t.box * 128;
+    int it = 0;
+    for (; ok && !w.done(); w.next()) {
+      const int len = w.req.ctx + w.req.n;
+      const int32_t* const row = p.table + (size_t)w.b * p.table_stride;
+      int page = 0, token = 0;
+      auto find_page = [&](int kb) {
+        const int j = kb * kKeys + box * t.box;
+        if (box < n_box && j < len) {
+          const int i = j / p.page_size;
+          token = j - i * p.page_size;
+          page = row[i];
+          if ((unsigned)page >= (unsigned)p.n_pages) {
+            page = p.n_pages;  // outside the map: zeros
+            if (p.status) atomicOr(p.status, GDN_STATUS_BAD_PAGE);
+          }
+        }
+      };
+      find_page(w.kb0);
+      for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
+        const int live = min(n_box, (len - kb * kKeys + t.box - 1) / t.box);
+        const uint32_t bytes = (uint32_t)live * t.box * kD * 2;
+        const bool mine = box < live;
+        const int my_page = page, my_token = token;
+        if (kb + 1 < w.kb1) find_page(kb + 1);  // its latency hides behind the waits below
+        const int ks = it % S::kK, vs = it % S::kV;
+        if (!(ok = warp_wait(k_empty(ks), ((it / S::kK) & 1) ^ 1, &gave_up))) break;
+        if (lane == 0) bar_expect(k_full(ks), bytes);
+        __syncwarp();
+        if (mine) tma_box(&k_map, k_s + ks * S::kTileBytes + at, k_full(ks), chunk * 64, my_token, w.h, my_page);
+        k_sent = it + 1;
+        if (!(ok = warp_wait(v_empty(vs), ((it / S::kV) & 1) ^ 1, &gave_up))) break;
+        if (lane == 0) bar_expect(v_full(vs), bytes);
+        __syncwarp();
+        if (mine) tma_box(&v_map, v_s + vs * S::kTileBytes + at, v_full(vs), chunk * 64, my_token, w.h, my_page);
+        v_sent = it + 1;
+      }
+    }
+  } else if (any) {
+    // ---- Q rows into the swizzled layout, and the V rows behind the last token
+    const int q_tid = tid - 192;
+    int it = 0, seg = 0, cuts = 0;
+    for (; ok && !w.done(); w.next(), ++seg) {
+      const int rows = (int)min((long long)kTcRows, (long long)w.req.n * p.G - (long long)w.m * kTcRows);
+      if (seg > 0 && !(ok = bar_wait(q_empty, (seg - 1) & 1, &gave_up))) break;
+      constexpr int kUnits = kD / 8;  // 16-byte units of a row
+#pragma unroll 8
+      for (int i = q_tid; i < rows * kUnits; i += 64) {
+        const int r = i / kUnits, u = i % kUnits, at = w.m * kTcRows + r;
+        uint4 x = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + (int64_t)(w.req.row0 + at / p.G) * p.q_row +
+                                                  (int64_t)(w.h * p.G + at % p.G) * p.q_head + u * 8);
+        x.x ^= t.q_flip;
+        x.y ^= t.q_flip;
+        x.z ^= t.q_flip;
+        x.w ^= t.q_flip;
+        const uint32_t dst = q_s + (u / 8) * (kTcRows * 128) + r * 128 + (((u & 7) ^ (r & 7)) << 4);
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
+      }
+      fence_async();
+      bar_arrive(q_full);
+      it += w.kb1 - w.kb0;
+      const int valid = w.req.ctx + w.req.n - (w.kb1 - 1) * kKeys;
+      if (valid < kKeys) {
+        const int vi = it - 1, st = vi % S::kV;
+        if (!(ok = bar_wait(v_full(st), (vi / S::kV) & 1, &gave_up))) break;
+        for (int i = q_tid; i < (kKeys - valid) * kUnits; i += 64) {
+          const int r = valid + i / kUnits, u = i % kUnits;
+          const uint32_t dst = v_s + st * S::kTileBytes + (u / 8) * (kKeys * 128) + r * 128 + ((u & 7) << 4);
+          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst), "r"(0) : "memory");
+        }
+        fence_async();
+        bar_arrive(v_clear(cuts));
+        ++cuts;
+      }
+    }
+  }
+  if (tid == 0) p.notes[blockIdx.x] = note;
+  __syncthreads();
+  if (gave_up) {
+    // products and copies that may still be in flight, with a bound again
+    const unsigned long long end = now_ns() + kWaitNs;
+    if (tid == 128) {
+      tc_commit(drained);
+      while (!bar_try(drained, 0) && now_ns() < end) {
+      }
+    }
+    if (tid == 160) {
+      for (int i = max(0, k_sent - S::kK); i < k_sent; ++i)
+        while (!bar_try(k_full(i % S::kK), (i / S::kK) & 1) && now_ns() < end) {
+        }
+      for (int i = max(0, v_sent - S::kV); i < v_sent; ++i)
+        while (!bar_try(v_full(i % S::kV), (i / S::kV) & 1) && now_ns() < end) {
+        }
+    }
+    if (tid == 0 && p.status) atomicOr(p.status, GDN_STATUS_TIMEOUT);
+    __syncthreads();
+  }
+  if (warp == 4) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                              CUtensorMapFloatOOBfill);
+
+EncodeFn encoder() {
+  static EncodeFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) == cudaSuccess &&
+        found == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeFn>(f);
+  });
+  return fn;
+}
+
+bool make_map(CUtensorMap* map, const Params& p, const void* base, int64_t token, int64_t head, int64_t page, int box) {
+  const EncodeFn encode = encoder();
+  if (!encode) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)p.d, (cuuint64_t)p.page_size, (cuuint64_t)p.H_kv, (cuuint64_t)p.n_pages};
+  // the stride of a dimension of one entry is never used, but must be a valid one
+  const cuuint64_t strides[3] = {(cuuint64_t)token * 2, (cuuint64_t)(p.H_kv > 1 ? head : token) * 2,
+                                 (cuuint64_t)(p.n_pages > 1 ? page : token) * 2};
+  const cuuint32_t box_dims[4] = {64, (cuuint32_t)box, 1, 1}, steps[4] = {1, 1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box_dims, steps,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int tc_blocks() { return kTcBlocks; }
+int tc_rows() { return kTcRows; }
+
+template <int kD>
+int run(TcParams& t, cudaStream_t st) {
+  using S = Shape<kD>;
+  if (cudaFuncSetAttribute(tc_kernel<kD>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem) != cudaSuccess) return GDN_ERR_LAUNCH;
+  t.box = 16;
+  while (t.box * 2 <= S::kKeys && t.p.page_size % (t.box * 2) == 0) t.box *= 2;
+  CUtensorMap k_map, v_map;
+  if (!make_map(&k_map, t.p, t.p.k, t.p.k_token, t.p.k_head, t.p.k_page, t.box) ||
+      !make_map(&v_map, t.p, t.p.v, t.p.v_token, t.p.v_head, t.p.v_page, t.box))
+    return GDN_ERR_LAUNCH;
+  t.p.n_blocks = kTcBlocks;
+  const int rc = launch(tc_kernel<kD>, dim3(kTcBlocks), dim3(kTcThreads), S::kSmem, st, t, k_map, v_map);
+  if (rc != GDN_OK) return rc;
+  return launch(combine_kernel<__nv_bfloat16, kD, kTcRows>, dim3(kTcBlocks, kCombineRows / 4), dim3(128), 0, st, t.p);
+}
+
+int run_tc(Params& p, cudaStream_t st) {
+  TcParams t{p, 0, 0};
+  if (t.p.scale_log2 < 0.f) {
+    t.q_flip = 0x80008000u;
+    t.p.scale_log2 = -t.p.scale_log2;
+  }
+  // a hidden score is -inf, and -inf * 0 would be NaN
+  if (t.p.scale_log2 < 1e-30f) t.p.scale_log2 = 1e-30f;
+  return p.d == 64 ? run<64>(t, st) : p.d == 128 ? run<128>(t, st) : run<256>(t, st);
+}
+
+}  // namespace gdnattn

@@ -214,8 +214,8 @@ GDN_API size_t gdn_paged_attention_work_bytes(const gdn_paged_attn_args* args);
  *   drafts  [B][R-1] int32 (NULL: no accept_len wanted, or R == 1); n_rows [B]
  *   target  [B][R] int32, prob [B][R] fp32 (may be NULL): rows t >= n_rows[b] are not written
  *   accept_len [B] int32 (NULL: not wanted); 0 for inactive requests and for a bad n_rows
- * Supported: V <= 2^20, B, R <= 65535.  Rows are staged in shared memory across
- * a cluster of blocks: V up to GDN_SAMPLE_MAX_STAGED bytes of logits. */
+ * Supported: V <= GDN_SAMPLE_MAX_V (a row is staged in the shared memory of at
+ * most eight blocks), B, R <= 65535. */
 typedef struct gdn_sample_args {
   int32_t B, R, V;
   int32_t in_dtype;
@@ -233,7 +233,7 @@ typedef struct gdn_sample_args {
   int32_t* accept_len;
   int32_t* status;
 } gdn_sample_args;
-#define GDN_SAMPLE_MAX_STAGED ((size_t)8 * 192 * 1024)
+#define GDN_SAMPLE_MAX_V 393216
 GDN_API int gdn_sample_accept(const gdn_sample_args* args, void* stream);
 
 #ifdef __cplusplus

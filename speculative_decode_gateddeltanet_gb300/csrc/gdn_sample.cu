@@ -2,16 +2,29 @@
 // top-p and min-p from given random numbers.
 //
 // The order of a row's tokens (largest logit first, equal logits by lowest
-// index) makes top-k and top-p prefixes of one order, so no sort is needed: a
-// prefix is a threshold key and the number of tokens with exactly that key that
-// belong to it.  Both are found by radix selection over the logits' ordered
-// bits, eight bits a level, with counts (top-k) or weight sums (top-p) per
-// digit.  The weights are whole numbers (32 bits of exp), their sums exact in
-// 64 bits, so atomics and any split of the row give the same sums, and the
-// drawn token does not depend on either.
+// index) makes top-k and top-p prefixes of one order, so no row is sorted: a
+// prefix is a threshold key (the logit's ordered bits) and the number of tokens
+// with exactly that key that belong to it.  The weights are whole numbers (32
+// bits of exp), their sums exact in 64 bits, so atomics and any split of the row
+// give the same sums, and the drawn token does not depend on either.
 //
-// sample_kernel: one block per verify row.  accept_kernel: one thread per
-// request.
+// sample_kernel: a cluster of 1 to 8 blocks per verify row.  Each block stages
+//   its slice of the row in shared memory (the logits are read from HBM once)
+//   and keeps the maximum of each thread's elements.
+//   - top_k up to kList / 2: the k-th largest thread maximum is a bound that at
+//     least k tokens reach, and few more do.  Those are appended to one list
+//     in the first block, which sorts it and finishes alone: no other pass over
+//     the row.
+//   - otherwise (or if equal logits overflow the list): a histogram of weight
+//     sums (top-p) or counts (a large top_k) over kBins equal steps of the
+//     logit below the maximum finds the step that holds the prefix' end, and
+//     8-bit digits of the keys inside that step find the key.  Equal steps, not
+//     the keys' own leading digits, spread the bulk of the logits over the bins,
+//     so few lanes of a warp add to the same one.  The kept weights are then
+//     summed in index order and the draw located.
+//   A row of some 10^5 tokens is bound by instructions (a pass with exp costs
+//   several times the HBM read) and by the cluster's barriers, not by HBM.
+// accept_kernel: one thread per request.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -21,16 +34,18 @@
 namespace gdnsample {
 
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kThreads = 1024;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kMaxCluster = 8;
+constexpr int kBins = 1024;
+constexpr int kList = 2048;  // candidates that the first block can sort
+constexpr int kMaxSlice = 49152;  // elements a block stages: 192 KB in 32 bits; sums of 16-bit halves fit 32 bits
+static_assert(kMaxSlice * kMaxCluster == GDN_SAMPLE_MAX_V, "a row is staged by one cluster");
 
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 using u64 = unsigned long long;
-
-__device__ __forceinline__ float value(const float* p) { return __ldg(p); }
-__device__ __forceinline__ float value(const __nv_bfloat16* p) { return __bfloat162float(__ldg(p)); }
 
 // bits that order as the values do; 0 for NaN, which takes no part.  -0 equals +0.
 __device__ __forceinline__ uint32_t key_of(float x) {
@@ -62,202 +77,568 @@ __device__ __forceinline__ u64 warp_sum(u64 v) {
   return v;
 }
 
-__device__ __forceinline__ u64 block_sum(u64 v, u64* part) {
-  v = warp_sum(v);
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t peer(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void put(uint32_t at, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
+__device__ __forceinline__ void put(uint32_t at, u64 v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t get(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 get4(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t add_at(uint32_t at, uint32_t v) {
+  uint32_t old;
+  asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(old) : "r"(at), "r"(v) : "memory");
+  return old;
+}
+__device__ __forceinline__ void min_at(uint32_t at, uint32_t v) {
+  asm volatile("red.shared::cluster.min.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ float number(float x) { return x; }
+__device__ __forceinline__ float number(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// inclusive prefix over the block's threads
+__device__ __forceinline__ u64 block_scan(u64 v, u64* part) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const u64 o = __shfl_up_sync(kFull, v, off);
+    if (lane >= off) v += o;
+  }
+  if (lane == 31) part[warp] = v;
   __syncthreads();
-  u64 s = 0;
-  for (int w = 0; w < kWarps; ++w) s += part[w];
+  for (int w = 0; w < warp; ++w) v += part[w];
   __syncthreads();
-  return s;
+  return v;
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) sample_kernel(const gdn_sample_args p) {
-  __shared__ u64 hist[256];
-  __shared__ u64 part[kWarps], part2[kWarps];
-  __shared__ uint32_t s_key;
-  __shared__ u64 s_sum;
+struct Unit {  // the elements of 16 bytes
+  static constexpr int kN = 16 / sizeof(T);
+  float x[kN];
+  __device__ explicit Unit(const uint4& w) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 2) {
+        x[2 * i] = __uint_as_float(u[i] << 16);
+        x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+      } else {
+        x[i] = __uint_as_float(u[i]);
+      }
+    }
+  }
+};
+
+// descending order of n = a power of two of 64-bit words in shared memory
+__device__ void sort_descending(u64* v, int n) {
+  for (int k = 2; k <= n; k <<= 1)
+    for (int j = k >> 1; j > 0; j >>= 1) {
+      for (int i = threadIdx.x; i < n / 2; i += kThreads) {
+        const int a = 2 * i - (i & (j - 1)), b = a + j;
+        const u64 x = v[a], y = v[b];
+        if ((x < y) == ((a & k) == 0)) {
+          v[a] = y;
+          v[b] = x;
+        }
+      }
+      __syncthreads();
+    }
+}
+
+__device__ __forceinline__ int pow2_at_least(int n) { return n <= 1 ? 1 : 1 << (32 - __clz(n - 1)); }
+
+struct News {  // what the first block tells the others
+  u64 left;
+  uint32_t top_key, bound, low, digit;  // low: the smallest thread maximum
+};
+
+// the rest of a row whose candidates lie in `list`: the first c of its m in order are the top-k tokens
+template <typename T>
+__device__ void finish_list(const gdn_sample_args& p, size_t at, const T* row, u64* list, int m, int c, float top_p, float floor_w,
+                            u64 u, const Weight& weight, u64* part) {
+  const int tid = threadIdx.x;
+  constexpr int kMost = kList / 2 / kThreads;
+  __shared__ u64 total_s;
+  __shared__ int kept_s;
+  const int padded = pow2_at_least(m);
+  for (int i = m + tid; i < padded; i += kThreads) list[i] = 0;
+  __syncthreads();
+  sort_descending(list, padded);
+  // a thread has `per` neighbours of the order
+  int per = (c + kThreads - 1) / kThreads, i0 = min(c, tid * per), i1 = min(c, i0 + per);
+  u64 words[kMost];
+  uint32_t W[kMost];
+  u64 sum = 0;
+#pragma unroll
+  for (int j = 0; j < kMost; ++j) {
+    if (i0 + j < i1) {
+      words[j] = list[i0 + j];
+      W[j] = weight.whole(of_key(words[j] >> 32));
+      sum += W[j];
+    }
+  }
+  u64 upto = block_scan(sum, part);
+  if (tid == kThreads - 1) total_s = upto;
+  if (tid == 0) kept_s = 0;
+  __syncthreads();
+  const u64 limit = top_p < 1.f ? shift_mul(total_s, fraction(top_p, 1.f)) : ~0ull;
+  u64 before = upto - sum;
+  int kept = 0;
+#pragma unroll
+  for (int j = 0; j < kMost; ++j) {
+    if (i0 + j < i1) {
+      const bool in = before < limit || i0 + j == 0;
+      before += W[j];
+      kept += in;
+      // ascending index, the weight beside it; a token that a filter drops keeps its place with no weight
+      list[i0 + j] = in && weight.w(of_key(words[j] >> 32)) >= floor_w ? words[j] << 32 | W[j] : in ? words[j] << 32 : 0;
+    }
+  }
+  if (kept) atomicAdd(&kept_s, kept);
+  __syncthreads();
+  c = kept_s;
+  const int padded_c = pow2_at_least(c);
+  for (int i = c + tid; i < padded_c; i += kThreads) list[i] = 0;
+  __syncthreads();
+  sort_descending(list, padded_c);
+  per = (c + kThreads - 1) / kThreads;
+  i0 = min(c, tid * per);
+  i1 = min(c, i0 + per);
+  sum = 0;
+  for (int i = i0; i < i1; ++i) sum += (uint32_t)list[i];
+  upto = block_scan(sum, part);
+  if (tid == kThreads - 1) total_s = upto;
+  __syncthreads();
+  const u64 drawn = shift_mul(total_s, u);
+  before = upto - sum;
+  if (before <= drawn && drawn < upto) {
+    int i = i0;
+    while (before + (uint32_t)list[i] <= drawn) before += (uint32_t)list[i++];
+    const int token = (int)~(uint32_t)(list[i] >> 32);
+    p.target[at] = token;
+    if (p.prob) p.prob[at] = weight.w(number(row[token])) * 2147483648.f / (float)total_s;
+  }
+}
+
+struct Place {  // a block's kept weight above the threshold, and its tokens on it
+  u64 sum, equal;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) sample_kernel(const gdn_sample_args p, int blocks, int slice_units) {
+  constexpr int kN = Unit<T>::kN;
+  extern __shared__ uint4 slice[];                      // [slice_units], then the scratch below
+  uint32_t* const scratch = reinterpret_cast<uint32_t*>(slice + slice_units);
+  u64* const list = reinterpret_cast<u64*>(scratch);     // [kList]
+  uint32_t* const lo = scratch;                          // [kBins] sums of the weights' low halves
+  uint32_t* const hi = scratch + kBins;                  // [kBins] and high halves
+  uint32_t* const maxima = scratch;                      // [blocks][kThreads]
+  __shared__ u64 part[kWarps];
+  __shared__ News news;
+  __shared__ Place places[kMaxCluster], warps[kWarps];
+  __shared__ uint32_t count, lowest, all_s, digits[256];
+  __shared__ u64 total_s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int t = blockIdx.x, b = blockIdx.y, V = p.V;
+  const uint32_t rank = cluster_rank();
+  const int t = blockIdx.x / blocks, b = blockIdx.y;
   pdl_wait();
   pdl_trigger();
   const int n = p.n_rows[b];
-  if (n <= 0 || n > p.R || t >= n) return;
+  if (n <= 0 || n > p.R || t >= n) return;  // the whole cluster
+  cluster_arrive();  // every block of the cluster runs before any writes to another's shared memory
   const size_t at = (size_t)b * p.R + t;
-  const T* row = static_cast<const T*>(p.logits) + at * p.row_stride;
+  const T* const row = static_cast<const T*>(p.logits) + at * p.row_stride;
   const float temp = p.temperature ? p.temperature[b] : 1.f;
   const int k = p.top_k ? p.top_k[b] : 0;
   const float top_p = p.top_p ? p.top_p[b] : 1.f, min_p = p.min_p ? p.min_p[b] : 0.f;
+  const u64 u = fraction(p.u[at], 1.f - 1.f / 16777216.f);
 
-  // the largest key, lowest index: one 64-bit maximum of (key, ~index)
-  u64 best = 0;
-  for (int i = tid; i < V; i += kThreads) {
-    const u64 c = (u64)key_of(value(row + i)) << 32 | (uint32_t)~i;
-    best = c > best ? c : best;
-  }
+  // stage the slice in units of 16 aligned bytes; what is not of the row is NaN
+  const int shift = (int)(reinterpret_cast<uintptr_t>(row) % 16 / sizeof(T));
+  const int units = (p.V + shift + kN - 1) / kN, per = (units + blocks - 1) / blocks;
+  const int u0 = min(units, (int)rank * per), own = min(units, u0 + per) - u0;
+  const int first = u0 * kN - shift;  // the row's index of the slice's first element
+  const uint4* const src = reinterpret_cast<const uint4*>(row - shift) + u0;
+  float top = __uint_as_float(0x7fffffffu);  // NaN: no element yet
+  constexpr int kUnroll = 8;
+  for (int i0 = tid; i0 < own; i0 += kUnroll * kThreads) {
+    uint4 w[kUnroll];
 #pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) {
-    const u64 o = __shfl_xor_sync(kFull, best, off);
-    best = o > best ? o : best;
+    for (int j = 0; j < kUnroll; ++j) {
+      const int i = i0 + j * kThreads, e = first + i * kN;
+      if (i < own) {
+        if (e >= 0 && e + kN <= p.V) {
+          w[j] = __ldcs(src + i);  // read once
+        } else {
+          T x[kN];
+#pragma unroll
+          for (int c = 0; c < kN; ++c) {
+            if constexpr (sizeof(T) == 2) x[c] = e + c >= 0 && e + c < p.V ? row[e + c] : __ushort_as_bfloat16(0x7fff);
+            else x[c] = e + c >= 0 && e + c < p.V ? row[e + c] : __uint_as_float(0x7fffffffu);
+          }
+          w[j] = *reinterpret_cast<uint4*>(x);
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kUnroll; ++j) {
+      const int i = i0 + j * kThreads;
+      if (i < own) {
+        slice[i] = w[j];
+        const Unit<T> x(w[j]);
+#pragma unroll
+        for (int c = 0; c < kN; ++c) top = fmaxf(top, x.x[c]);  // NaN loses
+      }
+    }
   }
-  if (lane == 0) part[warp] = best;
-  __syncthreads();
-  for (int w = 0; w < kWarps; ++w) best = part[w] > best ? part[w] : best;
-  __syncthreads();
-  const uint32_t top_key = best >> 32;
+  cluster_wait();
+  put(peer(maxima + rank * kThreads + tid, 0), key_of(top));
+  if (tid == 0) {
+    count = 0;
+    lowest = 0xffffffffu;
+  }
+  cluster_sync();
+
+  // the first block: the row's largest key, and for a top_k that a list can hold the k-th largest thread maximum
+  const bool listed = k > 0 && k < p.V && k <= kList / 2 && temp > 0.f;
+  if (rank == 0) {
+    uint32_t mine[kMaxCluster], best = 0;
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r) {
+      mine[r] = r < blocks ? maxima[r * kThreads + tid] : 0;
+      best = max(best, mine[r]);
+    }
+    best = __reduce_max_sync(kFull, best);
+    if (lane == 0) part[warp] = best;
+    __syncthreads();
+    for (int w = 0; w < kWarps; ++w) best = max(best, (uint32_t)part[w]);
+    uint32_t bound = 1;  // every key but NaN's
+    if (listed) {
+      uint32_t prefix = 0, left = (uint32_t)k;
+      for (int s = 24; s >= (sizeof(T) == 2 ? 16 : 0); s -= 8) {
+        digits[tid] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r)
+          if (mine[r] != 0 && (s == 24 || (mine[r] ^ prefix) >> (s + 8) == 0)) atomicAdd(&digits[mine[r] >> s & 255], 1u);
+        __syncthreads();
+        // thread tid looks at digit 255 - tid: the prefix from the top
+        const uint32_t here = digits[255 - tid];
+        const uint32_t upto = (uint32_t)block_scan(here, part);
+        if (upto - here < left && left <= upto) {
+          news.digit = 255 - tid;
+          news.left = upto - here;
+        }
+        if (tid == kThreads - 1) all_s = upto;
+        __syncthreads();
+        if (all_s < left) {  // fewer maxima than k: every token is a candidate
+          prefix = 0;
+          break;  // at the first digit only
+        }
+        prefix |= news.digit << s;
+        left -= (uint32_t)news.left;
+        __syncthreads();
+      }
+      // a negative bf16's low bits, turned over
+      bound = prefix == 0 ? 1u : sizeof(T) == 2 && !(prefix & 0x80000000u) ? prefix | 0xffff : prefix;
+    }
+    uint32_t low = 0xffffffffu;
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r) low = mine[r] != 0 ? min(low, mine[r]) : low;
+    low = __reduce_min_sync(kFull, low);
+    __syncthreads();
+    if (lane == 0) part[warp] = low;
+    __syncthreads();
+    for (int w = 0; w < kWarps; ++w) low = min(low, (uint32_t)part[w]);
+    if (tid < blocks) {
+      put(peer(&news.top_key, tid), best);
+      put(peer(&news.bound, tid), bound);
+      put(peer(&news.low, tid), low);
+    }
+  }
+  cluster_sync();
+  const uint32_t top_key = news.top_key;
+  const float peak = of_key(top_key);
+
   if (!(temp > 0.f) || top_key == 0) {  // greedy, or a row of NaN alone
-    if (tid == 0) {
-      p.target[at] = top_key == 0 ? 0 : (int)~(uint32_t)best;
+    if (top_key != 0) {
+      uint32_t mine = 0xffffffffu;
+      for (int i = tid; i < own; i += kThreads) {
+        const Unit<T> x(slice[i]);
+#pragma unroll
+        for (int c = kN - 1; c >= 0; --c)
+          if (x.x[c] == peak) mine = min(mine, (uint32_t)(first + i * kN + c));
+      }
+      mine = __reduce_min_sync(kFull, mine);
+      if (lane == 0 && mine != 0xffffffffu) min_at(peer(&lowest, 0), mine);
+    }
+    cluster_sync();
+    if (rank == 0 && tid == 0) {
+      p.target[at] = top_key == 0 ? 0 : (int)lowest;
       if (p.prob) p.prob[at] = 1.f;
     }
     return;
   }
-  const Weight weight{of_key(top_key), 1.f / temp};
-
-  // kept: keys above thr, and the first `ties` tokens (by index) of key thr
-  uint32_t thr = 1;  // every key but NaN's
-  u64 ties = (u64)V;
-  if (k > 0 && k < V) {
-    uint32_t prefix = 0;
-    u64 left = (u64)k;
-    bool all = false;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      for (int i = tid; i < 256; i += kThreads) hist[i] = 0;
-      __syncthreads();
-      for (int i = tid; i < V; i += kThreads) {
-        const uint32_t key = key_of(value(row + i));
-        if (key != 0 && (shift == 24 || (key ^ prefix) >> (shift + 8) == 0)) atomicAdd(&hist[key >> shift & 255], 1ull);
-      }
-      __syncthreads();
-      if (tid == 0) {
-        int d = 255;
-        u64 above = 0;
-        while (d > 0 && above + hist[d] < left) above += hist[d--];
-        s_key = d;
-        s_sum = above;
-        part[0] = hist[d];
-      }
-      __syncthreads();
-      if (shift == 24 && s_sum + part[0] < left) all = true;  // fewer than k tokens that are not NaN
-      prefix |= s_key << shift;
-      left -= s_sum;
-      __syncthreads();
-      if (all) break;
-    }
-    if (!all) {
-      thr = prefix;
-      ties = left;
-    }
-  }
-  if (top_p < 1.f) {
-    u64 sum = 0;
-    for (int i = tid; i < V; i += kThreads) {
-      const float x = value(row + i);
-      if (key_of(x) > thr || (key_of(x) == thr && ties >= (u64)V)) sum += weight.whole(x);
-    }
-    const u64 edge = ties >= (u64)V ? 0 : ties * weight.whole(of_key(thr));  // the tied tokens' share
-    const u64 limit = shift_mul(block_sum(sum, part) + edge, fraction(top_p, 1.f));
-    if (limit == 0) {
-      thr = top_key;
-      ties = 1;
-    } else {
-      uint32_t prefix = 0;
-      u64 left = limit;
-      for (int shift = 24; shift >= 0; shift -= 8) {
-        for (int i = tid; i < 256; i += kThreads) hist[i] = 0;
-        __syncthreads();
-        for (int i = tid; i < V; i += kThreads) {
-          const float x = value(row + i);
-          const uint32_t key = key_of(x);
-          if ((key > thr || (key == thr && ties >= (u64)V)) && (shift == 24 || (key ^ prefix) >> (shift + 8) == 0)) {
-            const uint32_t W = weight.whole(x);
-            if (W) atomicAdd(&hist[key >> shift & 255], (u64)W);
-          }
-        }
-        __syncthreads();
-        if (tid == 0) {
-          if (edge && (shift == 24 || (thr ^ prefix) >> (shift + 8) == 0)) hist[thr >> shift & 255] += edge;
-          int d = 255;
-          u64 above = 0;
-          while (d > 0 && above + hist[d] < left) above += hist[d--];
-          s_key = d;
-          s_sum = above;
-        }
-        __syncthreads();
-        prefix |= s_key << shift;
-        left -= s_sum;
-        __syncthreads();
-      }
-      // tokens of the last key are kept while what came before them is below the limit
-      const u64 W = weight.whole(of_key(prefix));
-      const u64 fit = (left + W - 1) / W;
-      ties = prefix == thr && ties < fit ? ties : fit;
-      thr = prefix;
-    }
-  }
+  const Weight weight{peak, 1.f / temp};
   const float floor_w = min_p > 0.f ? fminf(min_p, 1.f) : 0.f;
-  const bool thr_in = weight.w(of_key(thr)) >= floor_w;
-  const u64 thr_w = thr_in ? weight.whole(of_key(thr)) : 0;
 
-  // index order: each warp has a run of tokens; its kept weight is that of the
-  // keys above thr and of its share of the tied ones
-  const int per = ((V + kWarps - 1) / kWarps + 31) / 32 * 32;
-  const int i0 = min(V, warp * per), i1 = min(V, i0 + per);
-  u64 sum = 0, equal = 0;
-  for (int i = i0 + lane; i < i1; i += 32) {
-    const float x = value(row + i);
-    const uint32_t key = key_of(x);
-    if (key > thr && weight.w(x) >= floor_w) sum += weight.whole(x);
-    equal += key == thr;
-  }
-  sum = warp_sum(sum);
-  equal = warp_sum(equal);
-  if (lane == 0) {
-    part[warp] = sum;
-    part2[warp] = equal;
-  }
-  __syncthreads();
-  u64 total = 0, seen = 0, before = 0, eq_before = 0;
-  for (int w = 0; w < kWarps; ++w) {
-    if (w == warp) {
-      before = total;
-      eq_before = seen;
-    }
-    const u64 eq = seen >= ties ? 0 : min(part2[w], ties - seen);
-    total += part[w] + eq * thr_w;
-    seen += part2[w];
-  }
-  const u64 own_eq = eq_before >= ties ? 0 : min(equal, ties - eq_before);
-  const u64 drawn = shift_mul(total, fraction(p.u[at], 1.f - 1.f / 16777216.f));
-  if (!(before <= drawn && drawn < before + sum + own_eq * thr_w)) return;
-  // the one warp whose run holds the drawn weight walks it
-  for (int i = i0; i < i1; i += 32) {
-    float x = 0.f;
-    uint32_t key = 0;
-    if (i + lane < i1) {
-      x = value(row + i + lane);
-      key = key_of(x);
-    }
-    const unsigned eq = __ballot_sync(kFull, key == thr);
-    const u64 rank = eq_before + __popc(eq & ((1u << lane) - 1));
-    u64 W = key > thr && weight.w(x) >= floor_w ? weight.whole(x) : key == thr && rank < ties ? thr_w : 0;
-    u64 inc = W;
+  if (listed) {
+    const float bound = of_key(news.bound);
+    const bool every = news.bound == 1;
+    const uint32_t counter = peer(&count, 0), to = peer(list, 0);
+    for (int i = tid; i < own; i += kThreads) {
+      const Unit<T> x(slice[i]);
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const u64 o = __shfl_up_sync(kFull, inc, off);
-      if (lane >= off) inc += o;
+      for (int c = 0; c < kN; ++c)
+        if (x.x[c] >= bound || (every && x.x[c] == x.x[c])) {
+          const uint32_t place = add_at(counter, 1u);
+          if (place < kList) put(to + place * 8, (u64)key_of(x.x[c]) << 32 | (uint32_t)~(first + i * kN + c));
+        }
     }
-    const unsigned hit = __ballot_sync(kFull, before + inc > drawn);
-    if (hit) {
-      if (lane == __ffs(hit) - 1) {
-        p.target[at] = i + lane;
-        if (p.prob) p.prob[at] = weight.w(x) * 2147483648.f / (float)total;
+    cluster_sync();
+    const int found = (int)get(counter);
+    if (found <= kList) {
+      if (rank != 0) return;
+      finish_list(p, at, row, list, found, min(k, found), top_p, floor_w, u, weight, part);
+      cluster_sync();  // the others have read `count`, or have left
+      return;
+    }
+    cluster_sync();  // the list's place is the histogram's
+  }
+
+  // ---- the general way.  kept: keys above thr, and the first `ties` tokens (by index) of key thr
+  uint32_t thr = 1;
+  u64 ties = ~0ull;
+  auto narrow = [&](bool weights, float range, u64 want) {
+    // the new threshold: the prefix of the kept tokens whose counts, or weights, reach `want` (for weights: that
+    // share of their sum)
+    const float steps = kBins / range;
+    const bool edged = ties != ~0ull;
+    auto bin_of = [&](float x) { return min(kBins - 1, (int)((peak - x) * steps)); };  // NaN (x == peak): 0
+    auto add = [&](float x, int i) {
+      const uint32_t v = weights ? weight.whole(x) : 1u;
+      if (v & 0xffff) atomicAdd(&lo[i], v & 0xffff);
+      if (v >> 16) atomicAdd(&hi[i], v >> 16);
+    };
+    const u64 edge = edged ? ties * (weights ? weight.whole(of_key(thr)) : 1u) : 0;  // tokens of key thr, not swept
+    const int edge_bin = edged ? bin_of(of_key(thr)) : -1;
+    for (int i = tid; i < kBins; i += kThreads) lo[i] = hi[i] = 0;
+    __syncthreads();
+    for (int i = tid; i < own; i += kThreads) {
+      const Unit<T> x(slice[i]);
+#pragma unroll
+      for (int c = 0; c < kN; ++c) {
+        const uint32_t key = key_of(x.x[c]);
+        if (key > thr || (key == thr && !edged)) add(x.x[c], bin_of(x.x[c]));
+      }
+    }
+    cluster_sync();
+    if (rank == 0) {
+      u64 s[4] = {0, 0, 0, 0};
+      for (int r = 0; r < blocks; ++r) {
+        const uint4 l = get4(peer(lo + 4 * tid, r)), h = get4(peer(hi + 4 * tid, r));
+        s[0] += l.x + ((u64)h.x << 16);
+        s[1] += l.y + ((u64)h.y << 16);
+        s[2] += l.z + ((u64)h.z << 16);
+        s[3] += l.w + ((u64)h.w << 16);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (4 * tid + i == edge_bin) s[i] += edge;
+      u64 upto = block_scan(s[0] + s[1] + s[2] + s[3], part);
+      if (tid == kThreads - 1) total_s = upto;
+      __syncthreads();
+      const u64 limit = weights ? shift_mul(total_s, want) : want;
+      upto -= s[0] + s[1] + s[2] + s[3];
+      if (limit == 0 || total_s < limit) {
+        if (tid < blocks) put(peer(&news.left, tid), 0ull);
+        if (tid < blocks) put(peer(&news.digit, tid), limit == 0 ? 0u : 1u);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (upto < limit && limit <= upto + s[i])
+            for (int r = 0; r < blocks; ++r) {
+              put(peer(&news.left, r), limit - upto);
+              put(peer(&news.digit, r), (uint32_t)(4 * tid + i));
+            }
+          upto += s[i];
+        }
+      }
+    }
+    cluster_sync();
+    u64 left = news.left;
+    if (left == 0) {  // nothing asked for: the first token; or fewer tokens than asked for: all of them
+      if (news.digit == 0) {
+        thr = top_key;
+        ties = 1;
       }
       return;
     }
-    before += __shfl_sync(kFull, inc, 31);
-    eq_before += __popc(eq);
+    const int bin = (int)news.digit;
+    uint32_t prefix = 0;
+    for (int s = 24; s >= (sizeof(T) == 2 ? 16 : 0); s -= 8) {
+      for (int i = tid; i < 256; i += kThreads) lo[i] = hi[i] = 0;
+      __syncthreads();
+      for (int i = tid; i < own; i += kThreads) {
+        const Unit<T> x(slice[i]);
+#pragma unroll
+        for (int c = 0; c < kN; ++c) {
+          if (bin_of(x.x[c]) != bin) continue;
+          const uint32_t key = key_of(x.x[c]);
+          if ((key > thr || (key == thr && !edged)) && (s == 24 || (key ^ prefix) >> (s + 8) == 0)) add(x.x[c], key >> s & 255);
+        }
+      }
+      cluster_sync();
+      if (rank == 0) {
+        const int d = 255 - tid;  // digits from the top
+        u64 v = 0;
+        for (int r = 0; r < blocks; ++r) v += get(peer(lo + d, r)) + ((u64)get(peer(hi + d, r)) << 16);
+        if (edge_bin == bin && (s == 24 || (thr ^ prefix) >> (s + 8) == 0) && (int)(thr >> s & 255) == d) v += edge;
+        const u64 upto = block_scan(v, part);
+        if (upto - v < left && left <= upto)
+          for (int r = 0; r < blocks; ++r) {
+            put(peer(&news.left, r), left - (upto - v));
+            put(peer(&news.digit, r), (uint32_t)d);
+          }
+      }
+      cluster_sync();
+      left = news.left;
+      prefix |= news.digit << s;
+    }
+    if (sizeof(T) == 2 && !(prefix & 0x80000000u)) prefix |= 0xffff;  // a negative bf16's low bits, turned over
+    const u64 W = weights ? weight.whole(of_key(prefix)) : 1;
+    const u64 fit = (left + W - 1) / W;  // tokens of the last key before which the sum is still short
+    ties = edged && prefix == thr ? min(ties, fit) : fit;
+    thr = prefix;
+  };
+  if (k > 0 && k < p.V) narrow(false, 2.f * (peak - of_key(max(news.low, 1u))), (u64)k);
+  if (top_p < 1.f) narrow(true, 22.f * temp, fraction(top_p, 1.f));  // 2^31 exp(-22) < 1/2: weights beyond are 0
+  const bool edged = ties != ~0ull;
+  const bool thr_in = edged && weight.w(of_key(thr)) >= floor_w;
+  const u64 thr_w = thr_in ? weight.whole(of_key(thr)) : 0;
+
+  // index order: each warp has a run of units; its kept weight is that of the keys above thr and of its share of the
+  // tied ones
+  const int run = (own + kWarps - 1) / kWarps, r0 = min(own, warp * run), r1 = min(own, r0 + run);
+  auto above = [&](float x, uint32_t key) -> u64 {
+    if (!(key > thr || (key == thr && !edged))) return 0;
+    return floor_w > 0.f && weight.w(x) < floor_w ? 0 : weight.whole(x);
+  };
+  u64 sum = 0, equal = 0;
+  for (int i = r0 + lane; i < r1; i += 32) {
+    const Unit<T> x(slice[i]);
+#pragma unroll
+    for (int c = 0; c < kN; ++c) {
+      const uint32_t key = key_of(x.x[c]);
+      sum += above(x.x[c], key);
+      equal += edged && key == thr;
+    }
+  }
+  sum = warp_sum(sum);
+  equal = warp_sum(equal);
+  if (lane == 0) warps[warp] = {sum, equal};
+  __syncthreads();
+  if (tid < blocks) {
+    u64 s = 0, e = 0;
+    for (int w = 0; w < kWarps; ++w) {
+      s += warps[w].sum;
+      e += warps[w].equal;
+    }
+    const uint32_t to = peer(&places[rank], tid);
+    put(to, s);
+    put(to + 8, e);
+  }
+  cluster_sync();
+  u64 total = 0, seen = 0, before = 0, eq_before = 0;
+  auto pass = [&](const Place& q) {
+    const u64 take = seen >= ties ? 0 : min(q.equal, ties - seen);
+    seen += q.equal;
+    return q.sum + take * thr_w;
+  };
+  for (int r = 0; r < blocks; ++r) {
+    if (r == (int)rank) {
+      before = total;
+      eq_before = seen;
+    }
+    total += pass(places[r]);
+  }
+  const u64 drawn = shift_mul(total, u);
+  seen = eq_before;
+  for (int w = 0; w < warp; ++w) before += pass(warps[w]);
+  eq_before = seen;
+  const u64 mine = pass(warps[warp]);
+  if (!(before <= drawn && drawn < before + mine)) return;
+  // the one warp whose run holds the drawn weight walks it
+  for (int i0 = r0; i0 < r1; i0 += 32) {
+    const int i = i0 + lane;
+    u64 W[kN], W_all = 0;
+    uint32_t eq = 0;
+    uint4 w = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+    if (i < r1) w = slice[i];
+    const Unit<T> x(w);
+#pragma unroll
+    for (int c = 0; c < kN; ++c) eq += edged && key_of(x.x[c]) == thr;
+    uint32_t eq_upto = eq;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const uint32_t o = __shfl_up_sync(kFull, eq_upto, off);
+      if (lane >= off) eq_upto += o;
+    }
+    u64 place = eq_before + eq_upto - eq;
+#pragma unroll
+    for (int c = 0; c < kN; ++c) {
+      const uint32_t key = key_of(x.x[c]);
+      W[c] = above(x.x[c], key);
+      if (edged && key == thr) W[c] = place++ < ties ? thr_w : 0;
+      W_all += W[c];
+    }
+    u64 upto = W_all;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const u64 o = __shfl_up_sync(kFull, upto, off);
+      if (lane >= off) upto += o;
+    }
+    const unsigned hit = __ballot_sync(kFull, before + upto > drawn);
+    if (hit) {
+      if (lane == __ffs(hit) - 1) {
+        u64 s = before + upto - W_all;
+#pragma unroll
+        for (int c = 0; c < kN; ++c) {
+          if (s <= drawn && drawn < s + W[c]) {
+            p.target[at] = first + i * kN + c;
+            if (p.prob) p.prob[at] = weight.w(x.x[c]) * 2147483648.f / (float)total;
+          }
+          s += W[c];
+        }
+      }
+      return;
+    }
+    before += __shfl_sync(kFull, upto, 31);
+    eq_before += __shfl_sync(kFull, eq_upto, 31);
   }
 }
 
@@ -279,18 +660,23 @@ __global__ void __launch_bounds__(256) accept_kernel(const gdn_sample_args p) {
   p.accept_len[b] = a;
 }
 
-template <typename Kernel>
-int launch(Kernel kernel, dim3 grid, dim3 block, cudaStream_t st, const gdn_sample_args& p) {
+template <typename Kernel, typename... Args>
+int launch(Kernel kernel, dim3 grid, dim3 block, int cluster, size_t smem, cudaStream_t st, const Args&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kernel, p) != cudaSuccess) return GDN_ERR_LAUNCH;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) return GDN_ERR_LAUNCH;
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_LAUNCH;
 }
 
@@ -299,7 +685,7 @@ int check(const gdn_sample_args* a) {
   if (a->B < 0 || a->R < 1 || a->V < 1 || a->row_stride < a->V) return GDN_ERR_INVALID_ARG;
   if (a->in_dtype != GDN_DTYPE_BF16 && a->in_dtype != GDN_DTYPE_F32) return GDN_ERR_UNSUPPORTED;
   const size_t size = a->in_dtype == GDN_DTYPE_BF16 ? 2 : 4;
-  if (a->V > (1 << 20) || a->V * size > GDN_SAMPLE_MAX_STAGED || a->B > 65535 || a->R > 65535) return GDN_ERR_UNSUPPORTED;
+  if (a->V > GDN_SAMPLE_MAX_V || a->B > 65535 || a->R > 65535) return GDN_ERR_UNSUPPORTED;
   if (a->B == 0) return GDN_OK;
   if (!a->logits || !a->u || !a->n_rows || !a->target || (a->R > 1 && a->accept_len && !a->drafts))
     return GDN_ERR_INVALID_ARG;
@@ -312,6 +698,29 @@ int check(const gdn_sample_args* a) {
   return GDN_OK;
 }
 
+// Blocks per row: enough that a slice is at most 40 KB (four blocks of 256 threads fit an SM beside their scratch),
+// and more, down to slices of 2 KB, while the rows alone do not give every SM two blocks.
+int cluster_of(int64_t rows, int64_t bytes) {
+  int c = 1;
+  while (c < kMaxCluster && bytes > 40 * 1024 * (int64_t)c) c *= 2;
+  while (c < kMaxCluster && rows * c < 304 && bytes > 2048 * (int64_t)c) c *= 2;
+  return c;
+}
+
+template <typename T>
+int run(const gdn_sample_args& p, cudaStream_t st) {
+  constexpr int kN = Unit<T>::kN;
+  const int blocks = cluster_of((int64_t)p.B * p.R, (int64_t)p.V * sizeof(T));
+  const int units = (p.V + 2 * (kN - 1)) / kN;  // at the worst alignment
+  const int slice_units = (units + blocks - 1) / blocks;
+  const int smem = slice_units * 16 + kList * 8;
+  // the largest slice's size, so that calls of any V from any thread set the same value
+  if (smem > 40 * 1024 &&
+      cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024) != cudaSuccess)
+    return GDN_ERR_LAUNCH;
+  return launch(sample_kernel<T>, dim3(p.R * blocks, p.B), dim3(kThreads), blocks, smem, st, p, blocks, slice_units);
+}
+
 }  // namespace gdnsample
 
 using namespace gdnsample;
@@ -321,9 +730,7 @@ extern "C" GDN_API int gdn_sample_accept(const gdn_sample_args* args, void* stre
   if (rc != GDN_OK || args->B == 0) return rc;
   const gdn_sample_args p = *args;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const dim3 grid(p.R, p.B);
-  const int r = p.in_dtype == GDN_DTYPE_BF16 ? launch(sample_kernel<__nv_bfloat16>, grid, dim3(kThreads), st, p)
-                                             : launch(sample_kernel<float>, grid, dim3(kThreads), st, p);
+  const int r = p.in_dtype == GDN_DTYPE_BF16 ? run<__nv_bfloat16>(p, st) : run<float>(p, st);
   if (r != GDN_OK || !p.accept_len) return r;
-  return launch(accept_kernel, dim3((p.B + 255) / 256), dim3(256), st, p);
+  return launch(accept_kernel, dim3((p.B + 255) / 256), dim3(256), 1, 0, st, p);
 }

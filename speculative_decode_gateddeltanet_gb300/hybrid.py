@@ -16,7 +16,7 @@ import torch
 from .gdn import BF16, F32, _check, _lib, _ptr, _stream
 
 STATUS_NO_PAGES, STATUS_TABLE_FULL, STATUS_BAD_PAGE, STATUS_BAD_LENGTH, STATUS_ROWS_FULL = 32, 64, 128, 256, 512
-SAMPLE_MAX_STAGED = 8 * 192 * 1024
+SAMPLE_MAX_V = 393216
 
 _I32, _I64, _F32, _P = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p
 

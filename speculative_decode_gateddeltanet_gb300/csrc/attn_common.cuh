@@ -32,11 +32,23 @@ constexpr unsigned kFull = 0xffffffffu;
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// x / d for 0 <= x < 2^31 as a multiplication and a shift
+struct Div {
+  uint32_t mul, shift;
+};
+__device__ __forceinline__ uint32_t quotient(uint32_t x, const Div& k) { return k.mul ? __umulhi(x, k.mul) >> k.shift : x; }
+inline Div make_div(uint32_t d) {
+  if (d == 1) return {0, 0};
+  const uint32_t l = 31 - __builtin_clz(d) - ((d & (d - 1)) == 0);  // a power of two: the multiplier is 2^31
+  return {(uint32_t)(((uint64_t(1) << (32 + l)) + d - 1) / d), l};
+}
+
 struct Params {
   int B, R, H_kv, G, d;
   int page_size, n_pages, table_stride, n_q_rows;
   int64_t max_tokens;  // max_pages * page_size
   float scale_log2;    // scale * log2(e): scores are kept in the exponent of 2
+  Div by_G, by_page;
   const void* q;
   int64_t q_row, q_head;
   const void *k, *v;
@@ -94,10 +106,11 @@ __device__ inline long long floor_sum(long long n, long long m, long long a, lon
 
 template <int kRows, int kKeys>
 struct Tiles {
-  __device__ static int count(const Params& p, const Request& r) { return ((long long)r.n * p.G + kRows - 1) / kRows; }
+  __device__ static int count(const Params& p, const Request& r) { return (int)(((unsigned long long)r.n * p.G + kRows - 1) / kRows); }
   __device__ static int blocks(const Params& p, const Request& r, int m) {
     const long long last = min((long long)(m + 1) * kRows, (long long)r.n * p.G) - 1;
-    return (int)((r.ctx + last / p.G) / kKeys) + 1;
+    const int token = last >> 31 ? (int)(last / p.G) : (int)quotient((uint32_t)last, p.by_G);
+    return (int)((unsigned)(r.ctx + token) / kKeys) + 1;
   }
   // key blocks of the tiles before m
   __device__ static long long before(const Params& p, const Request& r, int m) {
@@ -145,23 +158,30 @@ struct Walk {
 };
 
 struct Start {
-  long long off;  // units from the request's first to the block's first
-  long long total;
-  int b;
-  int per;
+  long long total;  // units of the call
+  long long off;    // units from the first request's first to the block's first
+  long long head;   // units of one kv head of that request
+  Request req;      // the request the block begins in
+  int b, per;
 };
 
 // Every thread of the block calls this; all get the block's first unit.  scan:
-// kThreads/32 words of shared memory.
+// kThreads/32 words of shared memory.  The thread that meets the block's first
+// unit passes its request on, so nothing is read twice before the first tile.
 template <int kRows, int kKeys, int kThreads>
-__device__ void find_start(const Params& p, int min_units, long long* scan, Start* out) {
+__device__ __forceinline__ void find_start(const Params& p, int min_units, long long* scan, Start* out) {
   using T = Tiles<kRows, kKeys>;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int each = (p.B + kThreads - 1) / kThreads;
   const int b0 = threadIdx.x * each, b1 = min(p.B, b0 + each);
-  long long mine = 0;
+  long long mine = 0, head = 0;
+  Request req = {0, 0, 0};
   int why = 0;
-  for (int b = b0; b < b1; ++b) mine += p.H_kv * T::sum(p, request(p, b, &why));
+  for (int b = b0; b < b1; ++b) {
+    req = request(p, b, &why);
+    head = T::sum(p, req);
+    mine += p.H_kv * head;
+  }
   if (why && blockIdx.x == 0 && p.status) atomicOr(p.status, why);
   long long inc = mine;
 #pragma unroll
@@ -172,12 +192,16 @@ __device__ void find_start(const Params& p, int min_units, long long* scan, Star
   if (lane == 31) scan[warp] = inc;
   __syncthreads();
   long long before = 0, total = 0;
+#pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) before += scan[w];
     total += scan[w];
   }
   const long long at = before + inc - mine;
-  const long long per = max((total + p.n_blocks - 1) / p.n_blocks, (long long)min_units);
+  // 32-bit division where the sum allows it
+  const long long want = total >> 31 ? (total + p.n_blocks - 1) / p.n_blocks
+                                     : (long long)(((uint32_t)total + (uint32_t)p.n_blocks - 1) / (uint32_t)p.n_blocks);
+  const long long per = max(want, (long long)min_units);
   const long long first = per * blockIdx.x;
   if (threadIdx.x == 0) {
     out->total = total;
@@ -186,31 +210,35 @@ __device__ void find_start(const Params& p, int min_units, long long* scan, Star
   if (first >= at && first < at + mine) {  // one thread at most
     long long off = first - at;
     int b = b0;
-    for (;; ++b) {
-      const long long c = p.H_kv * T::sum(p, request(p, b));
-      if (off < c) break;
-      off -= c;
+    if (each > 1) {
+      for (;; ++b) {
+        req = request(p, b);
+        head = T::sum(p, req);
+        if (off < p.H_kv * head) break;
+        off -= p.H_kv * head;
+      }
     }
     out->b = b;
     out->off = off;
+    out->head = head;
+    out->req = req;
   }
   __syncthreads();
 }
 
 template <int kRows, int kKeys>
-__device__ bool begin(Walk<kRows, kKeys>& w, const Params& p, const Start& s) {
+__device__ __forceinline__ bool begin(Walk<kRows, kKeys>& w, const Params& p, const Start& s) {
   using T = Tiles<kRows, kKeys>;
   w.p = &p;
   const long long first = (long long)s.per * blockIdx.x;
   w.left = (int)max(0ll, min((long long)s.per, s.total - first));
   if (w.left <= 0) return false;
   w.b = s.b;
-  w.req = request(p, s.b);
+  w.req = s.req;
   w.tiles = T::count(p, w.req);
-  const long long S = T::sum(p, w.req);
   long long off = s.off;
-  w.h = (int)(off / S);
-  off -= w.h * S;
+  w.h = (off | s.head) >> 31 ? (int)(off / s.head) : (int)((uint32_t)off / (uint32_t)s.head);
+  off -= w.h * s.head;
   int lo = 0, hi = w.tiles;  // before(lo) <= off < before(hi)
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -234,66 +262,85 @@ __device__ __forceinline__ float* partial(const Params& p, int block, int slot, 
   return p.partials + (size_t)(block * 2 + slot) * rows * (p.d + 2);
 }
 
-constexpr int kCombineRows = 32;  // rows that the combine blocks of one split tile take at a time
+constexpr int kCombineBlocks = 8;  // blocks that share the rows of one split tile
+constexpr int kCombineWarps = 4;
+constexpr int kCombineBatch = 8;   // partials whose loads are in flight at once
 
-// one warp per row: joins the partials of the split tile that block
-// blockIdx.x begins, in block order
+// Joins the partials of the split tile that block blockIdx.x of the attention
+// begins.  Up to eight partials: a warp per row.  More (few tiles, long
+// contexts): a block per row, warp w taking partials w, w + 4, ..., and the warps'
+// sums added in warp order.  Either way the order is fixed by the lengths alone.
 template <typename T, int kD, int kRows>
-__global__ void __launch_bounds__(128) combine_kernel(const Params p) {
+__global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const Params p) {
+  constexpr int kPer = kD / 32;
+  __shared__ float sums[kCombineWarps][kD];
   pdl_wait();
   pdl_trigger();
   const int4 note = p.notes[blockIdx.x];
   const int parts = note.x + 1;
   if (parts <= 1) return;
   const Request req = request(p, note.y);
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rows = (int)min((long long)kRows, (long long)req.n * p.G - (long long)note.w * kRows);
+  const bool shared = parts > kCombineBatch;
   auto part = [&](int i) { return partial(p, blockIdx.x + i, i == 0, kRows); };
-  for (int row = blockIdx.y * 4 + (threadIdx.x >> 5); row < rows; row += kCombineRows) {
-    auto stats = [&](int i) { return reinterpret_cast<const float2*>(part(i) + (size_t)kRows * kD)[row]; };
-    float top = -INFINITY;
-    for (int i = lane; i < parts; i += 32) top = fmaxf(top, stats(i).x);
-  #pragma unroll
+  auto stats = [&](int i, int row) { return reinterpret_cast<const float2*>(part(i) + (size_t)kRows * kD)[row]; };
+  const int first = shared ? (int)blockIdx.y : (int)blockIdx.y * kCombineWarps + warp;
+  const int step = shared ? kCombineBlocks : kCombineBlocks * kCombineWarps;
+  const int i_first = shared ? warp : 0, i_step = shared ? kCombineWarps : 1;
+  for (int row = first; row < rows; row += step) {
+    float top = -INFINITY, sum = 0.f;
+    for (int i = lane; i < parts; i += 32) top = fmaxf(top, stats(i, row).x);
+#pragma unroll
     for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
     if (top == -INFINITY) top = 0.f;
-    constexpr int kPer = kD / 32;
+    for (int i = lane; i < parts; i += 32) {
+      const float2 s = stats(i, row);
+      sum += s.y * exp2f(s.x - top);
+    }
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) sum += __shfl_xor_sync(kFull, sum, off);
     float acc[kPer] = {};
-    float sum = 0.f;
-    for (int i0 = 0; i0 < parts; i0 += 32) {
-      float w = 0.f, l = 0.f;
-      if (i0 + lane < parts) {
-        const float2 s = stats(i0 + lane);
-        w = exp2f(s.x - top);
-        l = s.y * w;
-      }
-  #pragma unroll
-      for (int off = 16; off >= 1; off >>= 1) l += __shfl_xor_sync(kFull, l, off);
-      sum += l;
-      const int n = min(32, parts - i0);
-  #pragma unroll 4
-      for (int i = 0; i < n; ++i) {
-        const float wi = __shfl_sync(kFull, w, i);
-        const float* src = part(i0 + i) + (size_t)row * kD;
-  #pragma unroll
+    for (int i0 = i_first; i0 < parts; i0 += i_step * kCombineBatch) {
+      float x[kCombineBatch][kPer], weight[kCombineBatch];
+#pragma unroll
+      for (int j = 0; j < kCombineBatch; ++j) {
+        const int i = min(i0 + j * i_step, parts - 1);
+        weight[j] = i0 + j * i_step < parts ? exp2f(stats(i, row).x - top) : 0.f;
+        const float* src = part(i) + (size_t)row * kD + lane * 2;
+#pragma unroll
         for (int c = 0; c < kPer / 2; ++c) {
-          const float2 x = reinterpret_cast<const float2*>(src)[c * 32 + lane];
-          acc[2 * c] += wi * x.x;
-          acc[2 * c + 1] += wi * x.y;
+          const float2 v = *reinterpret_cast<const float2*>(src + c * 64);
+          x[j][2 * c] = v.x;
+          x[j][2 * c + 1] = v.y;
         }
       }
+#pragma unroll
+      for (int j = 0; j < kCombineBatch; ++j)
+#pragma unroll
+        for (int c = 0; c < kPer; ++c) acc[c] = i0 + j * i_step < parts ? fmaf(weight[j], x[j][c], acc[c]) : acc[c];
+    }
+    if (shared) {
+#pragma unroll
+      for (int c = 0; c < kPer / 2; ++c)
+        *reinterpret_cast<float2*>(&sums[warp][c * 64 + lane * 2]) = make_float2(acc[2 * c], acc[2 * c + 1]);
+      __syncthreads();
+#pragma unroll
+      for (int c = 0; c < kPer; ++c) {
+        acc[c] = 0.f;
+        for (int w = 0; w < kCombineWarps; ++w) acc[c] += sums[w][(c / 2) * 64 + lane * 2 + (c & 1)];
+      }
+      __syncthreads();
+      if (warp != 0) continue;
     }
     const float inv = 1.f / sum;
-    const int at = note.w * kRows + row;
-    const int token = at / p.G, head = note.z * p.G + at % p.G;
-    T* dst = static_cast<T*>(p.o) + (int64_t)(req.row0 + token) * p.o_row + head * p.o_head;
-  #pragma unroll
+    const int at = note.w * kRows + row, token = at / p.G, head = note.z * p.G + at % p.G;
+    T* dst = static_cast<T*>(p.o) + (int64_t)(req.row0 + token) * p.o_row + head * p.o_head + lane * 2;
+#pragma unroll
     for (int c = 0; c < kPer / 2; ++c) {
-      const int col = (c * 32 + lane) * 2;
-      if constexpr (sizeof(T) == 2) {
-        *reinterpret_cast<__nv_bfloat162*>(dst + col) = __floats2bfloat162_rn(acc[2 * c] * inv, acc[2 * c + 1] * inv);
-      } else {
-        *reinterpret_cast<float2*>(dst + col) = make_float2(acc[2 * c] * inv, acc[2 * c + 1] * inv);
-      }
+      const float a = acc[2 * c] * inv, b = acc[2 * c + 1] * inv;
+      if constexpr (sizeof(T) == 2) *reinterpret_cast<__nv_bfloat162*>(dst + c * 64) = __floats2bfloat162_rn(a, b);
+      else *reinterpret_cast<float2*>(dst + c * 64) = make_float2(a, b);
     }
   }
 }

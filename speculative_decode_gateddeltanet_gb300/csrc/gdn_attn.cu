@@ -199,7 +199,7 @@ int run_simt(Params& p, cudaStream_t st) {
   p.n_blocks = simt_blocks(kD);
   const int rc = launch(simt_kernel<kD>, dim3(p.n_blocks), dim3(kSimtThreads), smem, st, p);
   if (rc != GDN_OK) return rc;
-  return launch(combine_kernel<float, kD, kSimtRows>, dim3(p.n_blocks, kCombineRows / 4), dim3(128), 0, st, p);
+  return launch(combine_kernel<float, kD, kSimtRows>, dim3(p.n_blocks, kCombineBlocks), dim3(32 * kCombineWarps), 0, st, p);
 }
 
 int run_simt(Params& p, cudaStream_t st) {
@@ -262,6 +262,8 @@ extern "C" GDN_API int gdn_paged_attention(const gdn_paged_attn_args* a, void* s
   p.n_q_rows = a->n_q_rows;
   p.max_tokens = (int64_t)a->max_pages * a->page_size;
   p.scale_log2 = (float)((double)a->scale * 1.4426950408889634);
+  p.by_G = make_div((uint32_t)p.G);
+  p.by_page = make_div((uint32_t)p.page_size);
   p.q = a->q;
   p.q_row = a->q_row_stride;
   p.q_head = a->q_head_stride;

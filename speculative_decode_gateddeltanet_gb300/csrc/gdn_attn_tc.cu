@@ -10,9 +10,15 @@
 // S has two buffers: the tensor cores form S of block j+1 while the softmax
 // works on block j, so the two overlap and the longer of them sets the pace.
 //
-// Roles (256 threads): warps 0-3 softmax and output, warp 4 issues the MMAs,
-// warp 5 the TMA copies of K and V, warps 6-7 stage Q and clear the V rows
-// behind a request's last token.
+// Roles (384 threads): warps 0-3 softmax and output, warp 4 issues the MMAs,
+// warps 5 and 6 the TMA copies of K and of V, warps 7-11 stage Q.
+//
+// Few rows.  A TMEM lane belongs to one warp, so 32 rows would leave three of
+// the four softmax warps idle, and one warp's 128 exponentials a row take longer
+// than the block's K and V take to arrive.  A tile of at most 64 (32) rows is
+// therefore staged twice (four times) over: each copy keeps the softmax of its
+// half (quarter) of a block's keys, its P is zero for the others, and the copies
+// are joined once per tile.  The MMA's 128 rows are paid for anyway.
 //
 // A page is copied in boxes of 64 columns by a power of two of tokens that
 // divides the page, straight into the 128-byte-swizzled layout the MMA reads;
@@ -30,6 +36,7 @@
 #include <cuda.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "attn_common.cuh"
 #include "attn_tc.h"
@@ -37,10 +44,11 @@
 namespace gdnattn {
 
 constexpr int kTcRows = 128;
-constexpr int kTcThreads = 256;
+constexpr int kTcThreads = 384;
+constexpr int kQThreads = 160;
 constexpr int kTcBlocks = 152;  // one block per SM of a GB300
 constexpr int kTcMinUnits = 1;
-constexpr unsigned long long kWaitNs = 2000000000ull;
+constexpr unsigned long long kWaitNs = 500000000ull;
 
 template <int kD>
 struct Shape {
@@ -83,7 +91,7 @@ __device__ __forceinline__ unsigned long long now_ns() {
 }
 
 // false when the wait ran out or another role gave up
-__device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, volatile int* gave_up) {
+__device__ __forceinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity, volatile int* gave_up) {
   const unsigned long long end = now_ns() + kWaitNs;
   while (!bar_try(bar, parity)) {
     if (*gave_up) return false;
@@ -149,6 +157,22 @@ __device__ __forceinline__ void tmem_store(uint32_t at, const uint32_t (&r)[32])
       GDN_W4(r, 0), GDN_W4(r, 4), GDN_W4(r, 8), GDN_W4(r, 12), GDN_W4(r, 16), GDN_W4(r, 20), GDN_W4(r, 24), GDN_W4(r, 28)
       : "memory");
 }
+__device__ __forceinline__ void tmem_load(uint32_t (&r)[16], uint32_t at) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : GDN_R4(r, 0), GDN_R4(r, 4), GDN_R4(r, 8), GDN_R4(r, 12)
+      : "r"(at));
+}
+__device__ __forceinline__ void tmem_store(uint32_t at, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(at),
+      GDN_W4(r, 0), GDN_W4(r, 4), GDN_W4(r, 8), GDN_W4(r, 12)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_store(uint32_t at, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(at), GDN_W4(r, 0), GDN_W4(r, 4)
+               : "memory");
+}
 __device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -173,6 +197,86 @@ __host__ __device__ constexpr uint32_t instruction(int n, bool transpose_b) {
   return 1u << 4 | 1u << 7 | 1u << 10 | (transpose_b ? 1u << 16 : 0) | (uint32_t)(n >> 3) << 17 | (uint32_t)(kTcRows >> 4) << 24;
 }
 
+__device__ __forceinline__ int copies_of(int rows) { return rows <= 32 ? 4 : rows <= 64 ? 2 : 1; }
+
+// a row's running softmax
+struct RowState {
+  float top, sum;
+};
+
+// One key block for this thread's row and the kKeys / kCopies columns of its
+// copy: s_at is S in TMEM (this warp's lanes), edge the last column the row sees.
+// rescale(shrink) multiplies the row's O; it is called for whole warps.
+template <int kKeys, int kCopies, typename Rescale>
+__device__ __forceinline__ bool softmax_block(RowState& st, uint32_t s_at, int copy, int edge, float scale_log2, Rescale rescale) {
+  // at most 64 columns are held at a time: of 128, the first 64 are read last for the maximum and stay, the others are
+  // read again (a second TMEM read costs less than the registers)
+  constexpr int kC = kKeys / kCopies, kHeld = kC < 64 ? kC : 64, kGroups = kC / kHeld;
+  constexpr int kPart = kHeld < 32 ? kHeld : 32;  // columns of one TMEM load
+  uint32_t x[kHeld / kPart][kPart];
+  edge -= copy * kC;
+  auto load = [&](int g) {
+#pragma unroll
+    for (int c = 0; c < kHeld / kPart; ++c) tmem_load(x[c], s_at + copy * kC + g * kHeld + c * kPart);
+    tmem_wait_load();
+    if (edge < (g + 1) * kHeld - 1) {
+#pragma unroll
+      for (int c = 0; c < kHeld / kPart; ++c)
+#pragma unroll
+        for (int i = 0; i < kPart; ++i)
+          if (g * kHeld + c * kPart + i > edge) x[c][i] = 0xff800000u;
+    }
+  };
+  float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int g = kGroups - 1; g >= 0; --g) {
+    load(g);
+#pragma unroll
+    for (int c = 0; c < kHeld / kPart; ++c)
+#pragma unroll
+      for (int i = 0; i < kPart; ++i) m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(x[c][i]));
+  }
+  const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * scale_log2;
+  const bool raise = mx > st.top + 8.f;  // also the first time: top is -inf
+  if (__any_sync(kFull, raise)) {
+    const float shrink = raise ? ex2(st.top - mx) : 1.f;
+    st.sum *= shrink;
+    if (raise) st.top = mx;
+    if (!rescale(shrink)) return false;
+  }
+  const float sub = st.top == -INFINITY ? 0.f : st.top;
+  float s4[4] = {0.f, 0.f, 0.f, 0.f};
+  constexpr int kW = kHeld / 2 < 16 ? kHeld / 2 : 16;  // words of one TMEM store
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) {
+    if (g > 0) load(g);
+#pragma unroll
+    for (int c = 0; c < kHeld / 2; c += kW) {
+      uint32_t pk[kW];
+#pragma unroll
+      for (int i = 0; i < kW; ++i) {
+        const int j = 2 * (c + i);
+        const float e0 = ex2(fmaf(__uint_as_float(x[j / kPart][j % kPart]), scale_log2, -sub));
+        const float e1 = ex2(fmaf(__uint_as_float(x[j / kPart][j % kPart + 1]), scale_log2, -sub));
+        s4[j & 3] += e0;
+        s4[(j + 1) & 3] += e1;
+        pk[i] = pack_bf16(e0, e1);
+      }
+      tmem_store(s_at + (copy * kC + g * kHeld) / 2 + c, pk);  // over columns that were read
+    }
+  }
+  if constexpr (kCopies > 1) {
+    // the other copies' keys: weight 0.  (S of those columns belongs to this warp's lanes alone: no one waits for it.)
+    constexpr uint32_t zero[kW] = {};
+#pragma unroll
+    for (int c = 0; c < kKeys / 2; c += kW)
+      if (c / (kC / 2) != copy) tmem_store(s_at + c, zero);
+  }
+  st.sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+  tmem_wait_store();
+  return true;
+}
+
 struct TcParams {
   Params p;
   int box;          // tokens per TMA box: a power of two that divides the page and kKeys
@@ -191,6 +295,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __shared__ Start start;
   __shared__ uint32_t tmem_base;
   __shared__ int gave_up;
+  __shared__ float2 stats[128];  // maxima and sums of a tile's copies
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
   const uint32_t q_s = base, k_s = q_s + S::kQBytes, v_s = k_s + S::kK * S::kTileBytes;
@@ -202,10 +307,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   constexpr int kRest = 2 * S::kK + 2 * S::kV;
   auto s_full = [&](int i) { return b0 + 8 * (kRest + i); };    // S of a block is in TMEM
   auto p_ready = [&](int i) { return b0 + 8 * (kRest + 2 + i); };  // its P is
-  const uint32_t pv_done = b0 + 8 * (kRest + 4), q_full = b0 + 8 * (kRest + 5), q_empty = b0 + 8 * (kRest + 6),
-                 o_free = b0 + 8 * (kRest + 7), drained = b0 + 8 * (kRest + 10);
-  // the Q warps may clear for the next segment before the MMA warp asks for this one's: two in turn
-  auto v_clear = [&](int i) { return b0 + 8 * (kRest + 8 + (i & 1)); };
+  // A wait names a phase by its parity, so a barrier may be at most one phase ahead of any of its waiters: what two
+  // blocks in a row signal has two barriers in turn.
+  auto pv_done = [&](int i) { return b0 + 8 * (kRest + 4 + (i & 1)); };  // O holds the products of block i
+  const uint32_t q_full = b0 + 8 * (kRest + 6), q_empty = b0 + 8 * (kRest + 7), o_free = b0 + 8 * (kRest + 8),
+                 joined = b0 + 8 * (kRest + 9), drained = b0 + 8 * (kRest + 10);
   if (tid == 0) {
     gave_up = 0;
     for (int i = 0; i < S::kK; ++i) {
@@ -220,12 +326,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       bar_init(s_full(i), 1);
       bar_init(p_ready(i), 128);
     }
-    bar_init(pv_done, 1);
-    bar_init(q_full, 64);
+    bar_init(pv_done(0), 1);
+    bar_init(pv_done(1), 1);
+    bar_init(q_full, kQThreads);
     bar_init(q_empty, 1);
     bar_init(o_free, 128);
-    bar_init(v_clear(0), 64);
-    bar_init(v_clear(1), 64);
+    bar_init(joined, 128);
     bar_init(drained, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -246,88 +352,63 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   Walk<kTcRows, kKeys> w;
   const bool any = begin(w, p, s);
   bool ok = true;
-  int k_sent = 0, v_sent = 0;  // tiles whose copies were issued
+  int sent = 0;  // tiles whose copies this warp issued
 
   if (any && warp < 4) {
-    // ---- softmax and output: one thread per row
+    // ---- softmax and output: one thread per row (and copy)
     const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
-    int it = 0, seen = 0;
-    // O holds the products of blocks up to i.  A parity tells the current phase of pv_done from the one before it
-    // only, so its phases are waited for one by one, each once.
-    auto products = [&](int i) {
-      for (; seen <= i; ++seen)
-        if (!warp_wait(pv_done, seen & 1, &gave_up)) return false;
-      return true;
-    };
+    int it = 0;
+    auto products = [&](int i) { return warp_wait(pv_done(i), (i >> 1) & 1, &gave_up); };
     for (; ok && !w.done(); w.next()) {
       const int rows = (int)min((long long)kTcRows, (long long)w.req.n * p.G - (long long)w.m * kTcRows);
-      const bool active = warp * 32 < rows;  // a warp with no row only keeps step
-      const int at = w.m * kTcRows + tid;
-      const int last = tid < rows ? w.req.ctx + at / p.G : -1;
-      float top = -INFINITY, sum = 0.f;
+      const int copies = copies_of(rows), spread = 4 / copies;  // warps of one copy
+      const int copy = warp / spread, row = (warp % spread) * 32 + lane;
+      const bool active = (warp % spread) * 32 < rows;  // a warp with no row only keeps step
+      const int at = w.m * kTcRows + row;
+      const int token = (int)quotient(at, p.by_G), head = w.h * p.G + at - token * p.G;
+      const int last = row < rows ? w.req.ctx + token : -1;
+      RowState st = {-INFINITY, 0.f};
       for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
         const int buf = it & 1;
         if (!(ok = warp_wait(s_full(buf), (it >> 1) & 1, &gave_up))) break;
-        if (!(ok = products(it - 2))) break;
+        if (it >= 2 && !(ok = products(it - 2))) break;  // each block's, in turn
         if (active) {
           tc_fence_after();
-          uint32_t x[kKeys / 32][32];
-#pragma unroll
-          for (int c = 0; c < kKeys / 32; ++c) tmem_load(x[c], lanes + buf * kKeys + c * 32);
-          tmem_wait_load();
-          const int edge = last - kb * kKeys;  // columns up to edge are seen
-          if (edge < kKeys - 1) {
-#pragma unroll
-            for (int c = 0; c < kKeys / 32; ++c)
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (c * 32 + i > edge) x[c][i] = 0xff800000u;
-          }
-          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int c = 0; c < kKeys / 32; ++c)
-#pragma unroll
-            for (int i = 0; i < 32; ++i) m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(x[c][i]));
-          const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.scale_log2;
-          const bool raise = mx > top + 8.f;  // also the first time: top is -inf
-          if (__any_sync(kFull, raise)) {
-            const float m = raise ? mx : top;
-            const float shrink = raise ? ex2(top - mx) : 1.f;
-            sum *= shrink;
-            top = m;
-            if (kb > w.kb0) {
-              if (!(ok = products(it - 1))) break;
-              tc_fence_after();
+          auto rescale = [&](float shrink) {
+            if (kb == w.kb0) return true;
+            if (!products(it - 1)) return false;
+            tc_fence_after();
 #pragma unroll 1
-              for (int c = 0; c < kD / 32; ++c) {
-                uint32_t o[32];
-                tmem_load(o, lanes + kOCol + c * 32);
-                tmem_wait_load();
+            for (int c = 0; c < kD / 32; ++c) {
+              uint32_t o[32];
+              tmem_load(o, lanes + kOCol + c * 32);
+              tmem_wait_load();
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * shrink);
-                tmem_store(lanes + kOCol + c * 32, o);
-              }
-              tmem_wait_store();
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * shrink);
+              tmem_store(lanes + kOCol + c * 32, o);
             }
-          }
-          const float sub = top == -INFINITY ? 0.f : top;
-          float s4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int c = 0; c < kKeys / 32; c += 2) {
-            uint32_t pk[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float e0 = ex2(fmaf(__uint_as_float(x[c + i / 16][(2 * i) & 31]), p.scale_log2, -sub));
-              const float e1 = ex2(fmaf(__uint_as_float(x[c + i / 16][(2 * i + 1) & 31]), p.scale_log2, -sub));
-              s4[(2 * i) & 3] += e0;
-              s4[(2 * i + 1) & 3] += e1;
-              pk[i] = pack_bf16(e0, e1);
-            }
-            tmem_store(lanes + buf * kKeys + c * 16, pk);
-          }
-          sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
-          tmem_wait_store();
+            tmem_wait_store();
+            return true;
+          };
+          const int edge = last - kb * kKeys;
+          const uint32_t s_at = lanes + buf * kKeys;
+          if (copies == 1) ok = softmax_block<kKeys, 1>(st, s_at, 0, edge, p.scale_log2, rescale);
+          else if (copies == 2) ok = softmax_block<kKeys, 2>(st, s_at, copy, edge, p.scale_log2, rescale);
+          else ok = softmax_block<kKeys, 4>(st, s_at, copy, edge, p.scale_log2, rescale);
+          if (!ok) break;
           tc_fence_before();
+        }
+        const int valid = w.req.ctx + w.req.n - kb * kKeys;
+        if (valid < kKeys) {
+          // The V rows behind the request's last token: their weight is 0, but 0 times what a page holds there may be NaN.
+          const int vs = it % S::kV;
+          if (!(ok = warp_wait(v_full(vs), (it / S::kV) & 1, &gave_up))) break;
+          for (int i = tid; i < (kKeys - valid) * (kD / 8); i += 128) {
+            const int r = valid + i / (kD / 8), u = i % (kD / 8);
+            const uint32_t to = v_s + vs * S::kTileBytes + (u / 8) * (kKeys * 128) + r * 128 + ((u & 7) << 4);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(to), "r"(0) : "memory");
+          }
+          fence_async();
         }
         bar_arrive(p_ready(buf));
       }
@@ -335,35 +416,99 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const bool whole = w.kb0 == 0 && w.kb1 == w.blocks;
       const int slot = w.kb0 == 0 ? 1 : 0;
       if (!whole && slot == 1) note = {followers(w, s), w.b, w.h, w.m};
-      if (active) {
-        tc_fence_after();
-        float* const out = partial(p, blockIdx.x, slot, kTcRows);
-        const float inv = 1.f / sum;
-        __nv_bfloat16* const dst = static_cast<__nv_bfloat16*>(p.o) + (int64_t)(w.req.row0 + at / p.G) * p.o_row +
-                                   (int64_t)(w.h * p.G + at % p.G) * p.o_head;
+      tc_fence_after();
+      float* const out = partial(p, blockIdx.x, slot, kTcRows);
+      __nv_bfloat16* const dst =
+          static_cast<__nv_bfloat16*>(p.o) + (int64_t)(w.req.row0 + token) * p.o_row + (int64_t)head * p.o_head;
+      if (copies == 1) {
+        if (active) {
+          const float inv = 1.f / st.sum;
 #pragma unroll 1
-        for (int c = 0; c < kD / 32; ++c) {
-          uint32_t o[32];
-          tmem_load(o, lanes + kOCol + c * 32);
-          tmem_wait_load();
-          if (tid < rows) {
-            if (whole) {
-              uint32_t pk[16];
+          for (int c = 0; c < kD / 32; ++c) {
+            uint32_t o[32];
+            tmem_load(o, lanes + kOCol + c * 32);
+            tmem_wait_load();
+            if (row < rows) {
+              if (whole) {
+                uint32_t pk[16];
 #pragma unroll
-              for (int i = 0; i < 16; ++i) pk[i] = pack_bf16(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
+                for (int i = 0; i < 16; ++i) pk[i] = pack_bf16(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                reinterpret_cast<uint4*>(dst + c * 32)[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
-            } else {
+                for (int i = 0; i < 4; ++i)
+                  reinterpret_cast<uint4*>(dst + c * 32)[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+              } else {
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                reinterpret_cast<uint4*>(out + tid * kD + c * 32)[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                for (int i = 0; i < 8; ++i)
+                  reinterpret_cast<uint4*>(out + row * kD + c * 32)[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+              }
             }
           }
         }
-        if (!whole && tid < rows) reinterpret_cast<float2*>(out + kTcRows * kD)[tid] = make_float2(top, sum);
-        tc_fence_before();
+      } else {
+        // Join the copies, half of the columns at a time, through Q's place (the products with Q are done, and the Q
+        // warps wait for `joined` before they stage the next tile): each warp brings its rows scaled to the common
+        // maximum, then sums its share of their 16-byte units over the copies.
+        const int span = 128 / copies;
+        stats[tid] = make_float2(st.top, st.sum);
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        float top = -INFINITY, sum = 0.f;
+        for (int c = 0; c < copies; ++c) top = fmaxf(top, stats[c * span + row].x);
+        const float sub = top == -INFINITY ? 0.f : top;
+        for (int c = 0; c < copies; ++c) sum += stats[c * span + row].y * ex2(stats[c * span + row].x - sub);
+        const float scale = ex2(st.top - sub) * (whole ? 1.f / sum : 1.f);
+        st.top = top;
+        constexpr int kHalf = kD / 2, kHalfUnits = kHalf / 4;
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          if (half) asm volatile("bar.sync 1, 128;" ::: "memory");  // the first half has been read
+#pragma unroll
+          for (int c = 0; c < kHalf / 32; ++c) {
+            uint32_t o[32];
+            tmem_load(o, lanes + kOCol + half * kHalf + c * 32);
+            tmem_wait_load();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint32_t to = q_s + tid * (kHalf * 4) + (((c * 8 + i) ^ (lane & 7)) << 4);
+              asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(__uint_as_float(o[4 * i]) * scale),
+                           "f"(__uint_as_float(o[4 * i + 1]) * scale), "f"(__uint_as_float(o[4 * i + 2]) * scale),
+                           "f"(__uint_as_float(o[4 * i + 3]) * scale)
+                           : "memory");
+            }
+          }
+          asm volatile("bar.sync 1, 128;" ::: "memory");
+          if (row < rows) {
+            auto sum_units = [&](auto copies_c) {
+              constexpr int kC = decltype(copies_c)::value;
+#pragma unroll
+              for (int i = 0; i < kHalfUnits / kC; ++i) {
+                const int unit = copy * (kHalfUnits / kC) + i;
+                float4 a = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int j = 0; j < kC; ++j) {
+                  float4 v;
+                  asm("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                      : "r"(q_s + (j * (128 / kC) + row) * (kHalf * 4) + ((unit ^ (lane & 7)) << 4))
+                      : "memory");
+                  a.x += v.x;
+                  a.y += v.y;
+                  a.z += v.z;
+                  a.w += v.w;
+                }
+                const int col = half * kHalf + unit * 4;
+                if (whole) *reinterpret_cast<uint2*>(dst + col) = make_uint2(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w));
+                else *reinterpret_cast<float4*>(out + row * kD + col) = a;
+              }
+            };
+            if (copies == 4) sum_units(std::integral_constant<int, 4>());
+            else sum_units(std::integral_constant<int, 2>());
+          }
+        }
+        st.sum = sum;
+        bar_arrive(joined);
       }
+      if (!whole && row < rows && copy == 0) reinterpret_cast<float2*>(out + kTcRows * kD)[row] = make_float2(st.top, st.sum);
+      tc_fence_before();
       bar_arrive(o_free);
     }
   } else if (any && warp == 4) {
@@ -371,10 +516,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (lane == 0) {
       constexpr uint32_t kQk = instruction(kKeys, false), kPv = instruction(kD, true);
       int it = 0, seg = 0;
-      int cuts = 0;
       for (; ok && !w.done(); w.next(), ++seg) {
         if (!(ok = bar_wait(q_full, seg & 1, &gave_up))) break;
-        const int len = w.req.ctx + w.req.n;
         for (int kb = w.kb0; kb <= w.kb1; ++kb) {
           if (kb < w.kb1) {
             const int i = it + kb - w.kb0, st = i % S::kK, buf = i & 1;
@@ -392,13 +535,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           if (kb > w.kb0) {
             const int i = it + kb - 1 - w.kb0, buf = i & 1, st = i % S::kV;
-            const bool first = kb - 1 == w.kb0, cut = kb * kKeys > len;  // block kb - 1 reaches behind the last token
+            const bool first = kb - 1 == w.kb0;
             ok = bar_wait(p_ready(buf), (i >> 1) & 1, &gave_up) && bar_wait(v_full(st), (i / S::kV) & 1, &gave_up);
             if (ok && first && seg > 0) ok = bar_wait(o_free, (seg - 1) & 1, &gave_up);
-            if (ok && cut) {
-              ok = bar_wait(v_clear(cuts), (cuts >> 1) & 1, &gave_up);
-              ++cuts;
-            }
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
@@ -406,90 +545,100 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               mma_ts(tmem + kOCol, tmem + buf * kKeys + k * 8, operand(v_s + st * S::kTileBytes + k * 2048, kKeys * 128, 1024),
                      kPv, !(first && k == 0));
             tc_commit(v_empty(st));
-            tc_commit(pv_done);
+            tc_commit(pv_done(i));
           }
         }
         it += w.kb1 - w.kb0;
       }
     }
     __syncwarp();
-  } else if (any && warp == 5) {
-    // ---- K and V tiles by TMA: lane (box, chunk) copies its box of 64 columns
+  } else if (any && warp < 7) {
+    // ---- K (warp 5) and V (warp 6) tiles by TMA: lane (box, chunk) copies its box of 64 columns
+    const bool is_v = warp == 6;
+    const int stages = is_v ? S::kV : S::kK;
+    const uint32_t tiles = is_v ? v_s : k_s, full = is_v ? v_full(0) : k_full(0), empty = is_v ? v_empty(0) : k_empty(0);
+    const CUtensorMap* const map = is_v ? &v_map : &k_map;
     const int n_box = kKeys / t.box, box = lane / kChunks, chunk = lane % kChunks;
     const uint32_t at = (uint32_t)chunk * (kKeys * 128) + (uint32_t)box * t.box * 128;
-    int it = 0;
+    int stage = 0;
+    uint32_t phase = 1;  // of `empty`: the first round finds the stages free
     for (; ok && !w.done(); w.next()) {
       const int len = w.req.ctx + w.req.n;
       const int32_t* const row = p.table + (size_t)w.b * p.table_stride;
-      int page = 0, token = 0;
-      auto find_page = [&](int kb) {
-        const int j = kb * kKeys + box * t.box;
-        if (box < n_box && j < len) {
-          const int i = j / p.page_size;
-          token = j - i * p.page_size;
-          page = row[i];
-          if ((unsigned)page >= (unsigned)p.n_pages) {
-            page = p.n_pages;  // outside the map: zeros
-            if (p.status) atomicOr(p.status, GDN_STATUS_BAD_PAGE);
-          }
-        }
+      struct Box {
+        int page, token;
       };
-      find_page(w.kb0);
-      for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
+      auto find_page = [&](int kb) -> Box {
+        const int j = kb * kKeys + box * t.box;
+        if (kb >= w.kb1 || box >= n_box || j >= len) return {0, 0};
+        const int i = (int)quotient(j, p.by_page);
+        return {row[i], j - i * p.page_size};
+      };
+      Box next[2] = {find_page(w.kb0), find_page(w.kb0 + 1)};  // two blocks ahead: a table entry is a round trip to L2
+      for (int kb = w.kb0; kb < w.kb1; ++kb) {
         const int live = min(n_box, (len - kb * kKeys + t.box - 1) / t.box);
-        const uint32_t bytes = (uint32_t)live * t.box * kD * 2;
-        const bool mine = box < live;
-        const int my_page = page, my_token = token;
-        if (kb + 1 < w.kb1) find_page(kb + 1);  // its latency hides behind the waits below
-        const int ks = it % S::kK, vs = it % S::kV;
-        if (!(ok = warp_wait(k_empty(ks), ((it / S::kK) & 1) ^ 1, &gave_up))) break;
-        if (lane == 0) bar_expect(k_full(ks), bytes);
+        int my_page = next[0].page;
+        const int my_token = next[0].token;
+        next[0] = next[1];
+        next[1] = find_page(kb + 2);
+        if (!(ok = warp_wait(empty + 8 * stage, phase, &gave_up))) break;
+        if (lane == 0) bar_expect(full + 8 * stage, (uint32_t)live * t.box * kD * 2);
         __syncwarp();
-        if (mine) tma_box(&k_map, k_s + ks * S::kTileBytes + at, k_full(ks), chunk * 64, my_token, w.h, my_page);
-        k_sent = it + 1;
-        if (!(ok = warp_wait(v_empty(vs), ((it / S::kV) & 1) ^ 1, &gave_up))) break;
-        if (lane == 0) bar_expect(v_full(vs), bytes);
-        __syncwarp();
-        if (mine) tma_box(&v_map, v_s + vs * S::kTileBytes + at, v_full(vs), chunk * 64, my_token, w.h, my_page);
-        v_sent = it + 1;
+        if ((unsigned)my_page >= (unsigned)p.n_pages) {
+          my_page = p.n_pages;  // outside the map: zeros
+          if (p.status) atomicOr(p.status, GDN_STATUS_BAD_PAGE);
+        }
+        if (box < live) tma_box(map, tiles + stage * S::kTileBytes + at, full + 8 * stage, chunk * 64, my_token, w.h, my_page);
+        ++sent;
+        if (++stage == stages) {
+          stage = 0;
+          phase ^= 1;
+        }
       }
     }
   } else if (any) {
-    // ---- Q rows into the swizzled layout, and the V rows behind the last token
-    const int q_tid = tid - 192;
-    int it = 0, seg = 0, cuts = 0;
+    // ---- Q rows into the swizzled layout
+    const int q_tid = tid - (kTcThreads - kQThreads);
+    constexpr int kUnits = kD / 8;  // 16-byte units of a row
+    constexpr int kBatch = 8;       // units a thread holds: 32 rows of 256 columns at once, nearly
+    int seg = 0, joins = 0, copies = 1;
     for (; ok && !w.done(); w.next(), ++seg) {
       const int rows = (int)min((long long)kTcRows, (long long)w.req.n * p.G - (long long)w.m * kTcRows);
-      if (seg > 0 && !(ok = bar_wait(q_empty, (seg - 1) & 1, &gave_up))) break;
-      constexpr int kUnits = kD / 8;  // 16-byte units of a row
-#pragma unroll 8
-      for (int i = q_tid; i < rows * kUnits; i += 64) {
-        const int r = i / kUnits, u = i % kUnits, at = w.m * kTcRows + r;
-        uint4 x = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + (int64_t)(w.req.row0 + at / p.G) * p.q_row +
-                                                  (int64_t)(w.h * p.G + at % p.G) * p.q_head + u * 8);
-        x.x ^= t.q_flip;
-        x.y ^= t.q_flip;
-        x.z ^= t.q_flip;
-        x.w ^= t.q_flip;
-        const uint32_t dst = q_s + (u / 8) * (kTcRows * 128) + r * 128 + (((u & 7) ^ (r & 7)) << 4);
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
+      const int before = copies;
+      copies = copies_of(rows);
+      for (int i0 = 0; i0 < rows * kUnits; i0 += kBatch * kQThreads) {
+        uint4 x[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          // past the tile's rows its last one again: no load hides behind a branch
+          const int i = i0 + j * kQThreads + q_tid, r = min(i / kUnits, rows - 1), u = i % kUnits, at = w.m * kTcRows + r;
+          const int token = (int)quotient(at, p.by_G), head = w.h * p.G + at - token * p.G;
+          x[j] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + (int64_t)(w.req.row0 + token) * p.q_row +
+                                                      (int64_t)head * p.q_head + u * 8));
+        }
+        // the rows are on their way while the last tile's products with Q, and its join through Q's place, end
+        if (i0 == 0 && seg > 0) {
+          ok = bar_wait(q_empty, (seg - 1) & 1, &gave_up);
+          if (ok && before > 1) ok = bar_wait(joined, joins++ & 1, &gave_up);
+          if (!ok) break;
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          const int i = i0 + j * kQThreads + q_tid;
+          if (i < rows * kUnits) {
+            const int r = i / kUnits, u = i % kUnits;
+            const uint4 y = make_uint4(x[j].x ^ t.q_flip, x[j].y ^ t.q_flip, x[j].z ^ t.q_flip, x[j].w ^ t.q_flip);
+            for (int c = 0; c < copies; ++c) {
+              const int to_row = r + c * (kTcRows / copies);
+              const uint32_t dst = q_s + (u / 8) * (kTcRows * 128) + to_row * 128 + (((u & 7) ^ (r & 7)) << 4);
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w) : "memory");
+            }
+          }
+        }
       }
+      if (!ok) break;
       fence_async();
       bar_arrive(q_full);
-      it += w.kb1 - w.kb0;
-      const int valid = w.req.ctx + w.req.n - (w.kb1 - 1) * kKeys;
-      if (valid < kKeys) {
-        const int vi = it - 1, st = vi % S::kV;
-        if (!(ok = bar_wait(v_full(st), (vi / S::kV) & 1, &gave_up))) break;
-        for (int i = q_tid; i < (kKeys - valid) * kUnits; i += 64) {
-          const int r = valid + i / kUnits, u = i % kUnits;
-          const uint32_t dst = v_s + st * S::kTileBytes + (u / 8) * (kKeys * 128) + r * 128 + ((u & 7) << 4);
-          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst), "r"(0) : "memory");
-        }
-        fence_async();
-        bar_arrive(v_clear(cuts));
-        ++cuts;
-      }
     }
   }
   if (tid == 0) p.notes[blockIdx.x] = note;
@@ -502,12 +651,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       while (!bar_try(drained, 0) && now_ns() < end) {
       }
     }
-    if (tid == 160) {
-      for (int i = max(0, k_sent - S::kK); i < k_sent; ++i)
-        while (!bar_try(k_full(i % S::kK), (i / S::kK) & 1) && now_ns() < end) {
-        }
-      for (int i = max(0, v_sent - S::kV); i < v_sent; ++i)
-        while (!bar_try(v_full(i % S::kV), (i / S::kV) & 1) && now_ns() < end) {
+    if (lane == 0 && (warp == 5 || warp == 6)) {
+      const int stages = warp == 5 ? S::kK : S::kV;
+      for (int i = max(0, sent - stages); i < sent; ++i)
+        while (!bar_try((warp == 5 ? k_full(0) : v_full(0)) + 8 * (i % stages), (i / stages) & 1) && now_ns() < end) {
         }
     }
     if (tid == 0 && p.status) atomicOr(p.status, GDN_STATUS_TIMEOUT);
@@ -562,7 +709,7 @@ int run(TcParams& t, cudaStream_t st) {
   t.p.n_blocks = kTcBlocks;
   const int rc = launch(tc_kernel<kD>, dim3(kTcBlocks), dim3(kTcThreads), S::kSmem, st, t, k_map, v_map);
   if (rc != GDN_OK) return rc;
-  return launch(combine_kernel<__nv_bfloat16, kD, kTcRows>, dim3(kTcBlocks, kCombineRows / 4), dim3(128), 0, st, t.p);
+  return launch(combine_kernel<__nv_bfloat16, kD, kTcRows>, dim3(kTcBlocks, kCombineBlocks), dim3(32 * kCombineWarps), 0, st, t.p);
 }
 
 int run_tc(Params& p, cudaStream_t st) {

@@ -225,6 +225,9 @@ ATTENTION = [
     ([(31, 200), (0, 1), (400, 17)], 6, 2, 256, 16, "tokens", 0),
     ([(0, 1500)], 5, 1, 128, 32, "heads", 0),
     ([(3, 2)] * 200, 8, 4, 128, 16, "heads", 2),               # more tiles than blocks
+    ([(700 + 3 * i, 1 + i % 5) for i in range(150)], 32, 4, 128, 16, "tokens", 0),  # several long tiles a block, of 8 to 40 rows
+    ([(900 - 5 * i, 1 + i % 9) for i in range(100)], 32, 4, 64, 32, "heads", 9),
+    ([(600 + i, 1 + i % 12) for i in range(90)], 32, 4, 256, 64, "heads", 0),       # 8 to 96 rows
 ]
 
 

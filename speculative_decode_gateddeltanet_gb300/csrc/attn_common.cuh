@@ -56,7 +56,7 @@ struct Params {
   const int32_t *table, *ctx_len, *n_rows, *row_start;
   void* o;
   int64_t o_row, o_head;
-  int4* notes;      // [blocks] {blocks that follow (0: none), b, h, m} of a split tile's first block
+  int4* notes;      // [blocks] note_of a split tile's first block; zeros where the block begins none
   float* partials;  // [blocks][2 slots][kRows][d + 2]: outputs, then the rows' maxima and sums
   int32_t* status;
   int n_blocks;     // blocks of the attention launch
@@ -251,11 +251,13 @@ __device__ __forceinline__ bool begin(Walk<kRows, kKeys>& w, const Params& p, co
   return true;
 }
 
-// the blocks that follow this one in a tile it begins and does not finish
+// The note of a split tile at its first block: the blocks that follow this one
+// in it, its request's first row, kv head and rows, and its first row's number.
 template <int kRows, int kKeys>
-__device__ __forceinline__ int followers(const Walk<kRows, kKeys>& w, const Start& s) {
-  const int rest = w.blocks - w.kb1;
-  return (rest + s.per - 1) / s.per;
+__device__ __forceinline__ int4 note_of(const Walk<kRows, kKeys>& w, const Start& s) {
+  const int followers = (w.blocks - w.kb1 + s.per - 1) / s.per;
+  const int rows = (int)min((long long)kRows, (long long)w.req.n * w.p->G - (long long)w.m * kRows);
+  return {followers, w.req.row0, w.h << 8 | rows, w.m * kRows};
 }
 
 __device__ __forceinline__ float* partial(const Params& p, int block, int slot, int rows) {
@@ -279,9 +281,8 @@ __global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const Param
   const int4 note = p.notes[blockIdx.x];
   const int parts = note.x + 1;
   if (parts <= 1) return;
-  const Request req = request(p, note.y);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int rows = (int)min((long long)kRows, (long long)req.n * p.G - (long long)note.w * kRows);
+  const int rows = note.z & 255, kv_head = note.z >> 8;
   const bool shared = parts > kCombineBatch;
   auto part = [&](int i) { return partial(p, blockIdx.x + i, i == 0, kRows); };
   auto stats = [&](int i, int row) { return reinterpret_cast<const float2*>(part(i) + (size_t)kRows * kD)[row]; };
@@ -289,6 +290,22 @@ __global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const Param
   const int step = shared ? kCombineBlocks : kCombineBlocks * kCombineWarps;
   const int i_first = shared ? warp : 0, i_step = shared ? kCombineWarps : 1;
   for (int row = first; row < rows; row += step) {
+    float x[kCombineBatch][kPer], tops[kCombineBatch], acc[kPer] = {};
+    auto load = [&](int i0) {
+#pragma unroll
+      for (int j = 0; j < kCombineBatch; ++j) {
+        const int i = min(i0 + j * i_step, parts - 1);
+        tops[j] = stats(i, row).x;
+        const float* src = part(i) + (size_t)row * kD + lane * 2;
+#pragma unroll
+        for (int c = 0; c < kPer / 2; ++c) {
+          const float2 v = *reinterpret_cast<const float2*>(src + c * 64);
+          x[j][2 * c] = v.x;
+          x[j][2 * c + 1] = v.y;
+        }
+      }
+    };
+    load(i_first);  // on their way while the maximum and the sum are formed
     float top = -INFINITY, sum = 0.f;
     for (int i = lane; i < parts; i += 32) top = fmaxf(top, stats(i, row).x);
 #pragma unroll
@@ -300,25 +317,15 @@ __global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const Param
     }
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) sum += __shfl_xor_sync(kFull, sum, off);
-    float acc[kPer] = {};
     for (int i0 = i_first; i0 < parts; i0 += i_step * kCombineBatch) {
-      float x[kCombineBatch][kPer], weight[kCombineBatch];
+      if (i0 != i_first) load(i0);
 #pragma unroll
       for (int j = 0; j < kCombineBatch; ++j) {
-        const int i = min(i0 + j * i_step, parts - 1);
-        weight[j] = i0 + j * i_step < parts ? exp2f(stats(i, row).x - top) : 0.f;
-        const float* src = part(i) + (size_t)row * kD + lane * 2;
+        if (i0 + j * i_step >= parts) break;
+        const float weight = exp2f(tops[j] - top);
 #pragma unroll
-        for (int c = 0; c < kPer / 2; ++c) {
-          const float2 v = *reinterpret_cast<const float2*>(src + c * 64);
-          x[j][2 * c] = v.x;
-          x[j][2 * c + 1] = v.y;
-        }
+        for (int c = 0; c < kPer; ++c) acc[c] = fmaf(weight, x[j][c], acc[c]);
       }
-#pragma unroll
-      for (int j = 0; j < kCombineBatch; ++j)
-#pragma unroll
-        for (int c = 0; c < kPer; ++c) acc[c] = i0 + j * i_step < parts ? fmaf(weight[j], x[j][c], acc[c]) : acc[c];
     }
     if (shared) {
 #pragma unroll
@@ -334,8 +341,8 @@ __global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const Param
       if (warp != 0) continue;
     }
     const float inv = 1.f / sum;
-    const int at = note.w * kRows + row, token = at / p.G, head = note.z * p.G + at % p.G;
-    T* dst = static_cast<T*>(p.o) + (int64_t)(req.row0 + token) * p.o_row + head * p.o_head + lane * 2;
+    const int at = note.w + row, token = (int)quotient(at, p.by_G), head = kv_head * p.G + at - token * p.G;
+    T* dst = static_cast<T*>(p.o) + (int64_t)(note.y + token) * p.o_row + (int64_t)head * p.o_head + lane * 2;
 #pragma unroll
     for (int c = 0; c < kPer / 2; ++c) {
       const float a = acc[2 * c] * inv, b = acc[2 * c + 1] * inv;

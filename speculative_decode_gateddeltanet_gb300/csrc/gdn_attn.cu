@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kSimtThreads) simt_kernel(const Params p) {
       }
       const bool whole = w.kb0 == 0 && w.kb1 == w.blocks;
       const int slot = w.kb0 == 0 ? 1 : 0;
-      if (!whole && slot == 1) note = {followers(w, s), w.b, w.h, w.m};
+      if (!whole && slot == 1) note = note_of(w, s);
       float* const out = partial(p, blockIdx.x, slot, kR);
 #pragma unroll
       for (int r = 0; r < kWarpRows; ++r) {

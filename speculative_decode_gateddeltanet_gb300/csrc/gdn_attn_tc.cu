@@ -8,10 +8,13 @@
 //                   TMEM as bf16 over S's columns
 //   O += P V        tcgen05.mma, P from TMEM, V from shared memory, O in TMEM
 // S has two buffers: the tensor cores form S of block j+1 while the softmax
-// works on block j, so the two overlap and the longer of them sets the pace.
+// works on block j, so the two overlap and the longer of them sets the pace.  O
+// has two where TMEM holds them (d <= 128): a tile is written out while the next
+// one runs, so the copies of K and V never wait for a tile's end.
 //
-// Roles (384 threads): warps 0-3 softmax and output, warp 4 issues the MMAs,
-// warps 5 and 6 the TMA copies of K and of V, warps 7-11 stage Q.
+// Roles (384 threads): warps 0-3 softmax, warp 4 issues the MMAs, warps 5 and 6
+// the TMA copies of K and of V, warps 8-11 stage Q and write the tiles out
+// (a TMEM lane is read by the warps of its quarter only: 0-3 and 8-11 match).
 //
 // Few rows.  A TMEM lane belongs to one warp, so 32 rows would leave three of
 // the four softmax warps idle, and one warp's 128 exponentials a row take longer
@@ -45,7 +48,6 @@ namespace gdnattn {
 
 constexpr int kTcRows = 128;
 constexpr int kTcThreads = 384;
-constexpr int kQThreads = 160;
 constexpr int kTcBlocks = 152;  // one block per SM of a GB300
 constexpr int kTcMinUnits = 1;
 constexpr unsigned long long kWaitNs = 500000000ull;
@@ -56,9 +58,11 @@ struct Shape {
   static constexpr int kChunks = kD / 64;                 // 128-byte column chunks of a row
   static constexpr int kQBytes = kTcRows * kD * 2;
   static constexpr int kTileBytes = kKeys * kD * 2;       // a K or V tile
-  static constexpr int kK = kD == 64 ? 6 : 3;             // K tiles in flight
-  static constexpr int kV = kD == 64 ? 6 : kD == 128 ? 3 : 2;
-  static constexpr int kSmem = 1024 + kQBytes + (kK + kV) * kTileBytes;
+  static constexpr int kK = kD == 64 ? 6 : kD == 128 ? 3 : 2;  // K tiles in flight
+  static constexpr int kV = kD == 64 ? 5 : 2;
+  static constexpr int kOs = kD == 256 ? 1 : 2;           // O buffers: 2 * kKeys + kOs * kD of 512 TMEM columns
+  static constexpr int kJoinBytes = 128 * 32 * 4;         // 32 columns of every copy's rows
+  static constexpr int kSmem = 1024 + kQBytes + (kK + kV) * kTileBytes + kJoinBytes;
 };
 static_assert(Shape<128>::kSmem <= 230 * 1024 && Shape<256>::kSmem <= 230 * 1024 && Shape<64>::kSmem <= 230 * 1024);
 
@@ -289,29 +293,32 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   using S = Shape<kD>;
   constexpr int kKeys = S::kKeys, kChunks = S::kChunks;
   const Params& p = t.p;
+  const uint32_t q_flip = t.q_flip;
   extern __shared__ uint8_t raw[];
-  __shared__ __align__(8) uint64_t bars[2 * S::kK + 2 * S::kV + 11];
+  __shared__ __align__(8) uint64_t bars[2 * S::kK + 2 * S::kV + 15];
   __shared__ long long scan[kTcThreads / 32];
   __shared__ Start start;
   __shared__ uint32_t tmem_base;
   __shared__ int gave_up;
-  __shared__ float2 stats[128];  // maxima and sums of a tile's copies
+  __shared__ float2 stats[2][128];  // maxima and sums of a tile's rows (and copies)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
-  const uint32_t q_s = base, k_s = q_s + S::kQBytes, v_s = k_s + S::kK * S::kTileBytes;
+  const uint32_t q_s = base, k_s = q_s + S::kQBytes, v_s = k_s + S::kK * S::kTileBytes, join_s = v_s + S::kV * S::kTileBytes;
+  // A wait names a phase by its parity, so a barrier may be at most one phase ahead of any of its waiters, and each
+  // waiter takes every phase in turn; what may be signalled twice before it is waited for has two barriers.
   const uint32_t b0 = smem_addr(bars);
   auto k_full = [&](int i) { return b0 + 8 * i; };
   auto k_empty = [&](int i) { return b0 + 8 * (S::kK + i); };
   auto v_full = [&](int i) { return b0 + 8 * (2 * S::kK + i); };
   auto v_empty = [&](int i) { return b0 + 8 * (2 * S::kK + S::kV + i); };
   constexpr int kRest = 2 * S::kK + 2 * S::kV;
-  auto s_full = [&](int i) { return b0 + 8 * (kRest + i); };    // S of a block is in TMEM
-  auto p_ready = [&](int i) { return b0 + 8 * (kRest + 2 + i); };  // its P is
-  // A wait names a phase by its parity, so a barrier may be at most one phase ahead of any of its waiters: what two
-  // blocks in a row signal has two barriers in turn.
-  auto pv_done = [&](int i) { return b0 + 8 * (kRest + 4 + (i & 1)); };  // O holds the products of block i
-  const uint32_t q_full = b0 + 8 * (kRest + 6), q_empty = b0 + 8 * (kRest + 7), o_free = b0 + 8 * (kRest + 8),
-                 joined = b0 + 8 * (kRest + 9), drained = b0 + 8 * (kRest + 10);
+  auto s_full = [&](int i) { return b0 + 8 * (kRest + (i & 1)); };       // S of block i is in TMEM
+  auto p_ready = [&](int i) { return b0 + 8 * (kRest + 2 + (i & 1)); };  // its P is
+  auto pv_done = [&](int i) { return b0 + 8 * (kRest + 4 + (i & 1)); };  // O holds its products
+  auto st_ready = [&](int g) { return b0 + 8 * (kRest + 6 + (g & 1)); };  // tile g's maxima and sums are in `stats`
+  auto o_full = [&](int g) { return b0 + 8 * (kRest + 8 + (g & 1)); };    // tile g's O is whole
+  auto o_free = [&](int g) { return b0 + 8 * (kRest + 10 + (g & 1)); };   // and has been written out
+  const uint32_t q_full = b0 + 8 * (kRest + 12), q_empty = b0 + 8 * (kRest + 13), drained = b0 + 8 * (kRest + 14);
   if (tid == 0) {
     gave_up = 0;
     for (int i = 0; i < S::kK; ++i) {
@@ -325,19 +332,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     for (int i = 0; i < 2; ++i) {
       bar_init(s_full(i), 1);
       bar_init(p_ready(i), 128);
+      bar_init(pv_done(i), 1);
+      bar_init(st_ready(i), 128);
+      bar_init(o_full(i), 1);
+      bar_init(o_free(i), 128);
     }
-    bar_init(pv_done(0), 1);
-    bar_init(pv_done(1), 1);
-    bar_init(q_full, kQThreads);
+    bar_init(q_full, 128);
     bar_init(q_empty, 1);
-    bar_init(o_free, 128);
-    bar_init(joined, 128);
     bar_init(drained, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 4) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&tmem_base)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (warp == 5 && lane == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&k_map) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&v_map) : "memory");
   }
   tc_fence_before();
   __syncthreads();
@@ -348,29 +359,166 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   find_start<kTcRows, kKeys, kTcThreads>(p, kTcMinUnits, scan, &start);
   const Start s = start;
   constexpr uint32_t kOCol = 2 * kKeys;  // TMEM columns: two S buffers, then O
-  int4 note = {0, 0, 0, 0};
+  auto o_col = [&](int g) { return kOCol + (S::kOs == 2 ? (g & 1) * kD : 0); };
   Walk<kTcRows, kKeys> w;
   const bool any = begin(w, p, s);
   bool ok = true;
   int sent = 0;  // tiles whose copies this warp issued
+  auto rows_of = [&](const Walk<kTcRows, kKeys>& t) {
+    return (int)min((long long)kTcRows, (long long)t.req.n * p.G - (long long)t.m * kTcRows);
+  };
 
-  if (any && warp < 4) {
-    // ---- softmax and output: one thread per row (and copy)
+  if (warp >= 8) {
+    // ---- Q into the swizzled layout, and the tiles out of TMEM
+    int4 note = {0, 0, 0, 0};
+    if (any) {
+      const int e_tid = tid - 256, quarter = warp - 8;
+      const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+      constexpr int kUnits = kD / 8;  // 16-byte units of a row
+      constexpr int kBatch = 8;       // units a thread holds: 32 rows of 256 columns at once
+      auto stage_q = [&](const Walk<kTcRows, kKeys>& t, int g) {
+        const int rows = rows_of(t), copies = copies_of(rows);
+        for (int i0 = 0; i0 < rows * kUnits; i0 += kBatch * 128) {
+          uint4 x[kBatch];
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j) {
+            // past the tile's rows its last one again: no load hides behind a branch
+            const int i = i0 + j * 128 + e_tid, r = min(i / kUnits, rows - 1), u = i % kUnits, at = t.m * kTcRows + r;
+            const int token = (int)quotient(at, p.by_G), head = t.h * p.G + at - token * p.G;
+            x[j] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + (int64_t)(t.req.row0 + token) * p.q_row +
+                                                        (int64_t)head * p.q_head + u * 8));
+          }
+          // the rows are on their way while the last tile's products with Q end
+          if (i0 == 0 && g > 0 && !bar_wait(q_empty, (g - 1) & 1, &gave_up)) return false;
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j) {
+            const int i = i0 + j * 128 + e_tid;
+            if (i < rows * kUnits) {
+              const int r = i / kUnits, u = i % kUnits;
+              const uint4 y = make_uint4(x[j].x ^ q_flip, x[j].y ^ q_flip, x[j].z ^ q_flip, x[j].w ^ q_flip);
+              for (int c = 0; c < copies; ++c) {
+                const uint32_t dst = q_s + (u / 8) * (kTcRows * 128) + (r + c * (kTcRows / copies)) * 128 + (((u & 7) ^ (r & 7)) << 4);
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w) : "memory");
+              }
+            }
+          }
+        }
+        fence_async();
+        bar_arrive(q_full);
+        return true;
+      };
+      ok = stage_q(w, 0);
+      for (int g = 0; ok && !w.done(); ++g) {
+        Walk<kTcRows, kKeys> next = w;
+        next.next();
+        if (!next.done() && !(ok = stage_q(next, g + 1))) break;
+        const int rows = rows_of(w), copies = copies_of(rows), spread = 4 / copies;
+        const int copy = quarter / spread, row = (quarter % spread) * 32 + lane;
+        const bool whole = w.kb0 == 0 && w.kb1 == w.blocks;
+        const int slot = w.kb0 == 0 ? 1 : 0;
+        if (!whole && slot == 1) note = note_of(w, s);
+        float* const out = partial(p, blockIdx.x, slot, kTcRows);
+        const int at = min(w.m * kTcRows + row, w.req.n * p.G - 1);
+        const int token = (int)quotient(at, p.by_G), head = w.h * p.G + at - token * p.G;
+        __nv_bfloat16* const dst =
+            static_cast<__nv_bfloat16*>(p.o) + (int64_t)(w.req.row0 + token) * p.o_row + (int64_t)head * p.o_head;
+        ok = warp_wait(st_ready(g), (g >> 1) & 1, &gave_up) && warp_wait(o_full(g), (g >> 1) & 1, &gave_up);
+        if (!ok) break;
+        tc_fence_after();
+        const float2* const st = stats[g & 1];
+        const uint32_t o_at = lanes + o_col(g);
+        if (copies == 1) {
+          const float2 mine = st[e_tid];
+          if (quarter * 32 < rows) {
+            const float inv = 1.f / mine.y;
+#pragma unroll 1
+            for (int c = 0; c < kD / 32; ++c) {
+              uint32_t o[32];
+              tmem_load(o, o_at + c * 32);
+              tmem_wait_load();
+              if (row < rows) {
+                if (whole) {
+                  uint32_t pk[16];
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) pk[i] = pack_bf16(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
+#pragma unroll
+                  for (int i = 0; i < 4; ++i)
+                    reinterpret_cast<uint4*>(dst + c * 32)[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+                } else {
+#pragma unroll
+                  for (int i = 0; i < 8; ++i)
+                    reinterpret_cast<uint4*>(out + row * kD + c * 32)[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                }
+              }
+            }
+            if (!whole && row < rows) reinterpret_cast<float2*>(out + kTcRows * kD)[row] = mine;
+          }
+        } else {
+          // Join the copies, 32 columns at a time: each warp brings its rows scaled to the common maximum, then sums its
+          // share of their 16-byte units over the copies.
+          const int span = 128 / copies;
+          float top = -INFINITY, sum = 0.f;
+          for (int c = 0; c < copies; ++c) top = fmaxf(top, st[c * span + row].x);
+          const float sub = top == -INFINITY ? 0.f : top;
+          for (int c = 0; c < copies; ++c) sum += st[c * span + row].y * ex2(st[c * span + row].x - sub);
+          const float scale = ex2(st[e_tid].x - sub) * (whole ? 1.f / sum : 1.f);
+#pragma unroll 1
+          for (int c = 0; c < kD / 32; ++c) {
+            uint32_t o[32];
+            tmem_load(o, o_at + c * 32);
+            tmem_wait_load();
+            if (c > 0) asm volatile("bar.sync 1, 128;" ::: "memory");  // the last columns have been read
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint32_t to = join_s + e_tid * 128 + ((i ^ (lane & 7)) << 4);
+              asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(__uint_as_float(o[4 * i]) * scale),
+                           "f"(__uint_as_float(o[4 * i + 1]) * scale), "f"(__uint_as_float(o[4 * i + 2]) * scale),
+                           "f"(__uint_as_float(o[4 * i + 3]) * scale)
+                           : "memory");
+            }
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            if (row < rows) {
+              for (int i = copy * (8 / copies); i < (copy + 1) * (8 / copies); ++i) {
+                float4 a = {0.f, 0.f, 0.f, 0.f};
+                for (int j = 0; j < copies; ++j) {
+                  float4 v;
+                  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                               : "r"(join_s + (j * span + row) * 128 + ((i ^ (lane & 7)) << 4))
+                               : "memory");
+                  a.x += v.x;
+                  a.y += v.y;
+                  a.z += v.z;
+                  a.w += v.w;
+                }
+                const int col = c * 32 + i * 4;
+                if (whole) *reinterpret_cast<uint2*>(dst + col) = make_uint2(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w));
+                else *reinterpret_cast<float4*>(out + row * kD + col) = a;
+              }
+            }
+          }
+          if (!whole && row < rows && copy == 0) reinterpret_cast<float2*>(out + kTcRows * kD)[row] = make_float2(top, sum);
+          asm volatile("bar.sync 1, 128;" ::: "memory");  // the last columns have been read
+        }
+        tc_fence_before();
+        bar_arrive(o_free(g));
+        w = next;
+      }
+    }
+    if (tid == 256) p.notes[blockIdx.x] = note;
+  } else if (any && warp < 4) {
+    // ---- softmax: one thread per row (and copy)
     const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
-    int it = 0;
+    int it = 0, g = 0;
     auto products = [&](int i) { return warp_wait(pv_done(i), (i >> 1) & 1, &gave_up); };
-    for (; ok && !w.done(); w.next()) {
-      const int rows = (int)min((long long)kTcRows, (long long)w.req.n * p.G - (long long)w.m * kTcRows);
-      const int copies = copies_of(rows), spread = 4 / copies;  // warps of one copy
+    for (; ok && !w.done(); w.next(), ++g) {
+      const int rows = rows_of(w), copies = copies_of(rows), spread = 4 / copies;  // warps of one copy
       const int copy = warp / spread, row = (warp % spread) * 32 + lane;
       const bool active = (warp % spread) * 32 < rows;  // a warp with no row only keeps step
-      const int at = w.m * kTcRows + row;
-      const int token = (int)quotient(at, p.by_G), head = w.h * p.G + at - token * p.G;
-      const int last = row < rows ? w.req.ctx + token : -1;
+      const int last = row < rows ? w.req.ctx + (int)quotient(w.m * kTcRows + row, p.by_G) : -1;
       RowState st = {-INFINITY, 0.f};
       for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
-        const int buf = it & 1;
-        if (!(ok = warp_wait(s_full(buf), (it >> 1) & 1, &gave_up))) break;
+        if (!(ok = warp_wait(s_full(it), (it >> 1) & 1, &gave_up))) break;
         if (it >= 2 && !(ok = products(it - 2))) break;  // each block's, in turn
         if (active) {
           tc_fence_after();
@@ -381,17 +529,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll 1
             for (int c = 0; c < kD / 32; ++c) {
               uint32_t o[32];
-              tmem_load(o, lanes + kOCol + c * 32);
+              tmem_load(o, lanes + o_col(g) + c * 32);
               tmem_wait_load();
 #pragma unroll
               for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * shrink);
-              tmem_store(lanes + kOCol + c * 32, o);
+              tmem_store(lanes + o_col(g) + c * 32, o);
             }
             tmem_wait_store();
             return true;
           };
           const int edge = last - kb * kKeys;
-          const uint32_t s_at = lanes + buf * kKeys;
+          const uint32_t s_at = lanes + (it & 1) * kKeys;
           if (copies == 1) ok = softmax_block<kKeys, 1>(st, s_at, 0, edge, p.scale_log2, rescale);
           else if (copies == 2) ok = softmax_block<kKeys, 2>(st, s_at, copy, edge, p.scale_log2, rescale);
           else ok = softmax_block<kKeys, 4>(st, s_at, copy, edge, p.scale_log2, rescale);
@@ -399,153 +547,65 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           tc_fence_before();
         }
         const int valid = w.req.ctx + w.req.n - kb * kKeys;
-        if (valid < kKeys) {
-          // The V rows behind the request's last token: their weight is 0, but 0 times what a page holds there may be NaN.
+        if (valid < kKeys && valid % 16 != 0) {
+          // The V rows between the request's last token and the last 16 that the MMA reads: their weight is 0, but 0
+          // times what a page holds there may be NaN.
           const int vs = it % S::kV;
           if (!(ok = warp_wait(v_full(vs), (it / S::kV) & 1, &gave_up))) break;
-          for (int i = tid; i < (kKeys - valid) * (kD / 8); i += 128) {
+          for (int i = tid; i < (16 - valid % 16) * (kD / 8); i += 128) {
             const int r = valid + i / (kD / 8), u = i % (kD / 8);
             const uint32_t to = v_s + vs * S::kTileBytes + (u / 8) * (kKeys * 128) + r * 128 + ((u & 7) << 4);
             asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(to), "r"(0) : "memory");
           }
           fence_async();
         }
-        bar_arrive(p_ready(buf));
+        bar_arrive(p_ready(it));
       }
-      if (!ok || !(ok = products(it - 1))) break;
-      const bool whole = w.kb0 == 0 && w.kb1 == w.blocks;
-      const int slot = w.kb0 == 0 ? 1 : 0;
-      if (!whole && slot == 1) note = {followers(w, s), w.b, w.h, w.m};
-      tc_fence_after();
-      float* const out = partial(p, blockIdx.x, slot, kTcRows);
-      __nv_bfloat16* const dst =
-          static_cast<__nv_bfloat16*>(p.o) + (int64_t)(w.req.row0 + token) * p.o_row + (int64_t)head * p.o_head;
-      if (copies == 1) {
-        if (active) {
-          const float inv = 1.f / st.sum;
-#pragma unroll 1
-          for (int c = 0; c < kD / 32; ++c) {
-            uint32_t o[32];
-            tmem_load(o, lanes + kOCol + c * 32);
-            tmem_wait_load();
-            if (row < rows) {
-              if (whole) {
-                uint32_t pk[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) pk[i] = pack_bf16(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  reinterpret_cast<uint4*>(dst + c * 32)[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
-              } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  reinterpret_cast<uint4*>(out + row * kD + c * 32)[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-              }
-            }
-          }
-        }
-      } else {
-        // Join the copies, half of the columns at a time, through Q's place (the products with Q are done, and the Q
-        // warps wait for `joined` before they stage the next tile): each warp brings its rows scaled to the common
-        // maximum, then sums its share of their 16-byte units over the copies.
-        const int span = 128 / copies;
-        stats[tid] = make_float2(st.top, st.sum);
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        float top = -INFINITY, sum = 0.f;
-        for (int c = 0; c < copies; ++c) top = fmaxf(top, stats[c * span + row].x);
-        const float sub = top == -INFINITY ? 0.f : top;
-        for (int c = 0; c < copies; ++c) sum += stats[c * span + row].y * ex2(stats[c * span + row].x - sub);
-        const float scale = ex2(st.top - sub) * (whole ? 1.f / sum : 1.f);
-        st.top = top;
-        constexpr int kHalf = kD / 2, kHalfUnits = kHalf / 4;
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          if (half) asm volatile("bar.sync 1, 128;" ::: "memory");  // the first half has been read
-#pragma unroll
-          for (int c = 0; c < kHalf / 32; ++c) {
-            uint32_t o[32];
-            tmem_load(o, lanes + kOCol + half * kHalf + c * 32);
-            tmem_wait_load();
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const uint32_t to = q_s + tid * (kHalf * 4) + (((c * 8 + i) ^ (lane & 7)) << 4);
-              asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(__uint_as_float(o[4 * i]) * scale),
-                           "f"(__uint_as_float(o[4 * i + 1]) * scale), "f"(__uint_as_float(o[4 * i + 2]) * scale),
-                           "f"(__uint_as_float(o[4 * i + 3]) * scale)
-                           : "memory");
-            }
-          }
-          asm volatile("bar.sync 1, 128;" ::: "memory");
-          if (row < rows) {
-            auto sum_units = [&](auto copies_c) {
-              constexpr int kC = decltype(copies_c)::value;
-#pragma unroll
-              for (int i = 0; i < kHalfUnits / kC; ++i) {
-                const int unit = copy * (kHalfUnits / kC) + i;
-                float4 a = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int j = 0; j < kC; ++j) {
-                  float4 v;
-                  asm("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                      : "r"(q_s + (j * (128 / kC) + row) * (kHalf * 4) + ((unit ^ (lane & 7)) << 4))
-                      : "memory");
-                  a.x += v.x;
-                  a.y += v.y;
-                  a.z += v.z;
-                  a.w += v.w;
-                }
-                const int col = half * kHalf + unit * 4;
-                if (whole) *reinterpret_cast<uint2*>(dst + col) = make_uint2(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w));
-                else *reinterpret_cast<float4*>(out + row * kD + col) = a;
-              }
-            };
-            if (copies == 4) sum_units(std::integral_constant<int, 4>());
-            else sum_units(std::integral_constant<int, 2>());
-          }
-        }
-        st.sum = sum;
-        bar_arrive(joined);
-      }
-      if (!whole && row < rows && copy == 0) reinterpret_cast<float2*>(out + kTcRows * kD)[row] = make_float2(st.top, st.sum);
-      tc_fence_before();
-      bar_arrive(o_free);
+      if (ok && g >= 2) ok = warp_wait(o_free(g), ((g >> 1) - 1) & 1, &gave_up);  // tile g - 2 is done with its place in stats
+      if (!ok) break;
+      stats[g & 1][tid] = make_float2(st.top, st.sum);
+      bar_arrive(st_ready(g));
     }
   } else if (any && warp == 4) {
     // ---- the MMAs, issued by one thread
     if (lane == 0) {
       constexpr uint32_t kQk = instruction(kKeys, false), kPv = instruction(kD, true);
-      int it = 0, seg = 0;
-      for (; ok && !w.done(); w.next(), ++seg) {
-        if (!(ok = bar_wait(q_full, seg & 1, &gave_up))) break;
+      int it = 0, g = 0;
+      for (; ok && !w.done(); w.next(), ++g) {
+        if (!(ok = bar_wait(q_full, g & 1, &gave_up))) break;
+        const int len = w.req.ctx + w.req.n;
         for (int kb = w.kb0; kb <= w.kb1; ++kb) {
           if (kb < w.kb1) {
-            const int i = it + kb - w.kb0, st = i % S::kK, buf = i & 1;
+            const int i = it + kb - w.kb0, st = i % S::kK;
             if (!(ok = bar_wait(k_full(st), (i / S::kK) & 1, &gave_up))) break;
             tc_fence_after();
 #pragma unroll
             for (int k = 0; k < kD / 16; ++k) {
               const uint32_t q_at = q_s + (k / 4) * (kTcRows * 128) + (k % 4) * 32;
               const uint32_t k_at = k_s + st * S::kTileBytes + (k / 4) * (kKeys * 128) + (k % 4) * 32;
-              mma_ss(tmem + buf * kKeys, operand(q_at, 16, 1024), operand(k_at, 16, 1024), kQk, k > 0);
+              mma_ss(tmem + (i & 1) * kKeys, operand(q_at, 16, 1024), operand(k_at, 16, 1024), kQk, k > 0);
             }
             tc_commit(k_empty(st));
-            tc_commit(s_full(buf));
+            tc_commit(s_full(i));
             if (kb == w.kb1 - 1) tc_commit(q_empty);
           }
           if (kb > w.kb0) {
-            const int i = it + kb - 1 - w.kb0, buf = i & 1, st = i % S::kV;
+            const int i = it + kb - 1 - w.kb0, st = i % S::kV;
             const bool first = kb - 1 == w.kb0;
-            ok = bar_wait(p_ready(buf), (i >> 1) & 1, &gave_up) && bar_wait(v_full(st), (i / S::kV) & 1, &gave_up);
-            if (ok && first && seg > 0) ok = bar_wait(o_free, (seg - 1) & 1, &gave_up);
+            ok = bar_wait(p_ready(i), (i >> 1) & 1, &gave_up) && bar_wait(v_full(st), (i / S::kV) & 1, &gave_up);
+            // the buffer's last tile has been written out
+            if (ok && first && g >= S::kOs) ok = bar_wait(o_free(g - S::kOs), ((g - S::kOs) >> 1) & 1, &gave_up);
             if (!ok) break;
             tc_fence_after();
+            const int steps = min(kKeys / 16, (len - (kb - 1) * kKeys + 15) / 16);  // no V row behind the last 16 with a token
 #pragma unroll
             for (int k = 0; k < kKeys / 16; ++k)
-              mma_ts(tmem + kOCol, tmem + buf * kKeys + k * 8, operand(v_s + st * S::kTileBytes + k * 2048, kKeys * 128, 1024),
-                     kPv, !(first && k == 0));
+              if (k < steps)
+                mma_ts(tmem + o_col(g), tmem + (i & 1) * kKeys + k * 8, operand(v_s + st * S::kTileBytes + k * 2048, kKeys * 128, 1024),
+                       kPv, !(first && k == 0));
             tc_commit(v_empty(st));
             tc_commit(pv_done(i));
+            if (kb == w.kb1) tc_commit(o_full(g));
           }
         }
         it += w.kb1 - w.kb0;
@@ -596,52 +656,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
       }
     }
-  } else if (any) {
-    // ---- Q rows into the swizzled layout
-    const int q_tid = tid - (kTcThreads - kQThreads);
-    constexpr int kUnits = kD / 8;  // 16-byte units of a row
-    constexpr int kBatch = 8;       // units a thread holds: 32 rows of 256 columns at once, nearly
-    int seg = 0, joins = 0, copies = 1;
-    for (; ok && !w.done(); w.next(), ++seg) {
-      const int rows = (int)min((long long)kTcRows, (long long)w.req.n * p.G - (long long)w.m * kTcRows);
-      const int before = copies;
-      copies = copies_of(rows);
-      for (int i0 = 0; i0 < rows * kUnits; i0 += kBatch * kQThreads) {
-        uint4 x[kBatch];
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-          // past the tile's rows its last one again: no load hides behind a branch
-          const int i = i0 + j * kQThreads + q_tid, r = min(i / kUnits, rows - 1), u = i % kUnits, at = w.m * kTcRows + r;
-          const int token = (int)quotient(at, p.by_G), head = w.h * p.G + at - token * p.G;
-          x[j] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + (int64_t)(w.req.row0 + token) * p.q_row +
-                                                      (int64_t)head * p.q_head + u * 8));
-        }
-        // the rows are on their way while the last tile's products with Q, and its join through Q's place, end
-        if (i0 == 0 && seg > 0) {
-          ok = bar_wait(q_empty, (seg - 1) & 1, &gave_up);
-          if (ok && before > 1) ok = bar_wait(joined, joins++ & 1, &gave_up);
-          if (!ok) break;
-        }
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-          const int i = i0 + j * kQThreads + q_tid;
-          if (i < rows * kUnits) {
-            const int r = i / kUnits, u = i % kUnits;
-            const uint4 y = make_uint4(x[j].x ^ t.q_flip, x[j].y ^ t.q_flip, x[j].z ^ t.q_flip, x[j].w ^ t.q_flip);
-            for (int c = 0; c < copies; ++c) {
-              const int to_row = r + c * (kTcRows / copies);
-              const uint32_t dst = q_s + (u / 8) * (kTcRows * 128) + to_row * 128 + (((u & 7) ^ (r & 7)) << 4);
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w) : "memory");
-            }
-          }
-        }
-      }
-      if (!ok) break;
-      fence_async();
-      bar_arrive(q_full);
-    }
   }
-  if (tid == 0) p.notes[blockIdx.x] = note;
   __syncthreads();
   if (gave_up) {
     // products and copies that may still be in flight, with a bound again

@@ -7,12 +7,12 @@
 //   A tile needs the blocks up to its last row's position:
 //     c(m) = floor((ctx + floor((last row of m) / G)) / kKeys) + 1.
 // Division.  All (request, kv head, tile, key block) units of a call form one
-//   line; block i takes units [i*per, (i+1)*per).  Every block so has the same
-//   number of key blocks however ragged the lengths are: a long context is
-//   split over many blocks, many short ones share a block.  The line's length
-//   needs only sums of c(m), which a floor-sum gives without a loop over tiles,
-//   so each block finds its own part in a scan over the requests, with no
-//   planning launch before it.
+//   line, with some units more for each tile's own cost (its q rows in, its o
+//   rows out); block i takes units [i*per, (i+1)*per).  Every block so has the
+//   same work however ragged the lengths are: a long context is split over many
+//   blocks, many short ones share a block.  The line's length needs only sums of
+//   c(m), which a floor-sum gives without a loop over tiles, so each block finds
+//   its own part in a scan over the requests, with no planning launch before it.
 // Join.  A tile whose units lie in several blocks is split: its first block
 //   writes a head partial (slot 1) and a note of how many blocks follow, each
 //   of those writes a tail partial (slot 0): the running maximum, sum and
@@ -112,16 +112,19 @@ struct Tiles {
     const int token = last >> 31 ? (int)(last / p.G) : (int)quotient((uint32_t)last, p.by_G);
     return (int)((unsigned)(r.ctx + token) / kKeys) + 1;
   }
-  // key blocks of the tiles before m
+  // units that a tile costs beside its key blocks: a tile of 128 rows takes about three blocks' time from its last
+  // product to the next one's first, one of a few rows hides behind the copies of the next one's keys
+  __device__ static int extra(const Params& p, const Request& r) { return kRows < 128 ? 0 : (long long)r.n * p.G > 64 ? 3 : 1; }
+  // units of the tiles before m
   __device__ static long long before(const Params& p, const Request& r, int m) {
     if (m == 0) return 0;
-    return m + floor_sum(m, (long long)p.G * kKeys, kRows, (long long)p.G * r.ctx + kRows - 1);
+    return (long long)m * (1 + extra(p, r)) + floor_sum(m, (long long)p.G * kKeys, kRows, (long long)p.G * r.ctx + kRows - 1);
   }
-  // key blocks of one kv head of the request
+  // units of one kv head of the request
   __device__ static long long sum(const Params& p, const Request& r) {
     if (r.n <= 0) return 0;
     const int M = count(p, r);
-    return before(p, r, M - 1) + blocks(p, r, M - 1);
+    return before(p, r, M - 1) + extra(p, r) + blocks(p, r, M - 1);
   }
 };
 
@@ -131,17 +134,21 @@ struct Walk {
   using T = Tiles<kRows, kKeys>;
   Request req;
   int b, h, m, tiles, left;  // left: units still to do
-  int kb0, kb1, blocks;      // this segment's key blocks, and how many the whole tile has
+  int at;                    // the segment's first unit within its tile: the tile's own units come first
+  int kb0, kb1, blocks;      // its key blocks, and how many the whole tile has
 
   __device__ void segment() {
     blocks = T::blocks(*p, req, m);
-    kb1 = min(blocks, kb0 + left);
+    const int own = T::extra(*p, req), end = min(own + blocks, at + left);
+    kb0 = max(0, at - own);
+    kb1 = end - own;
+    if (kb1 <= kb0) left = 0;  // the block's part ends before the tile's first key block
   }
   __device__ bool done() const { return left <= 0; }
   __device__ void next() {
-    left -= kb1 - kb0;
+    left -= kb1 + T::extra(*p, req) - at;
     if (left <= 0) return;
-    kb0 = 0;
+    at = 0;
     if (++m == tiles) {
       m = 0;
       if (++h == p->H_kv) {
@@ -246,9 +253,9 @@ __device__ __forceinline__ bool begin(Walk<kRows, kKeys>& w, const Params& p, co
     else hi = mid;
   }
   w.m = lo;
-  w.kb0 = (int)(off - T::before(p, w.req, lo));
+  w.at = (int)(off - T::before(p, w.req, lo));
   w.segment();
-  return true;
+  return !w.done();
 }
 
 // The note of a split tile at its first block: the blocks that follow this one

@@ -7,14 +7,18 @@
 //   P = 2^(s - m)   one thread per row: running maximum m, running sum, P to
 //                   TMEM as bf16 over S's columns
 //   O += P V        tcgen05.mma, P from TMEM, V from shared memory, O in TMEM
-// S has two buffers: the tensor cores form S of block j+1 while the softmax
-// works on block j, so the two overlap and the longer of them sets the pace.  O
-// has two where TMEM holds them (d <= 128): a tile is written out while the next
-// one runs, so the copies of K and V never wait for a tile's end.
+// Two streams (d <= 128).  A thread's 128 exponentials and what goes with them
+// take longer than the two products, so two warpgroups halve a block's keys: each
+// has its own O in TMEM and its own running maximum and sum, and the two are
+// joined when the tile is written out; no word passes between them before that.
+// Where O fills TMEM (d = 256) blocks have 64 keys and one warpgroup.  S has two
+// buffers: the tensor cores form the next S while the softmax works on this one.
 //
-// Roles (384 threads): warps 0-3 softmax, warp 4 issues the MMAs, warps 5 and 6
-// the TMA copies of K and of V, warps 8-11 stage Q and write the tiles out
-// (a TMEM lane is read by the warps of its quarter only: 0-3 and 8-11 match).
+// Roles (512 threads): warps 0-3 and 4-7 softmax, warps 8-11 stage Q and write
+// the tiles out (a TMEM lane is read by the warps of its quarter only), warp 12
+// issues the first product's MMAs, warp 15 the second's (one thread for both would
+// leave the tensor cores idle at each of its waits), warps 13 and 14 the TMA copies
+// of K and of V.
 //
 // Few rows.  A TMEM lane belongs to one warp, so 32 rows would leave three of
 // the four softmax warps idle, and one warp's 128 exponentials a row take longer
@@ -47,9 +51,9 @@
 namespace gdnattn {
 
 constexpr int kTcRows = 128;
-constexpr int kTcThreads = 384;
+constexpr int kTcThreads = 512;
 constexpr int kTcBlocks = 152;  // one block per SM of a GB300
-constexpr int kTcMinUnits = 1;
+constexpr int kTcMinUnits = 2;
 constexpr unsigned long long kWaitNs = 500000000ull;
 
 template <int kD>
@@ -60,7 +64,7 @@ struct Shape {
   static constexpr int kTileBytes = kKeys * kD * 2;       // a K or V tile
   static constexpr int kK = kD == 64 ? 6 : kD == 128 ? 3 : 2;  // K tiles in flight
   static constexpr int kV = kD == 64 ? 5 : 2;
-  static constexpr int kOs = kD == 256 ? 1 : 2;           // O buffers: 2 * kKeys + kOs * kD of 512 TMEM columns
+  static constexpr int kStreams = kD == 256 ? 1 : 2;      // TMEM: two S buffers and an O for each stream, of 512 columns
   static constexpr int kJoinBytes = 128 * 32 * 4;         // 32 columns of every copy's rows
   static constexpr int kSmem = 1024 + kQBytes + (kK + kV) * kTileBytes + kJoinBytes;
 };
@@ -79,12 +83,14 @@ __device__ __forceinline__ void bar_arrive(uint32_t bar) {
 __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
+// One try suspends the warp for up to a millisecond: a poll is a shared-memory access, and warps that poll at full
+// speed take that bandwidth from the MMA's operands.
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.b32 %0, 1, 0, p;\n\t}"
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.b32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
-      : "r"(bar), "r"(parity)
+      : "r"(bar), "r"(parity), "r"(1000000u)
       : "memory");
   return ok;
 }
@@ -129,16 +135,21 @@ __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+// The two products' steps.  The operand descriptors are taken as their low words (address and leading stride, what
+// changes from step to step) and a constant high word: the issuing thread has 64 clocks per step, and 64-bit arithmetic
+// on whole descriptors took longer than that.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc, uint32_t add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(add)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t hi, uint32_t idesc, uint32_t add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(hi), "r"(idesc), "r"(add)
       : "memory");
 }
 
@@ -191,11 +202,10 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
-// shared-memory operand descriptor, 128-byte swizzle: start address, the two
-// strides in 16-byte units, version 1
-__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead, uint32_t stride) {
-  return (uint64_t)((addr >> 4) & 0x3fff) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(stride >> 4) << 32 | 1ull << 46 | 2ull << 61;
-}
+// shared-memory operand descriptor, 128-byte swizzle: start address and leading stride in 16-byte units (low word);
+// groups of eight rows 1024 bytes apart, version 1 (high word)
+__device__ __forceinline__ uint32_t operand_lo(uint32_t addr, uint32_t lead) { return addr >> 4 | (lead >> 4) << 16; }
+constexpr uint32_t kOperandHi = 1024 >> 4 | 1u << 14 | 2u << 29;
 // bf16 x bf16 -> 32-bit, M = 128; transpose_b: B's N is its contiguous dimension
 __host__ __device__ constexpr uint32_t instruction(int n, bool transpose_b) {
   return 1u << 4 | 1u << 7 | 1u << 10 | (transpose_b ? 1u << 16 : 0) | (uint32_t)(n >> 3) << 17 | (uint32_t)(kTcRows >> 4) << 24;
@@ -213,33 +223,24 @@ struct RowState {
 // rescale(shrink) multiplies the row's O; it is called for whole warps.
 template <int kKeys, int kCopies, typename Rescale>
 __device__ __forceinline__ bool softmax_block(RowState& st, uint32_t s_at, int copy, int edge, float scale_log2, Rescale rescale) {
-  // at most 64 columns are held at a time: of 128, the first 64 are read last for the maximum and stay, the others are
-  // read again (a second TMEM read costs less than the registers)
-  constexpr int kC = kKeys / kCopies, kHeld = kC < 64 ? kC : 64, kGroups = kC / kHeld;
-  constexpr int kPart = kHeld < 32 ? kHeld : 32;  // columns of one TMEM load
-  uint32_t x[kHeld / kPart][kPart];
+  constexpr int kC = kKeys / kCopies, kPart = kC < 32 ? kC : 32;  // columns, and of one TMEM load
+  uint32_t x[kC / kPart][kPart];
+#pragma unroll
+  for (int c = 0; c < kC / kPart; ++c) tmem_load(x[c], s_at + copy * kC + c * kPart);
+  tmem_wait_load();
   edge -= copy * kC;
-  auto load = [&](int g) {
+  if (edge < kC - 1) {
 #pragma unroll
-    for (int c = 0; c < kHeld / kPart; ++c) tmem_load(x[c], s_at + copy * kC + g * kHeld + c * kPart);
-    tmem_wait_load();
-    if (edge < (g + 1) * kHeld - 1) {
+    for (int c = 0; c < kC / kPart; ++c)
 #pragma unroll
-      for (int c = 0; c < kHeld / kPart; ++c)
-#pragma unroll
-        for (int i = 0; i < kPart; ++i)
-          if (g * kHeld + c * kPart + i > edge) x[c][i] = 0xff800000u;
-    }
-  };
+      for (int i = 0; i < kPart; ++i)
+        if (c * kPart + i > edge) x[c][i] = 0xff800000u;
+  }
   float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-  for (int g = kGroups - 1; g >= 0; --g) {
-    load(g);
+  for (int c = 0; c < kC / kPart; ++c)
 #pragma unroll
-    for (int c = 0; c < kHeld / kPart; ++c)
-#pragma unroll
-      for (int i = 0; i < kPart; ++i) m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(x[c][i]));
-  }
+    for (int i = 0; i < kPart; ++i) m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(x[c][i]));
   const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * scale_log2;
   const bool raise = mx > st.top + 8.f;  // also the first time: top is -inf
   if (__any_sync(kFull, raise)) {
@@ -250,24 +251,20 @@ __device__ __forceinline__ bool softmax_block(RowState& st, uint32_t s_at, int c
   }
   const float sub = st.top == -INFINITY ? 0.f : st.top;
   float s4[4] = {0.f, 0.f, 0.f, 0.f};
-  constexpr int kW = kHeld / 2 < 16 ? kHeld / 2 : 16;  // words of one TMEM store
+  constexpr int kW = kC / 2 < 16 ? kC / 2 : 16;  // words of one TMEM store
 #pragma unroll
-  for (int g = 0; g < kGroups; ++g) {
-    if (g > 0) load(g);
+  for (int c = 0; c < kC / 2; c += kW) {
+    uint32_t pk[kW];
 #pragma unroll
-    for (int c = 0; c < kHeld / 2; c += kW) {
-      uint32_t pk[kW];
-#pragma unroll
-      for (int i = 0; i < kW; ++i) {
-        const int j = 2 * (c + i);
-        const float e0 = ex2(fmaf(__uint_as_float(x[j / kPart][j % kPart]), scale_log2, -sub));
-        const float e1 = ex2(fmaf(__uint_as_float(x[j / kPart][j % kPart + 1]), scale_log2, -sub));
-        s4[j & 3] += e0;
-        s4[(j + 1) & 3] += e1;
-        pk[i] = pack_bf16(e0, e1);
-      }
-      tmem_store(s_at + (copy * kC + g * kHeld) / 2 + c, pk);  // over columns that were read
+    for (int i = 0; i < kW; ++i) {
+      const int j = 2 * (c + i);
+      const float e0 = ex2(fmaf(__uint_as_float(x[j / kPart][j % kPart]), scale_log2, -sub));
+      const float e1 = ex2(fmaf(__uint_as_float(x[j / kPart][j % kPart + 1]), scale_log2, -sub));
+      s4[j & 3] += e0;
+      s4[(j + 1) & 3] += e1;
+      pk[i] = pack_bf16(e0, e1);
     }
+    tmem_store(s_at + copy * (kC / 2) + c, pk);  // over columns that were read
   }
   if constexpr (kCopies > 1) {
     // the other copies' keys: weight 0.  (S of those columns belongs to this warp's lanes alone: no one waits for it.)
@@ -295,12 +292,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const Params& p = t.p;
   const uint32_t q_flip = t.q_flip;
   extern __shared__ uint8_t raw[];
-  __shared__ __align__(8) uint64_t bars[2 * S::kK + 2 * S::kV + 15];
+  __shared__ __align__(8) uint64_t bars[2 * S::kK + 2 * S::kV + 17];
   __shared__ long long scan[kTcThreads / 32];
   __shared__ Start start;
   __shared__ uint32_t tmem_base;
   __shared__ int gave_up;
-  __shared__ float2 stats[2][128];  // maxima and sums of a tile's rows (and copies)
+  __shared__ float2 stats[2][2][128];  // maxima and sums of a tile's rows (and copies), by tile and stream
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
   const uint32_t q_s = base, k_s = q_s + S::kQBytes, v_s = k_s + S::kK * S::kTileBytes, join_s = v_s + S::kV * S::kTileBytes;
@@ -313,12 +310,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   auto v_empty = [&](int i) { return b0 + 8 * (2 * S::kK + S::kV + i); };
   constexpr int kRest = 2 * S::kK + 2 * S::kV;
   auto s_full = [&](int i) { return b0 + 8 * (kRest + (i & 1)); };       // S of block i is in TMEM
-  auto p_ready = [&](int i) { return b0 + 8 * (kRest + 2 + (i & 1)); };  // its P is
-  auto pv_done = [&](int i) { return b0 + 8 * (kRest + 4 + (i & 1)); };  // O holds its products
-  auto st_ready = [&](int g) { return b0 + 8 * (kRest + 6 + (g & 1)); };  // tile g's maxima and sums are in `stats`
-  auto o_full = [&](int g) { return b0 + 8 * (kRest + 8 + (g & 1)); };    // tile g's O is whole
-  auto o_free = [&](int g) { return b0 + 8 * (kRest + 10 + (g & 1)); };   // and has been written out
-  const uint32_t q_full = b0 + 8 * (kRest + 12), q_empty = b0 + 8 * (kRest + 13), drained = b0 + 8 * (kRest + 14);
+  auto p_ready = [&](int i, int x) { return b0 + 8 * (kRest + 2 + (i & 1) * 2 + x); };  // stream x's P of it is
+  auto pv_done = [&](int i) { return b0 + 8 * (kRest + 6 + (i & 1)); };   // O holds its products
+  auto st_ready = [&](int g) { return b0 + 8 * (kRest + 8 + (g & 1)); };  // tile g's maxima and sums are in `stats`
+  auto o_full = [&](int g) { return b0 + 8 * (kRest + 10 + (g & 1)); };   // tile g's O is whole
+  auto o_free = [&](int g) { return b0 + 8 * (kRest + 12 + (g & 1)); };   // and has been written out
+  const uint32_t q_full = b0 + 8 * (kRest + 14), q_empty = b0 + 8 * (kRest + 15), drained = b0 + 8 * (kRest + 16);
   if (tid == 0) {
     gave_up = 0;
     for (int i = 0; i < S::kK; ++i) {
@@ -331,22 +328,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(s_full(i), 1);
-      bar_init(p_ready(i), 128);
+      bar_init(p_ready(i, 0), 128);
+      bar_init(p_ready(i, 1), 128);
       bar_init(pv_done(i), 1);
-      bar_init(st_ready(i), 128);
+      bar_init(st_ready(i), 128 * S::kStreams);
       bar_init(o_full(i), 1);
       bar_init(o_free(i), 128);
     }
     bar_init(q_full, 128);
     bar_init(q_empty, 1);
-    bar_init(drained, 1);
+    bar_init(drained, 2);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 4) {
+  if (warp == 12) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&tmem_base)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  if (warp == 5 && lane == 0) {
+  if (warp == 13 && lane == 0) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(&k_map) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(&v_map) : "memory");
   }
@@ -359,7 +357,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   find_start<kTcRows, kKeys, kTcThreads>(p, kTcMinUnits, scan, &start);
   const Start s = start;
   constexpr uint32_t kOCol = 2 * kKeys;  // TMEM columns: two S buffers, then O
-  auto o_col = [&](int g) { return kOCol + (S::kOs == 2 ? (g & 1) * kD : 0); };
+  constexpr int kCols = kKeys / S::kStreams;  // a stream's keys of a block
   Walk<kTcRows, kKeys> w;
   const bool any = begin(w, p, s);
   bool ok = true;
@@ -368,14 +366,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     return (int)min((long long)kTcRows, (long long)t.req.n * p.G - (long long)t.m * kTcRows);
   };
 
-  if (warp >= 8) {
+  if (warp >= 8 && warp < 12) {
     // ---- Q into the swizzled layout, and the tiles out of TMEM
     int4 note = {0, 0, 0, 0};
     if (any) {
       const int e_tid = tid - 256, quarter = warp - 8;
       const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
       constexpr int kUnits = kD / 8;  // 16-byte units of a row
-      constexpr int kBatch = 8;       // units a thread holds: 32 rows of 256 columns at once
+      constexpr int kBatch = 16;      // units a thread holds: 128 rows of 128 columns at once
       auto stage_q = [&](const Walk<kTcRows, kKeys>& t, int g) {
         const int rows = rows_of(t), copies = copies_of(rows);
         for (int i0 = 0; i0 < rows * kUnits; i0 += kBatch * 128) {
@@ -425,55 +423,69 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         ok = warp_wait(st_ready(g), (g >> 1) & 1, &gave_up) && warp_wait(o_full(g), (g >> 1) & 1, &gave_up);
         if (!ok) break;
         tc_fence_after();
-        const float2* const st = stats[g & 1];
-        const uint32_t o_at = lanes + o_col(g);
+        // the second stream has no O where the tile's only block ends before its keys
+        const int n_parts = S::kStreams == 1 || (w.kb1 - w.kb0 == 1 && w.req.ctx + w.req.n - w.kb0 * kKeys <= kCols) ? 1 : 2;
+        auto st = [&](int part, int lane_row) { return stats[g & 1][part][lane_row]; };
+        float shares[2];  // 2^(own maximum - common maximum) of this lane's O's
+        // 32 columns of this lane's row, the streams added up
+        auto columns = [&](float (&v)[32], int c) {
+          uint32_t o[32];
+          tmem_load(o, lanes + kOCol + c * 32);
+          tmem_wait_load();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(o[i]) * shares[0];
+          if (n_parts == 2) {
+            tmem_load(o, lanes + kOCol + kD + c * 32);
+            tmem_wait_load();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = fmaf(__uint_as_float(o[i]), shares[1], v[i]);
+          }
+        };
+        const int span = 128 / copies;
+        float top = -INFINITY, sum = 0.f;
+        for (int c = 0; c < copies; ++c)
+          for (int j = 0; j < n_parts; ++j) top = fmaxf(top, st(j, c * span + row).x);
+        const float sub = top == -INFINITY ? 0.f : top;
+        for (int c = 0; c < copies; ++c)
+          for (int j = 0; j < n_parts; ++j) sum += st(j, c * span + row).y * ex2(st(j, c * span + row).x - sub);
+        const float norm = whole ? 1.f / sum : 1.f;
+        shares[0] = ex2(st(0, e_tid).x - sub) * norm;
+        shares[1] = n_parts == 2 ? ex2(st(1, e_tid).x - sub) * norm : 0.f;
         if (copies == 1) {
-          const float2 mine = st[e_tid];
           if (quarter * 32 < rows) {
-            const float inv = 1.f / mine.y;
 #pragma unroll 1
             for (int c = 0; c < kD / 32; ++c) {
-              uint32_t o[32];
-              tmem_load(o, o_at + c * 32);
-              tmem_wait_load();
+              float v[32];
+              columns(v, c);
               if (row < rows) {
                 if (whole) {
                   uint32_t pk[16];
 #pragma unroll
-                  for (int i = 0; i < 16; ++i) pk[i] = pack_bf16(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
+                  for (int i = 0; i < 16; ++i) pk[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
 #pragma unroll
                   for (int i = 0; i < 4; ++i)
                     reinterpret_cast<uint4*>(dst + c * 32)[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
                 } else {
 #pragma unroll
                   for (int i = 0; i < 8; ++i)
-                    reinterpret_cast<uint4*>(out + row * kD + c * 32)[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                    reinterpret_cast<float4*>(out + row * kD + c * 32)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
                 }
               }
             }
-            if (!whole && row < rows) reinterpret_cast<float2*>(out + kTcRows * kD)[row] = mine;
           }
         } else {
           // Join the copies, 32 columns at a time: each warp brings its rows scaled to the common maximum, then sums its
           // share of their 16-byte units over the copies.
-          const int span = 128 / copies;
-          float top = -INFINITY, sum = 0.f;
-          for (int c = 0; c < copies; ++c) top = fmaxf(top, st[c * span + row].x);
-          const float sub = top == -INFINITY ? 0.f : top;
-          for (int c = 0; c < copies; ++c) sum += st[c * span + row].y * ex2(st[c * span + row].x - sub);
-          const float scale = ex2(st[e_tid].x - sub) * (whole ? 1.f / sum : 1.f);
 #pragma unroll 1
           for (int c = 0; c < kD / 32; ++c) {
-            uint32_t o[32];
-            tmem_load(o, o_at + c * 32);
-            tmem_wait_load();
+            float v[32];
+            columns(v, c);
             if (c > 0) asm volatile("bar.sync 1, 128;" ::: "memory");  // the last columns have been read
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const uint32_t to = join_s + e_tid * 128 + ((i ^ (lane & 7)) << 4);
-              asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(__uint_as_float(o[4 * i]) * scale),
-                           "f"(__uint_as_float(o[4 * i + 1]) * scale), "f"(__uint_as_float(o[4 * i + 2]) * scale),
-                           "f"(__uint_as_float(o[4 * i + 3]) * scale)
+              asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(v[4 * i]), "f"(v[4 * i + 1]), "f"(v[4 * i + 2]),
+                           "f"(v[4 * i + 3])
                            : "memory");
             }
             asm volatile("bar.sync 1, 128;" ::: "memory");
@@ -481,15 +493,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               for (int i = copy * (8 / copies); i < (copy + 1) * (8 / copies); ++i) {
                 float4 a = {0.f, 0.f, 0.f, 0.f};
                 for (int j = 0; j < copies; ++j) {
-                  float4 v;
+                  float4 x;
                   asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                               : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
                                : "r"(join_s + (j * span + row) * 128 + ((i ^ (lane & 7)) << 4))
                                : "memory");
-                  a.x += v.x;
-                  a.y += v.y;
-                  a.z += v.z;
-                  a.w += v.w;
+                  a.x += x.x;
+                  a.y += x.y;
+                  a.z += x.z;
+                  a.w += x.w;
                 }
                 const int col = c * 32 + i * 4;
                 if (whole) *reinterpret_cast<uint2*>(dst + col) = make_uint2(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w));
@@ -497,124 +509,155 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               }
             }
           }
-          if (!whole && row < rows && copy == 0) reinterpret_cast<float2*>(out + kTcRows * kD)[row] = make_float2(top, sum);
           asm volatile("bar.sync 1, 128;" ::: "memory");  // the last columns have been read
         }
+        if (!whole && row < rows && copy == 0) reinterpret_cast<float2*>(out + kTcRows * kD)[row] = make_float2(top, sum);
         tc_fence_before();
         bar_arrive(o_free(g));
         w = next;
       }
     }
     if (tid == 256) p.notes[blockIdx.x] = note;
-  } else if (any && warp < 4) {
-    // ---- softmax: one thread per row (and copy)
-    const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
+  } else if (any && warp < 4 * S::kStreams) {
+    // ---- softmax: one thread per row (and copy) of the stream's keys
+    const int stream = warp >> 2, quarter = warp & 3, s_tid = tid & 127;
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
     int it = 0, g = 0;
-    auto products = [&](int i) { return warp_wait(pv_done(i), (i >> 1) & 1, &gave_up); };
     for (; ok && !w.done(); w.next(), ++g) {
       const int rows = rows_of(w), copies = copies_of(rows), spread = 4 / copies;  // warps of one copy
-      const int copy = warp / spread, row = (warp % spread) * 32 + lane;
-      const bool active = (warp % spread) * 32 < rows;  // a warp with no row only keeps step
+      const int copy = quarter / spread, row = (quarter % spread) * 32 + lane;
+      const bool active = (quarter % spread) * 32 < rows;  // a warp with no row only keeps step
       const int last = row < rows ? w.req.ctx + (int)quotient(w.m * kTcRows + row, p.by_G) : -1;
       RowState st = {-INFINITY, 0.f};
       for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
         if (!(ok = warp_wait(s_full(it), (it >> 1) & 1, &gave_up))) break;
-        if (it >= 2 && !(ok = products(it - 2))) break;  // each block's, in turn
+        if (it >= 2 && !(ok = warp_wait(pv_done(it), ((it >> 1) - 1) & 1, &gave_up))) break;  // block it - 2's, each in turn
         if (active) {
           tc_fence_after();
           auto rescale = [&](float shrink) {
             if (kb == w.kb0) return true;
-            if (!products(it - 1)) return false;
+            if (!warp_wait(pv_done(it - 1), ((it - 1) >> 1) & 1, &gave_up)) return false;
             tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < kD / 32; ++c) {
               uint32_t o[32];
-              tmem_load(o, lanes + o_col(g) + c * 32);
+              tmem_load(o, lanes + kOCol + stream * kD + c * 32);
               tmem_wait_load();
 #pragma unroll
               for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * shrink);
-              tmem_store(lanes + o_col(g) + c * 32, o);
+              tmem_store(lanes + kOCol + stream * kD + c * 32, o);
             }
             tmem_wait_store();
             return true;
           };
-          const int edge = last - kb * kKeys;
-          const uint32_t s_at = lanes + (it & 1) * kKeys;
-          if (copies == 1) ok = softmax_block<kKeys, 1>(st, s_at, 0, edge, p.scale_log2, rescale);
-          else if (copies == 2) ok = softmax_block<kKeys, 2>(st, s_at, copy, edge, p.scale_log2, rescale);
-          else ok = softmax_block<kKeys, 4>(st, s_at, copy, edge, p.scale_log2, rescale);
+          const int edge = last - kb * kKeys - stream * kCols;
+          const uint32_t s_at = lanes + (it & 1) * kKeys + stream * kCols;
+          if (copies == 1) ok = softmax_block<kCols, 1>(st, s_at, 0, edge, p.scale_log2, rescale);
+          else if (copies == 2) ok = softmax_block<kCols, 2>(st, s_at, copy, edge, p.scale_log2, rescale);
+          else ok = softmax_block<kCols, 4>(st, s_at, copy, edge, p.scale_log2, rescale);
           if (!ok) break;
           tc_fence_before();
         }
         const int valid = w.req.ctx + w.req.n - kb * kKeys;
-        if (valid < kKeys && valid % 16 != 0) {
+        if (valid < kKeys && valid % 16 != 0 && valid / kCols == stream) {
           // The V rows between the request's last token and the last 16 that the MMA reads: their weight is 0, but 0
           // times what a page holds there may be NaN.
           const int vs = it % S::kV;
           if (!(ok = warp_wait(v_full(vs), (it / S::kV) & 1, &gave_up))) break;
-          for (int i = tid; i < (16 - valid % 16) * (kD / 8); i += 128) {
+          for (int i = s_tid; i < (16 - valid % 16) * (kD / 8); i += 128) {
             const int r = valid + i / (kD / 8), u = i % (kD / 8);
             const uint32_t to = v_s + vs * S::kTileBytes + (u / 8) * (kKeys * 128) + r * 128 + ((u & 7) << 4);
             asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(to), "r"(0) : "memory");
           }
           fence_async();
         }
-        bar_arrive(p_ready(it));
+        bar_arrive(p_ready(it, stream));
       }
       if (ok && g >= 2) ok = warp_wait(o_free(g), ((g >> 1) - 1) & 1, &gave_up);  // tile g - 2 is done with its place in stats
       if (!ok) break;
-      stats[g & 1][tid] = make_float2(st.top, st.sum);
+      stats[g & 1][stream][s_tid] = make_float2(st.top, st.sum);
       bar_arrive(st_ready(g));
     }
-  } else if (any && warp == 4) {
-    // ---- the MMAs, issued by one thread
+  } else if (any && warp == 12) {
+    // ---- S = Q K^T, issued by one thread
     if (lane == 0) {
-      constexpr uint32_t kQk = instruction(kKeys, false), kPv = instruction(kD, true);
-      int it = 0, g = 0;
-      for (; ok && !w.done(); w.next(), ++g) {
-        if (!(ok = bar_wait(q_full, g & 1, &gave_up))) break;
-        const int len = w.req.ctx + w.req.n;
-        for (int kb = w.kb0; kb <= w.kb1; ++kb) {
-          if (kb < w.kb1) {
-            const int i = it + kb - w.kb0, st = i % S::kK;
-            if (!(ok = bar_wait(k_full(st), (i / S::kK) & 1, &gave_up))) break;
-            tc_fence_after();
+      constexpr uint32_t kQk = instruction(kKeys, false);
+      const uint32_t q_lo = operand_lo(q_s, 16), k_lo0 = operand_lo(k_s, 16);
+      uint32_t stage = 0, k_phase = 0, buf = 0, s_phase = 1, q_phase = 0;  // s_phase: of pv_done; the first round finds S free
+      for (; ok && !w.done(); w.next()) {
+        if (!(ok = bar_wait(q_full, q_phase, &gave_up))) break;
+        q_phase ^= 1;
+        for (int kb = w.kb0; kb < w.kb1; ++kb) {
+          // the products of the buffer's last P are done
+          ok = bar_wait(k_full(0) + 8 * stage, k_phase, &gave_up) && bar_wait(pv_done(0) + 8 * buf, s_phase, &gave_up);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t k_lo = k_lo0 + stage * (S::kTileBytes / 16), s_at = tmem + buf * kKeys;
 #pragma unroll
-            for (int k = 0; k < kD / 16; ++k) {
-              const uint32_t q_at = q_s + (k / 4) * (kTcRows * 128) + (k % 4) * 32;
-              const uint32_t k_at = k_s + st * S::kTileBytes + (k / 4) * (kKeys * 128) + (k % 4) * 32;
-              mma_ss(tmem + (i & 1) * kKeys, operand(q_at, 16, 1024), operand(k_at, 16, 1024), kQk, k > 0);
-            }
-            tc_commit(k_empty(st));
-            tc_commit(s_full(i));
-            if (kb == w.kb1 - 1) tc_commit(q_empty);
-          }
-          if (kb > w.kb0) {
-            const int i = it + kb - 1 - w.kb0, st = i % S::kV;
-            const bool first = kb - 1 == w.kb0;
-            ok = bar_wait(p_ready(i), (i >> 1) & 1, &gave_up) && bar_wait(v_full(st), (i / S::kV) & 1, &gave_up);
-            // the buffer's last tile has been written out
-            if (ok && first && g >= S::kOs) ok = bar_wait(o_free(g - S::kOs), ((g - S::kOs) >> 1) & 1, &gave_up);
-            if (!ok) break;
-            tc_fence_after();
-            const int steps = min(kKeys / 16, (len - (kb - 1) * kKeys + 15) / 16);  // no V row behind the last 16 with a token
-#pragma unroll
-            for (int k = 0; k < kKeys / 16; ++k)
-              if (k < steps)
-                mma_ts(tmem + o_col(g), tmem + (i & 1) * kKeys + k * 8, operand(v_s + st * S::kTileBytes + k * 2048, kKeys * 128, 1024),
-                       kPv, !(first && k == 0));
-            tc_commit(v_empty(st));
-            tc_commit(pv_done(i));
-            if (kb == w.kb1) tc_commit(o_full(g));
+          for (int k = 0; k < kD / 16; ++k)
+            mma_ss(s_at, q_lo + (k / 4) * (kTcRows * 8) + (k % 4) * 2, k_lo + (k / 4) * (kKeys * 8) + (k % 4) * 2, kOperandHi, kQk, k > 0);
+          tc_commit(s_full(0) + 8 * buf);
+          tc_commit(k_empty(0) + 8 * stage);
+          if (kb == w.kb1 - 1) tc_commit(q_empty);
+          s_phase ^= buf;
+          buf ^= 1;
+          if (++stage == S::kK) {
+            stage = 0;
+            k_phase ^= 1;
           }
         }
-        it += w.kb1 - w.kb0;
       }
     }
     __syncwarp();
-  } else if (any && warp < 7) {
-    // ---- K (warp 5) and V (warp 6) tiles by TMA: lane (box, chunk) copies its box of 64 columns
-    const bool is_v = warp == 6;
+  } else if (any && warp == 15) {
+    // ---- O += P V, issued by one thread
+    if (lane == 0) {
+      constexpr uint32_t kPv = instruction(kD, true);
+      const uint32_t v_lo0 = operand_lo(v_s, kKeys * 128);
+      uint32_t stage = 0, v_phase = 0, buf = 0, p_phase = 0, o_phase = 0;  // o_phase: of o_free's two barriers in turn
+      int g = 0;
+      for (; ok && !w.done(); w.next(), ++g) {
+        const int len = w.req.ctx + w.req.n;
+        for (int kb = w.kb0; kb < w.kb1; ++kb) {
+          const uint32_t fresh = kb > w.kb0;  // 0: the tile's first block overwrites O
+          const int valid = len - kb * kKeys;
+          const uint32_t v_lo = v_lo0 + stage * (S::kTileBytes / 16), p_at = tmem + buf * kKeys;
+          ok = bar_wait(v_full(0) + 8 * stage, v_phase, &gave_up);
+          if (!fresh && g > 0) {  // the last tile has been written out
+            ok = ok && bar_wait(o_free(g - 1), o_phase >> 1, &gave_up);
+            o_phase = (o_phase + 1) & 3;
+          }
+#pragma unroll
+          for (int x = 0; x < S::kStreams; ++x) {
+            ok = ok && bar_wait(p_ready(0, x) + 16 * buf, p_phase, &gave_up);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t o_at = tmem + kOCol + x * kD, px_at = p_at + x * kCols, v_at = v_lo + x * (kCols * 8);
+            if (valid >= (x + 1) * kCols) {
+#pragma unroll
+              for (int k = 0; k < kCols / 16; ++k) mma_ts(o_at, px_at + k * 8, v_at + k * 128, kOperandHi, kPv, k > 0 ? 1u : fresh);
+            } else {
+              const int steps = (valid - x * kCols + 15) >> 4;  // no V row behind the last 16 with a token
+              for (int k = 0; k < steps; ++k) mma_ts(o_at, px_at + k * 8, v_at + k * 128, kOperandHi, kPv, k > 0 ? 1u : fresh);
+            }
+          }
+          if (!ok) break;
+          tc_commit(pv_done(0) + 8 * buf);
+          tc_commit(v_empty(0) + 8 * stage);
+          if (kb == w.kb1 - 1) tc_commit(o_full(g));
+          p_phase ^= buf;
+          buf ^= 1;
+          if (++stage == S::kV) {
+            stage = 0;
+            v_phase ^= 1;
+          }
+        }
+      }
+    }
+    __syncwarp();
+  } else if (any && (warp == 13 || warp == 14)) {
+    // ---- K (warp 13) and V (warp 14) tiles by TMA: lane (box, chunk) copies its box of 64 columns
+    const bool is_v = warp == 14;
     const int stages = is_v ? S::kV : S::kK;
     const uint32_t tiles = is_v ? v_s : k_s, full = is_v ? v_full(0) : k_full(0), empty = is_v ? v_empty(0) : k_empty(0);
     const CUtensorMap* const map = is_v ? &v_map : &k_map;
@@ -661,21 +704,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (gave_up) {
     // products and copies that may still be in flight, with a bound again
     const unsigned long long end = now_ns() + kWaitNs;
-    if (tid == 128) {
+    if (tid == 12 * 32 || tid == 15 * 32) {
       tc_commit(drained);
       while (!bar_try(drained, 0) && now_ns() < end) {
       }
     }
-    if (lane == 0 && (warp == 5 || warp == 6)) {
-      const int stages = warp == 5 ? S::kK : S::kV;
+    if (lane == 0 && (warp == 13 || warp == 14)) {
+      const int stages = warp == 13 ? S::kK : S::kV;
       for (int i = max(0, sent - stages); i < sent; ++i)
-        while (!bar_try((warp == 5 ? k_full(0) : v_full(0)) + 8 * (i % stages), (i / stages) & 1) && now_ns() < end) {
+        while (!bar_try((warp == 13 ? k_full(0) : v_full(0)) + 8 * (i % stages), (i / stages) & 1) && now_ns() < end) {
         }
     }
     if (tid == 0 && p.status) atomicOr(p.status, GDN_STATUS_TIMEOUT);
     __syncthreads();
   }
-  if (warp == 4) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  if (warp == 12) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,

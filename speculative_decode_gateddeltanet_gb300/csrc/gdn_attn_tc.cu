@@ -388,18 +388,25 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           // the rows are on their way while the last tile's products with Q end
           if (i0 == 0 && g > 0 && !bar_wait(q_empty, (g - 1) & 1, &gave_up)) return false;
+          auto store = [&](auto copies_c) {
+            constexpr int kC = decltype(copies_c)::value;
 #pragma unroll
-          for (int j = 0; j < kBatch; ++j) {
-            const int i = i0 + j * 128 + e_tid;
-            if (i < rows * kUnits) {
-              const int r = i / kUnits, u = i % kUnits;
-              const uint4 y = make_uint4(x[j].x ^ q_flip, x[j].y ^ q_flip, x[j].z ^ q_flip, x[j].w ^ q_flip);
-              for (int c = 0; c < copies; ++c) {
-                const uint32_t dst = q_s + (u / 8) * (kTcRows * 128) + (r + c * (kTcRows / copies)) * 128 + (((u & 7) ^ (r & 7)) << 4);
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w) : "memory");
+            for (int j = 0; j < kBatch; ++j) {
+              const int i = i0 + j * 128 + e_tid;
+              if (i < rows * kUnits) {
+                const int r = i / kUnits, u = i % kUnits;
+                const uint32_t to = q_s + (u / 8) * (kTcRows * 128) + r * 128 + (((u & 7) ^ (r & 7)) << 4);
+#pragma unroll
+                for (int c = 0; c < kC; ++c)
+                  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + c * (kTcRows / kC) * 128), "r"(x[j].x ^ q_flip),
+                               "r"(x[j].y ^ q_flip), "r"(x[j].z ^ q_flip), "r"(x[j].w ^ q_flip)
+                               : "memory");
               }
             }
-          }
+          };
+          if (copies == 1) store(std::integral_constant<int, 1>());
+          else if (copies == 2) store(std::integral_constant<int, 2>());
+          else store(std::integral_constant<int, 4>());
         }
         fence_async();
         bar_arrive(q_full);
@@ -474,46 +481,68 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
           }
         } else {
-          // Join the copies, 32 columns at a time: each warp brings its rows scaled to the common maximum, then sums its
-          // share of their 16-byte units over the copies.
+          // Join the copies, 32 columns at a time: each warp brings its rows scaled to the common maximum, then the 128
+          // threads sum the rows' 16-byte units over the copies, eight neighbours a row.
+          auto join = [&](auto copies_c) {
+            constexpr int kC = decltype(copies_c)::value, kSpan = 128 / kC;
+            const int unit = e_tid & 7;
+            const int64_t out_base = (int64_t)w.req.row0 * p.o_row + (int64_t)w.h * p.G * p.o_head;
 #pragma unroll 1
-          for (int c = 0; c < kD / 32; ++c) {
-            float v[32];
-            columns(v, c);
-            if (c > 0) asm volatile("bar.sync 1, 128;" ::: "memory");  // the last columns have been read
+            for (int c = 0; c < kD / 32; ++c) {
+              float v[32];
+              columns(v, c);
+              if (c == kD / 32 - 1) {  // O has been read: the next tile may have it
+                tc_fence_before();
+                bar_arrive(o_free(g));
+              }
+              if (c > 0) asm volatile("bar.sync 1, 128;" ::: "memory");  // the last columns have been read
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const uint32_t to = join_s + e_tid * 128 + ((i ^ (lane & 7)) << 4);
-              asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(v[4 * i]), "f"(v[4 * i + 1]), "f"(v[4 * i + 2]),
-                           "f"(v[4 * i + 3])
-                           : "memory");
-            }
-            asm volatile("bar.sync 1, 128;" ::: "memory");
-            if (row < rows) {
-              for (int i = copy * (8 / copies); i < (copy + 1) * (8 / copies); ++i) {
-                float4 a = {0.f, 0.f, 0.f, 0.f};
-                for (int j = 0; j < copies; ++j) {
-                  float4 x;
-                  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                               : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
-                               : "r"(join_s + (j * span + row) * 128 + ((i ^ (lane & 7)) << 4))
-                               : "memory");
-                  a.x += x.x;
-                  a.y += x.y;
-                  a.z += x.z;
-                  a.w += x.w;
+              for (int i = 0; i < 8; ++i) {
+                const uint32_t to = join_s + e_tid * 128 + ((i ^ (lane & 7)) << 4);
+                asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(v[4 * i]), "f"(v[4 * i + 1]), "f"(v[4 * i + 2]),
+                             "f"(v[4 * i + 3])
+                             : "memory");
+              }
+              asm volatile("bar.sync 1, 128;" ::: "memory");
+#pragma unroll
+              for (int r0 = 0; r0 < kSpan; r0 += 16) {
+                const int r = r0 + (e_tid >> 3);
+                if (r < rows) {
+                  float4 a = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                  for (int j = 0; j < kC; ++j) {
+                    float4 x;
+                    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                 : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+                                 : "r"(join_s + (j * kSpan + r) * 128 + ((unit ^ (r & 7)) << 4))
+                                 : "memory");
+                    a.x += x.x;
+                    a.y += x.y;
+                    a.z += x.z;
+                    a.w += x.w;
+                  }
+                  const int col = c * 32 + unit * 4;
+                  if (whole) {
+                    const int row_at = w.m * kTcRows + r, tok = (int)quotient(row_at, p.by_G);
+                    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + out_base + (int64_t)tok * p.o_row +
+                                              (int64_t)(row_at - tok * p.G) * p.o_head + col) =
+                        make_uint2(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w));
+                  } else {
+                    *reinterpret_cast<float4*>(out + r * kD + col) = a;
+                  }
                 }
-                const int col = c * 32 + i * 4;
-                if (whole) *reinterpret_cast<uint2*>(dst + col) = make_uint2(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w));
-                else *reinterpret_cast<float4*>(out + row * kD + col) = a;
               }
             }
-          }
-          asm volatile("bar.sync 1, 128;" ::: "memory");  // the last columns have been read
+            asm volatile("bar.sync 1, 128;" ::: "memory");  // the last columns have been read
+          };
+          if (copies == 4) join(std::integral_constant<int, 4>());
+          else join(std::integral_constant<int, 2>());
         }
         if (!whole && row < rows && copy == 0) reinterpret_cast<float2*>(out + kTcRows * kD)[row] = make_float2(top, sum);
-        tc_fence_before();
-        bar_arrive(o_free(g));
+        if (copies == 1) {
+          tc_fence_before();
+          bar_arrive(o_free(g));
+        }
         w = next;
       }
     }

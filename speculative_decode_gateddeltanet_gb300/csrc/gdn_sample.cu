@@ -13,8 +13,7 @@
 //   and keeps the maximum of each thread's elements.
 //   - top_k up to kList / 2: the k-th largest thread maximum is a bound that at
 //     least k tokens reach, and few more do.  Those are appended to one list
-//     in the first block, which sorts it and finishes alone: no other pass over
-//     the row.
+//     in the first block, which finishes alone: no other pass over the row.
 //   - otherwise (or if equal logits overflow the list): a histogram of weight
 //     sums (top-p) or counts (a large top_k) over kBins equal steps of the
 //     logit below the maximum finds the step that holds the prefix' end, and
@@ -38,7 +37,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kBins = 1024;
-constexpr int kList = 2048;  // candidates that the first block can sort
+constexpr int kList = 1024;  // candidates that the first block can hold
 constexpr int kMaxSlice = 49152;  // elements a block stages: 192 KB in 32 bits; sums of 16-bit halves fit 32 bits
 static_assert(kMaxSlice * kMaxCluster == GDN_SAMPLE_MAX_V, "a row is staged by one cluster");
 
@@ -61,7 +60,7 @@ __device__ __forceinline__ float of_key(uint32_t k) {
 struct Weight {
   float top, inv_t;
   __device__ float w(float x) const { return x == top ? 1.f : expf((x - top) * inv_t); }
-  __device__ uint32_t whole(float x) const { return (uint32_t)__float2ll_rn(w(x) * 2147483648.f); }
+  __device__ uint32_t whole(float x) const { return __float2uint_rn(w(x) * 2147483648.f); }
 };
 
 __device__ __forceinline__ u64 shift_mul(u64 total, u64 frac) {
@@ -117,8 +116,50 @@ __device__ __forceinline__ void min_at(uint32_t at, uint32_t v) {
   asm volatile("red.shared::cluster.min.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
 }
 
-__device__ __forceinline__ float number(float x) { return x; }
-__device__ __forceinline__ float number(__nv_bfloat16 x) { return __bfloat162float(x); }
+// the whole block's sum, with a barrier before and after
+__device__ __forceinline__ u64 block_sum(u64 v, u64* part) {
+  v = warp_sum(v);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+  __syncthreads();
+  u64 s = 0;
+  for (int w = 0; w < kWarps; ++w) s += part[w];
+  return s;
+}
+
+// kN equal steps of the distance from the largest logit, a monotonous map whatever the range: adding 2^23 rounds to a
+// whole number without a conversion (those, like exp, run at a quarter of the rate of additions).  A distance of NaN
+// (both infinite) is 0, and so is every distance where the range is infinite.
+template <int kN>
+struct Steps {
+  float scale;
+  __device__ explicit Steps(float range) : scale(fminf(kN / range, 3e38f)) {}
+  __device__ int of(float distance) const {
+    const float s = fminf(fmaxf(distance * scale, 0.f), (float)(kN - 1));
+    return (int)(__float_as_uint(s + 8388608.f) & (2 * kN - 1));
+  }
+};
+
+struct Ends {
+  uint32_t most, least;
+  int count;
+};
+// the block's largest and smallest word and its count's sum
+__device__ __forceinline__ Ends block_ends(uint32_t most, uint32_t least, int count, u64* part) {
+  const uint32_t m = __reduce_max_sync(kFull, most), l = __reduce_min_sync(kFull, least);
+  const int c = __reduce_add_sync(kFull, count);
+  Ends* const words = reinterpret_cast<Ends*>(part);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) words[threadIdx.x >> 5] = {m, l, c};
+  __syncthreads();
+  Ends e = {0, 0xffffffffu, 0};
+  for (int w = 0; w < kWarps; ++w) {
+    e.most = max(e.most, words[w].most);
+    e.least = min(e.least, words[w].least);
+    e.count += words[w].count;
+  }
+  return e;
+}
 
 // inclusive prefix over the block's threads
 __device__ __forceinline__ u64 block_scan(u64 v, u64* part) {
@@ -153,95 +194,120 @@ struct Unit {  // the elements of 16 bytes
   }
 };
 
-// descending order of n = a power of two of 64-bit words in shared memory
-__device__ void sort_descending(u64* v, int n) {
-  for (int k = 2; k <= n; k <<= 1)
-    for (int j = k >> 1; j > 0; j >>= 1) {
-      for (int i = threadIdx.x; i < n / 2; i += kThreads) {
-        const int a = 2 * i - (i & (j - 1)), b = a + j;
-        const u64 x = v[a], y = v[b];
-        if ((x < y) == ((a & k) == 0)) {
-          v[a] = y;
-          v[b] = x;
-        }
-      }
-      __syncthreads();
-    }
-}
-
-__device__ __forceinline__ int pow2_at_least(int n) { return n <= 1 ? 1 : 1 << (32 - __clz(n - 1)); }
-
 struct News {  // what the first block tells the others
   u64 left;
   uint32_t top_key, bound, low, digit;  // low: the smallest thread maximum
 };
 
-// the rest of a row whose candidates lie in `list`: the first c of its m in order are the top-k tokens
-template <typename T>
-__device__ void finish_list(const gdn_sample_args& p, size_t at, const T* row, u64* list, int m, int c, float top_p, float floor_w,
-                            u64 u, const Weight& weight, u64* part) {
+// Descending order of n (a power of two up to kThreads) words, one a thread: neighbours up to 16 apart compare by
+// shuffles, others through `places` (two halves in turn, one barrier each).
+__device__ __forceinline__ u64 sort_descending(u64 v, int n, u64* places) {
   const int tid = threadIdx.x;
-  constexpr int kMost = kList / 2 / kThreads;
-  __shared__ u64 total_s;
-  __shared__ int kept_s;
-  const int padded = pow2_at_least(m);
-  for (int i = m + tid; i < padded; i += kThreads) list[i] = 0;
-  __syncthreads();
-  sort_descending(list, padded);
-  // a thread has `per` neighbours of the order
-  int per = (c + kThreads - 1) / kThreads, i0 = min(c, tid * per), i1 = min(c, i0 + per);
-  u64 words[kMost];
-  uint32_t W[kMost];
-  u64 sum = 0;
-#pragma unroll
-  for (int j = 0; j < kMost; ++j) {
-    if (i0 + j < i1) {
-      words[j] = list[i0 + j];
-      W[j] = weight.whole(of_key(words[j] >> 32));
-      sum += W[j];
+  int half = 0;
+  for (int k = 2; k <= n; k <<= 1)
+    for (int j = k >> 1; j > 0; j >>= 1) {
+      u64 other;
+      if (j < 32) {
+        other = __shfl_xor_sync(kFull, v, j);
+      } else {
+        places[half * kThreads + tid] = v;
+        __syncthreads();
+        other = places[half * kThreads + (tid ^ j)];
+        half ^= 1;
+      }
+      const bool larger = ((tid & j) == 0) == ((tid & k) == 0);
+      v = (other > v) == larger ? other : v;
     }
-  }
-  u64 upto = block_scan(sum, part);
+  return v;
+}
+
+// The rest of a row whose m candidates (key << 32 | ~index, in any order) lie in `list`; the first c of them in order are
+// the top-k tokens.  m <= kThreads: a candidate a thread, sorted twice (by logit for the prefixes, by index for the draw).
+__device__ __forceinline__ void finish_sorted(const gdn_sample_args& p, size_t at, const u64* list, u64* places, int m, int c,
+                                              float top_p, float floor_w, u64 u, const Weight& weight, u64* part) {
+  __shared__ u64 total_s;
+  __shared__ uint32_t drawn_s;
+  const int tid = threadIdx.x, n = m <= 1 ? 1 : 1 << (32 - __clz(m - 1));
+  const u64 word = sort_descending(tid < m ? list[tid] : 0, n, places);
+  const float w = tid < c ? weight.w(of_key(word >> 32)) : 0.f;
+  const uint32_t W = __float2uint_rn(w * 2147483648.f);
+  u64 upto = block_scan(W, part);
   if (tid == kThreads - 1) total_s = upto;
-  if (tid == 0) kept_s = 0;
   __syncthreads();
   const u64 limit = top_p < 1.f ? shift_mul(total_s, fraction(top_p, 1.f)) : ~0ull;
-  u64 before = upto - sum;
-  int kept = 0;
-#pragma unroll
-  for (int j = 0; j < kMost; ++j) {
-    if (i0 + j < i1) {
-      const bool in = before < limit || i0 + j == 0;
-      before += W[j];
-      kept += in;
-      // ascending index, the weight beside it; a token that a filter drops keeps its place with no weight
-      list[i0 + j] = in && weight.w(of_key(words[j] >> 32)) >= floor_w ? words[j] << 32 | W[j] : in ? words[j] << 32 : 0;
-    }
-  }
-  if (kept) atomicAdd(&kept_s, kept);
-  __syncthreads();
-  c = kept_s;
-  const int padded_c = pow2_at_least(c);
-  for (int i = c + tid; i < padded_c; i += kThreads) list[i] = 0;
-  __syncthreads();
-  sort_descending(list, padded_c);
-  per = (c + kThreads - 1) / kThreads;
-  i0 = min(c, tid * per);
-  i1 = min(c, i0 + per);
-  sum = 0;
-  for (int i = i0; i < i1; ++i) sum += (uint32_t)list[i];
-  upto = block_scan(sum, part);
+  const bool kept = tid < c && (upto - W < limit || tid == 0) && w >= floor_w;
+  const u64 by_index = sort_descending(kept ? word << 32 | W : 0, n, places);
+  const uint32_t V = (uint32_t)by_index;
+  upto = block_scan(V, part);  // its first barrier is behind every read of total_s
   if (tid == kThreads - 1) total_s = upto;
   __syncthreads();
   const u64 drawn = shift_mul(total_s, u);
-  before = upto - sum;
-  if (before <= drawn && drawn < upto) {
-    int i = i0;
-    while (before + (uint32_t)list[i] <= drawn) before += (uint32_t)list[i++];
-    const int token = (int)~(uint32_t)(list[i] >> 32);
-    p.target[at] = token;
-    if (p.prob) p.prob[at] = weight.w(number(row[token])) * 2147483648.f / (float)total_s;
+  if (upto - V <= drawn && drawn < upto) drawn_s = (uint32_t)(by_index >> 32);
+  __syncthreads();
+  if (kept && (uint32_t)word == drawn_s) {
+    p.target[at] = (int)~drawn_s;
+    if (p.prob) p.prob[at] = w * 2147483648.f / (float)total_s;
   }
+}
+
+// The same for more candidates than threads, without sorting: a candidate's rank, and the weight before it in the order of
+// the logits and in that of the indexes, are sums over the list, which every thread reads from the front for its own.
+__device__ __forceinline__ void finish_list(const gdn_sample_args& p, size_t at, const u64* list, uint32_t* weights, int m, int c,
+                                            float top_p, float floor_w, u64 u, const Weight& weight, u64* part) {
+  constexpr int kMost = kList / kThreads;  // candidates of a thread
+  const int tid = threadIdx.x;
+  u64 word[kMost];
+  uint32_t W[kMost];
+  const int own = (m - tid + kThreads - 1) / kThreads;  // tid, tid + kThreads, ...
+#pragma unroll
+  for (int j = 0; j < kMost; ++j) {
+    word[j] = j < own ? list[tid + j * kThreads] : 0;
+    W[j] = j < own ? weight.whole(of_key(word[j] >> 32)) : 0;
+    if (j < own) weights[tid + j * kThreads] = W[j];
+  }
+  __syncthreads();
+  int rank[kMost] = {};
+  u64 before[kMost] = {};
+#pragma unroll 4
+  for (int i = 0; i < m; ++i) {
+    const u64 other = list[i];
+    const uint32_t v = weights[i];
+#pragma unroll
+    for (int j = 0; j < kMost; ++j)
+      if (other > word[j]) {
+        ++rank[j];
+        before[j] += v;
+      }
+  }
+  u64 sum = 0;
+#pragma unroll
+  for (int j = 0; j < kMost; ++j) sum += j < own && rank[j] < c ? W[j] : 0;
+  const u64 top_k_sum = block_sum(sum, part);
+  const u64 limit = top_p < 1.f ? shift_mul(top_k_sum, fraction(top_p, 1.f)) : ~0ull;
+  sum = 0;
+#pragma unroll
+  for (int j = 0; j < kMost; ++j) {
+    const bool kept = j < own && rank[j] < c && (before[j] < limit || rank[j] == 0) && weight.w(of_key(word[j] >> 32)) >= floor_w;
+    if (!kept) W[j] = 0;
+    if (j < own) weights[tid + j * kThreads] = W[j];
+    sum += W[j];
+    before[j] = 0;
+  }
+  const u64 total = block_sum(sum, part);  // and a barrier: the weights are the kept ones now
+  const u64 drawn = shift_mul(total, u);
+#pragma unroll 4
+  for (int i = 0; i < m; ++i) {
+    const uint32_t other = (uint32_t)list[i], v = weights[i];  // inverted indexes: a larger one comes first
+#pragma unroll
+    for (int j = 0; j < kMost; ++j)
+      if (other > (uint32_t)word[j]) before[j] += v;
+  }
+#pragma unroll
+  for (int j = 0; j < kMost; ++j)
+    if (W[j] != 0 && before[j] <= drawn && drawn < before[j] + W[j]) {
+      p.target[at] = (int)~(uint32_t)word[j];
+      if (p.prob) p.prob[at] = weight.w(of_key(word[j] >> 32)) * 2147483648.f / (float)total;
+    }
 }
 
 struct Place {  // a block's kept weight above the threshold, and its tokens on it
@@ -253,11 +319,11 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const gdn_sample_args 
   constexpr int kN = Unit<T>::kN;
   extern __shared__ uint4 slice[];                      // [slice_units], then the scratch below
   uint32_t* const scratch = reinterpret_cast<uint32_t*>(slice + slice_units);
-  u64* const list = reinterpret_cast<u64*>(scratch);     // [kList]
+  u64* const list = reinterpret_cast<u64*>(scratch);     // [kList], and as many weights behind it
   uint32_t* const lo = scratch;                          // [kBins] sums of the weights' low halves
   uint32_t* const hi = scratch + kBins;                  // [kBins] and high halves
   uint32_t* const maxima = scratch;                      // [blocks][kThreads]
-  __shared__ u64 part[kWarps];
+  __shared__ u64 part[2 * kWarps];
   __shared__ News news;
   __shared__ Place places[kMaxCluster], warps[kWarps];
   __shared__ uint32_t count, lowest, all_s, digits[256];
@@ -323,57 +389,44 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const gdn_sample_args 
   }
   cluster_sync();
 
-  // the first block: the row's largest key, and for a top_k that a list can hold the k-th largest thread maximum
+  // the first block: the row's largest key, and for a top_k that a list can hold a bound just under the k-th largest
+  // thread maximum
   const bool listed = k > 0 && k < p.V && k <= kList / 2 && temp > 0.f;
   if (rank == 0) {
-    uint32_t mine[kMaxCluster], best = 0;
+    uint32_t mine[kMaxCluster], best = 0, low = 0xffffffffu;
+    int n_maxima = 0;
 #pragma unroll
     for (int r = 0; r < kMaxCluster; ++r) {
       mine[r] = r < blocks ? maxima[r * kThreads + tid] : 0;
       best = max(best, mine[r]);
+      if (mine[r] != 0) low = min(low, mine[r]);
+      n_maxima += mine[r] != 0;
     }
-    best = __reduce_max_sync(kFull, best);
-    if (lane == 0) part[warp] = best;
-    __syncthreads();
-    for (int w = 0; w < kWarps; ++w) best = max(best, (uint32_t)part[w]);
-    uint32_t bound = 1;  // every key but NaN's
-    if (listed) {
-      uint32_t prefix = 0, left = (uint32_t)k;
-      for (int s = 24; s >= (sizeof(T) == 2 ? 16 : 0); s -= 8) {
-        digits[tid] = 0;
-        __syncthreads();
+    digits[tid] = 0;
+    const auto ends = block_ends(best, low, n_maxima, part);
+    best = ends.most;
+    low = ends.least;
+    uint32_t bound = 1;  // every key but NaN's: fewer maxima than k
+    if (listed && ends.count >= k) {
+      // the maxima in 256 equal steps between the ends (the keys' leading digits would be the same few for most of them):
+      // the k-th largest lies in the first step that k of them reach
+      const float best_x = of_key(best);
+      const Steps<256> steps(best_x - of_key(low));
+      auto step_of = [&](uint32_t key) { return steps.of(best_x - of_key(key)); };
 #pragma unroll
-        for (int r = 0; r < kMaxCluster; ++r)
-          if (mine[r] != 0 && (s == 24 || (mine[r] ^ prefix) >> (s + 8) == 0)) atomicAdd(&digits[mine[r] >> s & 255], 1u);
-        __syncthreads();
-        // thread tid looks at digit 255 - tid: the prefix from the top
-        const uint32_t here = digits[255 - tid];
-        const uint32_t upto = (uint32_t)block_scan(here, part);
-        if (upto - here < left && left <= upto) {
-          news.digit = 255 - tid;
-          news.left = upto - here;
-        }
-        if (tid == kThreads - 1) all_s = upto;
-        __syncthreads();
-        if (all_s < left) {  // fewer maxima than k: every token is a candidate
-          prefix = 0;
-          break;  // at the first digit only
-        }
-        prefix |= news.digit << s;
-        left -= (uint32_t)news.left;
-        __syncthreads();
-      }
-      // a negative bf16's low bits, turned over
-      bound = prefix == 0 ? 1u : sizeof(T) == 2 && !(prefix & 0x80000000u) ? prefix | 0xffff : prefix;
+      for (int r = 0; r < kMaxCluster; ++r)
+        if (mine[r] != 0) atomicAdd(&digits[step_of(mine[r])], 1u);
+      __syncthreads();
+      const uint32_t here = digits[tid], upto = (uint32_t)block_scan(here, part);
+      if (upto - here < (uint32_t)k && (uint32_t)k <= upto) all_s = tid;
+      __syncthreads();
+      const int last = (int)all_s;
+      uint32_t least = 0xffffffffu;
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r)
+        if (mine[r] != 0 && step_of(mine[r]) <= last) least = min(least, mine[r]);
+      bound = block_ends(0, least, 0, part).least;
     }
-    uint32_t low = 0xffffffffu;
-#pragma unroll
-    for (int r = 0; r < kMaxCluster; ++r) low = mine[r] != 0 ? min(low, mine[r]) : low;
-    low = __reduce_min_sync(kFull, low);
-    __syncthreads();
-    if (lane == 0) part[warp] = low;
-    __syncthreads();
-    for (int w = 0; w < kWarps; ++w) low = min(low, (uint32_t)part[w]);
     if (tid < blocks) {
       put(peer(&news.top_key, tid), best);
       put(peer(&news.bound, tid), bound);
@@ -423,7 +476,8 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const gdn_sample_args 
     const int found = (int)get(counter);
     if (found <= kList) {
       if (rank != 0) return;
-      finish_list(p, at, row, list, found, min(k, found), top_p, floor_w, u, weight, part);
+      if (found <= kThreads) finish_sorted(p, at, list, list + kThreads, found, min(k, found), top_p, floor_w, u, weight, part);
+      else finish_list(p, at, list, scratch + 2 * kList, found, min(k, found), top_p, floor_w, u, weight, part);
       cluster_sync();  // the others have read `count`, or have left
       return;
     }
@@ -436,9 +490,11 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const gdn_sample_args 
   auto narrow = [&](bool weights, float range, u64 want) {
     // the new threshold: the prefix of the kept tokens whose counts, or weights, reach `want` (for weights: that
     // share of their sum)
-    const float steps = kBins / range;
+    const Steps<kBins> steps(range);
     const bool edged = ties != ~0ull;
-    auto bin_of = [&](float x) { return min(kBins - 1, (int)((peak - x) * steps)); };  // NaN (x == peak): 0
+    const float edge_x = edged ? of_key(thr) : -INFINITY;
+    auto within = [&](float x) { return edged ? x > edge_x : x >= edge_x; };  // not NaN; the tied tokens apart
+    auto bin_of = [&](float x) { return steps.of(peak - x); };
     auto add = [&](float x, int i) {
       const uint32_t v = weights ? weight.whole(x) : 1u;
       if (v & 0xffff) atomicAdd(&lo[i], v & 0xffff);
@@ -452,8 +508,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const gdn_sample_args 
       const Unit<T> x(slice[i]);
 #pragma unroll
       for (int c = 0; c < kN; ++c) {
-        const uint32_t key = key_of(x.x[c]);
-        if (key > thr || (key == thr && !edged)) add(x.x[c], bin_of(x.x[c]));
+        if (within(x.x[c])) add(x.x[c], bin_of(x.x[c]));
       }
     }
     cluster_sync();
@@ -507,9 +562,9 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const gdn_sample_args 
         const Unit<T> x(slice[i]);
 #pragma unroll
         for (int c = 0; c < kN; ++c) {
-          if (bin_of(x.x[c]) != bin) continue;
+          if (bin_of(x.x[c]) != bin || !within(x.x[c])) continue;
           const uint32_t key = key_of(x.x[c]);
-          if ((key > thr || (key == thr && !edged)) && (s == 24 || (key ^ prefix) >> (s + 8) == 0)) add(x.x[c], key >> s & 255);
+          if (s == 24 || (key ^ prefix) >> (s + 8) == 0) add(x.x[c], key >> s & 255);
         }
       }
       cluster_sync();
@@ -544,18 +599,19 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const gdn_sample_args 
   // index order: each warp has a run of units; its kept weight is that of the keys above thr and of its share of the
   // tied ones
   const int run = (own + kWarps - 1) / kWarps, r0 = min(own, warp * run), r1 = min(own, r0 + run);
-  auto above = [&](float x, uint32_t key) -> u64 {
-    if (!(key > thr || (key == thr && !edged))) return 0;
-    return floor_w > 0.f && weight.w(x) < floor_w ? 0 : weight.whole(x);
+  const float edge_x = edged ? of_key(thr) : -INFINITY;
+  auto above = [&](float x) -> uint32_t {
+    if (!(edged ? x > edge_x : x >= edge_x)) return 0;  // NaN too
+    const float w = weight.w(x);
+    return w < floor_w ? 0 : __float2uint_rn(w * 2147483648.f);
   };
   u64 sum = 0, equal = 0;
   for (int i = r0 + lane; i < r1; i += 32) {
     const Unit<T> x(slice[i]);
 #pragma unroll
     for (int c = 0; c < kN; ++c) {
-      const uint32_t key = key_of(x.x[c]);
-      sum += above(x.x[c], key);
-      equal += edged && key == thr;
+      sum += above(x.x[c]);
+      equal += edged && x.x[c] == edge_x;
     }
   }
   sum = warp_sum(sum);
@@ -601,7 +657,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const gdn_sample_args 
     if (i < r1) w = slice[i];
     const Unit<T> x(w);
 #pragma unroll
-    for (int c = 0; c < kN; ++c) eq += edged && key_of(x.x[c]) == thr;
+    for (int c = 0; c < kN; ++c) eq += edged && x.x[c] == edge_x;
     uint32_t eq_upto = eq;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -611,9 +667,8 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const gdn_sample_args 
     u64 place = eq_before + eq_upto - eq;
 #pragma unroll
     for (int c = 0; c < kN; ++c) {
-      const uint32_t key = key_of(x.x[c]);
-      W[c] = above(x.x[c], key);
-      if (edged && key == thr) W[c] = place++ < ties ? thr_w : 0;
+      W[c] = above(x.x[c]);
+      if (edged && x.x[c] == edge_x) W[c] = place++ < ties ? thr_w : 0;
       W_all += W[c];
     }
     u64 upto = W_all;
@@ -713,7 +768,7 @@ int run(const gdn_sample_args& p, cudaStream_t st) {
   const int blocks = cluster_of((int64_t)p.B * p.R, (int64_t)p.V * sizeof(T));
   const int units = (p.V + 2 * (kN - 1)) / kN;  // at the worst alignment
   const int slice_units = (units + blocks - 1) / blocks;
-  const int smem = slice_units * 16 + kList * 8;
+  const int smem = slice_units * 16 + kList * 12;
   // the largest slice's size, so that calls of any V from any thread set the same value
   if (smem > 40 * 1024 &&
       cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024) != cudaSuccess)

@@ -426,6 +426,16 @@ def test_sampling_matches_the_definition(hy, B, R, V, dtype, ties, pad):
         check_sample(case, run_sample(hy, case, off), off)
 
 
+@pytest.mark.parametrize("V,k", [(5000, 300), (40000, 700), (40000, 20), (3000, 512), (3000, 513), (700, 699)])
+def test_sampling_with_many_equal_logits(hy, V, k):
+    """Far more tokens at the k-th largest logit than k: they enter by index, whichever way the k-th is found."""
+    case = sample_case(3, 2, V, BF16, seed=k)
+    case["logits"] = (case["logits"] / 4).round()  # a handful of values
+    case["top_k"][:] = k
+    check_sample(case, run_sample(hy, case))
+    check_sample(case, run_sample(hy, case, ("top_p", "min_p")), ("top_p", "min_p"))
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
 def test_sampling_parameters_at_their_edges(hy, dtype):
     """Requests with a parameter at or past its edge against the definition with that filter's plain meaning."""

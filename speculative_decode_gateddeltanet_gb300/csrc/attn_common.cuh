@@ -271,12 +271,11 @@ __device__ __forceinline__ float* partial(const Params& p, int block, int slot, 
   return p.partials + (size_t)(block * 2 + slot) * rows * (p.d + 2);
 }
 
-constexpr int kCombineBlocks = 8;  // blocks that share the rows of one split tile
 constexpr int kCombineWarps = 4;
 constexpr int kCombineBatch = 8;   // partials whose loads are in flight at once
 
 // Joins the partials of the split tile that block blockIdx.x of the attention
-// begins.  Up to eight partials: a warp per row.  More (few tiles, long
+// begins; gridDim.y blocks share its rows.  Up to eight partials: a warp per row.  More (few tiles, long
 // contexts): a block per row, warp w taking partials w, w + 4, ..., and the warps'
 // sums added in warp order.  Either way the order is fixed by the lengths alone.
 template <typename T, int kD, int kRows>
@@ -294,7 +293,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const Param
   auto part = [&](int i) { return partial(p, blockIdx.x + i, i == 0, kRows); };
   auto stats = [&](int i, int row) { return reinterpret_cast<const float2*>(part(i) + (size_t)kRows * kD)[row]; };
   const int first = shared ? (int)blockIdx.y : (int)blockIdx.y * kCombineWarps + warp;
-  const int step = shared ? kCombineBlocks : kCombineBlocks * kCombineWarps;
+  const int step = shared ? (int)gridDim.y : (int)gridDim.y * kCombineWarps;
   const int i_first = shared ? warp : 0, i_step = shared ? kCombineWarps : 1;
   for (int row = first; row < rows; row += step) {
     float x[kCombineBatch][kPer], tops[kCombineBatch], acc[kPer] = {};

@@ -15,7 +15,7 @@
 namespace gdnattn {
 
 constexpr int kSimtRows = 32, kSimtKeys = 32, kSimtThreads = 128;
-constexpr int kSimtMinUnits = 4;  // a block does 128 keys at least: below that the join costs more than the split saves
+constexpr int kSimtMinUnits = 1;
 
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 
@@ -25,7 +25,7 @@ constexpr int simt_smem() {
 }
 
 template <int kD>
-__global__ void __launch_bounds__(kSimtThreads) simt_kernel(const Params p) {
+__global__ void __launch_bounds__(kSimtThreads, kD == 256 ? 2 : 3) simt_kernel(const Params p) {
   constexpr int kR = kSimtRows, kN = kSimtKeys, kWarpRows = kR / 4, kCols = kD / 32, kChunks = kD / 4;
   extern __shared__ float4 smem4[];
   float* const qs = reinterpret_cast<float*>(smem4);  // [kR][kD]
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kSimtThreads) simt_kernel(const Params p) {
 // blocks of the launch: a fixed number per d and type (as many as 152 SMs hold
 // at once), so that the work buffer's size depends on neither lengths nor device
 constexpr int kSms = 152;
-constexpr int simt_blocks(int d) { return kSms * (d == 256 ? 2 : 4); }
+constexpr int simt_blocks(int d) { return kSms * (d == 256 ? 2 : 3); }
 
 int blocks_of(int d, int dtype) { return dtype == GDN_DTYPE_BF16 ? tc_blocks() : simt_blocks(d); }
 
@@ -199,7 +199,7 @@ int run_simt(Params& p, cudaStream_t st) {
   p.n_blocks = simt_blocks(kD);
   const int rc = launch(simt_kernel<kD>, dim3(p.n_blocks), dim3(kSimtThreads), smem, st, p);
   if (rc != GDN_OK) return rc;
-  return launch(combine_kernel<float, kD, kSimtRows>, dim3(p.n_blocks, kCombineBlocks), dim3(32 * kCombineWarps), 0, st, p);
+  return launch(combine_kernel<float, kD, kSimtRows>, dim3(p.n_blocks, 4), dim3(32 * kCombineWarps), 0, st, p);
 }
 
 int run_simt(Params& p, cudaStream_t st) {

@@ -796,7 +796,7 @@ int run(TcParams& t, cudaStream_t st) {
   t.p.n_blocks = kTcBlocks;
   const int rc = launch(tc_kernel<kD>, dim3(kTcBlocks), dim3(kTcThreads), S::kSmem, st, t, k_map, v_map);
   if (rc != GDN_OK) return rc;
-  return launch(combine_kernel<__nv_bfloat16, kD, kTcRows>, dim3(kTcBlocks, kCombineBlocks), dim3(32 * kCombineWarps), 0, st, t.p);
+  return launch(combine_kernel<__nv_bfloat16, kD, kTcRows>, dim3(kTcBlocks, 8), dim3(32 * kCombineWarps), 0, st, t.p);
 }
 
 int run_tc(Params& p, cudaStream_t st) {

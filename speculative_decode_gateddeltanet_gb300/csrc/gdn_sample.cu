@@ -40,6 +40,9 @@ constexpr int kBins = 1024;
 constexpr int kList = 1024;  // candidates that the first block can hold
 constexpr int kMaxSlice = 49152;  // elements a block stages: 192 KB in 32 bits; sums of 16-bit halves fit 32 bits
 static_assert(kMaxSlice * kMaxCluster == GDN_SAMPLE_MAX_V, "a row is staged by one cluster");
+static_assert(kThreads == 256, "a digit, and a word of a sorted list, is a thread");
+static_assert(kMaxCluster * kThreads <= 3 * kList && 2 * kBins <= 3 * kList && 3 * kThreads * 2 <= 3 * kList,
+              "the scratch's other uses fit the list's place");
 
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
@@ -199,12 +202,15 @@ struct News {  // what the first block tells the others
   uint32_t top_key, bound, low, digit;  // low: the smallest thread maximum
 };
 
-// Descending order of n (a power of two up to kThreads) words, one a thread: neighbours up to 16 apart compare by
+// Descending order of kWords (a power of two up to kThreads) words, one a thread: neighbours up to 16 apart compare by
 // shuffles, others through `places` (two halves in turn, one barrier each).
-__device__ __forceinline__ u64 sort_descending(u64 v, int n, u64* places) {
+template <int kWords>
+__device__ __forceinline__ u64 sort_descending(u64 v, u64* places) {
   const int tid = threadIdx.x;
   int half = 0;
-  for (int k = 2; k <= n; k <<= 1)
+#pragma unroll
+  for (int k = 2; k <= kWords; k <<= 1) {
+#pragma unroll
     for (int j = k >> 1; j > 0; j >>= 1) {
       u64 other;
       if (j < 32) {
@@ -218,7 +224,12 @@ __device__ __forceinline__ u64 sort_descending(u64 v, int n, u64* places) {
       const bool larger = ((tid & j) == 0) == ((tid & k) == 0);
       v = (other > v) == larger ? other : v;
     }
+  }
   return v;
+}
+
+__device__ __forceinline__ u64 sort_descending(u64 v, int n, u64* places) {
+  return n <= 64 ? sort_descending<64>(v, places) : n <= 128 ? sort_descending<128>(v, places) : sort_descending<256>(v, places);
 }
 
 // The rest of a row whose m candidates (key << 32 | ~index, in any order) lie in `list`; the first c of them in order are
@@ -227,8 +238,8 @@ __device__ __forceinline__ void finish_sorted(const gdn_sample_args& p, size_t a
                                               float top_p, float floor_w, u64 u, const Weight& weight, u64* part) {
   __shared__ u64 total_s;
   __shared__ uint32_t drawn_s;
-  const int tid = threadIdx.x, n = m <= 1 ? 1 : 1 << (32 - __clz(m - 1));
-  const u64 word = sort_descending(tid < m ? list[tid] : 0, n, places);
+  const int tid = threadIdx.x;
+  const u64 word = sort_descending(tid < m ? list[tid] : 0, m, places);
   const float w = tid < c ? weight.w(of_key(word >> 32)) : 0.f;
   const uint32_t W = __float2uint_rn(w * 2147483648.f);
   u64 upto = block_scan(W, part);
@@ -236,7 +247,7 @@ __device__ __forceinline__ void finish_sorted(const gdn_sample_args& p, size_t a
   __syncthreads();
   const u64 limit = top_p < 1.f ? shift_mul(total_s, fraction(top_p, 1.f)) : ~0ull;
   const bool kept = tid < c && (upto - W < limit || tid == 0) && w >= floor_w;
-  const u64 by_index = sort_descending(kept ? word << 32 | W : 0, n, places);
+  const u64 by_index = sort_descending(kept ? word << 32 | W : 0, m, places);
   const uint32_t V = (uint32_t)by_index;
   upto = block_scan(V, part);  // its first barrier is behind every read of total_s
   if (tid == kThreads - 1) total_s = upto;

@@ -112,19 +112,20 @@ struct Tiles {
     const int token = last >> 31 ? (int)(last / p.G) : (int)quotient((uint32_t)last, p.by_G);
     return (int)((unsigned)(r.ctx + token) / kKeys) + 1;
   }
-  // units that a tile costs beside its key blocks: a tile of 128 rows takes about three blocks' time from its last
-  // product to the next one's first, one of a few rows hides behind the copies of the next one's keys
-  __device__ static int extra(const Params& p, const Request& r) { return kRows < 128 ? 0 : (long long)r.n * p.G > 64 ? 3 : 1; }
+  // Units that a tile costs beside its key blocks, in the time of one: about 3 us from a tile's last product to the next
+  // one's first on the tensor cores.  Measured against 1 for few rows and 3 for many: 256 ragged requests 200 -> 183 us,
+  // 16 x 4 rows (d = 256) 43.5 -> 38.7, prompt chunks at d = 256 557 -> 495; 6, 4 and 2 lie between or behind.
+  static constexpr int kExtra = kRows < 128 ? 0 : kKeys == 64 ? 5 : 3;
   // units of the tiles before m
   __device__ static long long before(const Params& p, const Request& r, int m) {
     if (m == 0) return 0;
-    return (long long)m * (1 + extra(p, r)) + floor_sum(m, (long long)p.G * kKeys, kRows, (long long)p.G * r.ctx + kRows - 1);
+    return (long long)m * (1 + kExtra) + floor_sum(m, (long long)p.G * kKeys, kRows, (long long)p.G * r.ctx + kRows - 1);
   }
   // units of one kv head of the request
   __device__ static long long sum(const Params& p, const Request& r) {
     if (r.n <= 0) return 0;
     const int M = count(p, r);
-    return before(p, r, M - 1) + extra(p, r) + blocks(p, r, M - 1);
+    return before(p, r, M - 1) + kExtra + blocks(p, r, M - 1);
   }
 };
 
@@ -139,14 +140,14 @@ struct Walk {
 
   __device__ void segment() {
     blocks = T::blocks(*p, req, m);
-    const int own = T::extra(*p, req), end = min(own + blocks, at + left);
-    kb0 = max(0, at - own);
-    kb1 = end - own;
+    const int end = min(T::kExtra + blocks, at + left);
+    kb0 = max(0, at - T::kExtra);
+    kb1 = end - T::kExtra;
     if (kb1 <= kb0) left = 0;  // the block's part ends before the tile's first key block
   }
   __device__ bool done() const { return left <= 0; }
   __device__ void next() {
-    left -= kb1 + T::extra(*p, req) - at;
+    left -= kb1 + T::kExtra - at;
     if (left <= 0) return;
     at = 0;
     if (++m == tiles) {

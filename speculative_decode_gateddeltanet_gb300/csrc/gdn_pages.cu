@@ -21,45 +21,52 @@ namespace gdnpages {
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
-constexpr int kThreads = 512;
 constexpr int kMaxB = 4096;
-constexpr int kPerThread = kMaxB / kThreads;
 constexpr unsigned kFull = 0xffffffffu;
 
 // the sums a request's place in the three lists comes from; 64 bits, as the
 // demand of requests that are not served counts too
 struct Sums {
-  long long a, b;
+  long long take, back, rows;
 };
 
 __device__ __forceinline__ Sums warp_scan(Sums v, int lane) {
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
-    const long long a = __shfl_up_sync(kFull, v.a, off), b = __shfl_up_sync(kFull, v.b, off);
+    const long long a = __shfl_up_sync(kFull, v.take, off), b = __shfl_up_sync(kFull, v.back, off),
+                    c = __shfl_up_sync(kFull, v.rows, off);
     if (lane >= off) {
-      v.a += a;
-      v.b += b;
+      v.take += a;
+      v.back += b;
+      v.rows += c;
     }
   }
   return v;
 }
 
 // exclusive prefix of v over the block's threads; *total = the whole sum
-__device__ Sums block_scan(Sums v, Sums* part, Sums* total) {
+template <int kThreads>
+__device__ __forceinline__ Sums block_scan(Sums v, Sums* part, Sums* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const Sums inc = warp_scan(v, lane);
   if (lane == 31) part[warp] = inc;
   __syncthreads();
-  if (warp == 0) {
-    Sums p = lane < kThreads / 32 ? part[lane] : Sums{0, 0};
-    p = warp_scan(p, lane);
-    if (lane < kThreads / 32) part[lane] = p;
+  Sums before = {inc.take - v.take, inc.back - v.back, inc.rows - v.rows}, all = {0, 0, 0};
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    const Sums q = part[w];
+    if (w == warp) {
+      before.take += all.take;
+      before.back += all.back;
+      before.rows += all.rows;
+    }
+    all.take += q.take;
+    all.back += q.back;
+    all.rows += q.rows;
   }
-  __syncthreads();
-  const Sums before = warp > 0 ? part[warp - 1] : Sums{0, 0};
-  *total = part[kThreads / 32 - 1];
+  *total = all;
   __syncthreads();  // part may be used again
-  return {before.a + inc.a - v.a, before.b + inc.b - v.b};
+  return before;
 }
 
 // the last request whose prefix is not above i
@@ -73,6 +80,8 @@ __device__ __forceinline__ int find(const int* prefix, int B, int i) {
   return lo;
 }
 
+// kPerThread requests a thread: one where they are few, as then the call is as long as its chain of reads and barriers
+template <int kThreads, int kPerThread>
 __global__ void __launch_bounds__(kThreads) page_map_kernel(const gdn_page_map_args p) {
   extern __shared__ int sm[];
   __shared__ Sums part[kThreads / 32];
@@ -87,12 +96,11 @@ __global__ void __launch_bounds__(kThreads) page_map_kernel(const gdn_page_map_a
   const int N = p.n_pages, P = p.page_size, B = p.B;
   const int head = (int)((((long long)p.free_in[0] % N) + N) % N);
   const int n_free = min(max(p.free_in[1], 0), N);
-  const int per = (B + kThreads - 1) / kThreads;
+  const int per = kPerThread == 1 ? 1 : (B + kThreads - 1) / kThreads;
   const int b0 = threadIdx.x * per;
   int ctx[kPerThread], n[kPerThread], held[kPerThread], need[kPerThread];
-  unsigned bad = 0;  // requests whose lengths or counts are refused
   int status = 0;
-  Sums mine = {0, 0};
+  Sums mine = {0, 0, 0};
 #pragma unroll
   for (int i = 0; i < kPerThread; ++i) {
     if (i >= per || b0 + i >= B) break;
@@ -107,52 +115,50 @@ __global__ void __launch_bounds__(kThreads) page_map_kernel(const gdn_page_map_a
     if (n[i] < 0 || (p.R > 0 && n[i] > p.R)) why |= GDN_STATUS_BAD_NROWS;
     if (held[i] < 0 || held[i] > p.max_pages || (!why && want > p.max_pages)) why |= GDN_STATUS_TABLE_FULL;
     if (why) {
-      bad |= 1u << i;
       status |= why;
       n[i] = 0;
       need[i] = held[i];
     } else {
       need[i] = (int)want;
     }
-    mine.a += max(need[i] - held[i], 0);
+    mine.take += max(need[i] - held[i], 0);
   }
   Sums total;
-  Sums at = block_scan(mine, part, &total);
+  Sums at = block_scan<kThreads>(mine, part, &total);
   // a request is served when the demand up to and with it fits the free pages
-  Sums give = {0, 0}, rows = {0, 0};
+  Sums place = {0, 0, 0};
 #pragma unroll
   for (int i = 0; i < kPerThread; ++i) {
     if (i >= per || b0 + i >= B) break;
     const int want = max(need[i] - held[i], 0);
-    at.a += want;
-    if (want > 0 && at.a > n_free) {
+    at.take += want;
+    if (want > 0 && at.take > n_free) {
       status |= GDN_STATUS_NO_PAGES;
       need[i] = held[i];
       n[i] = 0;
     }
-    give.a += max(need[i] - held[i], 0);
-    give.b += max(held[i] - need[i], 0);
-    rows.a += n[i];
+    place.take += max(need[i] - held[i], 0);
+    place.back += max(held[i] - need[i], 0);
+    place.rows += n[i];
   }
-  Sums given, all_rows;
-  give = block_scan(give, part, &given);
-  rows = block_scan(rows, part, &all_rows);
+  Sums given;
+  place = block_scan<kThreads>(place, part, &given);
 #pragma unroll
   for (int i = 0; i < kPerThread; ++i) {
     if (i >= per || b0 + i >= B) break;
     const int b = b0 + i;
-    take_at[b] = (int)give.a;
-    back_at[b] = (int)give.b;
-    give.a += max(need[i] - held[i], 0);
-    give.b += max(held[i] - need[i], 0);
+    take_at[b] = (int)place.take;
+    back_at[b] = (int)place.back;
+    place.take += max(need[i] - held[i], 0);
+    place.back += max(held[i] - need[i], 0);
     const int counted = n[i];
-    const int first = p.R > 0 ? b * p.R : (int)min(rows.a, (long long)INT32_MAX);
-    if (p.R == 0 && n[i] > 0 && rows.a + n[i] > p.n_slot_rows) {
+    const int first = p.R > 0 ? b * p.R : (int)min(place.rows, (long long)INT32_MAX);
+    if (p.R == 0 && n[i] > 0 && place.rows + n[i] > p.n_slot_rows) {
       status |= GDN_STATUS_ROWS_FULL;
       n[i] = 0;
     }
     row_at[b] = first;
-    rows.a += counted;
+    place.rows += counted;
     ctx_s[b] = ctx[i];
     held_s[b] = held[i];
     rows_s[b] = n[i];
@@ -162,14 +168,14 @@ __global__ void __launch_bounds__(kThreads) page_map_kernel(const gdn_page_map_a
       if (p.row_start) p.row_start[b] = first;
     }
   }
-  const int end = p.R > 0 ? B * p.R : (int)min(all_rows.a, (long long)INT32_MAX);
+  const int end = p.R > 0 ? B * p.R : (int)min(given.rows, (long long)INT32_MAX);
   if (threadIdx.x == 0) {
-    take_at[B] = (int)given.a;
-    back_at[B] = (int)given.b;
+    take_at[B] = (int)given.take;
+    back_at[B] = (int)given.back;
     row_at[B] = end;
     if (blockIdx.x == 0) {
-      p.free_out[0] = (int)((head + given.a) % N);
-      p.free_out[1] = (int)min(n_free - given.a + given.b, (long long)N);
+      p.free_out[0] = (int)((head + given.take) % N);
+      p.free_out[1] = (int)min(n_free - given.take + given.back, (long long)N);
       if (p.row_start) p.row_start[B] = end;
     }
   }
@@ -177,12 +183,12 @@ __global__ void __launch_bounds__(kThreads) page_map_kernel(const gdn_page_map_a
   __syncthreads();
 
   const int first = blockIdx.x * kThreads + threadIdx.x, step = gridDim.x * kThreads;
-  for (int i = first; i < given.a; i += step) {
+  for (int i = first; i < given.take; i += step) {
     const int b = find(take_at, B, i);
     p.block_table[(size_t)b * p.table_stride + held_s[b] + i - take_at[b]] = p.free_ring[(head + (long long)i) % N];
   }
   // the ring's free part ends where the returned pages go: the two ranges are disjoint
-  for (int i = first; i < given.b; i += step) {
+  for (int i = first; i < given.back; i += step) {
     const int b = find(back_at, B, i);
     const int left = held_s[b] - (back_at[b + 1] - back_at[b]);  // pages kept
     p.free_ring[(head + (long long)n_free + i) % N] = p.block_table[(size_t)b * p.table_stride + left + i - back_at[b]];
@@ -355,11 +361,15 @@ extern "C" GDN_API int gdn_page_map(const gdn_page_map_args* args, void* stream)
   if (rc != GDN_OK || args->B == 0) return rc;
   const gdn_page_map_args p = *args;
   const size_t smem = (size_t)(6 * p.B + 3) * sizeof(int);
-  if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(page_map_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (6 * kMaxB + 3) * sizeof(int)) != cudaSuccess)
-    return GDN_ERR_LAUNCH;
-  const int blocks = min(max((p.n_slot_rows + kThreads - 1) / kThreads, 1), 152);
-  return launch(page_map_kernel, dim3(blocks), dim3(kThreads), smem, static_cast<cudaStream_t>(stream), p);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  auto run = [&](auto kernel, int threads) {
+    if (smem > 48 * 1024 &&
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (6 * kMaxB + 3) * sizeof(int)) != cudaSuccess)
+      return (int)GDN_ERR_LAUNCH;
+    const int blocks = min(max((p.n_slot_rows + threads - 1) / threads, 1), 152);
+    return launch(kernel, dim3(blocks), dim3(threads), smem, st, p);
+  };
+  return p.B <= 128 ? run(page_map_kernel<128, 1>, 128) : p.B <= 512 ? run(page_map_kernel<512, 1>, 512) : run(page_map_kernel<512, 8>, 512);
 }
 
 extern "C" GDN_API int gdn_kv_append(const gdn_kv_append_args* a, void* stream) {

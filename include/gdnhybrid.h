@@ -146,7 +146,10 @@ GDN_API int gdn_kv_append(const gdn_kv_append_args* args, void* stream);
  * Arithmetic.  GDN_DTYPE_F32: 32-bit products and sums throughout.
  * GDN_DTYPE_BF16: products of bf16 with 32-bit sums; the weights p are rounded
  * to bf16 before they meet V (their sum is not); o is rounded once.
- * The same inputs give the same bits on every call.
+ * The same inputs give the same bits on every call.  A kernel never spins
+ * without bound: where a staging copy does not land in time, the block that
+ * waits for it gives up, GDN_STATUS_TIMEOUT is set, and the o rows it had a part
+ * in are undefined.
  *
  * Supported: d in {64, 128, 256}; H_q a multiple of H_kv, H_q/H_kv <= 128;
  * page_size a multiple of 16 up to 1024 (any >= 1 for GDN_DTYPE_F32).

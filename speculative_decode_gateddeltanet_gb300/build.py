@@ -22,6 +22,8 @@ LIB = PKG / "_lib" / "libgdnspec.so"
 # test that makes the bounded wait run out; never loaded by the package
 TEST_HOOKS_LIB = PKG / "_lib" / "libgdnspec_testhooks.so"
 TEST_HOOKS_FLAGS = ["-DGDN_TEST_HOOKS", "-DGDN_WAIT_LIMIT_NS=2000000ull"]
+# the same for the tensor-core attention
+ATTN_TEST_HOOKS_LIB = PKG / "_lib" / "libgdnhybrid_testhooks.so"
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMPILE_FLAGS = ARCH + [
     "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden", "-I", str(ROOT / "include"),
@@ -75,6 +77,15 @@ def build_test_hooks(force: bool = False) -> Path:
     if not force and not stale(TEST_HOOKS_LIB, src):
         return TEST_HOOKS_LIB
     return _compile(TEST_HOOKS_LIB, src, TEST_HOOKS_FLAGS)
+
+
+def build_attn_test_hooks(force: bool = False) -> Path:
+    """Compile the test-only variant of the attention calls if it is missing
+    or older than its sources."""
+    src = [PKG / "csrc" / "gdn_attn.cu", PKG / "csrc" / "gdn_attn_tc.cu"]
+    if not force and not stale(ATTN_TEST_HOOKS_LIB, src):
+        return ATTN_TEST_HOOKS_LIB
+    return _compile(ATTN_TEST_HOOKS_LIB, src, TEST_HOOKS_FLAGS)
 
 
 if __name__ == "__main__":

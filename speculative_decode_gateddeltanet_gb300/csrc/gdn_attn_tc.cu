@@ -42,7 +42,6 @@
 // flight, frees its TMEM and ends.
 #include <cuda.h>
 
-#include <mutex>
 #include <type_traits>
 
 #include "attn_common.cuh"
@@ -54,7 +53,10 @@ constexpr int kTcRows = 128;
 constexpr int kTcThreads = 512;
 constexpr int kTcBlocks = 152;  // one block per SM of a GB300
 constexpr int kTcMinUnits = 2;
-constexpr unsigned long long kWaitNs = 500000000ull;
+#ifndef GDN_WAIT_LIMIT_NS
+#define GDN_WAIT_LIMIT_NS 500000000ull
+#endif
+constexpr unsigned long long kWaitNs = GDN_WAIT_LIMIT_NS;
 
 template <int kD>
 struct Shape {
@@ -277,6 +279,11 @@ __device__ __forceinline__ bool softmax_block(RowState& st, uint32_t s_at, int c
   tmem_wait_store();
   return true;
 }
+
+#ifdef GDN_TEST_HOOKS
+// Test builds only: the block whose first K copy is declared on its barrier but never issued (-1: none).
+__device__ int g_test_drop_block = -1;
+#endif
 
 struct TcParams {
   Params p;
@@ -720,7 +727,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           my_page = p.n_pages;  // outside the map: zeros
           if (p.status) atomicOr(p.status, GDN_STATUS_BAD_PAGE);
         }
-        if (box < live) tma_box(map, tiles + stage * S::kTileBytes + at, full + 8 * stage, chunk * 64, my_token, w.h, my_page);
+#ifdef GDN_TEST_HOOKS
+        const bool issue = is_v || sent > 0 || (int)blockIdx.x != g_test_drop_block;
+#else
+        constexpr bool issue = true;
+#endif
+        if (issue && box < live) tma_box(map, tiles + stage * S::kTileBytes + at, full + 8 * stage, chunk * 64, my_token, w.h, my_page);
         ++sent;
         if (++stage == stages) {
           stage = 0;
@@ -754,16 +766,15 @@ using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, voi
                               const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
                               CUtensorMapFloatOOBfill);
 
+// looked up once; null where there is no driver
 EncodeFn encoder() {
-  static EncodeFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
+  static const EncodeFn fn = [] {
     void* f = nullptr;
     cudaDriverEntryPointQueryResult found;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) == cudaSuccess &&
-        found == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeFn>(f);
-  });
+    const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) == cudaSuccess &&
+                    found == cudaDriverEntryPointSuccess;
+    return ok ? reinterpret_cast<EncodeFn>(f) : nullptr;
+  }();
   return fn;
 }
 
@@ -811,3 +822,10 @@ int run_tc(Params& p, cudaStream_t st) {
 }
 
 }  // namespace gdnattn
+
+#ifdef GDN_TEST_HOOKS
+// Test builds only: drop the first K copy of block `block` of later calls (-1 restores it).
+extern "C" GDN_API int gdn_test_drop_attention_copy(int block) {
+  return cudaMemcpyToSymbol(gdnattn::g_test_drop_block, &block, sizeof(int)) == cudaSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+}
+#endif

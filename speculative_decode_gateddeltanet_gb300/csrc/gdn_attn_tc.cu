@@ -82,6 +82,11 @@ __device__ __forceinline__ void bar_init(uint32_t bar, int count) {
 __device__ __forceinline__ void bar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// one arrival for the warp, behind all its lanes' work (32 arrivals on one word are 32 shared-memory atomics in a row)
+__device__ __forceinline__ void warp_arrive(uint32_t bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) bar_arrive(bar);
+}
 __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
@@ -335,14 +340,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(s_full(i), 1);
-      bar_init(p_ready(i, 0), 128);
-      bar_init(p_ready(i, 1), 128);
+      bar_init(p_ready(i, 0), 4);
+      bar_init(p_ready(i, 1), 4);
       bar_init(pv_done(i), 1);
-      bar_init(st_ready(i), 128 * S::kStreams);
+      bar_init(st_ready(i), 4 * S::kStreams);
       bar_init(o_full(i), 1);
-      bar_init(o_free(i), 128);
+      bar_init(o_free(i), 4);
     }
-    bar_init(q_full, 128);
+    bar_init(q_full, 4);
     bar_init(q_empty, 1);
     bar_init(drained, 2);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -394,7 +399,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                                         (int64_t)head * p.q_head + u * 8));
           }
           // the rows are on their way while the last tile's products with Q end
-          if (i0 == 0 && g > 0 && !bar_wait(q_empty, (g - 1) & 1, &gave_up)) return false;
+          if (i0 == 0 && g > 0 && !warp_wait(q_empty, (g - 1) & 1, &gave_up)) return false;
           auto store = [&](auto copies_c) {
             constexpr int kC = decltype(copies_c)::value;
 #pragma unroll
@@ -416,7 +421,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           else store(std::integral_constant<int, 4>());
         }
         fence_async();
-        bar_arrive(q_full);
+        warp_arrive(q_full);
         return true;
       };
       ok = stage_q(w, 0);
@@ -500,7 +505,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               columns(v, c);
               if (c == kD / 32 - 1) {  // O has been read: the next tile may have it
                 tc_fence_before();
-                bar_arrive(o_free(g));
+                warp_arrive(o_free(g));
               }
               if (c > 0) asm volatile("bar.sync 1, 128;" ::: "memory");  // the last columns have been read
 #pragma unroll
@@ -548,7 +553,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (!whole && row < rows && copy == 0) reinterpret_cast<float2*>(out + kTcRows * kD)[row] = make_float2(top, sum);
         if (copies == 1) {
           tc_fence_before();
-          bar_arrive(o_free(g));
+          warp_arrive(o_free(g));
         }
         w = next;
       }
@@ -607,12 +612,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           fence_async();
         }
-        bar_arrive(p_ready(it, stream));
+        warp_arrive(p_ready(it, stream));
       }
       if (ok && g >= 2) ok = warp_wait(o_free(g), ((g >> 1) - 1) & 1, &gave_up);  // tile g - 2 is done with its place in stats
       if (!ok) break;
       stats[g & 1][stream][s_tid] = make_float2(st.top, st.sum);
-      bar_arrive(st_ready(g));
+      warp_arrive(st_ready(g));
     }
   } else if (any && warp == 12) {
     // ---- S = Q K^T, issued by one thread

@@ -24,6 +24,25 @@ __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.lau
 constexpr int kMaxB = 4096;
 constexpr unsigned kFull = 0xffffffffu;
 
+// x / d for 0 <= x < 2^31 by a multiplication and a shift
+struct Div {
+  uint32_t mul, shift, d;
+};
+
+__device__ __forceinline__ uint32_t div(uint32_t x, const Div& k) {
+  return k.d == 1 ? x : __umulhi(x, k.mul) >> k.shift;
+}
+
+Div make_div(uint32_t d) {
+  Div k{0, 0, d};
+  if (d == 1) return k;
+  uint32_t l = 31 - __builtin_clz(d);
+  if ((d & (d - 1)) == 0) l -= 1;  // a power of two: the multiplier is 2^31
+  k.shift = l;
+  k.mul = (uint32_t)(((uint64_t(1) << (32 + l)) + d - 1) / d);
+  return k;
+}
+
 // the sums a request's place in the three lists comes from; 64 bits, as the
 // demand of requests that are not served counts too
 struct Sums {
@@ -82,7 +101,7 @@ __device__ __forceinline__ int find(const int* prefix, int B, int i) {
 
 // kPerThread requests a thread: one where they are few, as then the call is as long as its chain of reads and barriers
 template <int kThreads, int kPerThread>
-__global__ void __launch_bounds__(kThreads) page_map_kernel(const gdn_page_map_args p) {
+__global__ void __launch_bounds__(kThreads) page_map_kernel(const gdn_page_map_args p, const Div page_div) {
   extern __shared__ int sm[];
   __shared__ Sums part[kThreads / 32];
   int* const take_at = sm;                    // [B+1] prefix of pages taken
@@ -109,7 +128,7 @@ __global__ void __launch_bounds__(kThreads) page_map_kernel(const gdn_page_map_a
     n[i] = p.n_rows[b];
     held[i] = p.held_in[b];
     const long long tokens = (long long)ctx[i] + n[i];
-    const long long want = (tokens + P - 1) / P;
+    const long long up = tokens + P - 1, want = up >> 31 ? up / P : div((uint32_t)up, page_div);  // a negative one is refused
     int why = 0;
     if (ctx[i] < 0) why |= GDN_STATUS_BAD_LENGTH;
     if (n[i] < 0 || (p.R > 0 && n[i] > p.R)) why |= GDN_STATUS_BAD_NROWS;
@@ -182,16 +201,21 @@ __global__ void __launch_bounds__(kThreads) page_map_kernel(const gdn_page_map_a
   if (blockIdx.x == 0 && status && p.status) atomicOr(p.status, status);
   __syncthreads();
 
+  // a position of the ring, less than twice round in a state that adds up
+  auto wrap = [&](long long x) {
+    if (x >= N) x -= N;
+    return (int)(x < N ? x : x % N);
+  };
   const int first = blockIdx.x * kThreads + threadIdx.x, step = gridDim.x * kThreads;
   for (int i = first; i < given.take; i += step) {
     const int b = find(take_at, B, i);
-    p.block_table[(size_t)b * p.table_stride + held_s[b] + i - take_at[b]] = p.free_ring[(head + (long long)i) % N];
+    p.block_table[(size_t)b * p.table_stride + held_s[b] + i - take_at[b]] = p.free_ring[wrap((long long)head + i)];
   }
   // the ring's free part ends where the returned pages go: the two ranges are disjoint
   for (int i = first; i < given.back; i += step) {
     const int b = find(back_at, B, i);
     const int left = held_s[b] - (back_at[b + 1] - back_at[b]);  // pages kept
-    p.free_ring[(head + (long long)n_free + i) % N] = p.block_table[(size_t)b * p.table_stride + left + i - back_at[b]];
+    p.free_ring[wrap((long long)head + n_free + i)] = p.block_table[(size_t)b * p.table_stride + left + i - back_at[b]];
   }
   if (!p.slot_map && !p.positions) return;
   for (int r = first; r < p.n_slot_rows; r += step) {
@@ -201,9 +225,9 @@ __global__ void __launch_bounds__(kThreads) page_map_kernel(const gdn_page_map_a
       const int t = r - row_at[b];
       if (t < rows_s[b]) {
         pos = ctx_s[b] + t;
-        const int i = pos / P;
+        const int i = (int)div(pos, page_div);
         const int page = i < held_s[b] ? p.block_table[(size_t)b * p.table_stride + i]
-                                       : p.free_ring[(head + (long long)take_at[b] + i - held_s[b]) % N];
+                                       : p.free_ring[wrap((long long)head + take_at[b] + i - held_s[b])];
         if ((unsigned)page < (unsigned)N) slot = page * P + pos - i * P;
         else if (p.status) atomicOr(p.status, GDN_STATUS_BAD_PAGE);
       }
@@ -211,25 +235,6 @@ __global__ void __launch_bounds__(kThreads) page_map_kernel(const gdn_page_map_a
     if (p.slot_map) p.slot_map[r] = slot;
     if (p.positions) p.positions[r] = pos;
   }
-}
-
-// x / d for 0 <= x < 2^31 by a multiplication and a shift
-struct Div {
-  uint32_t mul, shift, d;
-};
-
-__device__ __forceinline__ uint32_t div(uint32_t x, const Div& k) {
-  return k.d == 1 ? x : __umulhi(x, k.mul) >> k.shift;
-}
-
-Div make_div(uint32_t d) {
-  Div k{0, 0, d};
-  if (d == 1) return k;
-  uint32_t l = 31 - __builtin_clz(d);
-  if ((d & (d - 1)) == 0) l -= 1;  // a power of two: the multiplier is 2^31
-  k.shift = l;
-  k.mul = (uint32_t)(((uint64_t(1) << (32 + l)) + d - 1) / d);
-  return k;
 }
 
 struct AppendParams {
@@ -280,8 +285,8 @@ __global__ void __launch_bounds__(kCopyThreads) append_kernel(const AppendParams
     if (to[u] >= 0) dst[to[u]] = val[u];
 }
 
-template <typename Kernel, typename P>
-int launch(Kernel kernel, dim3 grid, dim3 block, size_t smem, cudaStream_t st, const P& p) {
+template <typename Kernel, typename... Args>
+int launch(Kernel kernel, dim3 grid, dim3 block, size_t smem, cudaStream_t st, const Args&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
@@ -292,7 +297,7 @@ int launch(Kernel kernel, dim3 grid, dim3 block, size_t smem, cudaStream_t st, c
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kernel, p) != cudaSuccess) return GDN_ERR_LAUNCH;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) return GDN_ERR_LAUNCH;
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_LAUNCH;
 }
 
@@ -367,7 +372,7 @@ extern "C" GDN_API int gdn_page_map(const gdn_page_map_args* args, void* stream)
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (6 * kMaxB + 3) * sizeof(int)) != cudaSuccess)
       return (int)GDN_ERR_LAUNCH;
     const int blocks = min(max((p.n_slot_rows + threads - 1) / threads, 1), 152);
-    return launch(kernel, dim3(blocks), dim3(threads), smem, st, p);
+    return launch(kernel, dim3(blocks), dim3(threads), smem, st, p, make_div((uint32_t)p.page_size));
   };
   return p.B <= 128 ? run(page_map_kernel<128, 1>, 128) : p.B <= 512 ? run(page_map_kernel<512, 1>, 512) : run(page_map_kernel<512, 8>, 512);
 }

@@ -23,7 +23,8 @@
 //     summed in index order and the draw located.
 //   A row of some 10^5 tokens is bound by instructions (a pass with exp costs
 //   several times the HBM read) and by the cluster's barriers, not by HBM.
-// accept_kernel: one thread per request.
+// accept_kernel: one warp per request; where there are no drafts (R = 1) the rows'
+//   blocks write the accept lengths, 0, themselves.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -345,6 +346,10 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const gdn_sample_args 
   pdl_wait();
   pdl_trigger();
   const int n = p.n_rows[b];
+  if (p.R == 1 && p.accept_len && rank == 0 && tid == 0) {
+    p.accept_len[b] = 0;
+    if ((n < 0 || n > 1) && p.status) atomicOr(p.status, GDN_STATUS_BAD_NROWS);
+  }
   if (n <= 0 || n > p.R || t >= n) return;  // the whole cluster
   cluster_arrive();  // every block of the cluster runs before any writes to another's shared memory
   const size_t at = (size_t)b * p.R + t;
@@ -708,22 +713,28 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const gdn_sample_args 
   }
 }
 
-// as gdn_greedy_accept's: the leading drafts equal to the target's tokens
+// as gdn_greedy_accept's: the leading drafts equal to the target's tokens.  A warp per request: every draft is compared at
+// once, where a loop that stops at the first difference would wait for a read of each.
 __global__ void __launch_bounds__(256) accept_kernel(const gdn_sample_args p) {
   pdl_wait();
   pdl_trigger();
-  const int b = blockIdx.x * blockDim.x + threadIdx.x;
+  const int b = (blockIdx.x * blockDim.x + threadIdx.x) >> 5, lane = threadIdx.x & 31;
   if (b >= p.B) return;
+  const int32_t* d = p.drafts + (size_t)b * (p.R - 1);
+  const int32_t* tg = p.target + (size_t)b * p.R;
   const int n = p.n_rows[b];
   int a = 0;
   if (n < 0 || n > p.R) {
-    if (p.status) atomicOr(p.status, GDN_STATUS_BAD_NROWS);
+    if (p.status && lane == 0) atomicOr(p.status, GDN_STATUS_BAD_NROWS);
   } else {
-    const int32_t* d = p.drafts + (size_t)b * (p.R - 1);
-    const int32_t* tg = p.target + (size_t)b * p.R;
-    while (a < n - 1 && d[a] == tg[a]) ++a;
+    for (int i0 = 0; i0 < n - 1; i0 += 32) {
+      const int i = i0 + lane;
+      const unsigned differ = __ballot_sync(kFull, i >= n - 1 || d[i] != tg[i]);
+      a += differ ? __ffs(differ) - 1 : 32;
+      if (differ) break;
+    }
   }
-  p.accept_len[b] = a;
+  if (lane == 0) p.accept_len[b] = a;
 }
 
 template <typename Kernel, typename... Args>
@@ -797,6 +808,6 @@ extern "C" GDN_API int gdn_sample_accept(const gdn_sample_args* args, void* stre
   const gdn_sample_args p = *args;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int r = p.in_dtype == GDN_DTYPE_BF16 ? run<__nv_bfloat16>(p, st) : run<float>(p, st);
-  if (r != GDN_OK || !p.accept_len) return r;
-  return launch(accept_kernel, dim3((p.B + 255) / 256), dim3(256), 1, 0, st, p);
+  if (r != GDN_OK || !p.accept_len || p.R == 1) return r;
+  return launch(accept_kernel, dim3((p.B + 7) / 8), dim3(256), 1, 0, st, p);
 }

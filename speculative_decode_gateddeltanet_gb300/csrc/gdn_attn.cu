@@ -2,13 +2,17 @@
 // launch, and the 32-bit kernel, on the CUDA cores.
 //
 // simt_kernel: one pass over K and V with the running maximum and sum of the
-//   softmax, 32-bit arithmetic throughout.  A block of four warps holds 32 rows
-//   (token, query head) of one kv head and walks blocks of 32 keys staged in
-//   shared memory.  Scores: a lane is a key, a warp's eight rows in registers;
-//   the row of K it reads is padded by four words so that the 16-byte reads of
-//   a quarter warp fall into different banks, q is broadcast.  Output: a lane
-//   owns d/32 columns of the eight rows.  Bound by the 32-bit multiply-add rate
-//   when a kv head has many rows, by HBM when it has few.
+//   softmax, 32-bit arithmetic throughout.  A block of four warps holds up to 32
+//   rows (token, query head) of one kv head and walks blocks of 32 keys staged in
+//   shared memory.  Scores: a lane is a key, a warp's rows (every fourth) in
+//   registers; the row of K it reads is padded by four words so that the 16-byte
+//   reads of a quarter warp fall into different banks, q is broadcast.  Output: a
+//   lane owns d/32 columns of the warp's rows.  A warp computes 1, 2, 4 or 8 rows,
+//   as few as the tile needs.  With many rows it is bound by shared-memory reads
+//   and the 32-bit multiply-add rate, with few by the latency of a key block's
+//   copy, of which an SM has three under way.
+#include <type_traits>
+
 #include "attn_common.cuh"
 #include "attn_tc.h"
 
@@ -26,7 +30,7 @@ constexpr int simt_smem() {
 
 template <int kD>
 __global__ void __launch_bounds__(kSimtThreads, kD == 256 ? 2 : 3) simt_kernel(const Params p) {
-  constexpr int kR = kSimtRows, kN = kSimtKeys, kWarpRows = kR / 4, kCols = kD / 32, kChunks = kD / 4;
+  constexpr int kR = kSimtRows, kN = kSimtKeys, kCols = kD / 32, kChunks = kD / 4;
   extern __shared__ float4 smem4[];
   float* const qs = reinterpret_cast<float*>(smem4);  // [kR][kD]
   float* const ks = qs + kR * kD;                     // [kN][kD + 4]
@@ -42,11 +46,10 @@ __global__ void __launch_bounds__(kSimtThreads, kD == 256 ? 2 : 3) simt_kernel(c
   const Start s = start;
   int4 note = {0, 0, 0, 0};
   Walk<kR, kN> w;
-  if (begin(w, p, s)) {
-    for (; !w.done(); w.next()) {
-      const int rows = (int)min((long long)kR, (long long)w.req.n * p.G - (long long)w.m * kR);
+  auto segment = [&](auto warp_rows, int rows) {
+      constexpr int kWarpRows = decltype(warp_rows)::value;
       __syncthreads();
-      for (int i = tid; i < kR * kChunks; i += kSimtThreads) {
+      for (int i = tid; i < 4 * kWarpRows * kChunks; i += kSimtThreads) {
         const int r = i / kChunks, c = i % kChunks, at = w.m * kR + r;
         float4 x = {0.f, 0.f, 0.f, 0.f};
         if (r < rows)
@@ -59,7 +62,7 @@ __global__ void __launch_bounds__(kSimtThreads, kD == 256 ? 2 : 3) simt_kernel(c
       for (int r = 0; r < kWarpRows; ++r) {
         top[r] = -INFINITY;
         sum[r] = 0.f;
-        last[r] = w.req.ctx + (w.m * kR + warp * kWarpRows + r) / p.G;
+        last[r] = w.req.ctx + (int)quotient(w.m * kR + r * 4 + warp, p.by_G);
 #pragma unroll
         for (int c = 0; c < kCols; ++c) acc[r][c] = 0.f;
       }
@@ -99,7 +102,7 @@ __global__ void __launch_bounds__(kSimtThreads, kD == 256 ? 2 : 3) simt_kernel(c
           const float4 kx = *reinterpret_cast<const float4*>(ks + lane * (kD + 4) + 4 * c);
 #pragma unroll
           for (int r = 0; r < kWarpRows; ++r) {
-            const float4 qx = *reinterpret_cast<const float4*>(qs + (warp * kWarpRows + r) * kD + 4 * c);
+            const float4 qx = *reinterpret_cast<const float4*>(qs + (r * 4 + warp) * kD + 4 * c);
             sc[r] = fmaf(qx.x, kx.x, sc[r]);
             sc[r] = fmaf(qx.y, kx.y, sc[r]);
             sc[r] = fmaf(qx.z, kx.z, sc[r]);
@@ -120,7 +123,7 @@ __global__ void __launch_bounds__(kSimtThreads, kD == 256 ? 2 : 3) simt_kernel(c
           sum[r] = sum[r] * shrink + e;  // this lane's share
 #pragma unroll
           for (int c = 0; c < kCols; ++c) acc[r][c] *= shrink;
-          ps[(warp * kWarpRows + r) * kN + lane] = e;
+          ps[(r * 4 + warp) * kN + lane] = e;
         }
         __syncwarp();
 #pragma unroll 2
@@ -136,7 +139,7 @@ __global__ void __launch_bounds__(kSimtThreads, kD == 256 ? 2 : 3) simt_kernel(c
             }
 #pragma unroll
           for (int r = 0; r < kWarpRows; ++r) {
-            const float4 e = *reinterpret_cast<const float4*>(ps + (warp * kWarpRows + r) * kN + j4);
+            const float4 e = *reinterpret_cast<const float4*>(ps + (r * 4 + warp) * kN + j4);
             const float es[4] = {e.x, e.y, e.z, e.w};
 #pragma unroll
             for (int u = 0; u < 4; ++u)
@@ -155,7 +158,7 @@ __global__ void __launch_bounds__(kSimtThreads, kD == 256 ? 2 : 3) simt_kernel(c
         float l = sum[r];
 #pragma unroll
         for (int off = 16; off >= 1; off >>= 1) l += __shfl_xor_sync(kFull, l, off);
-        const int row = warp * kWarpRows + r, at = w.m * kR + row;
+        const int row = r * 4 + warp, at = w.m * kR + row;
         if (row >= rows) continue;
         if (whole) {
           const float inv = 1.f / l;
@@ -173,6 +176,14 @@ __global__ void __launch_bounds__(kSimtThreads, kD == 256 ? 2 : 3) simt_kernel(c
           if (lane == 0) reinterpret_cast<float2*>(out + kR * kD)[row] = make_float2(top[r], l);
         }
       }
+  };
+  if (begin(w, p, s)) {
+    for (; !w.done(); w.next()) {
+      const int rows = (int)min((long long)kR, (long long)w.req.n * p.G - (long long)w.m * kR);
+      if (rows <= 4) segment(std::integral_constant<int, 1>(), rows);
+      else if (rows <= 8) segment(std::integral_constant<int, 2>(), rows);
+      else if (rows <= 16) segment(std::integral_constant<int, 4>(), rows);
+      else segment(std::integral_constant<int, 8>(), rows);
     }
   }
   if (tid == 0) p.notes[blockIdx.x] = note;

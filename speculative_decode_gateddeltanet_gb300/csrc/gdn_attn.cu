@@ -23,6 +23,11 @@ constexpr int kSimtMinUnits = 1;
 
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 
+// 16 bytes into shared memory, or zeros
+__device__ __forceinline__ void copy16(float* to, const float* from, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from), "r"(valid ? 16 : 0) : "memory");
+}
+
 template <int kD>
 constexpr int simt_smem() {
   return (kSimtRows * kD + kSimtKeys * (kD + 4) + kSimtKeys * kD + kSimtRows * kSimtKeys) * (int)sizeof(float);
@@ -66,35 +71,35 @@ __global__ void __launch_bounds__(kSimtThreads, kD == 256 ? 2 : 3) simt_kernel(c
 #pragma unroll
         for (int c = 0; c < kCols; ++c) acc[r][c] = 0.f;
       }
+      // a key's place in the caches, found a block ahead by the first kN threads
       const int len = w.req.ctx + w.req.n;
-      for (int kb = w.kb0; kb < w.kb1; ++kb) {
-        __syncthreads();
-        if (tid < kN) {
-          const int j = kb * kN + tid;
-          k_at[tid] = v_at[tid] = -1;
-          if (j < len) {
-            const int i = j / p.page_size, token = j - i * p.page_size;
-            const int page = p.table[(size_t)w.b * p.table_stride + i];
-            if ((unsigned)page < (unsigned)p.n_pages) {
-              k_at[tid] = page * p.k_page + w.h * p.k_head + token * p.k_token;
-              v_at[tid] = page * p.v_page + w.h * p.v_head + token * p.v_token;
-            } else if (p.status) {
-              atomicOr(p.status, GDN_STATUS_BAD_PAGE);
-            }
-          }
-        }
-        __syncthreads();
+      const int32_t* const pages = p.table + (size_t)w.b * p.table_stride;
+      auto page_of = [&](int j) { return j < len ? pages[quotient(j, p.by_page)] : -1; };
+      auto place = [&](int j, int page) {
+        const bool good = (unsigned)page < (unsigned)p.n_pages;
+        const int token = j - (int)quotient(j, p.by_page) * p.page_size;
+        k_at[tid] = good ? page * p.k_page + w.h * p.k_head + token * p.k_token : -1;
+        v_at[tid] = good ? page * p.v_page + w.h * p.v_head + token * p.v_token : -1;
+        if (!good && j < len && p.status) atomicOr(p.status, GDN_STATUS_BAD_PAGE);
+      };
+      auto fetch = [&](float* to, int stride, const void* from, const int64_t* at) {
 #pragma unroll 4
         for (int i = tid; i < kN * kChunks; i += kSimtThreads) {
           const int j = i / kChunks, c = i % kChunks;
-          float4 kx = {0.f, 0.f, 0.f, 0.f}, vx = kx;
-          if (k_at[j] >= 0) {
-            kx = load4(static_cast<const float*>(p.k) + k_at[j] + 4 * c);
-            vx = load4(static_cast<const float*>(p.v) + v_at[j] + 4 * c);
-          }
-          *reinterpret_cast<float4*>(ks + j * (kD + 4) + 4 * c) = kx;
-          *reinterpret_cast<float4*>(vs + j * kD + 4 * c) = vx;
+          const int64_t off = at[j];
+          copy16(to + j * stride + 4 * c, static_cast<const float*>(from) + (off >= 0 ? off + 4 * c : 0), off >= 0);
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      };
+      if (tid < kN) place(w.kb0 * kN + tid, page_of(w.kb0 * kN + tid));
+      __syncthreads();
+      fetch(ks, kD + 4, p.k, k_at);
+      fetch(vs, kD, p.v, v_at);
+      for (int kb = w.kb0; kb < w.kb1; ++kb) {
+        const bool more = kb + 1 < w.kb1;
+        const int ahead = (kb + 1) * kN + tid;
+        const int page = more && tid < kN ? page_of(ahead) : -1;
+        asm volatile("cp.async.wait_group 1;" ::: "memory");  // K; V may still be on its way
         __syncthreads();
         float sc[kWarpRows] = {};
 #pragma unroll 4
@@ -125,7 +130,12 @@ __global__ void __launch_bounds__(kSimtThreads, kD == 256 ? 2 : 3) simt_kernel(c
           for (int c = 0; c < kCols; ++c) acc[r][c] *= shrink;
           ps[(r * 4 + warp) * kN + lane] = e;
         }
-        __syncwarp();
+        if (more && tid < kN) place(ahead, page);
+        __syncthreads();
+        if (more) fetch(ks, kD + 4, p.k, k_at);
+        else asm volatile("cp.async.commit_group;" ::: "memory");
+        asm volatile("cp.async.wait_group 1;" ::: "memory");  // V
+        __syncthreads();
 #pragma unroll 2
         for (int j4 = 0; j4 < kN; j4 += 4) {
           float vx[4][kCols];
@@ -147,7 +157,8 @@ __global__ void __launch_bounds__(kSimtThreads, kD == 256 ? 2 : 3) simt_kernel(c
               for (int c = 0; c < kCols; ++c) acc[r][c] = fmaf(es[u], vx[u][c], acc[r][c]);
           }
         }
-        __syncwarp();
+        __syncthreads();
+        if (more) fetch(vs, kD, p.v, v_at);
       }
       const bool whole = w.kb0 == 0 && w.kb1 == w.blocks;
       const int slot = w.kb0 == 0 ? 1 : 0;

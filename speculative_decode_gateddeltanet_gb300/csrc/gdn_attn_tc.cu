@@ -20,12 +20,8 @@
 // leave the tensor cores idle at each of its waits), warps 13 and 14 the TMA copies
 // of K and of V.
 //
-// Few rows.  A TMEM lane belongs to one warp, so 32 rows would leave three of
-// the four softmax warps idle, and one warp's 128 exponentials a row take longer
-// than the block's K and V take to arrive.  A tile of at most 64 (32) rows is
-// therefore staged twice (four times) over: each copy keeps the softmax of its
-// half (quarter) of a block's keys, its P is zero for the others, and the copies
-// are joined once per tile.  The MMA's 128 rows are paid for anyway.
+// Few rows.  A tile with few rows leaves softmax warps without one; those only keep
+// step.  The MMA's 128 rows are paid for anyway.
 //
 // A page is copied in boxes of 64 columns by a power of two of tokens that
 // divides the page, straight into the 128-byte-swizzled layout the MMA reads;
@@ -67,8 +63,7 @@ struct Shape {
   static constexpr int kK = kD == 64 ? 6 : kD == 128 ? 3 : 2;  // K tiles in flight
   static constexpr int kV = kD == 64 ? 5 : 2;
   static constexpr int kStreams = kD == 256 ? 1 : 2;      // TMEM: two S buffers and an O for each stream, of 512 columns
-  static constexpr int kJoinBytes = 128 * 32 * 4;         // 32 columns of every copy's rows
-  static constexpr int kSmem = 1024 + kQBytes + (kK + kV) * kTileBytes + kJoinBytes;
+  static constexpr int kSmem = 1024 + kQBytes + (kK + kV) * kTileBytes;
 };
 static_assert(Shape<128>::kSmem <= 230 * 1024 && Shape<256>::kSmem <= 230 * 1024 && Shape<64>::kSmem <= 230 * 1024);
 
@@ -218,24 +213,21 @@ __host__ __device__ constexpr uint32_t instruction(int n, bool transpose_b) {
   return 1u << 4 | 1u << 7 | 1u << 10 | (transpose_b ? 1u << 16 : 0) | (uint32_t)(n >> 3) << 17 | (uint32_t)(kTcRows >> 4) << 24;
 }
 
-__device__ __forceinline__ int copies_of(int rows) { return rows <= 32 ? 4 : rows <= 64 ? 2 : 1; }
-
 // a row's running softmax
 struct RowState {
   float top, sum;
 };
 
-// One key block for this thread's row and the kKeys / kCopies columns of its
-// copy: s_at is S in TMEM (this warp's lanes), edge the last column the row sees.
-// rescale(shrink) multiplies the row's O; it is called for whole warps.
-template <int kKeys, int kCopies, typename Rescale>
-__device__ __forceinline__ bool softmax_block(RowState& st, uint32_t s_at, int copy, int edge, float scale_log2, Rescale rescale) {
-  constexpr int kC = kKeys / kCopies, kPart = kC < 32 ? kC : 32;  // columns, and of one TMEM load
+// One key block for this thread's row and its stream's kC columns: s_at is S in
+// TMEM (this warp's lanes), edge the last column the row sees.  rescale(shrink)
+// multiplies the row's O; it is called for whole warps.
+template <int kC, typename Rescale>
+__device__ __forceinline__ bool softmax_block(RowState& st, uint32_t s_at, int edge, float scale_log2, Rescale rescale) {
+  constexpr int kPart = 32;  // columns of one TMEM load
   uint32_t x[kC / kPart][kPart];
 #pragma unroll
-  for (int c = 0; c < kC / kPart; ++c) tmem_load(x[c], s_at + copy * kC + c * kPart);
+  for (int c = 0; c < kC / kPart; ++c) tmem_load(x[c], s_at + c * kPart);
   tmem_wait_load();
-  edge -= copy * kC;
   if (edge < kC - 1) {
 #pragma unroll
     for (int c = 0; c < kC / kPart; ++c)
@@ -258,7 +250,7 @@ __device__ __forceinline__ bool softmax_block(RowState& st, uint32_t s_at, int c
   }
   const float sub = st.top == -INFINITY ? 0.f : st.top;
   float s4[4] = {0.f, 0.f, 0.f, 0.f};
-  constexpr int kW = kC / 2 < 16 ? kC / 2 : 16;  // words of one TMEM store
+  constexpr int kW = 16;  // words of one TMEM store
 #pragma unroll
   for (int c = 0; c < kC / 2; c += kW) {
     uint32_t pk[kW];
@@ -271,14 +263,7 @@ __device__ __forceinline__ bool softmax_block(RowState& st, uint32_t s_at, int c
       s4[(j + 1) & 3] += e1;
       pk[i] = pack_bf16(e0, e1);
     }
-    tmem_store(s_at + copy * (kC / 2) + c, pk);  // over columns that were read
-  }
-  if constexpr (kCopies > 1) {
-    // the other copies' keys: weight 0.  (S of those columns belongs to this warp's lanes alone: no one waits for it.)
-    constexpr uint32_t zero[kW] = {};
-#pragma unroll
-    for (int c = 0; c < kKeys / 2; c += kW)
-      if (c / (kC / 2) != copy) tmem_store(s_at + c, zero);
+    tmem_store(s_at + c, pk);  // over columns that were read
   }
   st.sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
   tmem_wait_store();
@@ -309,10 +294,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __shared__ Start start;
   __shared__ uint32_t tmem_base;
   __shared__ int gave_up;
-  __shared__ float2 stats[2][2][128];  // maxima and sums of a tile's rows (and copies), by tile and stream
+  __shared__ float2 stats[2][2][128];  // maxima and sums of a tile's rows, by tile and stream
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
-  const uint32_t q_s = base, k_s = q_s + S::kQBytes, v_s = k_s + S::kK * S::kTileBytes, join_s = v_s + S::kV * S::kTileBytes;
+  const uint32_t q_s = base, k_s = q_s + S::kQBytes, v_s = k_s + S::kK * S::kTileBytes;
   // A wait names a phase by its parity, so a barrier may be at most one phase ahead of any of its waiters, and each
   // waiter takes every phase in turn; what may be signalled twice before it is waited for has two barriers.
   const uint32_t b0 = smem_addr(bars);
@@ -385,9 +370,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int e_tid = tid - 256, quarter = warp - 8;
       const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
       constexpr int kUnits = kD / 8;  // 16-byte units of a row
-      constexpr int kBatch = 16;      // units a thread holds: 128 rows of 128 columns at once
+      constexpr int kBatch = 8;       // units a thread has under way
       auto stage_q = [&](const Walk<kTcRows, kKeys>& t, int g) {
-        const int rows = rows_of(t), copies = copies_of(rows);
+        const int rows = rows_of(t);
         for (int i0 = 0; i0 < rows * kUnits; i0 += kBatch * 128) {
           uint4 x[kBatch];
 #pragma unroll
@@ -400,25 +385,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           // the rows are on their way while the last tile's products with Q end
           if (i0 == 0 && g > 0 && !warp_wait(q_empty, (g - 1) & 1, &gave_up)) return false;
-          auto store = [&](auto copies_c) {
-            constexpr int kC = decltype(copies_c)::value;
 #pragma unroll
-            for (int j = 0; j < kBatch; ++j) {
-              const int i = i0 + j * 128 + e_tid;
-              if (i < rows * kUnits) {
-                const int r = i / kUnits, u = i % kUnits;
-                const uint32_t to = q_s + (u / 8) * (kTcRows * 128) + r * 128 + (((u & 7) ^ (r & 7)) << 4);
-#pragma unroll
-                for (int c = 0; c < kC; ++c)
-                  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + c * (kTcRows / kC) * 128), "r"(x[j].x ^ q_flip),
-                               "r"(x[j].y ^ q_flip), "r"(x[j].z ^ q_flip), "r"(x[j].w ^ q_flip)
-                               : "memory");
-              }
+          for (int j = 0; j < kBatch; ++j) {
+            const int i = i0 + j * 128 + e_tid;
+            if (i < rows * kUnits) {
+              const int r = i / kUnits, u = i % kUnits;
+              const uint32_t to = q_s + (u / 8) * (kTcRows * 128) + r * 128 + (((u & 7) ^ (r & 7)) << 4);
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(x[j].x ^ q_flip), "r"(x[j].y ^ q_flip),
+                           "r"(x[j].z ^ q_flip), "r"(x[j].w ^ q_flip)
+                           : "memory");
             }
-          };
-          if (copies == 1) store(std::integral_constant<int, 1>());
-          else if (copies == 2) store(std::integral_constant<int, 2>());
-          else store(std::integral_constant<int, 4>());
+          }
         }
         fence_async();
         warp_arrive(q_full);
@@ -429,8 +406,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         Walk<kTcRows, kKeys> next = w;
         next.next();
         if (!next.done() && !(ok = stage_q(next, g + 1))) break;
-        const int rows = rows_of(w), copies = copies_of(rows), spread = 4 / copies;
-        const int copy = quarter / spread, row = (quarter % spread) * 32 + lane;
+        const int rows = rows_of(w), row = e_tid;
         const bool whole = w.kb0 == 0 && w.kb1 == w.blocks;
         const int slot = w.kb0 == 0 ? 1 : 0;
         if (!whole && slot == 1) note = note_of(w, s);
@@ -444,130 +420,63 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tc_fence_after();
         // the second stream has no O where the tile's only block ends before its keys
         const int n_parts = S::kStreams == 1 || (w.kb1 - w.kb0 == 1 && w.req.ctx + w.req.n - w.kb0 * kKeys <= kCols) ? 1 : 2;
-        auto st = [&](int part, int lane_row) { return stats[g & 1][part][lane_row]; };
-        float shares[2];  // 2^(own maximum - common maximum) of this lane's O's
-        // 32 columns of this lane's row, the streams added up
-        auto columns = [&](float (&v)[32], int c) {
-          uint32_t o[32];
-          tmem_load(o, lanes + kOCol + c * 32);
-          tmem_wait_load();
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(o[i]) * shares[0];
-          if (n_parts == 2) {
-            tmem_load(o, lanes + kOCol + kD + c * 32);
+        if (quarter * 32 < rows) {
+          const float2 st0 = stats[g & 1][0][row], st1 = n_parts == 2 ? stats[g & 1][1][row] : make_float2(-INFINITY, 0.f);
+          const float top = fmaxf(st0.x, st1.x), sub = top == -INFINITY ? 0.f : top;
+          float share0 = ex2(st0.x - sub), share1 = ex2(st1.x - sub);  // 2^(own maximum - common maximum)
+          const float sum = st0.y * share0 + st1.y * share1;
+          if (!whole && row < rows) reinterpret_cast<float2*>(out + kTcRows * kD)[row] = make_float2(top, sum);
+          if (whole) {
+            share0 /= sum;
+            share1 /= sum;
+          }
+          // 32 columns of this lane's row, the streams added up
+          auto columns = [&](float (&v)[32], int c) {
+            uint32_t o0[32], o1[32];
+            tmem_load(o0, lanes + kOCol + c * 32);
+            if (n_parts == 2) tmem_load(o1, lanes + kOCol + kD + c * 32);
             tmem_wait_load();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = fmaf(__uint_as_float(o[i]), shares[1], v[i]);
-          }
-        };
-        const int span = 128 / copies;
-        float top = -INFINITY, sum = 0.f;
-        for (int c = 0; c < copies; ++c)
-          for (int j = 0; j < n_parts; ++j) top = fmaxf(top, st(j, c * span + row).x);
-        const float sub = top == -INFINITY ? 0.f : top;
-        for (int c = 0; c < copies; ++c)
-          for (int j = 0; j < n_parts; ++j) sum += st(j, c * span + row).y * ex2(st(j, c * span + row).x - sub);
-        const float norm = whole ? 1.f / sum : 1.f;
-        shares[0] = ex2(st(0, e_tid).x - sub) * norm;
-        shares[1] = n_parts == 2 ? ex2(st(1, e_tid).x - sub) * norm : 0.f;
-        if (copies == 1) {
-          if (quarter * 32 < rows) {
-#pragma unroll 1
-            for (int c = 0; c < kD / 32; ++c) {
-              float v[32];
-              columns(v, c);
-              if (row < rows) {
-                if (whole) {
-                  uint32_t pk[16];
+            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(o0[i]) * share0;
+            if (n_parts == 2) {
 #pragma unroll
-                  for (int i = 0; i < 16; ++i) pk[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-#pragma unroll
-                  for (int i = 0; i < 4; ++i)
-                    reinterpret_cast<uint4*>(dst + c * 32)[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
-                } else {
-#pragma unroll
-                  for (int i = 0; i < 8; ++i)
-                    reinterpret_cast<float4*>(out + row * kD + c * 32)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-                }
-              }
+              for (int i = 0; i < 32; ++i) v[i] = fmaf(__uint_as_float(o1[i]), share1, v[i]);
             }
-          }
-        } else {
-          // Join the copies, 32 columns at a time: each warp brings its rows scaled to the common maximum, then the 128
-          // threads sum the rows' 16-byte units over the copies, eight neighbours a row.
-          auto join = [&](auto copies_c) {
-            constexpr int kC = decltype(copies_c)::value, kSpan = 128 / kC;
-            const int unit = e_tid & 7;
-            const int64_t out_base = (int64_t)w.req.row0 * p.o_row + (int64_t)w.h * p.G * p.o_head;
-#pragma unroll 1
-            for (int c = 0; c < kD / 32; ++c) {
-              float v[32];
-              columns(v, c);
-              if (c == kD / 32 - 1) {  // O has been read: the next tile may have it
-                tc_fence_before();
-                warp_arrive(o_free(g));
-              }
-              if (c > 0) asm volatile("bar.sync 1, 128;" ::: "memory");  // the last columns have been read
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const uint32_t to = join_s + e_tid * 128 + ((i ^ (lane & 7)) << 4);
-                asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(v[4 * i]), "f"(v[4 * i + 1]), "f"(v[4 * i + 2]),
-                             "f"(v[4 * i + 3])
-                             : "memory");
-              }
-              asm volatile("bar.sync 1, 128;" ::: "memory");
-#pragma unroll
-              for (int r0 = 0; r0 < kSpan; r0 += 16) {
-                const int r = r0 + (e_tid >> 3);
-                if (r < rows) {
-                  float4 a = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                  for (int j = 0; j < kC; ++j) {
-                    float4 x;
-                    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                                 : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
-                                 : "r"(join_s + (j * kSpan + r) * 128 + ((unit ^ (r & 7)) << 4))
-                                 : "memory");
-                    a.x += x.x;
-                    a.y += x.y;
-                    a.z += x.z;
-                    a.w += x.w;
-                  }
-                  const int col = c * 32 + unit * 4;
-                  if (whole) {
-                    const int row_at = w.m * kTcRows + r, tok = (int)quotient(row_at, p.by_G);
-                    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + out_base + (int64_t)tok * p.o_row +
-                                              (int64_t)(row_at - tok * p.G) * p.o_head + col) =
-                        make_uint2(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w));
-                  } else {
-                    *reinterpret_cast<float4*>(out + r * kD + col) = a;
-                  }
-                }
-              }
-            }
-            asm volatile("bar.sync 1, 128;" ::: "memory");  // the last columns have been read
           };
-          if (copies == 4) join(std::integral_constant<int, 4>());
-          else join(std::integral_constant<int, 2>());
+#pragma unroll 1
+          for (int c = 0; c < kD / 32; ++c) {
+            float v[32];
+            columns(v, c);
+            if (row < rows) {
+              if (whole) {
+                uint32_t pk[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) pk[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  reinterpret_cast<uint4*>(dst + c * 32)[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  reinterpret_cast<float4*>(out + row * kD + c * 32)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+              }
+            }
+          }
         }
-        if (!whole && row < rows && copy == 0) reinterpret_cast<float2*>(out + kTcRows * kD)[row] = make_float2(top, sum);
-        if (copies == 1) {
-          tc_fence_before();
-          warp_arrive(o_free(g));
-        }
+        tc_fence_before();
+        warp_arrive(o_free(g));
         w = next;
       }
     }
     if (tid == 256) p.notes[blockIdx.x] = note;
   } else if (any && warp < 4 * S::kStreams) {
-    // ---- softmax: one thread per row (and copy) of the stream's keys
+    // ---- softmax: one thread per row, the stream's keys
     const int stream = warp >> 2, quarter = warp & 3, s_tid = tid & 127;
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
     int it = 0, g = 0;
     for (; ok && !w.done(); w.next(), ++g) {
-      const int rows = rows_of(w), copies = copies_of(rows), spread = 4 / copies;  // warps of one copy
-      const int copy = quarter / spread, row = (quarter % spread) * 32 + lane;
-      const bool active = (quarter % spread) * 32 < rows;  // a warp with no row only keeps step
+      const int rows = rows_of(w), row = s_tid;
+      const bool active = quarter * 32 < rows;  // a warp with no row only keeps step
       const int last = row < rows ? w.req.ctx + (int)quotient(w.m * kTcRows + row, p.by_G) : -1;
       RowState st = {-INFINITY, 0.f};
       for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
@@ -593,9 +502,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           };
           const int edge = last - kb * kKeys - stream * kCols;
           const uint32_t s_at = lanes + (it & 1) * kKeys + stream * kCols;
-          if (copies == 1) ok = softmax_block<kCols, 1>(st, s_at, 0, edge, p.scale_log2, rescale);
-          else if (copies == 2) ok = softmax_block<kCols, 2>(st, s_at, copy, edge, p.scale_log2, rescale);
-          else ok = softmax_block<kCols, 4>(st, s_at, copy, edge, p.scale_log2, rescale);
+          ok = softmax_block<kCols>(st, s_at, edge, p.scale_log2, rescale);
           if (!ok) break;
           tc_fence_before();
         }

@@ -11,11 +11,11 @@
 // sample_kernel: a cluster of 1 to 8 blocks per verify row.  Each block stages
 //   its slice of the row in shared memory (the logits are read from HBM once)
 //   and keeps the maximum of each thread's elements.
-//   - top_k up to kList / 2: the k-th largest thread maximum is a bound that at
-//     least k tokens reach, and few more do.  Those are appended to one list
-//     in the first block, which finishes alone: no other pass over the row.
-//   - otherwise (or if equal logits overflow the list): a histogram of weight
-//     sums (top-p) or counts (a large top_k) over kBins equal steps of the
+//   - a small top_k: the k-th largest thread maximum is a bound that at least k
+//     tokens reach, and few more do.  Those are appended to one list in the first
+//     block, which sorts it and finishes alone: no other pass over the row.
+//   - otherwise (or if more tokens than a list holds reach the bound): a histogram
+//     of weight sums (top-p) or counts (a large top_k) over kBins equal steps of the
 //     logit below the maximum finds the step that holds the prefix' end, and
 //     8-bit digits of the keys inside that step find the key.  Equal steps, not
 //     the keys' own leading digits, spread the bulk of the logits over the bins,
@@ -38,12 +38,12 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kBins = 1024;
-constexpr int kList = 1024;  // candidates that the first block can hold
+constexpr int kList = kThreads;  // candidates that the first block can hold, a thread each
 constexpr int kMaxSlice = 49152;  // elements a block stages: 192 KB in 32 bits; sums of 16-bit halves fit 32 bits
 static_assert(kMaxSlice * kMaxCluster == GDN_SAMPLE_MAX_V, "a row is staged by one cluster");
 static_assert(kThreads == 256, "a digit, and a word of a sorted list, is a thread");
-static_assert(kMaxCluster * kThreads <= 3 * kList && 2 * kBins <= 3 * kList && 3 * kThreads * 2 <= 3 * kList,
-              "the scratch's other uses fit the list's place");
+constexpr int kScratch = 2048;  // words: the thread maxima, a histogram, or the list and its sort
+static_assert(kMaxCluster * kThreads <= kScratch && 2 * kBins <= kScratch && 2 * (kList + 2 * kThreads) <= kScratch, "each fits");
 
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
@@ -234,8 +234,8 @@ __device__ __forceinline__ u64 sort_descending(u64 v, int n, u64* places) {
 }
 
 // The rest of a row whose m candidates (key << 32 | ~index, in any order) lie in `list`; the first c of them in order are
-// the top-k tokens.  m <= kThreads: a candidate a thread, sorted twice (by logit for the prefixes, by index for the draw).
-__device__ __forceinline__ void finish_sorted(const gdn_sample_args& p, size_t at, const u64* list, u64* places, int m, int c,
+// the top-k tokens.  A candidate is a thread's, sorted twice (by logit for the prefixes, by index for the draw).
+__device__ __forceinline__ void finish(const gdn_sample_args& p, size_t at, const u64* list, u64* places, int m, int c,
                                               float top_p, float floor_w, u64 u, const Weight& weight, u64* part) {
   __shared__ u64 total_s;
   __shared__ uint32_t drawn_s;
@@ -262,66 +262,6 @@ __device__ __forceinline__ void finish_sorted(const gdn_sample_args& p, size_t a
   }
 }
 
-// The same for more candidates than threads, without sorting: a candidate's rank, and the weight before it in the order of
-// the logits and in that of the indexes, are sums over the list, which every thread reads from the front for its own.
-__device__ __forceinline__ void finish_list(const gdn_sample_args& p, size_t at, const u64* list, uint32_t* weights, int m, int c,
-                                            float top_p, float floor_w, u64 u, const Weight& weight, u64* part) {
-  constexpr int kMost = kList / kThreads;  // candidates of a thread
-  const int tid = threadIdx.x;
-  u64 word[kMost];
-  uint32_t W[kMost];
-  const int own = (m - tid + kThreads - 1) / kThreads;  // tid, tid + kThreads, ...
-#pragma unroll
-  for (int j = 0; j < kMost; ++j) {
-    word[j] = j < own ? list[tid + j * kThreads] : 0;
-    W[j] = j < own ? weight.whole(of_key(word[j] >> 32)) : 0;
-    if (j < own) weights[tid + j * kThreads] = W[j];
-  }
-  __syncthreads();
-  int rank[kMost] = {};
-  u64 before[kMost] = {};
-#pragma unroll 4
-  for (int i = 0; i < m; ++i) {
-    const u64 other = list[i];
-    const uint32_t v = weights[i];
-#pragma unroll
-    for (int j = 0; j < kMost; ++j)
-      if (other > word[j]) {
-        ++rank[j];
-        before[j] += v;
-      }
-  }
-  u64 sum = 0;
-#pragma unroll
-  for (int j = 0; j < kMost; ++j) sum += j < own && rank[j] < c ? W[j] : 0;
-  const u64 top_k_sum = block_sum(sum, part);
-  const u64 limit = top_p < 1.f ? shift_mul(top_k_sum, fraction(top_p, 1.f)) : ~0ull;
-  sum = 0;
-#pragma unroll
-  for (int j = 0; j < kMost; ++j) {
-    const bool kept = j < own && rank[j] < c && (before[j] < limit || rank[j] == 0) && weight.w(of_key(word[j] >> 32)) >= floor_w;
-    if (!kept) W[j] = 0;
-    if (j < own) weights[tid + j * kThreads] = W[j];
-    sum += W[j];
-    before[j] = 0;
-  }
-  const u64 total = block_sum(sum, part);  // and a barrier: the weights are the kept ones now
-  const u64 drawn = shift_mul(total, u);
-#pragma unroll 4
-  for (int i = 0; i < m; ++i) {
-    const uint32_t other = (uint32_t)list[i], v = weights[i];  // inverted indexes: a larger one comes first
-#pragma unroll
-    for (int j = 0; j < kMost; ++j)
-      if (other > (uint32_t)word[j]) before[j] += v;
-  }
-#pragma unroll
-  for (int j = 0; j < kMost; ++j)
-    if (W[j] != 0 && before[j] <= drawn && drawn < before[j] + W[j]) {
-      p.target[at] = (int)~(uint32_t)word[j];
-      if (p.prob) p.prob[at] = weight.w(of_key(word[j] >> 32)) * 2147483648.f / (float)total;
-    }
-}
-
 struct Place {  // a block's kept weight above the threshold, and its tokens on it
   u64 sum, equal;
 };
@@ -331,7 +271,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const gdn_sample_args 
   constexpr int kN = Unit<T>::kN;
   extern __shared__ uint4 slice[];                      // [slice_units], then the scratch below
   uint32_t* const scratch = reinterpret_cast<uint32_t*>(slice + slice_units);
-  u64* const list = reinterpret_cast<u64*>(scratch);     // [kList], and as many weights behind it
+  u64* const list = reinterpret_cast<u64*>(scratch);     // [kList], and twice as many words behind it for the sort
   uint32_t* const lo = scratch;                          // [kBins] sums of the weights' low halves
   uint32_t* const hi = scratch + kBins;                  // [kBins] and high halves
   uint32_t* const maxima = scratch;                      // [blocks][kThreads]
@@ -339,7 +279,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const gdn_sample_args 
   __shared__ News news;
   __shared__ Place places[kMaxCluster], warps[kWarps];
   __shared__ uint32_t count, lowest, all_s, digits[256];
-  __shared__ u64 total_s;
+  __shared__ u64 total_s, ranges[kMaxCluster];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = cluster_rank();
   const int t = blockIdx.x / blocks, b = blockIdx.y;
@@ -407,7 +347,8 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const gdn_sample_args 
 
   // the first block: the row's largest key, and for a top_k that a list can hold a bound just under the k-th largest
   // thread maximum
-  const bool listed = k > 0 && k < p.V && k <= kList / 2 && temp > 0.f;
+  const int n_threads = min(blocks * kThreads, units);
+  const bool listed = k > 0 && k < p.V && temp > 0.f && (p.V <= kList || k + k * (int64_t)k / n_threads <= kList - kList / 16);
   if (rank == 0) {
     uint32_t mine[kMaxCluster], best = 0, low = 0xffffffffu;
     int n_maxima = 0;
@@ -492,8 +433,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const gdn_sample_args 
     const int found = (int)get(counter);
     if (found <= kList) {
       if (rank != 0) return;
-      if (found <= kThreads) finish_sorted(p, at, list, list + kThreads, found, min(k, found), top_p, floor_w, u, weight, part);
-      else finish_list(p, at, list, scratch + 2 * kList, found, min(k, found), top_p, floor_w, u, weight, part);
+      finish(p, at, list, list + kList, found, min(k, found), top_p, floor_w, u, weight, part);
       cluster_sync();  // the others have read `count`, or have left
       return;
     }
@@ -570,8 +510,33 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const gdn_sample_args 
       return;
     }
     const int bin = (int)news.digit;
-    uint32_t prefix = 0;
-    for (int s = 24; s >= (sizeof(T) == 2 ? 16 : 0); s -= 8) {
+    // the keys in that step have leading bits in common, often all of them (bf16: a step is seldom wider than a value's)
+    uint32_t most = 0, least = 0xffffffffu;
+    for (int i = tid; i < own; i += kThreads) {
+      const Unit<T> x(slice[i]);
+#pragma unroll
+      for (int c = 0; c < kN; ++c) {
+        if (bin_of(x.x[c]) != bin || !within(x.x[c])) continue;
+        most = max(most, key_of(x.x[c]));
+        least = min(least, key_of(x.x[c]));
+      }
+    }
+    const auto ends = block_ends(most, least, 0, part);
+    if (tid < blocks) put(peer(&ranges[rank], tid), (u64)ends.most << 32 | ends.least);
+    cluster_sync();
+    most = edge_bin == bin ? thr : 0;
+    least = edge_bin == bin ? thr : 0xffffffffu;
+    for (int r = 0; r < blocks; ++r) {
+      most = max(most, (uint32_t)(ranges[r] >> 32));
+      least = min(least, (uint32_t)ranges[r]);
+    }
+    constexpr int kLast = sizeof(T) == 2 ? 16 : 0;  // a bf16's bits below are all equal
+    const int bits = 32 - __clz(most ^ least);
+    uint32_t prefix = bits == 32 ? 0 : most >> bits << bits;
+    for (int end = bits; end > kLast;) {
+      const int s = max(kLast, end - 8);
+      const uint32_t digit_bits = (1u << (end - s)) - 1;
+      auto fits = [&](uint32_t key) { return end == bits || (key ^ prefix) >> end == 0; };
       for (int i = tid; i < 256; i += kThreads) lo[i] = hi[i] = 0;
       __syncthreads();
       for (int i = tid; i < own; i += kThreads) {
@@ -580,7 +545,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const gdn_sample_args 
         for (int c = 0; c < kN; ++c) {
           if (bin_of(x.x[c]) != bin || !within(x.x[c])) continue;
           const uint32_t key = key_of(x.x[c]);
-          if (s == 24 || (key ^ prefix) >> (s + 8) == 0) add(x.x[c], key >> s & 255);
+          if (fits(key)) add(x.x[c], key >> s & digit_bits);
         }
       }
       cluster_sync();
@@ -588,7 +553,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const gdn_sample_args 
         const int d = 255 - tid;  // digits from the top
         u64 v = 0;
         for (int r = 0; r < blocks; ++r) v += get(peer(lo + d, r)) + ((u64)get(peer(hi + d, r)) << 16);
-        if (edge_bin == bin && (s == 24 || (thr ^ prefix) >> (s + 8) == 0) && (int)(thr >> s & 255) == d) v += edge;
+        if (edge_bin == bin && fits(thr) && (int)(thr >> s & digit_bits) == d) v += edge;
         const u64 upto = block_scan(v, part);
         if (upto - v < left && left <= upto)
           for (int r = 0; r < blocks; ++r) {
@@ -599,6 +564,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const gdn_sample_args 
       cluster_sync();
       left = news.left;
       prefix |= news.digit << s;
+      end = s;
     }
     if (sizeof(T) == 2 && !(prefix & 0x80000000u)) prefix |= 0xffff;  // a negative bf16's low bits, turned over
     const u64 W = weights ? weight.whole(of_key(prefix)) : 1;
@@ -790,7 +756,7 @@ int run(const gdn_sample_args& p, cudaStream_t st) {
   const int blocks = cluster_of((int64_t)p.B * p.R, (int64_t)p.V * sizeof(T));
   const int units = (p.V + 2 * (kN - 1)) / kN;  // at the worst alignment
   const int slice_units = (units + blocks - 1) / blocks;
-  const int smem = slice_units * 16 + kList * 12;
+  const int smem = slice_units * 16 + kScratch * 4;
   // the largest slice's size, so that calls of any V from any thread set the same value
   if (smem > 40 * 1024 &&
       cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024) != cudaSuccess)

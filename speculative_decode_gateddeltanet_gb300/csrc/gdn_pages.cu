@@ -8,9 +8,12 @@
 //   new table entries, returned pages and rows, each finding its request by a
 //   binary search of the prefix in shared memory.  A row's page is taken from
 //   the old table or straight from the ring, so no block reads what another
-//   writes.
-// append_kernel: a copy, bound by HBM.  A thread moves four 16-byte chunks, all
-//   four loads in flight before the first store.
+//   writes.  16 requests take 3.8 us, 1024 with prompts among them 7.5; an empty
+//   launch takes 2.  (More blocks than SMs, or a search per row in global memory,
+//   only add to the chain of dependent reads.)
+// append_kernel: a copy, bound by HBM.  A thread moves one or four 16-byte chunks,
+//   all loads in flight before the first store.  16381 rows of 8 heads of 128 in 32
+//   bits take 41.7 us: 6.4 TB/s, 0.95 of a plain copy's rate.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -249,8 +252,12 @@ struct AppendParams {
 };
 
 constexpr int kCopyThreads = 256;
-constexpr int kUnroll = 4;
+// One chunk a thread where they are few, as the call is then as long as one thread's chain of reads (64 rows of 8 heads of
+// 128 bf16: 1.8 us, with four chunks a thread 2.5; 2048 rows 3.8 and 4.5); four where HBM is the bound (4096 rows 6.2 and
+// 6.1, 16384 rows 24.6 and 22.9).
+constexpr uint32_t kOneEach = 1 << 18;
 
+template <int kUnroll>
 __global__ void __launch_bounds__(kCopyThreads) append_kernel(const AppendParams p) {
   pdl_wait();
   pdl_trigger();
@@ -374,7 +381,8 @@ extern "C" GDN_API int gdn_page_map(const gdn_page_map_args* args, void* stream)
     const int blocks = min(max((p.n_slot_rows + threads - 1) / threads, 1), 152);
     return launch(kernel, dim3(blocks), dim3(threads), smem, st, p, make_div((uint32_t)p.page_size));
   };
-  return p.B <= 128 ? run(page_map_kernel<128, 1>, 128) : p.B <= 512 ? run(page_map_kernel<512, 1>, 512) : run(page_map_kernel<512, 8>, 512);
+  // a thread per request and few warps to scan where they suffice: 16 requests 3.8 us, with 512 threads 4.8; 128 4.1 and 5.2
+  return p.B <= 128 ? run(page_map_kernel<128, 1>, 128) : run(page_map_kernel<512, 8>, 512);
 }
 
 extern "C" GDN_API int gdn_kv_append(const gdn_kv_append_args* a, void* stream) {
@@ -405,6 +413,9 @@ extern "C" GDN_API int gdn_kv_append(const gdn_kv_append_args* a, void* stream) 
   p.vc_token = a->v_token_stride / per16;
   p.status = a->status;
   const uint32_t total = (uint32_t)p.rows * p.per_row.d;
-  const dim3 grid((total + kCopyThreads * kUnroll - 1) / (kCopyThreads * kUnroll), 2);
-  return launch(append_kernel, grid, dim3(kCopyThreads), 0, static_cast<cudaStream_t>(stream), p);
+  auto run = [&](auto kernel, uint32_t unroll) {
+    const dim3 grid((total + kCopyThreads * unroll - 1) / (kCopyThreads * unroll), 2);
+    return launch(kernel, grid, dim3(kCopyThreads), 0, static_cast<cudaStream_t>(stream), p);
+  };
+  return total <= kOneEach ? run(append_kernel<1>, 1) : run(append_kernel<4>, 4);
 }

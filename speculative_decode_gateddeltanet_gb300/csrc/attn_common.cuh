@@ -23,6 +23,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "gdnhybrid.h"
 
 namespace gdnattn {
@@ -113,8 +115,9 @@ struct Tiles {
     return (int)((unsigned)(r.ctx + token) / kKeys) + 1;
   }
   // Units that a tile costs beside its key blocks, in the time of one: about 3 us from a tile's last product to the next
-  // one's first on the tensor cores.  Measured against 1 for few rows and 3 for many: 256 ragged requests 200 -> 183 us,
-  // 16 x 4 rows (d = 256) 43.5 -> 38.7, prompt chunks at d = 256 557 -> 495; 6, 4 and 2 lie between or behind.
+  // one's first on the tensor cores.  Measured (64-key blocks, 128-key blocks): 16 x 4 rows at d = 256 take 35.7 us with
+  // 5, 39.2 with 3 or 4, 36.1 with 10; prompt chunks of up to 4096 485 with 3, 493 with 2, 516 with 1, 504 with 6; 256
+  // ragged requests 172 with 3, 177 with 6.
   static constexpr int kExtra = kRows < 128 ? 0 : kKeys == 64 ? 5 : 3;
   // units of the tiles before m
   __device__ static long long before(const Params& p, const Request& r, int m) {
@@ -272,13 +275,18 @@ __device__ __forceinline__ float* partial(const Params& p, int block, int slot, 
   return p.partials + (size_t)(block * 2 + slot) * rows * (p.d + 2);
 }
 
-constexpr int kCombineWarps = 4;
-constexpr int kCombineBatch = 8;   // partials whose loads are in flight at once
+constexpr int kCombineWarps = 4;  // and eight blocks a tile: 4 lose 1 to 3 us where partials are many, 16 and 32 where few
 
 // Joins the partials of the split tile that block blockIdx.x of the attention
-// begins; gridDim.y blocks share its rows.  Up to eight partials: a warp per row.  More (few tiles, long
-// contexts): a block per row, warp w taking partials w, w + 4, ..., and the warps'
-// sums added in warp order.  Either way the order is fixed by the lengths alone.
+// begins; gridDim.y blocks share its rows.  Up to eight partials: a warp per row,
+// or per two rows at once where there are two partials, as in a prompt's tiles (3
+// prompts of 608 tokens over 9000: 250 -> 244 us, 8 of 300 over 700 at d = 256: 72 ->
+// 66).  More (few tiles, long contexts): a block per row, warp w taking partials w,
+// w + 4, ..., and the warps' sums added in warp order (one token over 65537: 54.3 us,
+// with a warp per row 55.8; the other way round 16 requests of 4 tokens take 44.1
+// instead of 40.0).  The order is fixed by the lengths alone.  Bound by the latency
+// of three dependent reads and by instruction misses: a third variant of the few
+// partials' loop made every call 0.5 to 1 us slower.
 template <typename T, int kD, int kRows>
 __global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const Params p) {
   constexpr int kPer = kD / 32;
@@ -290,29 +298,76 @@ __global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const Param
   if (parts <= 1) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rows = note.z & 255, kv_head = note.z >> 8;
-  const bool shared = parts > kCombineBatch;
   auto part = [&](int i) { return partial(p, blockIdx.x + i, i == 0, kRows); };
   auto stats = [&](int i, int row) { return reinterpret_cast<const float2*>(part(i) + (size_t)kRows * kD)[row]; };
-  const int first = shared ? (int)blockIdx.y : (int)blockIdx.y * kCombineWarps + warp;
-  const int step = shared ? (int)gridDim.y : (int)gridDim.y * kCombineWarps;
-  const int i_first = shared ? warp : 0, i_step = shared ? kCombineWarps : 1;
-  for (int row = first; row < rows; row += step) {
-    float x[kCombineBatch][kPer], tops[kCombineBatch], acc[kPer] = {};
-    auto load = [&](int i0) {
+  // this lane's columns of partial i's row
+  auto load = [&](float (&x)[kPer], int i, int row) {
+    const float* src = part(i) + (size_t)row * kD + lane * 2;
 #pragma unroll
-      for (int j = 0; j < kCombineBatch; ++j) {
-        const int i = min(i0 + j * i_step, parts - 1);
-        tops[j] = stats(i, row).x;
-        const float* src = part(i) + (size_t)row * kD + lane * 2;
+    for (int c = 0; c < kPer / 2; ++c) {
+      const float2 v = *reinterpret_cast<const float2*>(src + c * 64);
+      x[2 * c] = v.x;
+      x[2 * c + 1] = v.y;
+    }
+  };
+  auto write = [&](int row, const float (&acc)[kPer], float sum) {
+    const float inv = 1.f / sum;
+    const int at = note.w + row, token = (int)quotient(at, p.by_G), head = kv_head * p.G + at - token * p.G;
+    T* dst = static_cast<T*>(p.o) + (int64_t)(note.y + token) * p.o_row + (int64_t)head * p.o_head + lane * 2;
 #pragma unroll
-        for (int c = 0; c < kPer / 2; ++c) {
-          const float2 v = *reinterpret_cast<const float2*>(src + c * 64);
-          x[j][2 * c] = v.x;
-          x[j][2 * c + 1] = v.y;
+    for (int c = 0; c < kPer / 2; ++c) {
+      const float a = acc[2 * c] * inv, b = acc[2 * c + 1] * inv;
+      if constexpr (sizeof(T) == 2) *reinterpret_cast<__nv_bfloat162*>(dst + c * 64) = __floats2bfloat162_rn(a, b);
+      else *reinterpret_cast<float2*>(dst + c * 64) = make_float2(a, b);
+    }
+  };
+  // up to kMost partials, kAtOnce rows of this warp at a time
+  auto few = [&](auto most, auto at_once) {
+    constexpr int kMost = decltype(most)::value, kAtOnce = decltype(at_once)::value;
+    const int step = (int)gridDim.y * kCombineWarps;
+    for (int row0 = (int)blockIdx.y * kCombineWarps + warp; row0 < rows; row0 += step * kAtOnce) {
+      float x[kAtOnce][kMost][kPer];
+      float2 st[kAtOnce][kMost];
+#pragma unroll
+      for (int r = 0; r < kAtOnce; ++r)
+#pragma unroll
+        for (int i = 0; i < kMost; ++i) {
+          const int row = min(row0 + r * step, rows - 1), from = min(i, parts - 1);
+          st[r][i] = stats(from, row);
+          load(x[r][i], from, row);
         }
+#pragma unroll
+      for (int r = 0; r < kAtOnce; ++r) {
+        if (row0 + r * step >= rows) break;
+        float top = st[r][0].x, sum = 0.f, acc[kPer] = {};
+#pragma unroll
+        for (int i = 1; i < kMost; ++i) top = fmaxf(top, st[r][i].x);
+        if (top == -INFINITY) top = 0.f;
+#pragma unroll
+        for (int i = 0; i < kMost; ++i) {
+          const float weight = i < parts ? exp2f(st[r][i].x - top) : 0.f;
+          sum += st[r][i].y * weight;
+#pragma unroll
+          for (int c = 0; c < kPer; ++c) acc[c] = fmaf(weight, x[r][i][c], acc[c]);
+        }
+        write(row0 + r * step, acc, sum);
+      }
+    }
+  };
+  if (parts <= 2) return few(std::integral_constant<int, 2>(), std::integral_constant<int, 2>());
+  if (parts <= 8) return few(std::integral_constant<int, 8>(), std::integral_constant<int, 1>());
+  constexpr int kBatch = 8;  // partials whose loads are under way at once
+  for (int row = (int)blockIdx.y; row < rows; row += (int)gridDim.y) {
+    float x[kBatch][kPer], tops[kBatch], acc[kPer] = {};
+    auto batch = [&](int i0) {
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int i = min(i0 + j * kCombineWarps, parts - 1);
+        tops[j] = stats(i, row).x;
+        load(x[j], i, row);
       }
     };
-    load(i_first);  // on their way while the maximum and the sum are formed
+    batch(warp);  // on their way while the maximum and the sum are formed
     float top = -INFINITY, sum = 0.f;
     for (int i = lane; i < parts; i += 32) top = fmaxf(top, stats(i, row).x);
 #pragma unroll
@@ -324,38 +379,29 @@ __global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const Param
     }
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) sum += __shfl_xor_sync(kFull, sum, off);
-    for (int i0 = i_first; i0 < parts; i0 += i_step * kCombineBatch) {
-      if (i0 != i_first) load(i0);
+    for (int i0 = warp; i0 < parts; i0 += kCombineWarps * kBatch) {
+      if (i0 != warp) batch(i0);
 #pragma unroll
-      for (int j = 0; j < kCombineBatch; ++j) {
-        if (i0 + j * i_step >= parts) break;
+      for (int j = 0; j < kBatch; ++j) {
+        if (i0 + j * kCombineWarps >= parts) break;
         const float weight = exp2f(tops[j] - top);
 #pragma unroll
         for (int c = 0; c < kPer; ++c) acc[c] = fmaf(weight, x[j][c], acc[c]);
       }
     }
-    if (shared) {
 #pragma unroll
-      for (int c = 0; c < kPer / 2; ++c)
-        *reinterpret_cast<float2*>(&sums[warp][c * 64 + lane * 2]) = make_float2(acc[2 * c], acc[2 * c + 1]);
-      __syncthreads();
+    for (int c = 0; c < kPer / 2; ++c)
+      *reinterpret_cast<float2*>(&sums[warp][c * 64 + lane * 2]) = make_float2(acc[2 * c], acc[2 * c + 1]);
+    __syncthreads();
+    if (warp == 0) {
 #pragma unroll
       for (int c = 0; c < kPer; ++c) {
         acc[c] = 0.f;
         for (int w = 0; w < kCombineWarps; ++w) acc[c] += sums[w][(c / 2) * 64 + lane * 2 + (c & 1)];
       }
-      __syncthreads();
-      if (warp != 0) continue;
+      write(row, acc, sum);
     }
-    const float inv = 1.f / sum;
-    const int at = note.w + row, token = (int)quotient(at, p.by_G), head = kv_head * p.G + at - token * p.G;
-    T* dst = static_cast<T*>(p.o) + (int64_t)(note.y + token) * p.o_row + (int64_t)head * p.o_head + lane * 2;
-#pragma unroll
-    for (int c = 0; c < kPer / 2; ++c) {
-      const float a = acc[2 * c] * inv, b = acc[2 * c + 1] * inv;
-      if constexpr (sizeof(T) == 2) *reinterpret_cast<__nv_bfloat162*>(dst + c * 64) = __floats2bfloat162_rn(a, b);
-      else *reinterpret_cast<float2*>(dst + c * 64) = make_float2(a, b);
-    }
+    __syncthreads();
   }
 }
 

@@ -268,8 +268,11 @@ struct Place {  // a block's kept weight above the threshold, and its tokens on 
   u64 sum, equal;
 };
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) sample_kernel(const gdn_sample_args p, int blocks, int slice_units) {
+// kPerSm: blocks an SM holds at least, by registers.  Six instead of four hide more of the others' waits where the call has
+// more blocks than fit, but the fewer registers spill: 1152 rows of 50001 with a top-k take 88 us, with four 101; 64 rows
+// of 151936 (512 blocks) take 17.8 with four, 18.5 with six.
+template <typename T, int kPerSm>
+__global__ void __launch_bounds__(kThreads, kPerSm) sample_kernel(const gdn_sample_args p, int blocks, int slice_units) {
   constexpr int kN = Unit<T>::kN;
   extern __shared__ uint4 slice[];                      // [slice_units], then the scratch below
   uint32_t* const scratch = reinterpret_cast<uint32_t*>(slice + slice_units);
@@ -308,36 +311,26 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const gdn_sample_args 
   const int first = u0 * kN - shift;  // the row's index of the slice's first element
   const uint4* const src = reinterpret_cast<const uint4*>(row - shift) + u0;
   float top = __uint_as_float(0x7fffffffu);  // NaN: no element yet
-  constexpr int kUnroll = 8;
-  for (int i0 = tid; i0 < own; i0 += kUnroll * kThreads) {
-    uint4 w[kUnroll];
+  for (int i = tid; i < own; i += kThreads) {
+    const int e = first + i * kN;
+    if (e >= 0 && e + kN <= p.V) {
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(slice + i)), "l"(src + i) : "memory");
+    } else {
+      T x[kN];
 #pragma unroll
-    for (int j = 0; j < kUnroll; ++j) {
-      const int i = i0 + j * kThreads, e = first + i * kN;
-      if (i < own) {
-        if (e >= 0 && e + kN <= p.V) {
-          w[j] = __ldcs(src + i);  // read once
-        } else {
-          T x[kN];
-#pragma unroll
-          for (int c = 0; c < kN; ++c) {
-            if constexpr (sizeof(T) == 2) x[c] = e + c >= 0 && e + c < p.V ? row[e + c] : __ushort_as_bfloat16(0x7fff);
-            else x[c] = e + c >= 0 && e + c < p.V ? row[e + c] : __uint_as_float(0x7fffffffu);
-          }
-          w[j] = *reinterpret_cast<uint4*>(x);
-        }
+      for (int c = 0; c < kN; ++c) {
+        if constexpr (sizeof(T) == 2) x[c] = e + c >= 0 && e + c < p.V ? row[e + c] : __ushort_as_bfloat16(0x7fff);
+        else x[c] = e + c >= 0 && e + c < p.V ? row[e + c] : __uint_as_float(0x7fffffffu);
       }
+      slice[i] = *reinterpret_cast<uint4*>(x);
     }
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");  // a thread reads only what it copied itself, so far
+#pragma unroll 4
+  for (int i = tid; i < own; i += kThreads) {
+    const Unit<T> x(slice[i]);
 #pragma unroll
-    for (int j = 0; j < kUnroll; ++j) {
-      const int i = i0 + j * kThreads;
-      if (i < own) {
-        slice[i] = w[j];
-        const Unit<T> x(w[j]);
-#pragma unroll
-        for (int c = 0; c < kN; ++c) top = fmaxf(top, x.x[c]);  // NaN loses
-      }
-    }
+    for (int c = 0; c < kN; ++c) top = fmaxf(top, x.x[c]);  // NaN loses
   }
   cluster_wait();
   put(peer(maxima + rank * kThreads + tid, 0), key_of(top));
@@ -763,11 +756,13 @@ int run(const gdn_sample_args& p, cudaStream_t st) {
   const int units = (p.V + 2 * (kN - 1)) / kN;  // at the worst alignment
   const int slice_units = (units + blocks - 1) / blocks;
   const int smem = slice_units * 16 + kScratch * 4;
-  // the largest slice's size, so that calls of any V from any thread set the same value
-  if (smem > 40 * 1024 &&
-      cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024) != cudaSuccess)
-    return GDN_ERR_LAUNCH;
-  return launch(sample_kernel<T>, dim3(p.R * blocks, p.B), dim3(kThreads), blocks, smem, st, p, blocks, slice_units);
+  auto start = [&](auto kernel) {
+    // the largest slice's size, so that calls of any V from any thread set the same value
+    if (smem > 40 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024) != cudaSuccess)
+      return (int)GDN_ERR_LAUNCH;
+    return launch(kernel, dim3(p.R * blocks, p.B), dim3(kThreads), blocks, smem, st, p, blocks, slice_units);
+  };
+  return (int64_t)p.B * p.R * blocks <= 4 * 152 ? start(sample_kernel<T, 4>) : start(sample_kernel<T, 6>);
 }
 
 }  // namespace gdnsample

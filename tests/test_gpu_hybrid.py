@@ -240,6 +240,15 @@ def test_attention_matches_the_definition(hy, lens, H_q, H_kv, d, P, layout, R, 
     assert int(status.item()) == 0
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_attention_of_few_rows(hy, dtype, d):
+    """One to 33 rows a tile, each split over several blocks."""
+    lens = [(1500 - 7 * n, n) for n in (1, 2, 3, 4, 5, 7, 8, 9, 15, 16, 17, 31, 32, 33)]
+    case = hybrid_ref.make_attention(lens=lens, H_q=2, H_kv=2, d=d, P=16, dtype=dtype, seed=d)
+    check_attention(case, run_attention(hy, case))
+
+
 @pytest.mark.parametrize("P", [1, 7, 24, 3000])
 def test_attention_f32_with_any_page_size(hy, P):
     case = hybrid_ref.make_attention(lens=[(100, 3), (0, 40)], H_q=4, H_kv=2, d=64, P=P, dtype=F32, seed=P)
@@ -424,6 +433,13 @@ def test_sampling_matches_the_definition(hy, B, R, V, dtype, ties, pad):
     check_sample(case, run_sample(hy, case))
     for off in (("temperature", "top_k", "top_p", "min_p"), ("top_k",), ("top_p", "min_p"), ("top_k", "top_p")):
         check_sample(case, run_sample(hy, case, off), off)
+
+
+@pytest.mark.parametrize("B,R,V,dtype", [(160, 4, 1500, BF16), (77, 4, 14001, F32)])
+def test_sampling_of_more_rows_than_the_gpu_holds(hy, B, R, V, dtype):
+    case = sample_case(B, R, V, dtype, seed=B)
+    check_sample(case, run_sample(hy, case))
+    check_sample(case, run_sample(hy, case, ("top_k",)), ("top_k",))
 
 
 @pytest.mark.parametrize("V,k", [(5000, 300), (40000, 700), (40000, 20), (3000, 512), (3000, 513), (700, 699)])

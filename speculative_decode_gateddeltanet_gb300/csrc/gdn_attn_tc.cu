@@ -225,6 +225,29 @@ __host__ __device__ constexpr uint32_t instruction(int n, bool transpose_b) {
   return 1u << 4 | 1u << 7 | 1u << 10 | (transpose_b ? 1u << 16 : 0) | (uint32_t)(n >> 3) << 17 | (uint32_t)(kTcRows >> 4) << 24;
 }
 
+// two 32-bit numbers as one operand: half the instructions of the softmax's multiply-adds and sums (8192 tokens at d = 64
+// 401 -> 367 us, prompt chunks at d = 128 440 -> 431)
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 halves(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 // a row's running softmax
 struct RowState {
   float top, sum;
@@ -261,7 +284,8 @@ __device__ __forceinline__ bool softmax_block(RowState& st, uint32_t s_at, int e
     if (!rescale(shrink)) return false;
   }
   const float sub = st.top == -INFINITY ? 0.f : st.top;
-  float s4[4] = {0.f, 0.f, 0.f, 0.f};
+  const uint64_t scale2 = pair(scale_log2, scale_log2), sub2 = pair(-sub, -sub);
+  uint64_t s2[2] = {0, 0};
   constexpr int kW = 16;  // words of one TMEM store
 #pragma unroll
   for (int c = 0; c < kC / 2; c += kW) {
@@ -269,15 +293,15 @@ __device__ __forceinline__ bool softmax_block(RowState& st, uint32_t s_at, int e
 #pragma unroll
     for (int i = 0; i < kW; ++i) {
       const int j = 2 * (c + i);
-      const float e0 = ex2(fmaf(__uint_as_float(x[j / kPart][j % kPart]), scale_log2, -sub));
-      const float e1 = ex2(fmaf(__uint_as_float(x[j / kPart][j % kPart + 1]), scale_log2, -sub));
-      s4[j & 3] += e0;
-      s4[(j + 1) & 3] += e1;
-      pk[i] = pack_bf16(e0, e1);
+      const float* const xs = reinterpret_cast<const float*>(x[j / kPart]) + j % kPart;
+      const float2 y = halves(fma2(pair(xs[0], xs[1]), scale2, sub2)), e = {ex2(y.x), ex2(y.y)};
+      s2[i & 1] = add2(s2[i & 1], pair(e.x, e.y));
+      pk[i] = pack_bf16(e.x, e.y);
     }
     tmem_store(s_at + c, pk);  // over columns that were read
   }
-  st.sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+  const float2 total = halves(add2(s2[0], s2[1]));
+  st.sum += total.x + total.y;
   tmem_wait_store();
   return true;
 }
@@ -301,7 +325,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const Params& p = t.p;
   const uint32_t q_flip = t.q_flip;
   extern __shared__ uint8_t raw[];
-  __shared__ __align__(8) uint64_t bars[2 * S::kK + 2 * S::kV + 17];
+  __shared__ __align__(8) uint64_t bars[2 * S::kK + 2 * S::kV + 15];
   __shared__ long long scan[kTcThreads / 32];
   __shared__ Start start;
   __shared__ uint32_t tmem_base;
@@ -311,7 +335,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
   const uint32_t q_s = base, k_s = q_s + S::kQBytes, v_s = k_s + S::kK * S::kTileBytes;
   // A wait names a phase by its parity, so a barrier may be at most one phase ahead of any of its waiters, and each
-  // waiter takes every phase in turn; what may be signalled twice before it is waited for has two barriers.
+  // waiter takes every phase in turn, or knows from another wait that the one before has passed; what may be signalled
+  // twice before it is waited for has two barriers.  Waits are few on purpose: one costs some 50 ns even when it is over
+  // (a third wait a block in the softmax cost 5 % of a prompt's time, separate ones for the streams' P another 3 %), and
+  // polling instead of suspending 25 %.
   const uint32_t b0 = smem_addr(bars);
   auto k_full = [&](int i) { return b0 + 8 * i; };
   auto k_empty = [&](int i) { return b0 + 8 * (S::kK + i); };
@@ -319,12 +346,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   auto v_empty = [&](int i) { return b0 + 8 * (2 * S::kK + S::kV + i); };
   constexpr int kRest = 2 * S::kK + 2 * S::kV;
   auto s_full = [&](int i) { return b0 + 8 * (kRest + (i & 1)); };       // S of block i is in TMEM
-  auto p_ready = [&](int i, int x) { return b0 + 8 * (kRest + 2 + (i & 1) * 2 + x); };  // stream x's P of it is
-  auto pv_done = [&](int i) { return b0 + 8 * (kRest + 6 + (i & 1)); };   // O holds its products
-  auto st_ready = [&](int g) { return b0 + 8 * (kRest + 8 + (g & 1)); };  // tile g's maxima and sums are in `stats`
-  auto o_full = [&](int g) { return b0 + 8 * (kRest + 10 + (g & 1)); };   // tile g's O is whole
-  auto o_free = [&](int g) { return b0 + 8 * (kRest + 12 + (g & 1)); };   // and has been written out
-  const uint32_t q_full = b0 + 8 * (kRest + 14), q_empty = b0 + 8 * (kRest + 15), drained = b0 + 8 * (kRest + 16);
+  auto p_ready = [&](int i) { return b0 + 8 * (kRest + 2 + (i & 1)); };  // P of it is, of all streams
+  auto pv_done = [&](int i) { return b0 + 8 * (kRest + 4 + (i & 1)); };  // O holds its products
+  auto st_ready = [&](int g) { return b0 + 8 * (kRest + 6 + (g & 1)); };  // tile g's maxima and sums are in `stats`
+  auto o_full = [&](int g) { return b0 + 8 * (kRest + 8 + (g & 1)); };   // tile g's O is whole
+  auto o_free = [&](int g) { return b0 + 8 * (kRest + 10 + (g & 1)); };   // and has been written out
+  const uint32_t q_full = b0 + 8 * (kRest + 12), q_empty = b0 + 8 * (kRest + 13), drained = b0 + 8 * (kRest + 14);
   if (tid == 0) {
     gave_up = 0;
     for (int i = 0; i < S::kK; ++i) {
@@ -337,8 +364,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(s_full(i), 1);
-      bar_init(p_ready(i, 0), 4);
-      bar_init(p_ready(i, 1), 4);
+      bar_init(p_ready(i), 4 * S::kStreams);
       bar_init(pv_done(i), 1);
       bar_init(st_ready(i), 4 * S::kStreams);
       bar_init(o_full(i), 1);
@@ -493,11 +519,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       RowState st = {-INFINITY, 0.f};
       for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
         if (!(ok = warp_wait(s_full(it), (it >> 1) & 1, &gave_up))) break;
-        if (it >= 2 && !(ok = warp_wait(pv_done(it), ((it >> 1) - 1) & 1, &gave_up))) break;  // block it - 2's, each in turn
         if (active) {
           tc_fence_after();
           auto rescale = [&](float shrink) {
             if (kb == w.kb0) return true;
+            // this S was formed behind block it - 2's products, the one wait that is not taken
             if (!warp_wait(pv_done(it - 1), ((it - 1) >> 1) & 1, &gave_up)) return false;
             tc_fence_after();
 #pragma unroll 1
@@ -531,7 +557,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           fence_async();
         }
-        warp_arrive(p_ready(it, stream));
+        warp_arrive(p_ready(it));
       }
       if (ok && g >= 2) ok = warp_wait(o_free(g), ((g >> 1) - 1) & 1, &gave_up);  // tile g - 2 is done with its place in stats
       if (!ok) break;
@@ -587,11 +613,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             ok = ok && bar_wait(o_free(g - 1), o_phase >> 1, &gave_up);
             o_phase = (o_phase + 1) & 3;
           }
+          ok = ok && bar_wait(p_ready(0) + 8 * buf, p_phase, &gave_up);
+          if (!ok) break;
+          tc_fence_after();
 #pragma unroll
           for (int x = 0; x < S::kStreams; ++x) {
-            ok = ok && bar_wait(p_ready(0, x) + 16 * buf, p_phase, &gave_up);
-            if (!ok) break;
-            tc_fence_after();
             const uint32_t o_at = tmem + kOCol + x * kD, px_at = p_at + x * kCols, v_at = v_lo + x * (kCols * 8);
             if (valid >= (x + 1) * kCols) {
 #pragma unroll

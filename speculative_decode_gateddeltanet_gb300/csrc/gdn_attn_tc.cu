@@ -25,7 +25,7 @@
 // times, so that all warps share their exponentials, cost more in the join: 16
 // requests of 4 tokens at d = 256 took 40.0 us, without 35.7.  Only d = 64, where a
 // block's K and V arrive in less time than a warp needs for its rows, lost: 32
-// tokens over 16000 took 99 us and take 127.)
+// tokens over 16000 took 99 us and take 109.)
 //
 // A page is copied in boxes of 64 columns by a power of two of tokens that
 // divides the page, straight into the 128-byte-swizzled layout the MMA reads;
@@ -41,12 +41,13 @@
 // GDN_STATUS_TIMEOUT, waits (bounded) for its own copies and products in
 // flight, frees its TMEM and ends.
 //
-// Measured.  Prefill is bound by the softmax: a 128-key unit takes 0.95 us, its MMAs
-// 0.53 (8192 tokens at d = 128, 32 heads: 1.15 PFLOP/s, 0.61 of cuBLAS' bf16 rate;
-// d = 256 1.18, d = 64 0.63).  Decode is bound by HBM behind a start of some 4 us
+// Measured.  Prefill is bound by the chain of a block (scores, weights, products), of
+// which the softmax is the longest part: a 128-key unit takes 0.86 us, its MMAs 0.53
+// (8192 tokens at d = 128, 32 heads: 1.28 PFLOP/s, 0.68 of cuBLAS' bf16 rate; d = 256
+// 1.19, d = 64 0.76).  Decode is bound by HBM behind a start of some 4 us
 // (lengths, pages, the first copies) and an end of some 7 (tiles out, the join):
-// 256 ragged requests of 2 to 9 tokens 172 us (5.9 TB/s, 0.87 of a copy's rate), one
-// token over 65537 51.7 us (5.2 TB/s), 16 requests of 4 tokens over 1000 to 8000 at
+// 256 ragged requests of 2 to 9 tokens 169 us (6.0 TB/s, 0.88 of a copy's rate), one
+// token over 65537 51 us (5.3 TB/s), 16 requests of 4 tokens over 1000 to 8000 at
 // d = 256 35.4 us (4.1 TB/s).
 #include <cuda.h>
 
@@ -131,9 +132,11 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
   return bar_wait_slow(bar, parity, gave_up);
 }
 
-// the same for a whole warp: all lanes go on, or none
+// the same for a whole warp: all lanes go on, or none (one lane's try and a shuffle of its outcome: 432 -> 484 us for a
+// step of prompt chunks; a branch of each lane's own before the vote: 432, not 427)
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
-  return __all_sync(kFull, bar_wait(bar, parity, gave_up));
+  if (__all_sync(kFull, bar_try(bar, parity))) return true;
+  return __all_sync(kFull, bar_wait_slow(bar, parity, gave_up));
 }
 
 __device__ __forceinline__ void tma_box(const CUtensorMap* map, uint32_t dst, uint32_t bar, int col, int token, int head, int page) {

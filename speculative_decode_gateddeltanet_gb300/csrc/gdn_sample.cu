@@ -22,7 +22,7 @@
 //     so few lanes of a warp add to the same one.  The kept weights are then
 //     summed in index order and the draw located.
 //   Bound by the chain of cluster barriers and by instructions, not by HBM.  Rows of
-//   151936 bf16, 64 of them (19.4 MB, 2.9 us of HBM): greedy 10 us, top-k 19, weights
+//   151936 bf16, 64 of them (19.4 MB, 2.9 us of HBM): greedy 10 us, top-k 18, weights
 //   without a filter 34 (exp of every token, twice), top-p 63 (and the shared-memory
 //   atomics of the histogram).  One row of 32000: 4 to 16 us.
 // accept_kernel: one warp per request; where there are no drafts (R = 1) the rows'

@@ -189,23 +189,19 @@ __device__ __forceinline__ void tmem_store(uint32_t at, const uint32_t (&r)[32])
       GDN_W4(r, 0), GDN_W4(r, 4), GDN_W4(r, 8), GDN_W4(r, 12), GDN_W4(r, 16), GDN_W4(r, 20), GDN_W4(r, 24), GDN_W4(r, 28)
       : "memory");
 }
-__device__ __forceinline__ void tmem_load(uint32_t (&r)[16], uint32_t at) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-      : GDN_R4(r, 0), GDN_R4(r, 4), GDN_R4(r, 8), GDN_R4(r, 12)
-      : "r"(at));
-}
 __device__ __forceinline__ void tmem_store(uint32_t at, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(at),
       GDN_W4(r, 0), GDN_W4(r, 4), GDN_W4(r, 8), GDN_W4(r, 12)
       : "memory");
 }
-__device__ __forceinline__ void tmem_store(uint32_t at, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(at), GDN_W4(r, 0), GDN_W4(r, 4)
-               : "memory");
-}
 __device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// after the wait, for each load: nothing reads the registers ahead of it
+#define GDN_RW4(r, i) "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3])
+__device__ __forceinline__ void tmem_loaded(uint32_t (&r)[32]) {
+  asm volatile(""
+               : GDN_RW4(r, 0), GDN_RW4(r, 4), GDN_RW4(r, 8), GDN_RW4(r, 12), GDN_RW4(r, 16), GDN_RW4(r, 20), GDN_RW4(r, 24), GDN_RW4(r, 28));
+}
 __device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -266,6 +262,8 @@ __device__ __forceinline__ bool softmax_block(RowState& st, uint32_t s_at, int e
 #pragma unroll
   for (int c = 0; c < kC / kPart; ++c) tmem_load(x[c], s_at + c * kPart);
   tmem_wait_load();
+#pragma unroll
+  for (int c = 0; c < kC / kPart; ++c) tmem_loaded(x[c]);
   if (edge < kC - 1) {
 #pragma unroll
     for (int c = 0; c < kC / kPart; ++c)
@@ -477,9 +475,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             tmem_load(o0, lanes + kOCol + c * 32);
             if (n_parts == 2) tmem_load(o1, lanes + kOCol + kD + c * 32);
             tmem_wait_load();
+            tmem_loaded(o0);
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(o0[i]) * share0;
             if (n_parts == 2) {
+              tmem_loaded(o1);
 #pragma unroll
               for (int i = 0; i < 32; ++i) v[i] = fmaf(__uint_as_float(o1[i]), share1, v[i]);
             }
@@ -534,6 +534,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               uint32_t o[32];
               tmem_load(o, lanes + kOCol + stream * kD + c * 32);
               tmem_wait_load();
+              tmem_loaded(o);
 #pragma unroll
               for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * shrink);
               tmem_store(lanes + kOCol + stream * kD + c * 32, o);

@@ -122,17 +122,6 @@ __device__ __forceinline__ void min_at(uint32_t at, uint32_t v) {
   asm volatile("red.shared::cluster.min.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
 }
 
-// the whole block's sum, with a barrier before and after
-__device__ __forceinline__ u64 block_sum(u64 v, u64* part) {
-  v = warp_sum(v);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-  __syncthreads();
-  u64 s = 0;
-  for (int w = 0; w < kWarps; ++w) s += part[w];
-  return s;
-}
-
 // kN equal steps of the distance from the largest logit, a monotonous map whatever the range: adding 2^23 rounds to a
 // whole number without a conversion (those, like exp, run at a quarter of the rate of additions).  A distance of NaN
 // (both infinite) is 0, and so is every distance where the range is infinite.

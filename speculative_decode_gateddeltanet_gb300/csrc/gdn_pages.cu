@@ -375,7 +375,8 @@ extern "C" GDN_API int gdn_page_map(const gdn_page_map_args* args, void* stream)
   const size_t smem = (size_t)(6 * p.B + 3) * sizeof(int);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   auto run = [&](auto kernel, int threads) {
-    if (smem > 48 * 1024 &&
+    // what a block gets without asking, 48 KB, holds the kernel's static part too
+    if (smem > 40 * 1024 &&
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (6 * kMaxB + 3) * sizeof(int)) != cudaSuccess)
       return (int)GDN_ERR_LAUNCH;
     const int blocks = min(max((p.n_slot_rows + threads - 1) / threads, 1), 152);

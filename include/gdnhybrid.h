@@ -70,7 +70,8 @@ enum {
  *   free_out   [2] int32        the ring's head and free pages after the call
  *   rows_out   [B] int32        rows served: n_rows[b], or 0 (not served)
  *   row_start  [B+1] int32      b*R, or the packed prefix of rows_out; [B] = all rows
- *   slot_map, positions [n_slot_rows] int32   per row; -1 for rows of no token.  Padded: B*R of them
+ *   slot_map, positions [n_slot_rows] int32   per row; -1 for rows of no token.  Padded: B*R of them;
+ *              without either n_slot_rows does not matter
  *
  * held_out, free_out must not overlap held_in, free_in: a step's blocks read
  * the old counts while they write the new ones (keep two of each and

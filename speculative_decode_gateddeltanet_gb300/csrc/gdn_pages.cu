@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(kThreads) page_map_kernel(const gdn_page_map_a
     place.back += max(held[i] - need[i], 0);
     const int counted = n[i];
     const int first = p.R > 0 ? b * p.R : (int)min(place.rows, (long long)INT32_MAX);
-    if (p.R == 0 && n[i] > 0 && place.rows + n[i] > p.n_slot_rows) {
+    if (p.R == 0 && (p.slot_map || p.positions) && n[i] > 0 && place.rows + n[i] > p.n_slot_rows) {
       status |= GDN_STATUS_ROWS_FULL;
       n[i] = 0;
     }

@@ -35,3 +35,19 @@ def test_page_map_batches_around_the_default_shared_memory_limit():
     path = os.pathsep.join([os.path.dirname(here), here, os.environ.get("PYTHONPATH", "")])
     run = subprocess.run([sys.executable, "-c", FRESH], env=dict(os.environ, PYTHONPATH=path), capture_output=True, text=True, timeout=300)
     assert run.returncode == 0, run.stderr[-2000:]
+
+
+@pytest.mark.parametrize("arrays", [(), ("positions",)], ids=["none", "positions"])
+def test_packed_page_map_without_row_arrays_serves_every_request(hy, arrays):
+    ctx, n, held, ring, free, table, P, R, rows = base.page_case(40, 16, 0, 3)
+    ref = hybrid_ref.page_map(ctx, n, held, ring, free, table, P, R, rows)
+    t = dict(ctx_len=ints(ctx), n_rows=ints(n), held=ints(held), free_ring=ints(ring), free_state=ints(free), block_table=ints(table))
+    new = lambda *s: torch.full(s, -9, dtype=torch.int32, device="cuda")  # noqa: E731
+    out = dict(held_out=new(40), free_state_out=new(2), rows_out=new(40), row_start=new(41), status=torch.zeros(1, dtype=torch.int32, device="cuda"))
+    out |= {name: new(rows) for name in arrays}
+    hy.gdn_page_map(hy.make_page_map_args(**t, **out, page_size=P, R=R))
+    torch.cuda.synchronize()
+    assert int(out["status"].item()) == 0 and ref["status"] == 0
+    for key in ("held_out", "rows_out", "row_start", *arrays):
+        assert np.array_equal(out[key].cpu().numpy(), ref[key]), key
+    assert np.array_equal(t["block_table"].cpu().numpy(), ref["table"])

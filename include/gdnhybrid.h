@@ -78,7 +78,9 @@ enum {
  * alternate; GDN_ERR_INVALID_ARG otherwise).  A negative ctx_len or n_rows, or n_rows > R
  * when padded, leaves the request's pages as they are, rows_out 0
  * (GDN_STATUS_BAD_LENGTH, GDN_STATUS_BAD_NROWS).  Any output but
- * block_table, held_out, free_out, rows_out may be NULL.
+ * block_table, held_out, free_out, rows_out may be NULL.  With B = 0 the counts
+ * go from free_in to free_out and rows are written as rows of no token; without
+ * both of the two such a call does nothing.
  * Supported: B <= 4096, page_size >= 1, n_pages*page_size < 2^31. */
 typedef struct gdn_page_map_args {
   int32_t B, R;

@@ -323,9 +323,9 @@ int check(const gdn_page_map_args* a) {
   if (a->B > kMaxB || (int64_t)a->n_pages * a->page_size > INT32_MAX || (int64_t)a->B * a->R > INT32_MAX)
     return GDN_ERR_UNSUPPORTED;
   if (a->R > 0 && (a->slot_map || a->positions) && a->n_slot_rows != a->B * a->R) return GDN_ERR_INVALID_ARG;
-  if (a->B == 0) return GDN_OK;
-  if (!a->ctx_len || !a->n_rows || !a->held_in || !a->free_ring || !a->free_in || !a->block_table || !a->held_out ||
-      !a->free_out || !a->rows_out)
+  if (a->B == 0 && !a->free_in && !a->free_out) return GDN_OK;
+  if (!a->free_in || !a->free_out) return GDN_ERR_INVALID_ARG;
+  if (a->B > 0 && (!a->ctx_len || !a->n_rows || !a->held_in || !a->free_ring || !a->block_table || !a->held_out || !a->rows_out))
     return GDN_ERR_INVALID_ARG;
   const void* all[] = {a->ctx_len, a->n_rows, a->held_in, a->free_ring, a->free_in, a->block_table, a->held_out,
                        a->free_out, a->rows_out, a->row_start, a->slot_map, a->positions, a->status};
@@ -370,7 +370,7 @@ using namespace gdnpages;
 
 extern "C" GDN_API int gdn_page_map(const gdn_page_map_args* args, void* stream) {
   const int rc = check(args);
-  if (rc != GDN_OK || args->B == 0) return rc;
+  if (rc != GDN_OK || !args->free_out) return rc;
   const gdn_page_map_args p = *args;
   const size_t smem = (size_t)(6 * p.B + 3) * sizeof(int);
   cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -51,3 +51,19 @@ def test_packed_page_map_without_row_arrays_serves_every_request(hy, arrays):
     for key in ("held_out", "rows_out", "row_start", *arrays):
         assert np.array_equal(out[key].cpu().numpy(), ref[key]), key
     assert np.array_equal(t["block_table"].cpu().numpy(), ref["table"])
+
+
+@pytest.mark.parametrize("R", [0, 4])
+def test_empty_page_map_hands_the_counts_on(hy, R):
+    """A step without requests is a turn of the two copies of the counts like any other."""
+    new = lambda *s: torch.full(s, -9, dtype=torch.int32, device="cuda")  # noqa: E731
+    rows = 0 if R else 5
+    out = dict(held_out=new(0), free_state_out=new(2), rows_out=new(0), row_start=new(1), slot_map=new(rows), positions=new(rows), status=new(1))
+    out["status"].zero_()
+    ring = ints(np.arange(20)[::-1].copy())
+    hy.gdn_page_map(hy.make_page_map_args(ctx_len=new(0), n_rows=new(0), held=new(0), free_ring=ring, free_state=ints([17, 9]),
+                                          block_table=new(0, 6), **out, page_size=16, R=R))
+    torch.cuda.synchronize()
+    assert out["free_state_out"].tolist() == [17, 9] and out["row_start"].tolist() == [0] and int(out["status"].item()) == 0
+    assert out["slot_map"].tolist() == out["positions"].tolist() == [-1] * rows
+    assert ring.tolist() == list(range(19, -1, -1))

@@ -165,12 +165,15 @@ __global__ void __launch_bounds__(kThreads) page_map_kernel(const gdn_page_map_a
   }
   Sums given;
   place = block_scan<kThreads>(place, part, &given);
+  // what the free part leaves of the ring; counts that add up never return more, others are cut there
+  const long long most_back = N - n_free;
+  given.back = min(given.back, most_back);
 #pragma unroll
   for (int i = 0; i < kPerThread; ++i) {
     if (i >= per || b0 + i >= B) break;
     const int b = b0 + i;
     take_at[b] = (int)place.take;
-    back_at[b] = (int)place.back;
+    back_at[b] = (int)min(place.back, most_back);
     place.take += max(need[i] - held[i], 0);
     place.back += max(held[i] - need[i], 0);
     const int counted = n[i];
@@ -197,7 +200,7 @@ __global__ void __launch_bounds__(kThreads) page_map_kernel(const gdn_page_map_a
     row_at[B] = end;
     if (blockIdx.x == 0) {
       p.free_out[0] = (int)((head + given.take) % N);
-      p.free_out[1] = (int)min(n_free - given.take + given.back, (long long)N);
+      p.free_out[1] = (int)(n_free - given.take + given.back);
       if (p.row_start) p.row_start[B] = end;
     }
   }

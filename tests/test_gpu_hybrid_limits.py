@@ -61,9 +61,28 @@ def test_empty_page_map_hands_the_counts_on(hy, R):
     out = dict(held_out=new(0), free_state_out=new(2), rows_out=new(0), row_start=new(1), slot_map=new(rows), positions=new(rows), status=new(1))
     out["status"].zero_()
     ring = ints(np.arange(20)[::-1].copy())
-    hy.gdn_page_map(hy.make_page_map_args(ctx_len=new(0), n_rows=new(0), held=new(0), free_ring=ring, free_state=ints([17, 9]),
+    free = ints([17, 9])
+    hy.gdn_page_map(hy.make_page_map_args(ctx_len=new(0), n_rows=new(0), held=new(0), free_ring=ring, free_state=free,
                                           block_table=new(0, 6), **out, page_size=16, R=R))
     torch.cuda.synchronize()
     assert out["free_state_out"].tolist() == [17, 9] and out["row_start"].tolist() == [0] and int(out["status"].item()) == 0
     assert out["slot_map"].tolist() == out["positions"].tolist() == [-1] * rows
     assert ring.tolist() == list(range(19, -1, -1))
+
+
+def test_page_map_returns_no_more_pages_than_there_are(hy):
+    """Counts that do not add up: every request holds all pages and needs none.  Their sum passes 2^32; the ring takes
+    one turn, and nothing outside it or the tables is touched."""
+    B, N = 4096, 1 << 20
+    table = torch.arange(N, dtype=torch.int32, device="cuda")  # row 0; no other row is read
+    store = torch.full((N + 64,), -9, dtype=torch.int32, device="cuda")
+    new = lambda *s: torch.full(s, -9, dtype=torch.int32, device="cuda")  # noqa: E731
+    out = dict(held_out=new(B), free_state_out=new(2), rows_out=new(B), status=torch.zeros(1, dtype=torch.int32, device="cuda"))
+    zero, held, free = ints(np.zeros(B)), ints(np.full(B, N)), ints([5, 0])
+    args = hy.make_page_map_args(ctx_len=zero, n_rows=zero, held=held, free_ring=store[:N], free_state=free,
+                                 block_table=table[:4].expand(B, 4), **out, page_size=16, R=1)
+    args.max_pages = args.table_stride = N
+    hy.gdn_page_map(args)
+    torch.cuda.synchronize()
+    assert out["free_state_out"].tolist() == [5, N] and int(out["held_out"].max().item()) == 0
+    assert torch.equal(store[:N].roll(-5), table) and bool((store[N:] == -9).all())

@@ -212,19 +212,21 @@ __global__ void __launch_bounds__(kThreads) page_map_kernel(const gdn_page_map_a
     if (x >= N) x -= N;
     return (int)(x < N ? x : x % N);
   };
-  const int first = blockIdx.x * kThreads + threadIdx.x, step = gridDim.x * kThreads;
-  for (int i = first; i < given.take; i += step) {
+  // unsigned: the lists may end less than a step below 2^31
+  const uint32_t first = blockIdx.x * kThreads + threadIdx.x, step = gridDim.x * kThreads;
+  for (uint32_t i = first; i < given.take; i += step) {
     const int b = find(take_at, B, i);
     p.block_table[(size_t)b * p.table_stride + held_s[b] + i - take_at[b]] = p.free_ring[wrap((long long)head + i)];
   }
   // the ring's free part ends where the returned pages go: the two ranges are disjoint
-  for (int i = first; i < given.back; i += step) {
+  for (uint32_t i = first; i < given.back; i += step) {
     const int b = find(back_at, B, i);
     const int left = held_s[b] - (back_at[b + 1] - back_at[b]);  // pages kept
     p.free_ring[wrap((long long)head + n_free + i)] = p.block_table[(size_t)b * p.table_stride + left + i - back_at[b]];
   }
   if (!p.slot_map && !p.positions) return;
-  for (int r = first; r < p.n_slot_rows; r += step) {
+  for (uint32_t row = first; row < (uint32_t)p.n_slot_rows; row += step) {
+    const int r = (int)row;
     int pos = -1, slot = -1;
     if (r < end) {
       const int b = p.R > 0 ? r / p.R : find(row_at, B, r);
@@ -382,7 +384,7 @@ extern "C" GDN_API int gdn_page_map(const gdn_page_map_args* args, void* stream)
     if (smem > 40 * 1024 &&
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (6 * kMaxB + 3) * sizeof(int)) != cudaSuccess)
       return (int)GDN_ERR_LAUNCH;
-    const int blocks = min(max((p.n_slot_rows + threads - 1) / threads, 1), 152);
+    const int blocks = (int)min(max(((int64_t)p.n_slot_rows + threads - 1) / threads, (int64_t)1), (int64_t)152);
     return launch(kernel, dim3(blocks), dim3(threads), smem, st, p, make_div((uint32_t)p.page_size));
   };
   // a thread per request and few warps to scan where they suffice: 16 requests 3.8 us, with 512 threads 4.8; 128 4.1 and 5.2

@@ -86,3 +86,35 @@ def test_page_map_returns_no_more_pages_than_there_are(hy):
     torch.cuda.synchronize()
     assert out["free_state_out"].tolist() == [5, N] and int(out["held_out"].max().item()) == 0
     assert torch.equal(store[:N].roll(-5), table) and bool((store[N:] == -9).all())
+
+
+@pytest.mark.parametrize("B,R", [(3, 0), (4096, 524287)], ids=["packed", "padded"])
+def test_page_map_of_almost_2_31_rows(hy, B, R):
+    """A slot array that ends within one step of the blocks of 2^31: 8.6 GB."""
+    rows = B * R if R else 2**31 - 1
+    ctx, n = np.zeros(B, np.int64), np.zeros(B, np.int64)
+    ctx[:3], n[:3] = (5, 0, 31), (2, 1, 4)
+    held = -(-ctx // 16)
+    ids = np.arange(40)[::-1].copy()
+    table = np.full((B, 4), -1)
+    table[np.arange(4) < held[:, None]] = ids[:held.sum()]
+    ring = np.concatenate([ids[held.sum():], np.zeros(held.sum(), np.int64)])
+    free = [0, 40 - held.sum()]
+    # the plain form at a width it can hold: a request's rows stand at the front of its own
+    ref = hybrid_ref.page_map(ctx, n, held, ring, free, table, 16, 4 if R else 0, 4 * B if R else 16)
+    slots = torch.full((rows,), -9, dtype=torch.int32, device="cuda")
+    new = lambda *s: torch.full(s, -9, dtype=torch.int32, device="cuda")  # noqa: E731
+    t = dict(ctx_len=ints(ctx), n_rows=ints(n), held=ints(held), free_ring=ints(ring), free_state=ints(free), block_table=ints(table))
+    out = dict(held_out=new(B), free_state_out=new(2), rows_out=new(B), row_start=new(B + 1), status=torch.zeros(1, dtype=torch.int32, device="cuda"))
+    hy.gdn_page_map(hy.make_page_map_args(**t, **out, slot_map=slots, page_size=16, R=R))
+    torch.cuda.synchronize()
+    assert int(out["status"].item()) == 0 and np.array_equal(out["rows_out"].cpu().numpy(), n)
+    assert out["free_state_out"].tolist() == ref["free_out"].tolist()
+    if R:
+        for b in range(3):
+            assert slots[b * R:b * R + 4].tolist() == ref["slot_map"][4 * b:4 * b + 4].tolist()
+            slots[b * R:b * R + 4] = -1
+    else:
+        assert slots[:16].tolist() == ref["slot_map"].tolist()
+        slots[:16] = -1
+    assert int(slots.max().item()) == int(slots.min().item()) == -1

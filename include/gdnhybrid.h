@@ -41,7 +41,8 @@ extern "C" {
 enum {
   GDN_STATUS_NO_PAGES = 32,    /* the free pages did not suffice: request not served     */
   GDN_STATUS_TABLE_FULL = 64,  /* a request needs more pages than its table row holds,
-                                  or holds a count outside [0, max_pages]: not served    */
+                                  or holds a count outside [0, max_pages] or more pages
+                                  than there are: not served                             */
   GDN_STATUS_BAD_PAGE = 128,   /* a page or slot outside the pool: skipped, or read as
                                   zeros (gdn_paged_attention)                            */
   GDN_STATUS_BAD_LENGTH = 256, /* a negative ctx_len, or more tokens than the table row

@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kThreads) page_map_kernel(const gdn_page_map_a
     int why = 0;
     if (ctx[i] < 0) why |= GDN_STATUS_BAD_LENGTH;
     if (n[i] < 0 || (p.R > 0 && n[i] > p.R)) why |= GDN_STATUS_BAD_NROWS;
-    if (held[i] < 0 || held[i] > p.max_pages || (!why && want > p.max_pages)) why |= GDN_STATUS_TABLE_FULL;
+    if (held[i] < 0 || held[i] > min(p.max_pages, N) || (!why && want > p.max_pages)) why |= GDN_STATUS_TABLE_FULL;
     if (why) {
       status |= why;
       n[i] = 0;
@@ -154,7 +154,8 @@ __global__ void __launch_bounds__(kThreads) page_map_kernel(const gdn_page_map_a
     if (i >= per || b0 + i >= B) break;
     const int want = max(need[i] - held[i], 0);
     at.take += want;
-    if (want > 0 && at.take > n_free) {
+    // never more pages than there are, whatever the counts say: positions stay below 2^31
+    if (want > 0 && (at.take > n_free || need[i] > N)) {
       status |= GDN_STATUS_NO_PAGES;
       need[i] = held[i];
       n[i] = 0;

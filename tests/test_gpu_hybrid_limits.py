@@ -118,3 +118,27 @@ def test_page_map_of_almost_2_31_rows(hy, B, R):
         assert slots[:16].tolist() == ref["slot_map"].tolist()
         slots[:16] = -1
     assert int(slots.max().item()) == int(slots.min().item()) == -1
+
+
+def test_page_map_refuses_more_pages_than_there_are(hy):
+    """Counts above the pool's pages, and lengths above its tokens (with a position past 2^31 among them), in table rows
+    wide enough for both.  The widest are so by their stride alone: a call that used one would read out of range."""
+    new = lambda *s: torch.full(s, -9, dtype=torch.int32, device="cuda")  # noqa: E731
+    for ctx, n, held, want in (([3, 40], [2, 1], [1, 65], 64), ([2**31 - 4], [8], [2**27], 64), ([2**31 - 4], [8], [60], 32),
+                               ([64 * 16 - 1], [2], [63], 32)):
+        B = len(ctx)
+        table = ints(np.arange(B * 70).reshape(B, 70) % 64)
+        ring = ints(np.arange(64))
+        lengths = dict(ctx_len=ints(ctx), n_rows=ints(n), held=ints(held), free_state=ints([3, 64]))
+        out = dict(held_out=new(B), free_state_out=new(2), rows_out=new(B), row_start=new(B + 1), slot_map=new(B * 8), positions=new(B * 8),
+                   status=torch.zeros(1, dtype=torch.int32, device="cuda"))
+        before = table.clone()
+        args = hy.make_page_map_args(**lengths, free_ring=ring, block_table=table, **out, page_size=16, R=8)
+        if B == 1:
+            args.max_pages = args.table_stride = 2**27 + 1
+        hy.gdn_page_map(args)
+        torch.cuda.synchronize()
+        assert int(out["status"].item()) == want
+        assert out["rows_out"].tolist() == ([2, 0] if B == 2 else [0]) and out["held_out"].tolist() == held
+        assert out["free_state_out"].tolist() == [3, 64] and torch.equal(table, before) and ring.tolist() == list(range(64))
+        assert int((out["slot_map"] >= 0).sum()) == (2 if B == 2 else 0)

@@ -280,9 +280,9 @@ __global__ void __launch_bounds__(kThreads, kPerSm) sample_kernel(const gdn_samp
   pdl_wait();
   pdl_trigger();
   const int n = p.n_rows[b];
-  if (p.R == 1 && p.accept_len && rank == 0 && tid == 0) {
-    p.accept_len[b] = 0;
-    if ((n < 0 || n > 1) && p.status) atomicOr(p.status, GDN_STATUS_BAD_NROWS);
+  if (t == 0 && rank == 0 && tid == 0) {
+    if ((n < 0 || n > p.R) && p.status) atomicOr(p.status, GDN_STATUS_BAD_NROWS);
+    if (p.R == 1 && p.accept_len) p.accept_len[b] = 0;
   }
   if (n <= 0 || n > p.R || t >= n) return;  // the whole cluster
   cluster_arrive();  // every block of the cluster runs before any writes to another's shared memory
@@ -676,9 +676,7 @@ __global__ void __launch_bounds__(256) accept_kernel(const gdn_sample_args p) {
   const int32_t* tg = p.target + (size_t)b * p.R;
   const int n = p.n_rows[b];
   int a = 0;
-  if (n < 0 || n > p.R) {
-    if (p.status && lane == 0) atomicOr(p.status, GDN_STATUS_BAD_NROWS);
-  } else {
+  if (n <= p.R) {  // a bad count was flagged with the rows
     for (int i0 = 0; i0 < n - 1; i0 += 32) {
       const int i = i0 + lane;
       const unsigned differ = __ballot_sync(kFull, i >= n - 1 || d[i] != tg[i]);

@@ -142,3 +142,19 @@ def test_page_map_refuses_more_pages_than_there_are(hy):
         assert out["rows_out"].tolist() == ([2, 0] if B == 2 else [0]) and out["held_out"].tolist() == held
         assert out["free_state_out"].tolist() == [3, 64] and torch.equal(table, before) and ring.tolist() == list(range(64))
         assert int((out["slot_map"] >= 0).sum()) == (2 if B == 2 else 0)
+
+
+# ---- sampling ------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("R", [1, 3])
+def test_sampling_without_accept_lengths_flags_a_bad_row_count(hy, R):
+    for bad in (R + 1, -1):
+        case = base.sample_case(3, R, 100, F32, seed=1)
+        case["n_rows"] = torch.tensor([R, bad, 1], dtype=torch.int32)
+        dev = {k: v.cuda() for k, v in case.items() if k != "drafts"}
+        target, status = torch.full((3, R), -5, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+        hy.gdn_sample_accept(hy.make_sample_accept_args(**dev, target=target, status=status))
+        torch.cuda.synchronize()
+        assert int(status.item()) == 2
+        assert (target[1] == -5).all() and int(target[0].min()) >= 0 and int(target[2, 0]) >= 0

@@ -354,8 +354,9 @@ int check(const gdn_kv_append_args* a) {
   if (a->rows < 0 || a->H_kv < 1 || a->d < 1 || a->page_size < 1 || a->n_pages < 1) return GDN_ERR_INVALID_ARG;
   if (a->in_dtype != GDN_DTYPE_BF16 && a->in_dtype != GDN_DTYPE_F32) return GDN_ERR_UNSUPPORTED;
   const int size = a->in_dtype == GDN_DTYPE_BF16 ? 2 : 4;
+  const int64_t per_row = (int64_t)a->H_kv * ((int64_t)a->d * size / 16);  // chunks; below 2^60
   if ((int64_t)a->d * size % 16 != 0 || (int64_t)a->n_pages * a->page_size > INT32_MAX ||
-      (int64_t)a->rows * a->H_kv * a->d * size / 16 > INT32_MAX)
+      (a->rows > 0 && per_row > INT32_MAX / a->rows))
     return GDN_ERR_UNSUPPORTED;
   if (a->rows == 0) return GDN_OK;
   if (!a->k || !a->v || !a->slot_map || !a->k_cache || !a->v_cache) return GDN_ERR_INVALID_ARG;

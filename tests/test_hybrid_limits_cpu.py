@@ -1,0 +1,31 @@
+"""Arguments at the ends of their ranges, refused on the host."""
+from __future__ import annotations
+
+import ctypes
+import os
+import subprocess
+import sys
+
+
+import test_hybrid_abi_cpu as base
+from test_hybrid_abi_cpu import append_args
+
+hy = base.hy  # the module-wide fixture
+HERE = os.path.dirname(os.path.abspath(__file__))
+
+
+def fresh(code):
+    """The code in a process of its own, which a fault of the host's would end."""
+    path = os.pathsep.join([os.path.dirname(HERE), HERE, os.environ.get("PYTHONPATH", "")])
+    run = subprocess.run([sys.executable, "-c", code], env=dict(os.environ, PYTHONPATH=path), capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0, (run.returncode, run.stderr[-2000:])
+
+
+def test_append_of_sizes_whose_product_passes_64_bits(hy, cuda_lib):
+    """2^30 rows of 2^30 heads of 32: 2^66 bytes.  And a row of 2^32 chunks, and rows of the largest sizes there are."""
+    fresh("import ctypes, test_hybrid_abi_cpu as t\n"
+          "from speculative_decode_gateddeltanet_gb300 import gdn, hybrid\n"
+          "for over in (dict(rows=1 << 30, H_kv=1 << 30, d=32), dict(rows=1, H_kv=1 << 30, d=32),\n"
+          "             dict(rows=2**31 - 1, H_kv=2**31 - 1, d=2**31 - 8)):\n"
+          "    assert gdn._lib.gdn_kv_append(ctypes.byref(t.append_args(hybrid, **over)), None) == 2, over\n")
+    assert cuda_lib._lib.gdn_kv_append(ctypes.byref(append_args(hy, rows=0)), None) == 0

@@ -159,7 +159,8 @@ GDN_API int gdn_kv_append(const gdn_kv_append_args* args, void* stream);
  * page_size a multiple of 16 up to 1024 (any >= 1 for GDN_DTYPE_F32).
  * q, o, pools and work 16-byte aligned, strides multiples of 16 bytes.
  * A request with a negative ctx_len or with more tokens than max_pages pages,
- * n_rows outside [0, R] (padded) or rows outside q is skipped with its bit. */
+ * n_rows outside [0, R] (padded), rows outside q, or more than 2^31 - 1024
+ * tokens or rows times H_q/H_kv is skipped with its bit. */
 typedef struct gdn_paged_attn_args {
   int32_t B, R;
   int32_t H_q, H_kv, d;

@@ -30,6 +30,8 @@
 namespace gdnattn {
 
 constexpr unsigned kFull = 0xffffffffu;
+// the kernels' positions and row numbers are 32-bit, and run up to a block past a request's last
+constexpr int kMaxIndex = INT32_MAX - 1023;
 
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
@@ -48,7 +50,7 @@ inline Div make_div(uint32_t d) {
 struct Params {
   int B, R, H_kv, G, d;
   int page_size, n_pages, table_stride, n_q_rows;
-  int64_t max_tokens;  // max_pages * page_size
+  int max_tokens, max_rows;  // of a request: max_pages * page_size and kMaxIndex / G, below 2^31 by a block of keys and more
   float scale_log2;    // scale * log2(e): scores are kept in the exponent of 2
   Div by_G, by_page;
   const void* q;
@@ -76,7 +78,8 @@ __device__ __forceinline__ Request request(const Params& p, int b, int* why = nu
   r.row0 = p.row_start ? p.row_start[b] : b * p.R;
   int bad = 0;
   if (r.n < 0 || (p.R > 0 && r.n > p.R)) bad |= GDN_STATUS_BAD_NROWS;
-  if (r.n > 0 && (r.ctx < 0 || (int64_t)r.ctx + r.n > p.max_tokens || r.row0 < 0 || (int64_t)r.row0 + r.n > p.n_q_rows))
+  if (r.n > 0 && (r.ctx < 0 || (int64_t)r.ctx + r.n > p.max_tokens || r.n > p.max_rows || r.row0 < 0 ||
+                  (int64_t)r.row0 + r.n > p.n_q_rows))
     bad |= GDN_STATUS_BAD_LENGTH;
   if (bad) r.n = 0;
   if (why) *why |= bad;

@@ -14,6 +14,7 @@
 //   With few rows it is bound by HBM (that case: 4.8 TB/s, 0.71 of a copy's rate),
 //   with many by shared-memory reads and the 32-bit multiply-adds (a 4096-token
 //   prefill at d = 128: 4.5 ms, 30 TFLOP/s of some 76).
+#include <algorithm>
 #include <type_traits>
 
 #include "attn_common.cuh"
@@ -285,7 +286,8 @@ extern "C" GDN_API int gdn_paged_attention(const gdn_paged_attn_args* a, void* s
   p.n_pages = a->n_pages;
   p.table_stride = a->table_stride;
   p.n_q_rows = a->n_q_rows;
-  p.max_tokens = (int64_t)a->max_pages * a->page_size;
+  p.max_tokens = (int)std::min((int64_t)a->max_pages * a->page_size, (int64_t)kMaxIndex);
+  p.max_rows = kMaxIndex / p.G;
   p.scale_log2 = (float)((double)a->scale * 1.4426950408889634);
   p.by_G = make_div((uint32_t)p.G);
   p.by_page = make_div((uint32_t)p.page_size);

@@ -158,3 +158,27 @@ def test_sampling_without_accept_lengths_flags_a_bad_row_count(hy, R):
         torch.cuda.synchronize()
         assert int(status.item()) == 2
         assert (target[1] == -5).all() and int(target[0].min()) >= 0 and int(target[2, 0]) >= 0
+
+
+# ---- attention -----------------------------------------------------------------
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("ctx,n", [(2**31 - 2, 1), (2**31 - 1, 1), (2**31 - 1000, 7), (0, 2**31 // 128), (0, 2**31 - 5)])
+def test_attention_of_numbers_past_32_bits_is_flagged(hy, dtype, ctx, n):
+    """Positions up to 2^31, and rows (tokens times query heads of a kv head) of as many, in a table row and a q that are
+    wide enough by their sizes alone: the request is skipped with its bit, the one beside it is served."""
+    case = hybrid_ref.make_attention(lens=[(20, 2), (30, 2)], H_q=128, H_kv=1, d=64, P=16, dtype=dtype, seed=4)
+    good = base.run_attention(hy, dict(case, n=np.array([2, 0])))
+    q, k, v = (case[x].cuda() for x in ("q", "k_cache", "v_cache"))
+    out, status = torch.full_like(q, 7.0), torch.zeros(1, dtype=torch.int32, device="cuda")
+    t = dict(block_table=ints(case["table"]), ctx_len=ints([20, ctx]), n_rows=ints([2, n]), row_start=ints([0, 0]))
+    args = hy.make_paged_attention_args(q=q, k_cache=k, v_cache=v, **t, o=out, scale=case["scale"], status=status)
+    args.max_pages = args.table_stride = 2**27 + 100  # the second row is never read
+    args.n_q_rows = 2**31 - 1
+    work = torch.empty(hy.paged_attention_work_bytes(args), dtype=torch.uint8, device="cuda")
+    args.work = work.data_ptr()
+    hy.gdn_paged_attention(args)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 256
+    assert torch.equal(out[:2], good[:2]) and bool((out[2:] == 7.0).all())

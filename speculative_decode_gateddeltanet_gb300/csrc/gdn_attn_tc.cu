@@ -51,6 +51,7 @@
 // d = 256 35.4 us (4.1 TB/s).
 #include <cuda.h>
 
+#include <limits>
 #include <type_traits>
 
 #include "attn_common.cuh"
@@ -770,8 +771,8 @@ int run_tc(Params& p, cudaStream_t st) {
     t.q_flip = 0x80008000u;
     t.p.scale_log2 = -t.p.scale_log2;
   }
-  // a hidden score is -inf, and -inf * 0 would be NaN
-  if (t.p.scale_log2 < 1e-30f) t.p.scale_log2 = 1e-30f;
+  // a hidden score is -inf, and -inf * 0 would be NaN; the smallest number leaves no score as much as 1e-6
+  if (t.p.scale_log2 == 0.f) t.p.scale_log2 = std::numeric_limits<float>::denorm_min();
   return p.d == 64 ? run<64>(t, st) : p.d == 128 ? run<128>(t, st) : run<256>(t, st);
 }
 

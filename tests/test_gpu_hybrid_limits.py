@@ -182,3 +182,18 @@ def test_attention_of_numbers_past_32_bits_is_flagged(hy, dtype, ctx, n):
     torch.cuda.synchronize()
     assert int(status.item()) == 256
     assert torch.equal(out[:2], good[:2]) and bool((out[2:] == 7.0).all())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("scale", [0.0, 1e-37, -1e-37, 2e-39])
+def test_attention_with_scales_near_zero(hy, dtype, scale):
+    """Scores of 1e37 times these scales are moderate numbers, or 0: every key counts.  A 32-bit sum of 64 products of
+    some 1e36 is off by at most 64 * 2^-24 of 1e38, 4e-5 in the exponent here; a denormal scale of 2e-39 is one of 1.4e6
+    steps, and 3e-7 off in itself."""
+    case = hybrid_ref.make_attention(lens=[(300, 3), (0, 20)], H_q=4, H_kv=2, d=64, P=16, dtype=dtype, seed=6, scale=scale)
+    case["q"] = case["q"] * 1e18
+    case["k_cache"].mul_(1e18)
+    o = base.run_attention(hy, case).double().cpu().numpy()
+    ref, vmax = hybrid_ref.attention(*(case[k] for k in ("q", "k_cache", "v_cache", "table", "ctx", "n", "start", "scale")))
+    tol = (2.0**-9 if dtype == BF16 else 0.0) * (vmax[..., None] + np.abs(ref)) + 1e-3 * vmax[..., None]
+    assert (np.abs(o - ref) <= tol).all()

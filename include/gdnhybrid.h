@@ -168,7 +168,7 @@ typedef struct gdn_paged_attn_args {
   int32_t max_pages, table_stride;
   int32_t n_q_rows;
   int32_t in_dtype;
-  float scale; /* finite */
+  float scale; /* finite, and scale * log2(e) too: up to 2.35e38 */
   const void* q;
   int64_t q_row_stride, q_head_stride;
   const void* k_cache;

@@ -15,6 +15,7 @@
 //   with many by shared-memory reads and the 32-bit multiply-adds (a 4096-token
 //   prefill at d = 128: 4.5 ms, 30 TFLOP/s of some 76).
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "attn_common.cuh"
@@ -245,10 +246,13 @@ int check_sizes(const gdn_paged_attn_args* a) {
   return GDN_OK;
 }
 
+float scale_log2(const gdn_paged_attn_args* a) { return (float)((double)a->scale * 1.4426950408889634); }
+
 int check(const gdn_paged_attn_args* a) {
   const int rc = check_sizes(a);
   if (rc != GDN_OK) return rc;
   if (!(a->scale - a->scale == 0.f)) return GDN_ERR_INVALID_ARG;  // not finite
+  if (!std::isfinite(scale_log2(a))) return GDN_ERR_UNSUPPORTED;
   if (a->B == 0 || a->n_q_rows == 0) return GDN_OK;
   if (!a->q || !a->k_cache || !a->v_cache || !a->block_table || !a->ctx_len || !a->n_rows || !a->o || !a->work)
     return GDN_ERR_INVALID_ARG;
@@ -288,7 +292,7 @@ extern "C" GDN_API int gdn_paged_attention(const gdn_paged_attn_args* a, void* s
   p.n_q_rows = a->n_q_rows;
   p.max_tokens = (int)std::min((int64_t)a->max_pages * a->page_size, (int64_t)kMaxIndex);
   p.max_rows = kMaxIndex / p.G;
-  p.scale_log2 = (float)((double)a->scale * 1.4426950408889634);
+  p.scale_log2 = scale_log2(a);
   p.by_G = make_div((uint32_t)p.G);
   p.by_page = make_div((uint32_t)p.page_size);
   p.q = a->q;

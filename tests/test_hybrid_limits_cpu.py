@@ -6,9 +6,10 @@ import os
 import subprocess
 import sys
 
+import pytest
 
 import test_hybrid_abi_cpu as base
-from test_hybrid_abi_cpu import append_args
+from test_hybrid_abi_cpu import append_args, attn_args
 
 hy = base.hy  # the module-wide fixture
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -29,3 +30,11 @@ def test_append_of_sizes_whose_product_passes_64_bits(hy, cuda_lib):
           "             dict(rows=2**31 - 1, H_kv=2**31 - 1, d=2**31 - 8)):\n"
           "    assert gdn._lib.gdn_kv_append(ctypes.byref(t.append_args(hybrid, **over)), None) == 2, over\n")
     assert cuda_lib._lib.gdn_kv_append(ctypes.byref(append_args(hy, rows=0)), None) == 0
+
+
+@pytest.mark.parametrize("dtype", [0, 1], ids=["bf16", "f32"])
+@pytest.mark.parametrize("scale", [2.4e38, -3.4e38])
+def test_attention_scales_beyond_the_exponent_of_two_are_refused(hy, cuda_lib, dtype, scale):
+    """Scores are kept in the exponent of 2: a scale that log2(e) carries past the 32-bit range would be infinite there."""
+    args = attn_args(hy, in_dtype=dtype, scale=scale)
+    assert cuda_lib._lib.gdn_paged_attention(ctypes.byref(args), None) == cuda_lib.ERR_UNSUPPORTED

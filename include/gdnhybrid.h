@@ -17,10 +17,11 @@
  * The paged cache.  K and V pools of n_pages pages, each page holding
  * page_size consecutive tokens of one request for all H_kv heads.  A pool is
  * addressed as base + page*page_stride + head*head_stride + token*token_stride
- * (strides in elements; the d elements of a token and head are contiguous), so
- * head-major [pages][H_kv][P][d], token-major [pages][P][H_kv][d] and pools
- * that interleave K and V are all the same call.  block_table[b][i] is the
- * page of request b's tokens i*P .. i*P+P-1; a slot is page*P + token.
+ * (strides in elements, not negative; the d elements of a token and head are
+ * contiguous), so head-major [pages][H_kv][P][d], token-major
+ * [pages][P][H_kv][d] and pools that interleave K and V are all the same call.
+ * block_table[b][i] is the page of request b's tokens i*P .. i*P+P-1; a slot is
+ * page*P + token.
  *
  * Rows.  A step's new tokens are rows of q, k, v and o.  Request b has
  * n_rows[b] of them (0 = inactive) behind ctx_len[b] tokens that the cache

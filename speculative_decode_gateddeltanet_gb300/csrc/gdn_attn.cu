@@ -262,6 +262,8 @@ int check(const gdn_paged_attn_args* a) {
                              a->v_page_stride, a->v_head_stride, a->v_token_stride, a->o_row_stride, a->o_head_stride};
   for (int64_t s : strides)
     if (s * size % 16 != 0) return GDN_ERR_MISALIGNED;
+  for (int i = 2; i < 8; ++i)  // the pools': a negative offset is a key that is not there
+    if (strides[i] < 0) return GDN_ERR_INVALID_ARG;
   auto al = [](const void* ptr, uintptr_t n) { return reinterpret_cast<uintptr_t>(ptr) % n == 0; };
   if (!al(a->q, 16) || !al(a->k_cache, 16) || !al(a->v_cache, 16) || !al(a->o, 16) || !al(a->work, 16) ||
       !al(a->block_table, 4) || !al(a->ctx_len, 4) || !al(a->n_rows, 4) || !al(a->row_start, 4) || !al(a->status, 4))

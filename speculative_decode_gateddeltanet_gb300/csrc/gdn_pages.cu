@@ -365,6 +365,8 @@ int check(const gdn_kv_append_args* a) {
                              a->v_page_stride, a->v_cache_head_stride, a->v_token_stride};
   for (int64_t s : strides)
     if (s * size % 16 != 0) return GDN_ERR_MISALIGNED;
+  for (int i = 4; i < 10; ++i)  // the pools': a negative offset is a row that is not written
+    if (strides[i] < 0) return GDN_ERR_INVALID_ARG;
   if (!aligned(a->k, 16) || !aligned(a->v, 16) || !aligned(a->k_cache, 16) || !aligned(a->v_cache, 16) ||
       !aligned(a->slot_map, 4) || !aligned(a->status, 4))
     return GDN_ERR_MISALIGNED;

@@ -38,3 +38,15 @@ def test_attention_scales_beyond_the_exponent_of_two_are_refused(hy, cuda_lib, d
     """Scores are kept in the exponent of 2: a scale that log2(e) carries past the 32-bit range would be infinite there."""
     args = attn_args(hy, in_dtype=dtype, scale=scale)
     assert cuda_lib._lib.gdn_paged_attention(ctypes.byref(args), None) == cuda_lib.ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("call,make,names", [
+    ("gdn_kv_append", append_args, ("k_page_stride", "k_cache_head_stride", "k_token_stride", "v_page_stride", "v_cache_head_stride", "v_token_stride")),
+    ("gdn_paged_attention", attn_args, ("k_page_stride", "k_head_stride", "k_token_stride", "v_page_stride", "v_head_stride", "v_token_stride"))])
+def test_negative_pool_strides_are_refused(hy, cuda_lib, call, make, names):
+    """Both calls mark a token without a place by a negative offset."""
+    for name in names:
+        for dtype in (0, 1):
+            args = make(hy, in_dtype=dtype)
+            setattr(args, name, -getattr(args, name))
+            assert getattr(cuda_lib._lib, call)(ctypes.byref(args), None) == cuda_lib.ERR_INVALID_ARG, (name, dtype)

@@ -94,8 +94,10 @@ def work_bytes(args: GdnArgs) -> int:
 
 
 def _stream(stream) -> int | None:
+    """The stream's handle; None: the current stream of the current device.  The small calls take about as long as a Python
+    stream object costs to make (2.9 us on a Grace core), so the current handle is asked for directly (0.1 us)."""
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) or None
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream or None
     return stream or None

@@ -13,7 +13,7 @@ import ctypes
 
 import torch
 
-from .gdn import BF16, F32, _check, _lib, _ptr
+from .gdn import BF16, F32, _check, _lib, _ptr, _stream
 
 STATUS_NO_PAGES, STATUS_TABLE_FULL, STATUS_BAD_PAGE, STATUS_BAD_LENGTH, STATUS_ROWS_FULL = 32, 64, 128, 256, 512
 SAMPLE_MAX_V = 393216
@@ -66,19 +66,6 @@ for _name, _args in (("gdn_page_map", GdnPageMapArgs), ("gdn_kv_append", GdnKvAp
     getattr(_lib, _name).restype = ctypes.c_int
 _lib.gdn_paged_attention_work_bytes.argtypes = [ctypes.POINTER(GdnPagedAttnArgs)]
 _lib.gdn_paged_attention_work_bytes.restype = ctypes.c_size_t
-
-
-_raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
-
-
-def _stream(stream) -> int | None:
-    """The stream's handle; None: the current stream of the current device.  The small calls here take about as long as
-    a Python stream object costs to make (2.9 us on a Grace core), so the current handle is asked for directly (0.1 us)."""
-    if stream is None:
-        return _raw_stream(_device()) or None
-    if isinstance(stream, torch.cuda.Stream):
-        return stream.cuda_stream or None
-    return stream or None
 
 
 def _dtype(t: torch.Tensor) -> int:

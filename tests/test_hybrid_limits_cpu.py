@@ -50,3 +50,13 @@ def test_negative_pool_strides_are_refused(hy, cuda_lib, call, make, names):
             args = make(hy, in_dtype=dtype)
             setattr(args, name, -getattr(args, name))
             assert getattr(cuda_lib._lib, call)(ctypes.byref(args), None) == cuda_lib.ERR_INVALID_ARG, (name, dtype)
+
+
+def test_the_bindings_load_where_pytorch_has_no_cuda():
+    """PyTorch builds without CUDA lack the private functions that a call looks its stream up with."""
+    fresh("import torch\n"
+          "for name in ('_cuda_getCurrentRawStream', '_cuda_getDevice'):\n"
+          "    if hasattr(torch._C, name):\n"
+          "        delattr(torch._C, name)\n"
+          "from speculative_decode_gateddeltanet_gb300 import gdn, hybrid\n"
+          "assert hybrid._stream is gdn._stream and gdn._stream(5) == 5 and gdn._stream(0) is None\n")

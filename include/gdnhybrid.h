@@ -48,8 +48,8 @@ enum {
                                   zeros (gdn_paged_attention)                            */
   GDN_STATUS_BAD_LENGTH = 256, /* a negative ctx_len, or more tokens than the table row
                                   or the rows of q hold: request skipped                 */
-  GDN_STATUS_ROWS_FULL = 512   /* packed rows beyond the row arrays: request not served
-                                  rows this step                                         */
+  GDN_STATUS_ROWS_FULL = 512   /* packed rows beyond the row arrays: the request, and any
+                                  behind it, gets no rows this step                      */
 };
 
 /* ---- page map: tables, slots and positions from request lengths -----------
@@ -71,13 +71,15 @@ enum {
  *   held_out   [B] int32        pages held after the call
  *   free_out   [2] int32        the ring's head and free pages after the call
  *   rows_out   [B] int32        rows served: n_rows[b], or 0 (not served)
- *   row_start  [B+1] int32      b*R, or the packed prefix of rows_out; [B] = all rows
+ *   row_start  [B+1] int32      b*R, or packed the prefix of the rows that pages sufficed for; [B] = all of them.
+ *              Rows beyond the row arrays (GDN_STATUS_ROWS_FULL) count here although rows_out does not have them
  *   slot_map, positions [n_slot_rows] int32   per row; -1 for rows of no token.  Padded: B*R of them;
  *              without either n_slot_rows does not matter
  *
- * held_out, free_out must not overlap held_in, free_in: a step's blocks read
- * the old counts while they write the new ones (keep two of each and
- * alternate; GDN_ERR_INVALID_ARG otherwise).  A negative ctx_len or n_rows, or n_rows > R
+ * held_out and rows_out must not overlap ctx_len, n_rows, held_in or free_in,
+ * nor free_out free_in: a step's blocks read the old counts while they write the
+ * new ones (keep two of held and free and alternate; GDN_ERR_INVALID_ARG
+ * otherwise).  A negative ctx_len or n_rows, or n_rows > R
  * when padded, leaves the request's pages as they are, rows_out 0
  * (GDN_STATUS_BAD_LENGTH, GDN_STATUS_BAD_NROWS).  Any output but
  * block_table, held_out, free_out, rows_out may be NULL.  With B = 0 the counts
@@ -187,8 +189,8 @@ typedef struct gdn_paged_attn_args {
 } gdn_paged_attn_args;
 GDN_API int gdn_paged_attention(const gdn_paged_attn_args* args, void* stream);
 
-/* Bytes of `work`: a function of d, in_dtype and the device's SM count, not of
- * the lengths.  0 if the sizes are unsupported or there is no device. */
+/* Bytes of `work`: a function of d and in_dtype alone.  0 if the sizes are
+ * unsupported. */
 GDN_API size_t gdn_paged_attention_work_bytes(const gdn_paged_attn_args* args);
 
 /* ---- acceptance of drafts against sampled target tokens --------------------

@@ -86,7 +86,9 @@ __device__ __forceinline__ Request request(const Params& p, int b, int* why = nu
   return r;
 }
 
-// sum over i in [0, n) of floor((a*i + b) / m), by the Euclidean descent on (m, a)
+// sum over i in [0, n) of floor((a*i + b) / m), the lattice points under a line: whole multiples of m are taken out of a
+// and b, the points under what is left are counted along the other axis.  That is Euclid's algorithm on (m, a); the
+// exchange of axes is the reciprocity law of floor sums (Graham, Knuth, Patashnik: Concrete Mathematics, section 3.5).
 __device__ inline long long floor_sum(long long n, long long m, long long a, long long b) {
   long long s = 0;
   while (n > 0) {
@@ -278,7 +280,9 @@ __device__ __forceinline__ float* partial(const Params& p, int block, int slot, 
   return p.partials + (size_t)(block * 2 + slot) * rows * (p.d + 2);
 }
 
-constexpr int kCombineWarps = 4;  // and eight blocks a tile: 4 lose 1 to 3 us where partials are many, 16 and 32 where few
+// And blocks a tile: eight for bf16 (4 lose 1 to 3 us where partials are many, 16 and 32 where few), four for the smaller
+// tiles of 32 bits.
+constexpr int kCombineWarps = 4;
 
 // Joins the partials of the split tile that block blockIdx.x of the attention
 // begins; gridDim.y blocks share its rows.  Up to eight partials: a warp per row,

@@ -11,9 +11,11 @@
 //   as few as the tile needs (64 requests of one token over 4000, 4 rows a head:
 //   907 us, with 8 rows a warp throughout 1549).  K and V are copied asynchronously,
 //   each under the other's products (436 us, copies waited for 907).
-//   With few rows it is bound by HBM (that case: 4.8 TB/s, 0.71 of a copy's rate),
-//   with many by shared-memory reads and the 32-bit multiply-adds (a 4096-token
-//   prefill at d = 128: 4.5 ms, 30 TFLOP/s of some 76).
+//   With few rows that case runs at 4.8 TB/s, 0.71 of a copy's rate: four block
+//   barriers for each 32 keys, and no more than a block of K and one of V on their
+//   way.  With many rows shared memory is the bound: eight rows of a warp take nine
+//   16-byte reads (12 wavefronts) for 32 multiply-adds, 48 clocks of the SM's for the
+//   four warps' 32 (a 4096-token prefill at d = 128: 4.5 ms, 30 TFLOP/s of some 76).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>

@@ -41,14 +41,14 @@
 // GDN_STATUS_TIMEOUT, waits (bounded) for its own copies and products in
 // flight, frees its TMEM and ends.
 //
-// Measured.  Prefill is bound by the chain of a block (scores, weights, products), of
-// which the softmax is the longest part: a 128-key unit takes 0.86 us, its MMAs 0.53
-// (8192 tokens at d = 128, 32 heads: 1.28 PFLOP/s, 0.68 of cuBLAS' bf16 rate; d = 256
-// 1.19, d = 64 0.76).  Decode is bound by HBM behind a start of some 4 us
+// Measured.  Prefill is bound by the chain of a block (scores, weights, products): a
+// 128-key unit takes 0.86 us, where its MMAs alone take 0.53 and its softmax alone 0.40,
+// so the two hardly overlap (8192 tokens at d = 128, 32 heads: 1.28 PFLOP/s, 0.69 of
+// cuBLAS' bf16 rate; d = 256 1.19, d = 64 0.76).  Decode is bound by HBM behind a start of some 4 us
 // (lengths, pages, the first copies) and an end of some 7 (tiles out, the join):
-// 256 ragged requests of 2 to 9 tokens 169 us (6.0 TB/s, 0.88 of a copy's rate), one
-// token over 65537 51 us (5.3 TB/s), 16 requests of 4 tokens over 1000 to 8000 at
-// d = 256 35.4 us (4.1 TB/s).
+// 256 ragged requests of 2 to 9 tokens 167 to 170 us (6.0 TB/s, 0.88 of a copy's rate),
+// one token over 65537 51 us (5.3 TB/s), 16 requests of 4 tokens over 1000 to 8000 at
+// d = 256 35.1 us (4.1 TB/s).
 #include <cuda.h>
 
 #include <limits>

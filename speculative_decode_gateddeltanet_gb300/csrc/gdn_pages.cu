@@ -8,12 +8,12 @@
 //   new table entries, returned pages and rows, each finding its request by a
 //   binary search of the prefix in shared memory.  A row's page is taken from
 //   the old table or straight from the ring, so no block reads what another
-//   writes.  16 requests take 3.8 us, 1024 with prompts among them 7.5; an empty
+//   writes.  16 requests take 3.9 us, 1024 with prompts among them 7.3; an empty
 //   launch takes 2.  (More blocks than SMs, or a search per row in global memory,
 //   only add to the chain of dependent reads.)
 // append_kernel: a copy, bound by HBM.  A thread moves one or four 16-byte chunks,
 //   all loads in flight before the first store.  16381 rows of 8 heads of 128 in 32
-//   bits take 41.7 us: 6.4 TB/s, 0.95 of a plain copy's rate.
+//   bits take 41.4 us: 6.5 TB/s, 0.96 of a plain copy's rate.
 #include <cuda_runtime.h>
 #include <stdint.h>
 

@@ -21,10 +21,13 @@
 //     the keys' own leading digits, spread the bulk of the logits over the bins,
 //     so few lanes of a warp add to the same one.  The kept weights are then
 //     summed in index order and the draw located.
-//   Bound by the chain of cluster barriers and by instructions, not by HBM.  Rows of
-//   151936 bf16, 64 of them (19.4 MB, 2.9 us of HBM): greedy 10 us, top-k 18, weights
-//   without a filter 34 (exp of every token, twice), top-p 63 (and the shared-memory
-//   atomics of the histogram).  One row of 32000: 4 to 16 us.
+//   Bound by instructions and by the chain of steps between cluster barriers, not by
+//   HBM.  Rows of 151936 bf16, 64 of them (19.4 MB, 2.9 us of HBM): greedy 10 us, a small
+//   top_k 18, weights without a filter 34 (exp of every token, twice), top-p 63 (and the
+//   shared-memory atomics of the histogram), a large top_k 68.  One row of 32000 in 32
+//   bits: 4, 9, 8, 17 and 29.  Of a row with a small top_k (12 us of the call's 18) the
+//   slices take 3.4 us, the bound 2.3, the list 3.5, the first block's two sorts, two
+//   scans and draw 2.7.
 // accept_kernel: one warp per request; where there are no drafts (R = 1) the rows'
 //   blocks write the accept lengths, 0, themselves.
 #include <cuda_bf16.h>

@@ -29,6 +29,8 @@
 
 namespace gdnattn {
 
+int check(const gdn_paged_attn_args* a);  // the host checks of gdn_paged_attention
+
 constexpr unsigned kFull = 0xffffffffu;
 // the kernels' positions and row numbers are 32-bit, and run up to a block past a request's last
 constexpr int kMaxIndex = INT32_MAX - 1023;

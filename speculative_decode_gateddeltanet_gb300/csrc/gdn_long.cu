@@ -1,0 +1,507 @@
+// Long contexts in the paged cache: argument checks and launches of the shared-prefix attention, the attention weights,
+// the choice of tokens that leave and their moves.  Simple kernels: one pass each, no tiles.
+#include <algorithm>
+#include <cmath>
+
+#include "attn_common.cuh"
+#include "gdnlong.h"
+
+namespace gdnlong {
+
+using gdnattn::Div;
+using gdnattn::kFull;
+using gdnattn::kMaxIndex;
+using gdnattn::launch;
+using gdnattn::make_div;
+using gdnattn::Params;
+using gdnattn::pdl_trigger;
+using gdnattn::pdl_wait;
+using gdnattn::quotient;
+using gdnattn::request;
+using gdnattn::Request;
+
+template <typename T>
+__device__ __forceinline__ float to_float(T x) {
+  if constexpr (sizeof(T) == 2) return __bfloat162float(x);
+  else return x;
+}
+
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) x += __shfl_xor_sync(kFull, x, off);
+  return x;
+}
+
+// ---- attention: a warp per row and head ----------------------------------------------------------------------------------
+
+template <typename T>
+__global__ void __launch_bounds__(128) attention_simple(const Params p, float* lse, int64_t lse_row, const int32_t* group_start, int n_groups) {
+  pdl_wait();
+  pdl_trigger();
+  if (blockIdx.x == 0 && blockIdx.y == 0)
+    for (int g = threadIdx.x; g < n_groups; g += 128)
+      if ((group_start[g] < 0 || group_start[g + 1] < group_start[g] || group_start[g + 1] > p.B) && p.status) atomicOr(p.status, GDN_STATUS_BAD_GROUP);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int H_q = p.H_kv * p.G, per = p.d / 32;
+  for (int b = blockIdx.y; b < p.B; b += gridDim.y) {
+    int why = 0;
+    const Request r = request(p, b, &why);
+    if (why && blockIdx.x == 0 && threadIdx.x == 0 && p.status) atomicOr(p.status, why);
+    const int32_t* const pages = p.table + (size_t)b * p.table_stride;
+    for (int64_t item = (int64_t)blockIdx.x * 4 + warp; item < (int64_t)r.n * H_q; item += (int64_t)gridDim.x * 4) {
+      const int t = (int)(item / H_q), head = (int)(item - (int64_t)t * H_q), h = head / p.G;
+      const T* const q = static_cast<const T*>(p.q) + (int64_t)(r.row0 + t) * p.q_row + (int64_t)head * p.q_head;
+      float x[8], acc[8] = {}, top = -INFINITY, sum = 0.f;
+      for (int c = 0; c < per; ++c) x[c] = to_float(q[c * 32 + lane]) * p.scale_log2;
+      for (int j = 0; j <= r.ctx + t; ++j) {
+        const int i = (int)quotient(j, p.by_page), page = pages[i], token = j - i * p.page_size;
+        const bool good = (unsigned)page < (unsigned)p.n_pages;
+        if (!good && lane == 0 && p.status) atomicOr(p.status, GDN_STATUS_BAD_PAGE);
+        const T* const k = static_cast<const T*>(p.k) + page * p.k_page + h * p.k_head + token * p.k_token;
+        const T* const v = static_cast<const T*>(p.v) + page * p.v_page + h * p.v_head + token * p.v_token;
+        float s = 0.f;
+        for (int c = 0; c < per; ++c) s = fmaf(x[c], good ? to_float(k[c * 32 + lane]) : 0.f, s);
+        s = warp_sum(s);
+        const float m = fmaxf(top, s), base = m == -INFINITY ? 0.f : m, shrink = exp2f(top - base), e = exp2f(s - base);
+        top = m;
+        sum = sum * shrink + e;
+        for (int c = 0; c < per; ++c) acc[c] = fmaf(e, good ? to_float(v[c * 32 + lane]) : 0.f, acc[c] * shrink);
+      }
+      T* const o = static_cast<T*>(p.o) + (int64_t)(r.row0 + t) * p.o_row + (int64_t)head * p.o_head;
+      for (int c = 0; c < per; ++c) {
+        if constexpr (sizeof(T) == 2) o[c * 32 + lane] = __float2bfloat16(acc[c] / sum);
+        else o[c * 32 + lane] = acc[c] / sum;
+      }
+      if (lse && lane == 0) lse[(int64_t)(r.row0 + t) * lse_row + head] = (top + log2f(sum)) * 0.6931471805599453f;
+    }
+  }
+}
+
+// ---- weights: a warp per cached token --------------------------------------------------------------------------------------
+
+struct WeightParams {
+  Params p;  // o, v and the join's fields unused
+  float scale, keep;
+  int fresh;
+  const float* lse;
+  int64_t lse_row;
+  const int32_t *first, *position;
+  float* weight;
+  int32_t* born;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(128) weight_simple(const WeightParams w) {
+  pdl_wait();
+  pdl_trigger();
+  const Params& p = w.p;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, per = p.d / 32;
+  for (int b = blockIdx.y; b < p.B; b += gridDim.y) {
+    int why = 0;
+    const Request r = request(p, b, &why);
+    if (why && blockIdx.x == 0 && threadIdx.x == 0 && p.status) atomicOr(p.status, why);
+    if (r.n <= 0) continue;
+    const int first = w.first ? max(w.first[b], 0) : 0, len = r.ctx + r.n;
+    const int start = w.fresh && w.born ? min(first, r.ctx) : first;
+    for (int64_t j64 = start + (int64_t)blockIdx.x * 4 + warp; j64 < len; j64 += (int64_t)gridDim.x * 4) {
+      const int j = (int)j64, i = (int)quotient(j, p.by_page), page = p.table[(size_t)b * p.table_stride + i], token = j - i * p.page_size;
+      if ((unsigned)page >= (unsigned)p.n_pages) {
+        if (lane == 0 && p.status) atomicOr(p.status, GDN_STATUS_BAD_PAGE);
+        continue;
+      }
+      const int slot = page * p.page_size + token;
+      if (w.fresh && w.born && j >= r.ctx && lane == 0) w.born[slot] = (w.position ? w.position[b] : r.ctx) + j - r.ctx;
+      if (j < first) continue;
+      float got = 0.f;
+      for (int h = 0; h < p.H_kv; ++h) {
+        const T* const k = static_cast<const T*>(p.k) + page * p.k_page + h * p.k_head + token * p.k_token;
+        float x[8];
+        for (int c = 0; c < per; ++c) x[c] = to_float(k[c * 32 + lane]);
+        for (int t = max(0, j - r.ctx); t < r.n; ++t)
+          for (int g = 0; g < p.G; ++g) {
+            const T* const q = static_cast<const T*>(p.q) + (int64_t)(r.row0 + t) * p.q_row + (int64_t)(h * p.G + g) * p.q_head;
+            float s = 0.f;
+            for (int c = 0; c < per; ++c) s = fmaf(x[c], to_float(q[c * 32 + lane]), s);
+            got += expf(warp_sum(s) * w.scale - w.lse[(int64_t)(r.row0 + t) * w.lse_row + h * p.G + g]);
+          }
+      }
+      if (lane == 0) w.weight[slot] = w.fresh && j >= r.ctx ? got : fmaf(w.keep, w.weight[slot], got);
+    }
+  }
+}
+
+// ---- the choice: a block per request -----------------------------------------------------------------------------------------
+
+constexpr int kSelectThreads = 1024;
+
+// weights as whole numbers in the same order; NaN as -infinity, -0 as 0
+__device__ __forceinline__ uint32_t weight_key(float x) {
+  if (x != x) x = -INFINITY;
+  const uint32_t u = __float_as_uint(x + 0.f);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+// sums over the block's threads before this one, and in all
+__device__ __forceinline__ int block_before(int x, int* part, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int inc = x;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int v = __shfl_up_sync(kFull, inc, off);
+    if (lane >= off) inc += v;
+  }
+  if (lane == 31) part[warp] = inc;
+  __syncthreads();
+  int before = inc - x, all = 0;
+  for (int w = 0; w < kSelectThreads / 32; ++w) {
+    if (w < warp) before += part[w];
+    all += part[w];
+  }
+  __syncthreads();
+  *total = all;
+  return before;
+}
+
+__global__ void __launch_bounds__(kSelectThreads) select_simple(const gdn_evict_args p, const Div by_page) {
+  __shared__ int part[kSelectThreads / 32], hist[256], found[2], bad_page;
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x;
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+    const int L = p.ctx_len[b], budget = max(p.budget[b], 0), pinned = p.pinned ? max(p.pinned[b], 0) : 0;
+    const int keep_from = p.keep_from && p.born ? p.keep_from[b] : INT32_MAX;
+    const bool bound = p.keep_from && p.born;
+    const int32_t* const pages = p.block_table + (size_t)b * p.table_stride;
+    __syncthreads();
+    if (tid == 0) bad_page = 0;
+    __syncthreads();
+    const bool bad_length = L < 0 || L > (int64_t)p.max_pages * p.page_size;
+    if (!bad_length)
+      for (int i = tid; i < (L + p.page_size - 1) / p.page_size; i += kSelectThreads)
+        if ((unsigned)pages[i] >= (unsigned)p.n_pages) bad_page = 1;
+    __syncthreads();
+    if (bad_length || bad_page) {
+      if (tid == 0) {
+        p.ctx_out[b] = L;
+        p.n_moves[b] = 0;
+        if (p.status) atomicOr(p.status, bad_length ? GDN_STATUS_BAD_LENGTH : GDN_STATUS_BAD_PAGE);
+      }
+      continue;
+    }
+    auto slot_of = [&](int j) {
+      const int i = (int)quotient(j, by_page);
+      return pages[i] * p.page_size + j - i * p.page_size;
+    };
+    auto may_go = [&](int j, int slot) { return j >= pinned && (!bound || p.born[slot] < keep_from); };
+    int mine = 0, n_may;
+    for (int64_t j = tid; j < L; j += kSelectThreads) mine += may_go((int)j, slot_of((int)j));
+    block_before(mine, part, &n_may);
+    const int go = min(max(L - budget, 0), n_may), K = L - go;
+    // the go-th lightest key, eight bits at a time: `low` keys are lighter, and `ties` of those that equal it leave too
+    uint32_t key = 0, mask = 0;
+    int ties = go;
+    for (int shift = 24; shift >= 0 && go > 0; shift -= 8) {
+      for (int i = tid; i < 256; i += kSelectThreads) hist[i] = 0;
+      __syncthreads();
+      for (int64_t j = tid; j < L; j += kSelectThreads) {
+        const int slot = slot_of((int)j);
+        if (!may_go((int)j, slot)) continue;
+        const uint32_t k = weight_key(p.weight[slot]);
+        if ((k & mask) == key) atomicAdd(&hist[k >> shift & 255], 1);
+      }
+      __syncthreads();
+      if (tid == 0) {
+        int i = 0, left = ties;
+        while (left > hist[i]) left -= hist[i++];
+        found[0] = i;
+        found[1] = left;
+      }
+      __syncthreads();
+      key |= (uint32_t)found[0] << shift;
+      mask |= 255u << shift;
+      ties = found[1];
+    }
+    int equal = 0, n_equal;
+    for (int64_t j = tid; j < L && go > 0; j += kSelectThreads) {
+      const int slot = slot_of((int)j);
+      equal += may_go((int)j, slot) && weight_key(p.weight[slot]) == key;
+    }
+    block_before(equal, part, &n_equal);
+    int64_t done_equal = 0, gaps = 0, movers = 0;
+    // twice: the number of moves first, then the lists
+    for (int round = 0; round < 2; ++round) {
+      const int64_t moves = gaps;
+      if (round == 1 && moves > p.max_moves) break;
+      done_equal = gaps = movers = 0;
+      for (int64_t j0 = 0; j0 < L && go > 0; j0 += kSelectThreads) {
+        const int64_t j = j0 + tid;
+        const int slot = j < L ? slot_of((int)j) : 0;
+        const bool may = j < L && may_go((int)j, slot);
+        const uint32_t k = may ? weight_key(p.weight[slot]) : 0;
+        int n;
+        const int tie_at = block_before(may && k == key, part, &n);
+        const bool goes = may && (k < key || (k == key && done_equal + tie_at >= n_equal - ties));
+        done_equal += n;
+        const bool gap = goes && j < K, mover = j < L && !goes && j >= K;
+        const int gap_at = block_before(gap, part, &n);
+        if (round == 1 && gap) p.move_to[(size_t)b * p.max_moves + gaps + gap_at] = slot;
+        gaps += n;
+        const int mover_at = block_before(mover, part, &n);
+        if (round == 1 && mover) p.move_from[(size_t)b * p.max_moves + movers + mover_at] = slot;
+        movers += n;
+      }
+      if (round == 1 || moves > 0) continue;
+    }
+    const bool full = gaps > p.max_moves;
+    __syncthreads();
+    if (!full)
+      for (int64_t i = tid; i < gaps; i += kSelectThreads) {
+        const int from = p.move_from[(size_t)b * p.max_moves + i], to = p.move_to[(size_t)b * p.max_moves + i];
+        p.weight[to] = p.weight[from];
+        if (p.born) p.born[to] = p.born[from];
+      }
+    if (tid == 0) {
+      p.ctx_out[b] = full ? L : K;
+      p.n_moves[b] = full ? 0 : (int)gaps;
+      if (full && p.status) atomicOr(p.status, GDN_STATUS_MOVES_FULL);
+    }
+  }
+}
+
+// ---- moves -----------------------------------------------------------------------------------------------------------------
+
+struct MoveParams {
+  int B, max_moves, n_slots, chunks, H_kv;
+  Div page;
+  int page_size;
+  const int32_t *from, *to, *n;
+  uint4 *k, *v;  // strides in 16-byte chunks
+  int64_t k_page, k_head, k_token, v_page, v_head, v_token;
+  int32_t* status;
+};
+
+__global__ void __launch_bounds__(128) move_simple(const MoveParams p) {
+  pdl_wait();
+  pdl_trigger();
+  for (int b = blockIdx.y; b < p.B; b += gridDim.y) {
+    const int n = p.n[b];
+    if (n < 0 || n > p.max_moves) {
+      if (blockIdx.x == 0 && threadIdx.x == 0 && p.status) atomicOr(p.status, GDN_STATUS_BAD_LENGTH);
+      continue;
+    }
+    for (int i = blockIdx.x; i < n; i += gridDim.x) {
+      const int from = p.from[(size_t)b * p.max_moves + i], to = p.to[(size_t)b * p.max_moves + i];
+      if ((unsigned)from >= (unsigned)p.n_slots || (unsigned)to >= (unsigned)p.n_slots) {
+        if (threadIdx.x == 0 && p.status) atomicOr(p.status, GDN_STATUS_BAD_PAGE);
+        continue;
+      }
+      const int from_page = (int)quotient(from, p.page), from_token = from - from_page * p.page_size;
+      const int to_page = (int)quotient(to, p.page), to_token = to - to_page * p.page_size;
+      for (int x = threadIdx.x; x < 2 * p.H_kv * p.chunks; x += 128) {
+        const bool is_v = x >= p.H_kv * p.chunks;
+        const int y = is_v ? x - p.H_kv * p.chunks : x, h = y / p.chunks, c = y - h * p.chunks;
+        uint4* const pool = is_v ? p.v : p.k;
+        const int64_t page = is_v ? p.v_page : p.k_page, head = is_v ? p.v_head : p.k_head, token = is_v ? p.v_token : p.k_token;
+        pool[to_page * page + h * head + to_token * token + c] = pool[from_page * page + h * head + from_token * token + c];
+      }
+    }
+  }
+}
+
+// ---- host --------------------------------------------------------------------------------------------------------------------
+
+bool aligned(const void* ptr, uintptr_t n) { return reinterpret_cast<uintptr_t>(ptr) % n == 0; }
+float log2_of(float scale) { return (float)((double)scale * 1.4426950408889634); }
+
+int check_sizes(const gdn_shared_attn_args* a) {
+  if (!a) return GDN_ERR_INVALID_ARG;
+  if (gdn_paged_attention_work_bytes(&a->attn) == 0) return GDN_ERR_UNSUPPORTED;
+  if (a->n_groups < 0 || a->reserved != 0) return GDN_ERR_INVALID_ARG;
+  if (a->attn.B > 4096 || a->n_groups > 1024) return GDN_ERR_UNSUPPORTED;
+  return GDN_OK;
+}
+
+Params params_of(const gdn_paged_attn_args* a) {
+  Params p = {};
+  p.B = a->B;
+  p.R = a->R;
+  p.H_kv = a->H_kv;
+  p.G = a->H_q / a->H_kv;
+  p.d = a->d;
+  p.page_size = a->page_size;
+  p.n_pages = a->n_pages;
+  p.table_stride = a->table_stride;
+  p.n_q_rows = a->n_q_rows;
+  p.max_tokens = (int)std::min((int64_t)a->max_pages * a->page_size, (int64_t)kMaxIndex);
+  p.max_rows = kMaxIndex / p.G;
+  p.scale_log2 = log2_of(a->scale);
+  p.by_G = make_div((uint32_t)p.G);
+  p.by_page = make_div((uint32_t)p.page_size);
+  p.q = a->q;
+  p.q_row = a->q_row_stride;
+  p.q_head = a->q_head_stride;
+  p.k = a->k_cache;
+  p.k_page = a->k_page_stride;
+  p.k_head = a->k_head_stride;
+  p.k_token = a->k_token_stride;
+  p.v = a->v_cache;
+  p.v_page = a->v_page_stride;
+  p.v_head = a->v_head_stride;
+  p.v_token = a->v_token_stride;
+  p.table = a->block_table;
+  p.ctx_len = a->ctx_len;
+  p.n_rows = a->n_rows;
+  p.row_start = a->row_start;
+  p.o = a->o;
+  p.o_row = a->o_row_stride;
+  p.o_head = a->o_head_stride;
+  p.status = a->status;
+  return p;
+}
+
+}  // namespace gdnlong
+
+using namespace gdnlong;
+
+extern "C" GDN_API size_t gdn_shared_attention_work_bytes(const gdn_shared_attn_args* args) {
+  return check_sizes(args) == GDN_OK ? gdn_paged_attention_work_bytes(&args->attn) : 0;
+}
+
+extern "C" GDN_API int gdn_shared_attention(const gdn_shared_attn_args* a, void* stream) {
+  const int rc = a ? gdnattn::check(&a->attn) : (int)GDN_ERR_INVALID_ARG;
+  if (rc != GDN_OK) return rc;
+  if (const int rc2 = check_sizes(a); rc2 != GDN_OK) return rc2;
+  if (a->attn.B == 0 || a->attn.n_q_rows == 0) return GDN_OK;
+  if (a->n_groups > 0 && (!a->group_start || !a->prefix_len)) return GDN_ERR_INVALID_ARG;
+  if (a->lse && a->lse_row_stride < a->attn.H_q) return GDN_ERR_INVALID_ARG;
+  if (!aligned(a->group_start, 4) || !aligned(a->prefix_len, 4) || !aligned(a->lse, 4)) return GDN_ERR_MISALIGNED;
+  const Params p = params_of(&a->attn);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const dim3 grid(256, std::min(p.B, 1024));
+  return a->attn.in_dtype == GDN_DTYPE_BF16 ? launch(attention_simple<__nv_bfloat16>, grid, dim3(128), 0, st, p, a->lse, a->lse_row_stride, a->group_start, a->n_groups)
+                                            : launch(attention_simple<float>, grid, dim3(128), 0, st, p, a->lse, a->lse_row_stride, a->group_start, a->n_groups);
+}
+
+namespace gdnlong {
+
+// the attention's checks on what the two calls share
+gdn_paged_attn_args as_attention(const gdn_attn_weight_args* a) {
+  gdn_paged_attn_args t = {};
+  t.B = a->B;
+  t.R = a->R;
+  t.H_q = a->H_q;
+  t.H_kv = a->H_kv;
+  t.d = a->d;
+  t.page_size = a->page_size;
+  t.n_pages = a->n_pages;
+  t.max_pages = a->max_pages;
+  t.table_stride = a->table_stride;
+  t.n_q_rows = a->n_q_rows;
+  t.in_dtype = a->in_dtype;
+  t.scale = a->scale;
+  t.q = a->q;
+  t.q_row_stride = a->q_row_stride;
+  t.q_head_stride = a->q_head_stride;
+  t.k_cache = t.v_cache = a->k_cache;
+  t.k_page_stride = t.v_page_stride = a->k_page_stride;
+  t.k_head_stride = t.v_head_stride = a->k_head_stride;
+  t.k_token_stride = t.v_token_stride = a->k_token_stride;
+  t.block_table = a->block_table;
+  t.ctx_len = a->ctx_len;
+  t.n_rows = a->n_rows;
+  t.row_start = a->row_start;
+  t.o = a->work;  // nothing is written through it
+  t.work = a->work;
+  t.status = a->status;
+  return t;
+}
+
+}  // namespace gdnlong
+
+extern "C" GDN_API size_t gdn_attn_weight_work_bytes(const gdn_attn_weight_args* args) {
+  if (!args) return 0;
+  const gdn_paged_attn_args t = as_attention(args);
+  return gdn_paged_attention_work_bytes(&t) ? 16 : 0;
+}
+
+extern "C" GDN_API int gdn_attn_weight(const gdn_attn_weight_args* a, void* stream) {
+  if (!a) return GDN_ERR_INVALID_ARG;
+  const gdn_paged_attn_args t = as_attention(a);
+  const int rc = gdnattn::check(&t);
+  if (rc != GDN_OK) return rc;
+  if ((a->fresh != 0 && a->fresh != 1) || !std::isfinite(a->keep)) return GDN_ERR_INVALID_ARG;
+  if (a->B == 0 || a->n_q_rows == 0) return GDN_OK;
+  if (!a->lse || !a->weight || a->lse_row_stride < a->H_q) return GDN_ERR_INVALID_ARG;
+  if (!aligned(a->lse, 4) || !aligned(a->first, 4) || !aligned(a->position, 4) || !aligned(a->weight, 4) || !aligned(a->born, 4))
+    return GDN_ERR_MISALIGNED;
+  WeightParams w = {};
+  w.p = params_of(&t);
+  w.scale = a->scale;
+  w.keep = a->keep;
+  w.fresh = a->fresh;
+  w.lse = a->lse;
+  w.lse_row = a->lse_row_stride;
+  w.first = a->first;
+  w.position = a->position;
+  w.weight = a->weight;
+  w.born = a->born;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const dim3 grid(256, std::min(a->B, 1024));
+  return a->in_dtype == GDN_DTYPE_BF16 ? launch(weight_simple<__nv_bfloat16>, grid, dim3(128), 0, st, w)
+                                       : launch(weight_simple<float>, grid, dim3(128), 0, st, w);
+}
+
+extern "C" GDN_API int gdn_evict_select(const gdn_evict_args* a, void* stream) {
+  if (!a) return GDN_ERR_INVALID_ARG;
+  if (a->B < 0 || a->page_size < 1 || a->n_pages < 1 || a->max_pages < 0 || a->table_stride < a->max_pages || a->max_moves < 0)
+    return GDN_ERR_INVALID_ARG;
+  if (a->B > 65535 || (int64_t)a->n_pages * a->page_size > INT32_MAX || (int64_t)a->B * a->max_moves > INT32_MAX) return GDN_ERR_UNSUPPORTED;
+  if (a->B == 0) return GDN_OK;
+  if (!a->block_table || !a->ctx_len || !a->budget || !a->weight || !a->ctx_out || !a->n_moves || (a->max_moves > 0 && (!a->move_from || !a->move_to)))
+    return GDN_ERR_INVALID_ARG;
+  const void* all[] = {a->block_table, a->ctx_len, a->budget, a->pinned, a->keep_from, a->weight, a->born, a->ctx_out, a->n_moves, a->move_from, a->move_to, a->status};
+  for (const void* ptr : all)
+    if (!aligned(ptr, 4)) return GDN_ERR_MISALIGNED;
+  return launch(select_simple, dim3(a->B), dim3(kSelectThreads), 0, static_cast<cudaStream_t>(stream), *a, make_div((uint32_t)a->page_size));
+}
+
+extern "C" GDN_API int gdn_kv_move(const gdn_kv_move_args* a, void* stream) {
+  if (!a) return GDN_ERR_INVALID_ARG;
+  if (a->B < 0 || a->max_moves < 0 || a->H_kv < 1 || a->d < 1 || a->page_size < 1 || a->n_pages < 1 || a->reserved != 0) return GDN_ERR_INVALID_ARG;
+  if (a->in_dtype != GDN_DTYPE_BF16 && a->in_dtype != GDN_DTYPE_F32) return GDN_ERR_UNSUPPORTED;
+  const int size = a->in_dtype == GDN_DTYPE_BF16 ? 2 : 4, per16 = 16 / size;
+  if ((int64_t)a->d * size % 16 != 0 || (int64_t)a->H_kv * (a->d / per16) > INT32_MAX / 2 || (int64_t)a->n_pages * a->page_size > INT32_MAX ||
+      a->B > 65535 || (int64_t)a->B * a->max_moves > INT32_MAX)
+    return GDN_ERR_UNSUPPORTED;
+  if (a->B == 0 || a->max_moves == 0) return GDN_OK;
+  if (!a->move_from || !a->move_to || !a->n_moves || !a->k_cache || !a->v_cache) return GDN_ERR_INVALID_ARG;
+  const int64_t strides[] = {a->k_page_stride, a->k_head_stride, a->k_token_stride, a->v_page_stride, a->v_head_stride, a->v_token_stride};
+  for (int64_t s : strides) {
+    if (s * size % 16 != 0) return GDN_ERR_MISALIGNED;
+    if (s < 0) return GDN_ERR_INVALID_ARG;
+  }
+  if (!aligned(a->k_cache, 16) || !aligned(a->v_cache, 16) || !aligned(a->move_from, 4) || !aligned(a->move_to, 4) || !aligned(a->n_moves, 4) ||
+      !aligned(a->status, 4))
+    return GDN_ERR_MISALIGNED;
+  MoveParams p = {};
+  p.B = a->B;
+  p.max_moves = a->max_moves;
+  p.n_slots = a->n_pages * a->page_size;
+  p.chunks = a->d / per16;
+  p.H_kv = a->H_kv;
+  p.page = make_div((uint32_t)a->page_size);
+  p.page_size = a->page_size;
+  p.from = a->move_from;
+  p.to = a->move_to;
+  p.n = a->n_moves;
+  p.k = static_cast<uint4*>(a->k_cache);
+  p.v = static_cast<uint4*>(a->v_cache);
+  p.k_page = a->k_page_stride / per16;
+  p.k_head = a->k_head_stride / per16;
+  p.k_token = a->k_token_stride / per16;
+  p.v_page = a->v_page_stride / per16;
+  p.v_head = a->v_head_stride / per16;
+  p.v_token = a->v_token_stride / per16;
+  p.status = a->status;
+  return launch(move_simple, dim3(std::min(a->max_moves, 256), std::min(a->B, 1024)), dim3(128), 0, static_cast<cudaStream_t>(stream), p);
+}

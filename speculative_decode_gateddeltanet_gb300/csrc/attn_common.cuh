@@ -25,11 +25,10 @@
 
 #include <type_traits>
 
-#include "gdnhybrid.h"
+#include "gdnlong.h"
 
 namespace gdnattn {
 
-int check(const gdn_paged_attn_args* a);  // the host checks of gdn_paged_attention
 
 constexpr unsigned kFull = 0xffffffffu;
 // the kernels' positions and row numbers are 32-bit, and run up to a block past a request's last
@@ -68,8 +67,40 @@ struct Params {
   int n_blocks;     // blocks of the attention launch
 };
 
+// of gdn_paged_attention: its host checks, and the parameters but for the work buffer
+int check(const gdn_paged_attn_args* a);
+Params params_of(const gdn_paged_attn_args* a);
+
+struct Nothing {};
+
+// What a shared call has beside them.
+struct SharedParams {
+  int n_groups, key_align;  // a request's own keys begin at a multiple of key_align
+  const int32_t *group_start, *prefix_len;
+  float* lse;
+  int64_t lse_row;
+  float* dense;   // [2][n_q_rows * H_q][d]: first parts of prefixes and of requests, unnormalised
+  int4* entries;  // [2][n_q_rows * H_q]: a first part's maximum and sum, its block, and entry_word
+};
+
 struct Request {
   int ctx, n, row0;
+  static constexpr bool kFlat = false;
+  __device__ int flat() const { return 0; }
+  __device__ int len() const { return ctx + n; }                   // its keys' end
+  __device__ int last(int token) const { return ctx + token; }     // the last key that a row sees
+};
+
+// A line of a shared call: a request's rows over its own keys, or the rows of a group over its prefix.  Keys count from
+// k0; the first `front` of them are the prefix's still.
+struct Line {
+  int ctx, n, row0;  // group: prefix - 1, the rows of all its requests, the rank of the first among all such rows
+  int k0, front;
+  int b;       // table row
+  int prefix;  // request: tokens of its shared prefix; group: -1
+  __device__ int flat() const { return prefix < 0; }
+  __device__ int len() const { return prefix < 0 ? ctx + 1 : ctx + n; }
+  __device__ int last(int token) const { return prefix < 0 ? ctx : ctx + token; }
 };
 
 // request b's lengths; n = 0 where it takes no part
@@ -113,10 +144,11 @@ __device__ inline long long floor_sum(long long n, long long m, long long a, lon
   return s;
 }
 
-template <int kRows, int kKeys>
+template <int kRows, int kKeys, typename R = Request>
 struct Tiles {
-  __device__ static int count(const Params& p, const Request& r) { return (int)(((unsigned long long)r.n * p.G + kRows - 1) / kRows); }
-  __device__ static int blocks(const Params& p, const Request& r, int m) {
+  __device__ static int count(const Params& p, const R& r) { return (int)(((unsigned long long)r.n * p.G + kRows - 1) / kRows); }
+  __device__ static int blocks(const Params& p, const R& r, int m) {
+    if (r.flat()) return (int)((unsigned)r.ctx / kKeys) + 1;
     const long long last = min((long long)(m + 1) * kRows, (long long)r.n * p.G) - 1;
     const int token = last >> 31 ? (int)(last / p.G) : (int)quotient((uint32_t)last, p.by_G);
     return (int)((unsigned)(r.ctx + token) / kKeys) + 1;
@@ -127,24 +159,74 @@ struct Tiles {
   // ragged requests 172 with 3, 177 with 6.
   static constexpr int kExtra = kRows < 128 ? 0 : kKeys == 64 ? 5 : 3;
   // units of the tiles before m
-  __device__ static long long before(const Params& p, const Request& r, int m) {
+  __device__ static long long before(const Params& p, const R& r, int m) {
     if (m == 0) return 0;
+    if (r.flat()) return (long long)m * (blocks(p, r, 0) + kExtra);
     return (long long)m * (1 + kExtra) + floor_sum(m, (long long)p.G * kKeys, kRows, (long long)p.G * r.ctx + kRows - 1);
   }
   // units of one kv head of the request
-  __device__ static long long sum(const Params& p, const Request& r) {
+  __device__ static long long sum(const Params& p, const R& r) {
     if (r.n <= 0) return 0;
     const int M = count(p, r);
     return before(p, r, M - 1) + kExtra + blocks(p, r, M - 1);
   }
 };
 
+// Every line of a shared call, from its lengths and groups in shared memory.
+struct Lines {
+  int B, G;            // requests, then groups: line v < B is request v's
+  const int* starts;   // [G + 1]
+  const int* prefix;   // [G] tokens that the group's requests read together; 0: none
+  const int* rows;     // [B + 1] rows before request b of those that take part in a prefix
+  // the group that request b is in, or -1
+  __device__ int group_of(int b) const {
+    if (G == 0 || b < starts[0] || b >= starts[G]) return -1;
+    int lo = 0, hi = G;  // starts[lo] <= b < starts[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (starts[mid] <= b) lo = mid;
+      else hi = mid;
+    }
+    return lo;
+  }
+  // the request whose counted rows hold that rank
+  __device__ int request_of(int rank) const {
+    int lo = 0, hi = B;  // rows[lo] <= rank < rows[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (rows[mid] <= rank) lo = mid;
+      else hi = mid;
+    }
+    return lo;
+  }
+  __device__ Line own(const Request& r, int b, int align) const {
+    const int g = r.n > 0 ? group_of(b) : -1;
+    int L = g >= 0 ? prefix[g] : 0;
+    if (r.ctx < L) L = 0;
+    const int k0 = L - L % align;
+    return {r.ctx - k0, r.n, r.row0, k0, L - k0, b, L};
+  }
+  __device__ Line group(int g) const {
+    if (prefix[g] == 0) return {0, 0, 0, 0, 0, 0, -1};
+    const int first = rows[starts[g]];
+    return {prefix[g] - 1, rows[starts[g + 1]] - first, first, 0, 0, request_of(first), -1};
+  }
+  __device__ Line line(const Params& p, int v, int align) const { return v < B ? own(request(p, v), v, align) : group(v - B); }
+  // row of q and o of a line's token
+  __device__ int row_of(const Params& p, const Line& l, int token) const {
+    if (!l.flat()) return l.row0 + token;
+    const int rank = l.row0 + token, b = request_of(rank);
+    return (p.row_start ? p.row_start[b] : b * p.R) + rank - rows[b];
+  }
+};
+
 // one block's walk over its units, tile by tile
-template <int kRows, int kKeys>
+template <int kRows, int kKeys, bool kShared = false>
 struct Walk {
-  using T = Tiles<kRows, kKeys>;
-  Request req;
-  int b, h, m, tiles, left;  // left: units still to do
+  using R = std::conditional_t<kShared, Line, Request>;
+  using T = Tiles<kRows, kKeys, R>;
+  R req;
+  int b, h, m, tiles, left;  // b: request or line; left: units still to do
   int at;                    // the segment's first unit within its tile: the tile's own units come first
   int kb0, kb1, blocks;      // its key blocks, and how many the whole tile has
 
@@ -165,23 +247,36 @@ struct Walk {
       if (++h == p->H_kv) {
         h = 0;
         do {
-          req = request(*p, ++b);
+          if constexpr (kShared) req = lines->line(*p, ++b, align);
+          else req = request(*p, ++b);
         } while (req.n <= 0);
         tiles = T::count(*p, req);
       }
     }
     segment();
   }
+  __device__ int table_row() const {
+    if constexpr (kShared) return req.b;
+    else return b;
+  }
+  __device__ int first_key() const {
+    if constexpr (kShared) return req.k0;
+    else return 0;
+  }
   const Params* p;
+  const Lines* lines;
+  int align;
 };
 
-struct Start {
+template <typename R>
+struct StartOf {
   long long total;  // units of the call
   long long off;    // units from the first request's first to the block's first
   long long head;   // units of one kv head of that request
-  Request req;      // the request the block begins in
+  R req;            // the request the block begins in
   int b, per;
 };
+using Start = StartOf<Request>;
 
 // Every thread of the block calls this; all get the block's first unit.  scan:
 // kThreads/32 words of shared memory.  The thread that meets the block's first
@@ -244,9 +339,133 @@ __device__ __forceinline__ void find_start(const Params& p, int min_units, long 
   __syncthreads();
 }
 
-template <int kRows, int kKeys>
-__device__ __forceinline__ bool begin(Walk<kRows, kKeys>& w, const Params& p, const Start& s) {
-  using T = Tiles<kRows, kKeys>;
+// Words of shared memory that a shared call's lines take.
+constexpr int kMaxSharedB = 4096, kMaxGroups = 1024, kMaxLinesWords = kMaxSharedB + 2 * kMaxGroups + 2;
+inline size_t lines_words(int B, int n_groups) { return (size_t)B + 2 * (size_t)n_groups + 2; }
+
+// find_start for the lines of a shared call.  at: lines_words of shared memory, filled here; scan: 3 * kThreads/32 words.
+// Where group_start does not rise within [0, B], or the counted rows pass 32 bits, no prefix is shared, and what is
+// computed is the same.
+template <int kRows, int kKeys, int kThreads>
+__device__ __forceinline__ Lines find_lines(const Params& p, const SharedParams& sp, int min_units, int* at, long long* scan,
+                                            StartOf<Line>* out) {
+  using T = Tiles<kRows, kKeys, Line>;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int each = (p.B + kThreads - 1) / kThreads, b0 = tid * each, b1 = min(p.B, b0 + each);
+  int* const starts = at;
+  int* const prefix = starts + sp.n_groups + 1;
+  int* const rows = prefix + sp.n_groups;
+  int why = 0;
+  Request first = {0, 0, 0};
+  if (b0 < b1) first = request(p, b0, &why);
+  int broken = 0;
+  for (int g = tid; g <= sp.n_groups && sp.n_groups > 0; g += kThreads) {
+    const int x = sp.group_start[g], y = g < sp.n_groups ? sp.group_start[g + 1] : p.B;
+    starts[g] = x;
+    if (g < sp.n_groups) prefix[g] = max(sp.prefix_len[g], 0);
+    broken |= x < 0 || x > y || y > p.B;
+  }
+  broken = __syncthreads_or(broken);
+  if (broken && blockIdx.x == 0 && tid == 0 && p.status) atomicOr(p.status, GDN_STATUS_BAD_GROUP);
+  Lines lines = {p.B, broken ? 0 : sp.n_groups, starts, prefix, rows};
+  // exclusive sum of x over the threads, and the whole sum
+  auto sums = [&](long long x, long long* part, long long* total) {
+    long long inc = x;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long v = __shfl_up_sync(kFull, inc, off);
+      if (lane >= off) inc += v;
+    }
+    if (lane == 31) part[warp] = inc;
+    __syncthreads();
+    long long before = inc - x, all = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += part[w];
+      all += part[w];
+    }
+    *total = all;
+    return before;
+  };
+  if (lines.G > 0) {
+    auto counted = [&](const Request& r, int b) {
+      const int g = r.n > 0 ? lines.group_of(b) : -1;
+      return g >= 0 && prefix[g] > 0 && r.ctx >= prefix[g] ? r.n : 0;
+    };
+    long long mine = 0, total;
+    for (int b = b0; b < b1; ++b) mine += counted(b == b0 ? first : request(p, b, &why), b);
+    long long before = sums(mine, scan, &total);
+    if (total > min(p.max_rows, kMaxIndex)) {
+      lines.G = 0;  // uniform
+    } else {
+      for (int b = b0; b < b1; ++b) {
+        rows[b] = (int)before;
+        before += counted(b == b0 ? first : request(p, b), b);
+      }
+      if (tid == 0) rows[p.B] = (int)total;
+      __syncthreads();
+      // a prefix of one request is its own affair
+      for (int g = tid; g < lines.G; g += kThreads) {
+        const int n = rows[starts[g + 1]] - rows[starts[g]];
+        bool alone = n == 0;
+        if (n > 0) {
+          const int b = lines.request_of(rows[starts[g]]);
+          alone = rows[b + 1] - rows[b] == n;
+        }
+        if (alone) prefix[g] = 0;
+      }
+      __syncthreads();
+    }
+  } else {
+    for (int b = b0 + 1; b < b1; ++b) request(p, b, &why);
+  }
+  if (why && blockIdx.x == 0 && p.status) atomicOr(p.status, why);
+  long long mine = 0, mine_g = 0, head = 0, total, total_g = 0;
+  Line l = {};
+  for (int b = b0; b < b1; ++b) {
+    l = lines.own(b == b0 ? first : request(p, b), b, sp.key_align);
+    head = T::sum(p, l);
+    mine += p.H_kv * head;
+  }
+  const int each_g = (lines.G + kThreads - 1) / kThreads, g0 = tid * each_g, g1 = min(lines.G, g0 + each_g);
+  for (int g = g0; g < g1; ++g) mine_g += p.H_kv * T::sum(p, lines.group(g));
+  const long long mine_at = sums(mine, scan + kThreads / 32, &total);
+  long long g_at = 0;
+  if (lines.G > 0) g_at = sums(mine_g, scan + 2 * (kThreads / 32), &total_g) + total;
+  total += total_g;
+  const long long per = max(total >> 31 ? (total + p.n_blocks - 1) / p.n_blocks
+                                        : (long long)(((uint32_t)total + (uint32_t)p.n_blocks - 1) / (uint32_t)p.n_blocks),
+                            (long long)min_units);
+  const long long want = per * blockIdx.x;
+  if (tid == 0) {
+    out->total = total;
+    out->per = (int)min(per, (long long)INT32_MAX);
+  }
+  // one thread at most finds the block's first unit in its part, of requests or of groups
+  const bool in_own = want >= mine_at && want < mine_at + mine, in_group = want >= g_at && want < g_at + mine_g;
+  if (in_own || in_group) {
+    long long off = want - (in_own ? mine_at : g_at);
+    int v = in_own ? b0 : p.B + g0;
+    if (in_group || each > 1) {
+      for (;; ++v) {
+        l = lines.line(p, v, sp.key_align);
+        head = T::sum(p, l);
+        if (off < p.H_kv * head) break;
+        off -= p.H_kv * head;
+      }
+    }
+    out->b = v;
+    out->off = off;
+    out->head = head;
+    out->req = l;
+  }
+  __syncthreads();
+  return lines;
+}
+
+template <int kRows, int kKeys, bool kShared, typename S>
+__device__ __forceinline__ bool begin(Walk<kRows, kKeys, kShared>& w, const Params& p, const S& s) {
+  using T = typename Walk<kRows, kKeys, kShared>::T;
   w.p = &p;
   const long long first = (long long)s.per * blockIdx.x;
   w.left = (int)max(0ll, min((long long)s.per, s.total - first));
@@ -277,6 +496,19 @@ __device__ __forceinline__ int4 note_of(const Walk<kRows, kKeys>& w, const Start
   const int rows = (int)min((long long)kRows, (long long)w.req.n * w.p->G - (long long)w.m * kRows);
   return {followers, w.req.row0, w.h << 8 | rows, w.m * kRows};
 }
+
+// What a first part's entry says beside its maximum, sum and block: the blocks that follow, its row in the tile, whether
+// the row has a part over a prefix, and whether the row is done.
+constexpr int kEntryPrefix = 1 << 24, kEntryDone = 1 << 25;
+__device__ __forceinline__ int entry_word(int followers, int row, bool prefix, bool done) {
+  return followers | row << 16 | (prefix ? kEntryPrefix : 0) | (done ? kEntryDone : 0);
+}
+// blocks after the segment's that share its tile
+template <typename W, typename S>
+__device__ __forceinline__ int followers_of(const W& w, const S& s) {
+  return (w.blocks - w.kb1 + s.per - 1) / s.per;
+}
+constexpr float kLn2 = 0.693147180559945309f;
 
 __device__ __forceinline__ float* partial(const Params& p, int block, int slot, int rows) {
   return p.partials + (size_t)(block * 2 + slot) * rows * (p.d + 2);
@@ -412,6 +644,156 @@ __global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const Param
     }
     __syncthreads();
   }
+}
+
+// A shared call's rows: each joins the parts of its request's own keys and of its prefix, first parts at the row's place
+// in `dense`, others with the block that made them, in that order.  A warp takes a row, or the block's four warps one row
+// where it has more than eight parts.
+template <typename T, int kD, int kRows>
+__global__ void __launch_bounds__(32 * kCombineWarps) combine_shared(const Params p, const SharedParams sp) {
+  constexpr int kPer = kD / 32, kBatch = 8;
+  __shared__ float sums[kCombineWarps][kD];
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, H_q = p.H_kv * p.G;
+  const size_t places = (size_t)p.n_q_rows * H_q;
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+    const Request r = request(p, b);
+    const long long items = (long long)r.n * H_q;
+    for (long long item0 = (long long)blockIdx.y * kCombineWarps; item0 < items; item0 += (long long)gridDim.y * kCombineWarps) {
+      const int here = (int)min((long long)kCombineWarps, items - item0);
+      // what a row's join needs: its place, its entries and its number of parts
+      struct Row {
+        size_t at;
+        int token, head, parts_own, parts;
+        int4 own, pre;
+      };
+      auto row_of = [&](int i) {
+        Row x;
+        const long long item = item0 + i;
+        x.token = (int)(item / H_q);
+        x.head = (int)(item - (long long)x.token * H_q);
+        x.at = (size_t)(r.row0 + x.token) * H_q + x.head;
+        x.own = sp.entries[places + x.at];
+        x.pre = make_int4(0, 0, 0, 0);
+        const bool prefix = x.own.w & kEntryPrefix;
+        if (prefix) x.pre = sp.entries[x.at];
+        x.parts_own = x.own.w & kEntryDone ? 0 : 1 + (x.own.w & 0xffff);
+        x.parts = x.parts_own + (prefix ? 1 + (x.pre.w & 0xffff) : 0);
+        // where a block gave up, a row's entry may be anything
+        auto inside = [&](const int4& e) { return e.z >= 0 && e.z < p.n_blocks && (e.w & 0xffff) < p.n_blocks - e.z && (e.w >> 16 & 255) < kRows; };
+        if (!inside(x.own) || (prefix && !inside(x.pre))) x.parts = 0;
+        return x;
+      };
+      // part i of a row: its columns, and its maximum and sum
+      auto tail = [&](const int4& e, int i) { return partial(p, e.z + i, 0, kRows); };
+      auto columns = [&](const Row& x, int i) -> const float* {
+        const bool own = i < x.parts_own;
+        const int4& e = own ? x.own : x.pre;
+        const int k = own ? i : i - x.parts_own;
+        if (k == 0) return sp.dense + ((own ? places : 0) + x.at) * kD;
+        return tail(e, k) + (size_t)(e.w >> 16 & 255) * kD;
+      };
+      auto stats = [&](const Row& x, int i) -> float2 {
+        const bool own = i < x.parts_own;
+        const int4& e = own ? x.own : x.pre;
+        const int k = own ? i : i - x.parts_own;
+        if (k == 0) return make_float2(__int_as_float(e.x), __int_as_float(e.y));
+        return reinterpret_cast<const float2*>(tail(e, k) + (size_t)kRows * kD)[e.w >> 16 & 255];
+      };
+      auto load = [&](float (&v)[kPer], const float* src) {
+#pragma unroll
+        for (int c = 0; c < kPer / 2; ++c) {
+          const float2 y = *reinterpret_cast<const float2*>(src + c * 64 + lane * 2);
+          v[2 * c] = y.x;
+          v[2 * c + 1] = y.y;
+        }
+      };
+      auto write = [&](const Row& x, const float (&acc)[kPer], float top, float sum) {
+        const float inv = 1.f / sum;
+        T* const dst = static_cast<T*>(p.o) + (int64_t)(r.row0 + x.token) * p.o_row + (int64_t)x.head * p.o_head + lane * 2;
+#pragma unroll
+        for (int c = 0; c < kPer / 2; ++c) {
+          const float a = acc[2 * c] * inv, z = acc[2 * c + 1] * inv;
+          if constexpr (sizeof(T) == 2) *reinterpret_cast<__nv_bfloat162*>(dst + c * 64) = __floats2bfloat162_rn(a, z);
+          else *reinterpret_cast<float2*>(dst + c * 64) = make_float2(a, z);
+        }
+        if (sp.lse && lane == 0) sp.lse[(int64_t)(r.row0 + x.token) * sp.lse_row + x.head] = (top + log2f(sum)) * kLn2;
+      };
+      // parts i0, i0 + step, ... of a row into acc
+      auto add = [&](const Row& x, float top, int i0, int step, float (&acc)[kPer]) {
+        for (int j0 = i0; j0 < x.parts; j0 += step * kBatch) {
+          float v[kBatch][kPer], weight[kBatch];
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j) {
+            const int i = min(j0 + j * step, x.parts - 1);
+            weight[j] = j0 + j * step < x.parts ? exp2f(stats(x, i).x - top) : 0.f;
+            load(v[j], columns(x, i));
+          }
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j) {
+            if (j0 + j * step >= x.parts) break;
+#pragma unroll
+            for (int c = 0; c < kPer; ++c) acc[c] = fmaf(weight[j], v[j][c], acc[c]);
+          }
+        }
+      };
+      // a row's maximum and sum
+      auto total = [&](const Row& x, float* sum) {
+        float top = -INFINITY;
+        for (int i = lane; i < x.parts; i += 32) top = fmaxf(top, stats(x, i).x);
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
+        const float base = top == -INFINITY ? 0.f : top;
+        float s = 0.f;
+        for (int i = lane; i < x.parts; i += 32) {
+          const float2 st = stats(x, i);
+          s += st.y * exp2f(st.x - base);
+        }
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) s += __shfl_xor_sync(kFull, s, off);
+        *sum = s;
+        return base;
+      };
+      const Row mine = row_of(min(warp, here - 1));
+      if (!__syncthreads_or(mine.parts > kBatch)) {
+        if (warp < here && mine.parts > 0) {
+          float sum, acc[kPer] = {};
+          const float top = total(mine, &sum);
+          add(mine, top, 0, 1, acc);
+          write(mine, acc, top, sum);
+        }
+        continue;
+      }
+      for (int i = 0; i < here; ++i) {
+        const Row x = row_of(i);
+        if (x.parts == 0) continue;  // the same for all warps
+        float sum, acc[kPer] = {};
+        const float top = total(x, &sum);
+        add(x, top, warp, kCombineWarps, acc);
+        __syncthreads();
+#pragma unroll
+        for (int c = 0; c < kPer / 2; ++c)
+          *reinterpret_cast<float2*>(&sums[warp][c * 64 + lane * 2]) = make_float2(acc[2 * c], acc[2 * c + 1]);
+        __syncthreads();
+        if (warp == 0) {
+#pragma unroll
+          for (int c = 0; c < kPer; ++c) {
+            acc[c] = 0.f;
+            for (int w = 0; w < kCombineWarps; ++w) acc[c] += sums[w][(c / 2) * 64 + lane * 2 + (c & 1)];
+          }
+          write(x, acc, top, sum);
+        }
+      }
+    }
+  }
+}
+
+// blocks of the join: a request's rows are shared by as many as give the GPU some 16 warps an SM
+inline dim3 combine_shared_grid(const Params& p) {
+  const long long rows = (long long)p.n_q_rows * p.H_kv * p.G, per = (rows / p.B + kCombineWarps) / kCombineWarps;
+  const long long most = p.B >= 1024 ? 1 : 1024 / p.B + 1;
+  return dim3(p.B, (unsigned)(per < most ? per : most));
 }
 
 template <typename Kernel, typename... Args>

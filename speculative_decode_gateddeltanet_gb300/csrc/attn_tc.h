@@ -4,7 +4,9 @@
 
 namespace gdnattn {
 struct Params;
+struct SharedParams;
 int tc_blocks();  // blocks of its launch
 int tc_rows();    // rows of its tiles
 int run_tc(Params& p, cudaStream_t st);
+int run_shared_tc(const Params& p, const SharedParams& sp, cudaStream_t st);
 }  // namespace gdnattn

@@ -1,5 +1,5 @@
-// Long contexts in the paged cache: argument checks and launches of the shared-prefix attention, the attention weights,
-// the choice of tokens that leave and their moves.  Simple kernels: one pass each, no tiles.
+// Eviction from the paged cache: argument checks and launches of the attention weights, the choice of tokens that leave and
+// their moves.  Simple kernels: one pass each, no tiles.
 #include <algorithm>
 #include <cmath>
 
@@ -14,6 +14,7 @@ using gdnattn::kMaxIndex;
 using gdnattn::launch;
 using gdnattn::make_div;
 using gdnattn::Params;
+using gdnattn::params_of;
 using gdnattn::pdl_trigger;
 using gdnattn::pdl_wait;
 using gdnattn::quotient;
@@ -30,51 +31,6 @@ __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) x += __shfl_xor_sync(kFull, x, off);
   return x;
-}
-
-// ---- attention: a warp per row and head ----------------------------------------------------------------------------------
-
-template <typename T>
-__global__ void __launch_bounds__(128) attention_simple(const Params p, float* lse, int64_t lse_row, const int32_t* group_start, int n_groups) {
-  pdl_wait();
-  pdl_trigger();
-  if (blockIdx.x == 0 && blockIdx.y == 0)
-    for (int g = threadIdx.x; g < n_groups; g += 128)
-      if ((group_start[g] < 0 || group_start[g + 1] < group_start[g] || group_start[g + 1] > p.B) && p.status) atomicOr(p.status, GDN_STATUS_BAD_GROUP);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int H_q = p.H_kv * p.G, per = p.d / 32;
-  for (int b = blockIdx.y; b < p.B; b += gridDim.y) {
-    int why = 0;
-    const Request r = request(p, b, &why);
-    if (why && blockIdx.x == 0 && threadIdx.x == 0 && p.status) atomicOr(p.status, why);
-    const int32_t* const pages = p.table + (size_t)b * p.table_stride;
-    for (int64_t item = (int64_t)blockIdx.x * 4 + warp; item < (int64_t)r.n * H_q; item += (int64_t)gridDim.x * 4) {
-      const int t = (int)(item / H_q), head = (int)(item - (int64_t)t * H_q), h = head / p.G;
-      const T* const q = static_cast<const T*>(p.q) + (int64_t)(r.row0 + t) * p.q_row + (int64_t)head * p.q_head;
-      float x[8], acc[8] = {}, top = -INFINITY, sum = 0.f;
-      for (int c = 0; c < per; ++c) x[c] = to_float(q[c * 32 + lane]) * p.scale_log2;
-      for (int j = 0; j <= r.ctx + t; ++j) {
-        const int i = (int)quotient(j, p.by_page), page = pages[i], token = j - i * p.page_size;
-        const bool good = (unsigned)page < (unsigned)p.n_pages;
-        if (!good && lane == 0 && p.status) atomicOr(p.status, GDN_STATUS_BAD_PAGE);
-        const T* const k = static_cast<const T*>(p.k) + page * p.k_page + h * p.k_head + token * p.k_token;
-        const T* const v = static_cast<const T*>(p.v) + page * p.v_page + h * p.v_head + token * p.v_token;
-        float s = 0.f;
-        for (int c = 0; c < per; ++c) s = fmaf(x[c], good ? to_float(k[c * 32 + lane]) : 0.f, s);
-        s = warp_sum(s);
-        const float m = fmaxf(top, s), base = m == -INFINITY ? 0.f : m, shrink = exp2f(top - base), e = exp2f(s - base);
-        top = m;
-        sum = sum * shrink + e;
-        for (int c = 0; c < per; ++c) acc[c] = fmaf(e, good ? to_float(v[c * 32 + lane]) : 0.f, acc[c] * shrink);
-      }
-      T* const o = static_cast<T*>(p.o) + (int64_t)(r.row0 + t) * p.o_row + (int64_t)head * p.o_head;
-      for (int c = 0; c < per; ++c) {
-        if constexpr (sizeof(T) == 2) o[c * 32 + lane] = __float2bfloat16(acc[c] / sum);
-        else o[c * 32 + lane] = acc[c] / sum;
-      }
-      if (lse && lane == 0) lse[(int64_t)(r.row0 + t) * lse_row + head] = (top + log2f(sum)) * 0.6931471805599453f;
-    }
-  }
 }
 
 // ---- weights: a warp per cached token --------------------------------------------------------------------------------------
@@ -311,78 +267,6 @@ __global__ void __launch_bounds__(128) move_simple(const MoveParams p) {
 // ---- host --------------------------------------------------------------------------------------------------------------------
 
 bool aligned(const void* ptr, uintptr_t n) { return reinterpret_cast<uintptr_t>(ptr) % n == 0; }
-float log2_of(float scale) { return (float)((double)scale * 1.4426950408889634); }
-
-int check_sizes(const gdn_shared_attn_args* a) {
-  if (!a) return GDN_ERR_INVALID_ARG;
-  if (gdn_paged_attention_work_bytes(&a->attn) == 0) return GDN_ERR_UNSUPPORTED;
-  if (a->n_groups < 0 || a->reserved != 0) return GDN_ERR_INVALID_ARG;
-  if (a->attn.B > 4096 || a->n_groups > 1024) return GDN_ERR_UNSUPPORTED;
-  return GDN_OK;
-}
-
-Params params_of(const gdn_paged_attn_args* a) {
-  Params p = {};
-  p.B = a->B;
-  p.R = a->R;
-  p.H_kv = a->H_kv;
-  p.G = a->H_q / a->H_kv;
-  p.d = a->d;
-  p.page_size = a->page_size;
-  p.n_pages = a->n_pages;
-  p.table_stride = a->table_stride;
-  p.n_q_rows = a->n_q_rows;
-  p.max_tokens = (int)std::min((int64_t)a->max_pages * a->page_size, (int64_t)kMaxIndex);
-  p.max_rows = kMaxIndex / p.G;
-  p.scale_log2 = log2_of(a->scale);
-  p.by_G = make_div((uint32_t)p.G);
-  p.by_page = make_div((uint32_t)p.page_size);
-  p.q = a->q;
-  p.q_row = a->q_row_stride;
-  p.q_head = a->q_head_stride;
-  p.k = a->k_cache;
-  p.k_page = a->k_page_stride;
-  p.k_head = a->k_head_stride;
-  p.k_token = a->k_token_stride;
-  p.v = a->v_cache;
-  p.v_page = a->v_page_stride;
-  p.v_head = a->v_head_stride;
-  p.v_token = a->v_token_stride;
-  p.table = a->block_table;
-  p.ctx_len = a->ctx_len;
-  p.n_rows = a->n_rows;
-  p.row_start = a->row_start;
-  p.o = a->o;
-  p.o_row = a->o_row_stride;
-  p.o_head = a->o_head_stride;
-  p.status = a->status;
-  return p;
-}
-
-}  // namespace gdnlong
-
-using namespace gdnlong;
-
-extern "C" GDN_API size_t gdn_shared_attention_work_bytes(const gdn_shared_attn_args* args) {
-  return check_sizes(args) == GDN_OK ? gdn_paged_attention_work_bytes(&args->attn) : 0;
-}
-
-extern "C" GDN_API int gdn_shared_attention(const gdn_shared_attn_args* a, void* stream) {
-  const int rc = a ? gdnattn::check(&a->attn) : (int)GDN_ERR_INVALID_ARG;
-  if (rc != GDN_OK) return rc;
-  if (const int rc2 = check_sizes(a); rc2 != GDN_OK) return rc2;
-  if (a->attn.B == 0 || a->attn.n_q_rows == 0) return GDN_OK;
-  if (a->n_groups > 0 && (!a->group_start || !a->prefix_len)) return GDN_ERR_INVALID_ARG;
-  if (a->lse && a->lse_row_stride < a->attn.H_q) return GDN_ERR_INVALID_ARG;
-  if (!aligned(a->group_start, 4) || !aligned(a->prefix_len, 4) || !aligned(a->lse, 4)) return GDN_ERR_MISALIGNED;
-  const Params p = params_of(&a->attn);
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const dim3 grid(256, std::min(p.B, 1024));
-  return a->attn.in_dtype == GDN_DTYPE_BF16 ? launch(attention_simple<__nv_bfloat16>, grid, dim3(128), 0, st, p, a->lse, a->lse_row_stride, a->group_start, a->n_groups)
-                                            : launch(attention_simple<float>, grid, dim3(128), 0, st, p, a->lse, a->lse_row_stride, a->group_start, a->n_groups);
-}
-
-namespace gdnlong {
 
 // the attention's checks on what the two calls share
 gdn_paged_attn_args as_attention(const gdn_attn_weight_args* a) {
@@ -417,6 +301,8 @@ gdn_paged_attn_args as_attention(const gdn_attn_weight_args* a) {
 }
 
 }  // namespace gdnlong
+
+using namespace gdnlong;
 
 extern "C" GDN_API size_t gdn_attn_weight_work_bytes(const gdn_attn_weight_args* args) {
   if (!args) return 0;

@@ -1,0 +1,54 @@
+// gdn_shared_attention: argument checks and the launches.
+#include "attn_simt.cuh"
+#include "attn_tc.h"
+#include "gdnlong.h"
+
+namespace gdnattn {
+
+int check_sizes(const gdn_shared_attn_args* a) {
+  if (!a || a->n_groups < 0 || a->reserved != 0) return GDN_ERR_INVALID_ARG;
+  if (a->attn.B > kMaxSharedB || a->n_groups > kMaxGroups) return GDN_ERR_UNSUPPORTED;
+  return GDN_OK;
+}
+
+int check(const gdn_shared_attn_args* a) {
+  int rc = check_sizes(a);
+  if (rc == GDN_OK) rc = check(&a->attn);
+  if (rc != GDN_OK || a->attn.B == 0 || a->attn.n_q_rows == 0) return rc;
+  if (a->n_groups > 0 && (!a->group_start || !a->prefix_len)) return GDN_ERR_INVALID_ARG;
+  if (a->lse && a->lse_row_stride < a->attn.H_q) return GDN_ERR_INVALID_ARG;
+  auto al = [](const void* ptr) { return reinterpret_cast<uintptr_t>(ptr) % 4 == 0; };
+  return al(a->group_start) && al(a->prefix_len) && al(a->lse) ? GDN_OK : GDN_ERR_MISALIGNED;
+}
+
+// first parts of prefixes and of requests, one of each for a row and head
+size_t places(const gdn_paged_attn_args& a) { return 2 * (size_t)a.n_q_rows * a.H_q; }
+
+}  // namespace gdnattn
+
+using namespace gdnattn;
+
+// the attention's partials, and for every place its columns and its entry
+extern "C" GDN_API size_t gdn_shared_attention_work_bytes(const gdn_shared_attn_args* args) {
+  if (check_sizes(args) != GDN_OK) return 0;
+  const size_t partials = gdn_paged_attention_work_bytes(&args->attn);
+  return partials == 0 ? 0 : partials + places(args->attn) * (args->attn.d * sizeof(float) + sizeof(int4));
+}
+
+extern "C" GDN_API int gdn_shared_attention(const gdn_shared_attn_args* a, void* stream) {
+  const int rc = check(a);
+  if (rc != GDN_OK || a->attn.B == 0 || a->attn.n_q_rows == 0) return rc;
+  Params p = params_of(&a->attn);
+  SharedParams sp = {};
+  sp.n_groups = a->n_groups;
+  sp.key_align = 1;
+  sp.group_start = a->group_start;
+  sp.prefix_len = a->prefix_len;
+  sp.lse = a->lse;
+  sp.lse_row = a->lse_row_stride;
+  sp.entries = static_cast<int4*>(a->attn.work);
+  sp.dense = reinterpret_cast<float*>(sp.entries + places(a->attn));
+  p.partials = sp.dense + places(a->attn) * p.d;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return a->attn.in_dtype == GDN_DTYPE_BF16 ? run_shared_tc(p, sp, st) : run_simt<true>(p, sp, st);
+}

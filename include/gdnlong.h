@@ -59,7 +59,7 @@ enum {
  *                NULL: not wanted.  Rows of no request are not written
  *
  * Arithmetic, waits and limits are gdn_paged_attention's; lse is 32-bit
- * throughout.  Supported beside that: B <= 4096, n_groups <= 1024. */
+ * throughout.  Supported beside that: B <= 4096, n_groups <= 512. */
 typedef struct gdn_shared_attn_args {
   gdn_paged_attn_args attn;
   int32_t n_groups;

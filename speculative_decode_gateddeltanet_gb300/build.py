@@ -22,7 +22,7 @@ LIB = PKG / "_lib" / "libgdnspec.so"
 # test that makes the bounded wait run out; never loaded by the package
 TEST_HOOKS_LIB = PKG / "_lib" / "libgdnspec_testhooks.so"
 TEST_HOOKS_FLAGS = ["-DGDN_TEST_HOOKS", "-DGDN_WAIT_LIMIT_NS=2000000ull"]
-# the same for the tensor-core attention
+# the same for the tensor-core attention; prefixes are shared whatever it costs
 ATTN_TEST_HOOKS_LIB = PKG / "_lib" / "libgdnhybrid_testhooks.so"
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMPILE_FLAGS = ARCH + [
@@ -82,7 +82,7 @@ def build_test_hooks(force: bool = False) -> Path:
 def build_attn_test_hooks(force: bool = False) -> Path:
     """Compile the test-only variant of the attention calls if it is missing
     or older than its sources."""
-    src = [PKG / "csrc" / "gdn_attn.cu", PKG / "csrc" / "gdn_attn_tc.cu"]
+    src = [PKG / "csrc" / f"{name}.cu" for name in ("gdn_attn", "gdn_attn_tc", "gdn_shared", "gdn_shared_tc")]
     if not force and not stale(ATTN_TEST_HOOKS_LIB, src):
         return ATTN_TEST_HOOKS_LIB
     return _compile(ATTN_TEST_HOOKS_LIB, src, TEST_HOOKS_FLAGS)

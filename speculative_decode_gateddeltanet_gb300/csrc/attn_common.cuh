@@ -70,6 +70,7 @@ struct Params {
 // of gdn_paged_attention: its host checks, and the parameters but for the work buffer
 int check(const gdn_paged_attn_args* a);
 Params params_of(const gdn_paged_attn_args* a);
+void set_work(Params& p, int dtype, void* work);  // notes and partials, gdn_paged_attention_work_bytes
 
 struct Nothing {};
 
@@ -79,8 +80,11 @@ struct SharedParams {
   const int32_t *group_start, *prefix_len;
   float* lse;
   int64_t lse_row;
-  float* dense;   // [2][n_q_rows * H_q][d]: first parts of prefixes and of requests, unnormalised
-  int4* entries;  // [2][n_q_rows * H_q]: a first part's maximum and sum, its block, and entry_word
+  // rows that take part in a prefix, which are ranked request by request:
+  float* dense;       // [2][n_q_rows * H_q][d]: first parts over prefixes and over own keys, unnormalised
+  int4* entries;      // [2][n_q_rows * H_q]: a first part's maximum and sum, its block, and entry_word
+  int* rank_row;      // [n_q_rows] each rank's row, or -1
+  int* count;         // ranks
 };
 
 struct Request {
@@ -158,23 +162,28 @@ struct Tiles {
   // 5, 39.2 with 3 or 4, 36.1 with 10; prompt chunks of up to 4096 485 with 3, 493 with 2, 516 with 1, 504 with 6; 256
   // ragged requests 172 with 3, 177 with 6.
   static constexpr int kExtra = kRows < 128 ? 0 : kKeys == 64 ? 5 : 3;
+  __device__ static int extra(const Params& p, const Request&) { return kExtra; }
+  // In a shared call (128-key blocks: requests' tiles, prefixes' tiles) 64 single tokens behind 32768 take 99.4 us with 5 and
+  // 3, 106 with 3 and 3, 105 with 8 and 3; 16 requests of 4 tokens behind 8011 at d = 256 31.7 with 5 and 8, 34.0 with 5 and 5.
+  __device__ static int extra(const Params& p, const Line& l) { return kExtra == 0 ? 0 : kKeys == 64 && l.flat() ? 8 : 5 - 2 * l.flat(); }
   // units of the tiles before m
   __device__ static long long before(const Params& p, const R& r, int m) {
     if (m == 0) return 0;
-    if (r.flat()) return (long long)m * (blocks(p, r, 0) + kExtra);
-    return (long long)m * (1 + kExtra) + floor_sum(m, (long long)p.G * kKeys, kRows, (long long)p.G * r.ctx + kRows - 1);
+    if (r.flat()) return (long long)m * (blocks(p, r, 0) + extra(p, r));
+    return (long long)m * (1 + extra(p, r)) + floor_sum(m, (long long)p.G * kKeys, kRows, (long long)p.G * r.ctx + kRows - 1);
   }
   // units of one kv head of the request
   __device__ static long long sum(const Params& p, const R& r) {
     if (r.n <= 0) return 0;
     const int M = count(p, r);
-    return before(p, r, M - 1) + kExtra + blocks(p, r, M - 1);
+    return before(p, r, M - 1) + extra(p, r) + blocks(p, r, M - 1);
   }
 };
 
 // Every line of a shared call, from its lengths and groups in shared memory.
 struct Lines {
   int B, G;            // requests, then groups: line v < B is request v's
+  int most;            // rows of a request that takes part in a prefix
   const int* starts;   // [G + 1]
   const int* prefix;   // [G] tokens that the group's requests read together; 0: none
   const int* rows;     // [B + 1] rows before request b of those that take part in a prefix
@@ -199,15 +208,16 @@ struct Lines {
     }
     return lo;
   }
-  __device__ Line own(const Request& r, int b, int align) const {
-    const int g = r.n > 0 ? group_of(b) : -1;
-    int L = g >= 0 ? prefix[g] : 0;
-    if (r.ctx < L) L = 0;
+  __device__ Line own(const Request& r, int b, int align, int L) const {
     const int k0 = L - L % align;
     return {r.ctx - k0, r.n, r.row0, k0, L - k0, b, L};
   }
+  __device__ Line own(const Request& r, int b, int align) const {
+    const int g = r.n > 0 ? group_of(b) : -1, L = g >= 0 ? prefix[g] : 0;
+    return own(r, b, align, r.ctx < L || r.n > most ? 0 : L);
+  }
   __device__ Line group(int g) const {
-    if (prefix[g] == 0) return {0, 0, 0, 0, 0, 0, -1};
+    if (prefix[g] == 0 || rows[starts[g + 1]] == rows[starts[g]]) return {0, 0, 0, 0, 0, 0, -1};
     const int first = rows[starts[g]];
     return {prefix[g] - 1, rows[starts[g + 1]] - first, first, 0, 0, request_of(first), -1};
   }
@@ -232,14 +242,14 @@ struct Walk {
 
   __device__ void segment() {
     blocks = T::blocks(*p, req, m);
-    const int end = min(T::kExtra + blocks, at + left);
-    kb0 = max(0, at - T::kExtra);
-    kb1 = end - T::kExtra;
+    const int extra = T::extra(*p, req), end = min(extra + blocks, at + left);
+    kb0 = max(0, at - extra);
+    kb1 = end - extra;
     if (kb1 <= kb0) left = 0;  // the block's part ends before the tile's first key block
   }
   __device__ bool done() const { return left <= 0; }
   __device__ void next() {
-    left -= kb1 + T::kExtra - at;
+    left -= kb1 + T::extra(*p, req) - at;
     if (left <= 0) return;
     at = 0;
     if (++m == tiles) {
@@ -340,34 +350,73 @@ __device__ __forceinline__ void find_start(const Params& p, int min_units, long 
 }
 
 // Words of shared memory that a shared call's lines take.
-constexpr int kMaxSharedB = 4096, kMaxGroups = 1024, kMaxLinesWords = kMaxSharedB + 2 * kMaxGroups + 2;
-inline size_t lines_words(int B, int n_groups) { return (size_t)B + 2 * (size_t)n_groups + 2; }
+constexpr int kMaxSharedB = 4096, kMaxGroups = 512;
+constexpr int lines_words(int B, int n_groups) { return B + 4 * n_groups + 2; }
+constexpr int kMaxLinesWords = lines_words(kMaxSharedB, kMaxGroups);
 
-// find_start for the lines of a shared call.  at: lines_words of shared memory, filled here; scan: 3 * kThreads/32 words.
-// Where group_start does not rise within [0, B], or the counted rows pass 32 bits, no prefix is shared, and what is
-// computed is the same.
+// What a call must save by sharing, in units of one block: the join of every row's parts.  Measured (tensor cores, shared
+// and unshared): 16 requests of 1 row of 4 heads behind 2048 tokens (25 units a block unshared) 22.3 and 32.7 us, of 8 rows
+// 31.9 and 29.8; 4 of 4 rows of 8 heads behind 8192 at d = 256 28.2 and 22.1; 16 behind 16384 38.9 and 64.7.
+constexpr int kShareGain = 6;
+// And what a request's tile of its own and the join cost beside the units that the division counts: 64 requests of 16 tokens
+// of 4 heads behind 1000 tokens 98 us shared, 70 not; of 1 token 57 and 65.
+constexpr int kJoinUnits = 4;
+#ifdef GDN_TEST_HOOKS
+constexpr bool kShareAlways = true;  // test builds: whatever it costs
+#else
+constexpr bool kShareAlways = false;
+#endif
+
+// find_start for the lines of a shared call.  at: lines_words of shared memory, 8-byte aligned, filled here; scan:
+// 3 * kThreads/32 words.  Where group_start does not rise within [0, B], or the counted rows pass 32 bits, no prefix is
+// shared, and what is computed is the same.
+//
+// A request takes part in its group's prefix where its rows do not fill a tile: behind a full one K and V are read for 128
+// rows at least already, and the join of two parts costs more than the rows' closer packing gives (4 prompts of 400 to 1000
+// tokens behind 8192: 435 us shared, 330 not; 16 requests of 32 tokens of 4 heads behind 16384: 152 and 142, of 16 tokens 99
+// and 128).  A group shares where that leaves fewer units in all, and all groups together save more than kShareGain.
 template <int kRows, int kKeys, int kThreads>
 __device__ __forceinline__ Lines find_lines(const Params& p, const SharedParams& sp, int min_units, int* at, long long* scan,
                                             StartOf<Line>* out) {
   using T = Tiles<kRows, kKeys, Line>;
+  __shared__ unsigned long long gain;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int each = (p.B + kThreads - 1) / kThreads, b0 = tid * each, b1 = min(p.B, b0 + each);
-  int* const starts = at;
+  long long* const saved = reinterpret_cast<long long*>(at);  // [G] units of a kv head that a group's requests leave out
+  int* const starts = at + 2 * sp.n_groups;
   int* const prefix = starts + sp.n_groups + 1;
   int* const rows = prefix + sp.n_groups;
-  int why = 0;
+  int why = 0, broken = 0;
   Request first = {0, 0, 0};
-  if (b0 < b1) first = request(p, b0, &why);
-  int broken = 0;
-  for (int g = tid; g <= sp.n_groups && sp.n_groups > 0; g += kThreads) {
-    const int x = sp.group_start[g], y = g < sp.n_groups ? sp.group_start[g + 1] : p.B;
-    starts[g] = x;
-    if (g < sp.n_groups) prefix[g] = max(sp.prefix_len[g], 0);
-    broken |= x < 0 || x > y || y > p.B;
+  const int reads = sp.n_groups > 0 && tid <= sp.n_groups;
+  int x = 0, y = 0, length = 0;  // on their way with the request's
+  if (reads) {
+    x = sp.group_start[tid];
+    if (tid < sp.n_groups) {
+      y = sp.group_start[tid + 1];
+      length = sp.prefix_len[tid];
+    }
   }
+  if (b0 < b1) first = request(p, b0, &why);
+  for (int g = tid; g <= sp.n_groups && sp.n_groups > 0; g += kThreads) {
+    if (g != tid) {
+      x = sp.group_start[g];
+      if (g < sp.n_groups) {
+        y = sp.group_start[g + 1];
+        length = sp.prefix_len[g];
+      }
+    }
+    starts[g] = x;
+    if (g < sp.n_groups) {
+      prefix[g] = max(length, 0);
+      saved[g] = 0;
+    }
+    broken |= x < 0 || x > p.B || (g < sp.n_groups && x > y);
+  }
+  if (tid == 0) gain = 0;
   broken = __syncthreads_or(broken);
   if (broken && blockIdx.x == 0 && tid == 0 && p.status) atomicOr(p.status, GDN_STATUS_BAD_GROUP);
-  Lines lines = {p.B, broken ? 0 : sp.n_groups, starts, prefix, rows};
+  Lines lines = {p.B, broken ? 0 : sp.n_groups, (kRows - 1) / p.G, starts, prefix, rows};
   // exclusive sum of x over the threads, and the whole sum
   auto sums = [&](long long x, long long* part, long long* total) {
     long long inc = x;
@@ -388,38 +437,49 @@ __device__ __forceinline__ Lines find_lines(const Params& p, const SharedParams&
     return before;
   };
   if (lines.G > 0) {
-    auto counted = [&](const Request& r, int b) {
+    // rows of request b that may meet the prefix; what its own line then lacks goes to its group
+    auto counted = [&](const Request& r, int b, bool count) {
       const int g = r.n > 0 ? lines.group_of(b) : -1;
-      return g >= 0 && prefix[g] > 0 && r.ctx >= prefix[g] ? r.n : 0;
+      if (g < 0 || prefix[g] == 0 || r.ctx < prefix[g] || r.n > lines.most) return 0;
+      if (count) {
+        const long long whole = T::sum(p, lines.own(r, b, sp.key_align, 0)), own = T::sum(p, lines.own(r, b, sp.key_align, prefix[g]));
+        atomicAdd(reinterpret_cast<unsigned long long*>(&saved[g]), (unsigned long long)(whole - own - kJoinUnits));
+      }
+      return r.n;
     };
     long long mine = 0, total;
-    for (int b = b0; b < b1; ++b) mine += counted(b == b0 ? first : request(p, b, &why), b);
+    for (int b = b0; b < b1; ++b) mine += counted(b == b0 ? first : request(p, b, &why), b, true);
     long long before = sums(mine, scan, &total);
-    if (total > min(p.max_rows, kMaxIndex)) {
+    if (total > min(p.max_rows, p.n_q_rows)) {  // rows that overlap, or too many for a tile's numbers
       lines.G = 0;  // uniform
     } else {
       for (int b = b0; b < b1; ++b) {
         rows[b] = (int)before;
-        before += counted(b == b0 ? first : request(p, b), b);
+        before += counted(b == b0 ? first : request(p, b), b, false);
       }
       if (tid == 0) rows[p.B] = (int)total;
       __syncthreads();
-      // a prefix of one request is its own affair
       for (int g = tid; g < lines.G; g += kThreads) {
-        const int n = rows[starts[g + 1]] - rows[starts[g]];
-        bool alone = n == 0;
-        if (n > 0) {
-          const int b = lines.request_of(rows[starts[g]]);
-          alone = rows[b + 1] - rows[b] == n;
-        }
-        if (alone) prefix[g] = 0;
+        const long long less = saved[g] - T::sum(p, lines.group(g));
+        if (kShareAlways) continue;
+        if (less > 0) atomicAdd(&gain, (unsigned long long)(less * p.H_kv));
+        else prefix[g] = 0;
       }
       __syncthreads();
+      if (!kShareAlways && gain <= (unsigned long long)kShareGain * p.n_blocks) lines.G = 0;
     }
   } else {
     for (int b = b0 + 1; b < b1; ++b) request(p, b, &why);
   }
   if (why && blockIdx.x == 0 && p.status) atomicOr(p.status, why);
+  if (blockIdx.x == gridDim.x - 1) {  // for the join; this block has the least to do
+    for (int b = b0; b < b1 && lines.G > 0; ++b) {
+      const int n = rows[b + 1] - rows[b], row0 = n == 0 ? 0 : b == b0 ? first.row0 : request(p, b).row0;
+      const bool shares = n > 0 && prefix[lines.group_of(b)] > 0;
+      for (int t = 0; t < n; ++t) sp.rank_row[rows[b] + t] = shares ? row0 + t : -1;
+    }
+    if (tid == 0) *sp.count = lines.G > 0 ? rows[p.B] : 0;
+  }
   long long mine = 0, mine_g = 0, head = 0, total, total_g = 0;
   Line l = {};
   for (int b = b0; b < b1; ++b) {
@@ -488,26 +548,25 @@ __device__ __forceinline__ bool begin(Walk<kRows, kKeys, kShared>& w, const Para
   return !w.done();
 }
 
-// The note of a split tile at its first block: the blocks that follow this one
-// in it, its request's first row, kv head and rows, and its first row's number.
-template <int kRows, int kKeys>
-__device__ __forceinline__ int4 note_of(const Walk<kRows, kKeys>& w, const Start& s) {
-  const int followers = (w.blocks - w.kb1 + s.per - 1) / s.per;
-  const int rows = (int)min((long long)kRows, (long long)w.req.n * w.p->G - (long long)w.m * kRows);
-  return {followers, w.req.row0, w.h << 8 | rows, w.m * kRows};
-}
-
-// What a first part's entry says beside its maximum, sum and block: the blocks that follow, its row in the tile, whether
-// the row has a part over a prefix, and whether the row is done.
-constexpr int kEntryPrefix = 1 << 24, kEntryDone = 1 << 25;
-__device__ __forceinline__ int entry_word(int followers, int row, bool prefix, bool done) {
-  return followers | row << 16 | (prefix ? kEntryPrefix : 0) | (done ? kEntryDone : 0);
-}
 // blocks after the segment's that share its tile
 template <typename W, typename S>
 __device__ __forceinline__ int followers_of(const W& w, const S& s) {
   return (w.blocks - w.kb1 + s.per - 1) / s.per;
 }
+// The note of a split tile at its first block: the blocks that follow this one
+// in it, its request's first row, kv head and rows, and its first row's number.
+template <int kRows, int kKeys, bool kShared, typename S>
+__device__ __forceinline__ int4 note_of(const Walk<kRows, kKeys, kShared>& w, const S& s) {
+  const int rows = (int)min((long long)kRows, (long long)w.req.n * w.p->G - (long long)w.m * kRows);
+  return {followers_of(w, s), w.req.row0, w.h << 8 | rows, w.m * kRows};
+}
+
+// a row's place among its kv head's rows in `dense` and `entries`: a tile's rows lie together
+__device__ __forceinline__ size_t place_of(const Params& p, int row, int kv_head, int g) {
+  return ((size_t)kv_head * p.n_q_rows + row) * p.G + g;
+}
+// What a first part's entry says beside its maximum, sum and block: the blocks that follow, and its row in the tile.
+__device__ __forceinline__ int entry_word(int followers, int row) { return followers | row << 16; }
 constexpr float kLn2 = 0.693147180559945309f;
 
 __device__ __forceinline__ float* partial(const Params& p, int block, int slot, int rows) {
@@ -646,154 +705,148 @@ __global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const Param
   }
 }
 
-// A shared call's rows: each joins the parts of its request's own keys and of its prefix, first parts at the row's place
-// in `dense`, others with the block that made them, in that order.  A warp takes a row, or the block's four warps one row
-// where it has more than eight parts.
-template <typename T, int kD, int kRows>
+// A shared call's join.  The first kTileBlocks * n_blocks blocks take the rows of split tiles whose requests take part in no
+// prefix, the others the ranked rows, which join the parts over their request's own keys and over its prefix.  A row's parts
+// are added in one order: the first own one, those of the blocks that follow, the prefix's first and its followers.
+// kTeam warps share a row's parts: four where rows are few, and a tile is cut into many parts, one where they are many.
+// First parts and what says where the others lie are fetched at once.
+constexpr int kTileBlocks = 16;
+
+template <typename T, int kD, int kRows, int kTeam>
 __global__ void __launch_bounds__(32 * kCombineWarps) combine_shared(const Params p, const SharedParams sp) {
-  constexpr int kPer = kD / 32, kBatch = 8;
-  __shared__ float sums[kCombineWarps][kD];
+  constexpr int kPer = kD / 32, kBatch = 4, kRowsAtOnce = kCombineWarps / kTeam;
+  __shared__ float sums[kTeam > 1 ? kTeam : 1][kTeam > 1 ? kD : 1];
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, H_q = p.H_kv * p.G;
-  const size_t places = (size_t)p.n_q_rows * H_q;
-  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-    const Request r = request(p, b);
-    const long long items = (long long)r.n * H_q;
-    for (long long item0 = (long long)blockIdx.y * kCombineWarps; item0 < items; item0 += (long long)gridDim.y * kCombineWarps) {
-      const int here = (int)min((long long)kCombineWarps, items - item0);
-      // what a row's join needs: its place, its entries and its number of parts
-      struct Row {
-        size_t at;
-        int token, head, parts_own, parts;
-        int4 own, pre;
-      };
-      auto row_of = [&](int i) {
-        Row x;
-        const long long item = item0 + i;
-        x.token = (int)(item / H_q);
-        x.head = (int)(item - (long long)x.token * H_q);
-        x.at = (size_t)(r.row0 + x.token) * H_q + x.head;
-        x.own = sp.entries[places + x.at];
-        x.pre = make_int4(0, 0, 0, 0);
-        const bool prefix = x.own.w & kEntryPrefix;
-        if (prefix) x.pre = sp.entries[x.at];
-        x.parts_own = x.own.w & kEntryDone ? 0 : 1 + (x.own.w & 0xffff);
-        x.parts = x.parts_own + (prefix ? 1 + (x.pre.w & 0xffff) : 0);
-        // where a block gave up, a row's entry may be anything
-        auto inside = [&](const int4& e) { return e.z >= 0 && e.z < p.n_blocks && (e.w & 0xffff) < p.n_blocks - e.z && (e.w >> 16 & 255) < kRows; };
-        if (!inside(x.own) || (prefix && !inside(x.pre))) x.parts = 0;
-        return x;
-      };
-      // part i of a row: its columns, and its maximum and sum
-      auto tail = [&](const int4& e, int i) { return partial(p, e.z + i, 0, kRows); };
-      auto columns = [&](const Row& x, int i) -> const float* {
-        const bool own = i < x.parts_own;
-        const int4& e = own ? x.own : x.pre;
-        const int k = own ? i : i - x.parts_own;
-        if (k == 0) return sp.dense + ((own ? places : 0) + x.at) * kD;
-        return tail(e, k) + (size_t)(e.w >> 16 & 255) * kD;
-      };
-      auto stats = [&](const Row& x, int i) -> float2 {
-        const bool own = i < x.parts_own;
-        const int4& e = own ? x.own : x.pre;
-        const int k = own ? i : i - x.parts_own;
-        if (k == 0) return make_float2(__int_as_float(e.x), __int_as_float(e.y));
-        return reinterpret_cast<const float2*>(tail(e, k) + (size_t)kRows * kD)[e.w >> 16 & 255];
-      };
-      auto load = [&](float (&v)[kPer], const float* src) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, member = warp % kTeam, H_q = p.H_kv * p.G;
+  auto load = [&](float (&v)[kPer], const float* src) {
 #pragma unroll
-        for (int c = 0; c < kPer / 2; ++c) {
-          const float2 y = *reinterpret_cast<const float2*>(src + c * 64 + lane * 2);
-          v[2 * c] = y.x;
-          v[2 * c + 1] = y.y;
-        }
-      };
-      auto write = [&](const Row& x, const float (&acc)[kPer], float top, float sum) {
-        const float inv = 1.f / sum;
-        T* const dst = static_cast<T*>(p.o) + (int64_t)(r.row0 + x.token) * p.o_row + (int64_t)x.head * p.o_head + lane * 2;
+    for (int c = 0; c < kPer / 2; ++c) {
+      const float2 y = *reinterpret_cast<const float2*>(src + c * 64 + lane * 2);
+      v[2 * c] = y.x;
+      v[2 * c + 1] = y.y;
+    }
+  };
+  // One row: its first parts in acc and x_pre with their maxima and sums, then f_own parts of the blocks behind own_block at
+  // row own_row of their tile, and f_pre of the prefix.
+  auto join = [&](int row, int head, float (&acc)[kPer], const float (&x_pre)[kPer], float2 s_own, float2 s_pre, int own_block, int own_row,
+                  int f_own, int pre_block, int pre_row, int f_pre) {
+    const int f = f_own + f_pre;
+    auto part = [&](int i) {
+      return partial(p, i < f_own ? own_block + 1 + i : pre_block + 1 + i - f_own, 0, kRows) + (size_t)(i < f_own ? own_row : pre_row) * kD;
+    };
+    auto stats = [&](int i) {
+      return reinterpret_cast<const float2*>(partial(p, i < f_own ? own_block + 1 + i : pre_block + 1 + i - f_own, 0, kRows) +
+                                             (size_t)kRows * kD)[i < f_own ? own_row : pre_row];
+    };
+    float top = fmaxf(s_own.x, s_pre.x);
+    float2 s_lane = make_float2(-INFINITY, 0.f);  // of part `lane`: all of them in most calls
+    if (f > 0) {
+      if (lane < f) s_lane = stats(lane);
+      float t = s_lane.x;
+      for (int i = lane + 32; i < f; i += 32) t = fmaxf(t, stats(i).x);
 #pragma unroll
-        for (int c = 0; c < kPer / 2; ++c) {
-          const float a = acc[2 * c] * inv, z = acc[2 * c + 1] * inv;
-          if constexpr (sizeof(T) == 2) *reinterpret_cast<__nv_bfloat162*>(dst + c * 64) = __floats2bfloat162_rn(a, z);
-          else *reinterpret_cast<float2*>(dst + c * 64) = make_float2(a, z);
-        }
-        if (sp.lse && lane == 0) sp.lse[(int64_t)(r.row0 + x.token) * sp.lse_row + x.head] = (top + log2f(sum)) * kLn2;
-      };
-      // parts i0, i0 + step, ... of a row into acc
-      auto add = [&](const Row& x, float top, int i0, int step, float (&acc)[kPer]) {
-        for (int j0 = i0; j0 < x.parts; j0 += step * kBatch) {
-          float v[kBatch][kPer], weight[kBatch];
+      for (int off = 16; off >= 1; off >>= 1) t = fmaxf(t, __shfl_xor_sync(kFull, t, off));
+      top = fmaxf(top, t);
+    }
+    const float base = top == -INFINITY ? 0.f : top, w_own = exp2f(s_own.x - base), w_pre = exp2f(s_pre.x - base);
+    float sum = s_own.y * w_own + s_pre.y * w_pre;
 #pragma unroll
-          for (int j = 0; j < kBatch; ++j) {
-            const int i = min(j0 + j * step, x.parts - 1);
-            weight[j] = j0 + j * step < x.parts ? exp2f(stats(x, i).x - top) : 0.f;
-            load(v[j], columns(x, i));
-          }
-#pragma unroll
-          for (int j = 0; j < kBatch; ++j) {
-            if (j0 + j * step >= x.parts) break;
-#pragma unroll
-            for (int c = 0; c < kPer; ++c) acc[c] = fmaf(weight[j], v[j][c], acc[c]);
-          }
-        }
-      };
-      // a row's maximum and sum
-      auto total = [&](const Row& x, float* sum) {
-        float top = -INFINITY;
-        for (int i = lane; i < x.parts; i += 32) top = fmaxf(top, stats(x, i).x);
-#pragma unroll
-        for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
-        const float base = top == -INFINITY ? 0.f : top;
-        float s = 0.f;
-        for (int i = lane; i < x.parts; i += 32) {
-          const float2 st = stats(x, i);
-          s += st.y * exp2f(st.x - base);
-        }
-#pragma unroll
-        for (int off = 16; off >= 1; off >>= 1) s += __shfl_xor_sync(kFull, s, off);
-        *sum = s;
-        return base;
-      };
-      const Row mine = row_of(min(warp, here - 1));
-      if (!__syncthreads_or(mine.parts > kBatch)) {
-        if (warp < here && mine.parts > 0) {
-          float sum, acc[kPer] = {};
-          const float top = total(mine, &sum);
-          add(mine, top, 0, 1, acc);
-          write(mine, acc, top, sum);
-        }
-        continue;
+    for (int c = 0; c < kPer; ++c) acc[c] = kTeam == 1 || member == 0 ? acc[c] * w_own + x_pre[c] * w_pre : 0.f;
+    if (f > 0) {
+      float t = s_lane.y * exp2f(s_lane.x - base);
+      for (int i = lane + 32; i < f; i += 32) {
+        const float2 st = stats(i);
+        t += st.y * exp2f(st.x - base);
       }
-      for (int i = 0; i < here; ++i) {
-        const Row x = row_of(i);
-        if (x.parts == 0) continue;  // the same for all warps
-        float sum, acc[kPer] = {};
-        const float top = total(x, &sum);
-        add(x, top, warp, kCombineWarps, acc);
-        __syncthreads();
+#pragma unroll
+      for (int off = 16; off >= 1; off >>= 1) t += __shfl_xor_sync(kFull, t, off);
+      sum += t;
+      for (int i0 = member; i0 < f; i0 += kTeam * kBatch) {
+        float v[kBatch][kPer], weight[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          const int i = min(i0 + j * kTeam, f - 1);
+          load(v[j], part(i));
+          const float mine = f <= 32 ? __shfl_sync(kFull, s_lane.x, i) : stats(i).x;
+          weight[j] = i0 + j * kTeam < f ? exp2f(mine - base) : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          if (i0 + j * kTeam >= f) break;
+#pragma unroll
+          for (int c = 0; c < kPer; ++c) acc[c] = fmaf(weight[j], v[j][c], acc[c]);
+        }
+      }
+    }
+    if constexpr (kTeam > 1) {
+      if (f > 0) {  // the same for the row's warps, which are all the block's
 #pragma unroll
         for (int c = 0; c < kPer / 2; ++c)
           *reinterpret_cast<float2*>(&sums[warp][c * 64 + lane * 2]) = make_float2(acc[2 * c], acc[2 * c + 1]);
         __syncthreads();
-        if (warp == 0) {
+        if (member == 0) {
 #pragma unroll
           for (int c = 0; c < kPer; ++c) {
-            acc[c] = 0.f;
-            for (int w = 0; w < kCombineWarps; ++w) acc[c] += sums[w][(c / 2) * 64 + lane * 2 + (c & 1)];
+#pragma unroll
+            for (int w = 1; w < kTeam; ++w) acc[c] += sums[w][(c / 2) * 64 + lane * 2 + (c & 1)];
           }
-          write(x, acc, top, sum);
         }
+        __syncthreads();
       }
+      if (member > 0) return;
     }
+    const float inv = 1.f / sum;
+    T* const dst = static_cast<T*>(p.o) + (int64_t)row * p.o_row + (int64_t)head * p.o_head + lane * 2;
+#pragma unroll
+    for (int c = 0; c < kPer / 2; ++c) {
+      const float a = acc[2 * c] * inv, z = acc[2 * c + 1] * inv;
+      if constexpr (sizeof(T) == 2) *reinterpret_cast<__nv_bfloat162*>(dst + c * 64) = __floats2bfloat162_rn(a, z);
+      else *reinterpret_cast<float2*>(dst + c * 64) = make_float2(a, z);
+    }
+    if (sp.lse && lane == 0) sp.lse[(int64_t)row * sp.lse_row + head] = (base + log2f(sum)) * kLn2;
+  };
+  // the two kinds of rows are one loop's items, so that the join is compiled once
+  const bool tiles = (int)blockIdx.x < kTileBlocks * p.n_blocks;
+  const int block = tiles ? blockIdx.x % kTileBlocks : blockIdx.x - kTileBlocks * p.n_blocks;
+  const int blocks = tiles ? kTileBlocks : gridDim.x - kTileBlocks * p.n_blocks, x_block = blockIdx.x / kTileBlocks;
+  const int4 note = tiles ? p.notes[x_block] : make_int4(0, 0, 0, 0);
+  const long long items = !tiles ? (long long)*sp.count * H_q : note.x > 0 ? note.z & 255 : 0;
+  const size_t places = (size_t)p.n_q_rows * H_q;
+  // where a block gave up, a row's entry may be anything
+  auto inside = [&](const int4& e) { return e.z >= 0 && e.z < p.n_blocks && (e.w & 0xffff) < p.n_blocks - e.z && (e.w >> 16 & 255) < kRows; };
+  for (long long item = (long long)block * kRowsAtOnce + warp / kTeam; item < items; item += (long long)blocks * kRowsAtOnce) {
+    int row, head;
+    float acc[kPer], x_pre[kPer] = {};
+    int4 own, pre;
+    if (tiles) {
+      const int at = note.w + (int)item, token = (int)quotient(at, p.by_G);
+      row = note.y + token;
+      head = (note.z >> 8) * p.G + at - token * p.G;
+      const float* const first = partial(p, x_block, 1, kRows);
+      const float2 s = reinterpret_cast<const float2*>(first + (size_t)kRows * kD)[item];
+      own = make_int4(__float_as_int(s.x), __float_as_int(s.y), x_block, entry_word(note.x, (int)item));
+      pre = make_int4(__float_as_int(-INFINITY), 0, 0, 0);
+      if (kTeam == 1 || member == 0) load(acc, first + (size_t)item * kD);
+    } else {
+      const int rank = item >> 31 ? (int)(item / H_q) : (int)((uint32_t)item / (uint32_t)H_q);
+      head = (int)(item - (long long)rank * H_q);
+      row = sp.rank_row[rank];
+      if (row < 0) continue;
+      const int h = (int)quotient(head, p.by_G);
+      const size_t at = place_of(p, row, h, head - h * p.G);
+      own = sp.entries[places + at];
+      pre = sp.entries[at];
+      if (kTeam == 1 || member == 0) {
+        load(acc, sp.dense + (places + at) * kD);
+        load(x_pre, sp.dense + at * kD);
+      }
+      if (!inside(own) || !inside(pre)) continue;  // the same for the row's warps
+    }
+    join(row, head, acc, x_pre, make_float2(__int_as_float(own.x), __int_as_float(own.y)),
+         make_float2(__int_as_float(pre.x), __int_as_float(pre.y)), own.z, own.w >> 16 & 255, own.w & 0xffff, pre.z, pre.w >> 16 & 255,
+         pre.w & 0xffff);
   }
-}
-
-// blocks of the join: a request's rows are shared by as many as give the GPU some 16 warps an SM
-inline dim3 combine_shared_grid(const Params& p) {
-  const long long rows = (long long)p.n_q_rows * p.H_kv * p.G, per = (rows / p.B + kCombineWarps) / kCombineWarps;
-  const long long most = p.B >= 1024 ? 1 : 1024 / p.B + 1;
-  return dim3(p.B, (unsigned)(per < most ? per : most));
 }
 
 template <typename Kernel, typename... Args>
@@ -810,6 +863,16 @@ int launch(Kernel kernel, dim3 grid, dim3 block, size_t smem, cudaStream_t st, c
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) return GDN_ERR_LAUNCH;
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+}
+
+// A team of four warps a row where rows are so few that the GPU holds them all at once.
+template <typename T, int kD, int kRows>
+int launch_combine_shared(const Params& p, const SharedParams& sp, cudaStream_t st) {
+  const long long rows = (long long)p.n_q_rows * p.H_kv * p.G;
+  const dim3 block(32 * kCombineWarps);
+  auto grid = [&](long long blocks) { return dim3((unsigned)(kTileBlocks * p.n_blocks + (sp.n_groups == 0 ? 0 : blocks < 152 * 32 ? blocks : 152 * 32))); };
+  if (rows <= 152 * 16) return launch(combine_shared<T, kD, kRows, kCombineWarps>, grid(rows), block, 0, st, p, sp);
+  return launch(combine_shared<T, kD, kRows, 1>, grid((rows + kCombineWarps - 1) / kCombineWarps), block, 0, st, p, sp);
 }
 
 }  // namespace gdnattn

@@ -185,12 +185,11 @@ __global__ void __launch_bounds__(kSimtThreads, kD == 256 ? 2 : 3)
         __syncthreads();
         if (more) fetch(vs, kD, p.v, v_at);
       }
-      bool whole = w.kb0 == 0 && w.kb1 == w.blocks;
-      if constexpr (kShared) whole = whole && w.req.prefix == 0;
-      const int slot = !kShared && w.kb0 == 0 ? 1 : 0;
-      if constexpr (!kShared) {
-        if (!whole && slot == 1) note = note_of(w, s);
-      }
+      bool joins = false;  // the tile's rows have parts over a prefix and over their own keys
+      if constexpr (kShared) joins = w.req.prefix != 0;
+      const bool whole = w.kb0 == 0 && w.kb1 == w.blocks && !joins, first = joins && w.kb0 == 0;
+      const int slot = w.kb0 == 0 ? 1 : 0;
+      if (!whole && !first && slot == 1) note = note_of(w, s);
       float* const part = partial(p, blockIdx.x, slot, kR);
 #pragma unroll
       for (int r = 0; r < kWarpRows; ++r) {
@@ -205,15 +204,13 @@ __global__ void __launch_bounds__(kSimtThreads, kD == 256 ? 2 : 3)
         float2* out_stats = reinterpret_cast<float2*>(part + kR * kD) + row;
         if constexpr (kShared) {
           o_row = row_at[row];
-          if (w.kb0 == 0) {
-            const size_t place = (w.req.flat() ? 0 : (size_t)p.n_q_rows * p.H_kv * p.G) + (size_t)o_row * (p.H_kv * p.G) + head;
+          if (first) {
+            const size_t place = (w.req.flat() ? 0 : (size_t)p.n_q_rows * p.H_kv * p.G) + place_of(p, o_row, w.h, at % p.G);
             out = sp.dense + place * kD;
             out_stats = reinterpret_cast<float2*>(sp.entries + place);
-            if (lane == 0) {
-              reinterpret_cast<int2*>(out_stats)[1] = make_int2(blockIdx.x, entry_word(followers_of(w, s), row, w.req.prefix > 0, whole));
-              if (whole && sp.lse) sp.lse[(int64_t)o_row * sp.lse_row + head] = (top[r] + log2f(l)) * kLn2;
-            }
+            if (lane == 0) reinterpret_cast<int2*>(out_stats)[1] = make_int2(blockIdx.x, entry_word(followers_of(w, s), row));
           }
+          if (lane == 0 && whole && sp.lse) sp.lse[(int64_t)o_row * sp.lse_row + head] = (top[r] + log2f(l)) * kLn2;
         } else {
           o_row = w.req.row0 + at / p.G;
         }
@@ -243,7 +240,7 @@ __global__ void __launch_bounds__(kSimtThreads, kD == 256 ? 2 : 3)
       else segment(std::integral_constant<int, 8>(), rows);
     }
   }
-  if (!kShared && tid == 0) p.notes[blockIdx.x] = note;
+  if (tid == 0) p.notes[blockIdx.x] = note;
 }
 
 // blocks of the launch: a fixed number per d and type (as many as 152 SMs hold
@@ -265,7 +262,7 @@ int run_simt(Params p, const std::conditional_t<kShared, SharedParams, Nothing>&
   p.n_blocks = simt_blocks(kD);
   const int rc = launch(simt_kernel<kD, kShared>, dim3(p.n_blocks), dim3(kSimtThreads), smem, st, p, sp);
   if (rc != GDN_OK) return rc;
-  if constexpr (kShared) return launch(combine_shared<float, kD, kSimtRows>, combine_shared_grid(p), dim3(32 * kCombineWarps), 0, st, p, sp);
+  if constexpr (kShared) return launch_combine_shared<float, kD, kSimtRows>(p, sp, st);
   else return launch(combine_kernel<float, kD, kSimtRows>, dim3(p.n_blocks, 4), dim3(32 * kCombineWarps), 0, st, p);
 }
 

@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   constexpr int kKeys = S::kKeys, kChunks = S::kChunks;
   const Params& p = t.p;
   const uint32_t q_flip = t.q_flip;
-  extern __shared__ uint8_t raw[];
+  extern __shared__ __align__(16) uint8_t raw[];
   __shared__ __align__(8) uint64_t bars[2 * S::kK + 2 * S::kV + 15 + kShared];
   __shared__ long long scan[(kShared ? 3 : 1) * kTcThreads / 32];
   __shared__ StartOf<typename W::R> start;
@@ -248,6 +248,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const bool any = begin(w, p, s);
   bool ok = true;
   int sent = 0;  // tiles whose copies this warp issued
+  // whether the tile's rows have parts over a prefix and over their own keys
+  auto joins = [](const W& t) {
+    if constexpr (kShared) return t.req.prefix != 0;
+    else return false;
+  };
   auto rows_of = [&](const W& t) {
     return (int)min((long long)kTcRows, (long long)t.req.n * p.G - (long long)t.m * kTcRows);
   };
@@ -309,25 +314,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int rows = rows_of(w), row = e_tid;
         const int at = min(w.m * kTcRows + row, w.req.n * p.G - 1);
         const int token = (int)quotient(at, p.by_G), head = w.h * p.G + at - token * p.G;
-        // the row's place in o; in a shared call `whole` says that no other part of the row exists
-        bool whole;
-        float* out;  // this row's 32-bit columns
-        float2* out_stats;
+        const bool whole = w.kb0 == 0 && w.kb1 == w.blocks && !joins(w);
+        const int slot = w.kb0 == 0 ? 1 : 0;
+        float* const part = partial(p, blockIdx.x, slot, kTcRows);
+        float* out = part + row * kD;  // this row's 32-bit columns
+        float2* out_stats = reinterpret_cast<float2*>(part + kTcRows * kD) + row;
+        bool first = false;  // of a row that takes part in a prefix
         if constexpr (kShared) {
-          whole = w.kb0 == 0 && w.kb1 == w.blocks && w.req.prefix == 0;
-          const size_t place = (w.req.flat() ? 0 : (size_t)p.n_q_rows * p.H_kv * p.G) + (size_t)o_row * (p.H_kv * p.G) + head;
-          float* const tail = partial(p, blockIdx.x, 0, kTcRows);
-          out = w.kb0 == 0 ? sp.dense + place * kD : tail + row * kD;
-          out_stats = w.kb0 == 0 ? reinterpret_cast<float2*>(sp.entries + place) : reinterpret_cast<float2*>(tail + kTcRows * kD) + row;
+          if (joins(w) && w.kb0 == 0) {
+            const size_t place = (w.req.flat() ? 0 : (size_t)p.n_q_rows * p.H_kv * p.G) + place_of(p, o_row, w.h, head - w.h * p.G);
+            first = true;
+            out = sp.dense + place * kD;
+            out_stats = reinterpret_cast<float2*>(sp.entries + place);
+          }
         } else {
-          whole = w.kb0 == 0 && w.kb1 == w.blocks;
-          const int slot = w.kb0 == 0 ? 1 : 0;
-          if (!whole && slot == 1) note = note_of(w, s);
-          float* const part = partial(p, blockIdx.x, slot, kTcRows);
-          out = part + row * kD;
-          out_stats = reinterpret_cast<float2*>(part + kTcRows * kD) + row;
           o_row = w.req.row0 + token;
         }
+        if (!whole && !first && slot == 1) note = note_of(w, s);
         __nv_bfloat16* const dst = static_cast<__nv_bfloat16*>(p.o) + (int64_t)o_row * p.o_row + (int64_t)head * p.o_head;
         ok = warp_wait(st_ready(g), (g >> 1) & 1, &gave_up) && warp_wait(o_full(g), (g >> 1) & 1, &gave_up);
         if (!ok) break;
@@ -341,8 +344,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const float sum = st0.y * share0 + st1.y * share1;
           if (!whole && row < rows) *out_stats = make_float2(top, sum);
           if constexpr (kShared) {
-            if (row < rows && w.kb0 == 0)
-              reinterpret_cast<int2*>(out_stats)[1] = make_int2(blockIdx.x, entry_word(followers_of(w, s), row, w.req.prefix > 0, whole));
+            if (row < rows && first) reinterpret_cast<int2*>(out_stats)[1] = make_int2(blockIdx.x, entry_word(followers_of(w, s), row));
             if (row < rows && whole && sp.lse) sp.lse[(int64_t)o_row * sp.lse_row + head] = (top + log2f(sum)) * kLn2;
           }
           if (whole) {
@@ -389,7 +391,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         w = next;
       }
     }
-    if (!kShared && tid == 256) p.notes[blockIdx.x] = note;
+    if (tid == 256) p.notes[blockIdx.x] = note;
   } else if (any && warp < 4 * S::kStreams) {
     // ---- softmax: one thread per row, the stream's keys
     const int stream = warp >> 2, quarter = warp & 3, s_tid = tid & 127;
@@ -617,7 +619,7 @@ int run(TcParams& t, std::conditional_t<kShared, SharedParams, Nothing> sp, cuda
   t.p.n_blocks = kTcBlocks;
   const int rc = launch(tc_kernel<kD, kShared>, dim3(kTcBlocks), dim3(kTcThreads), smem, st, t, sp, k_map, v_map);
   if (rc != GDN_OK) return rc;
-  if constexpr (kShared) return launch(combine_shared<__nv_bfloat16, kD, kTcRows>, combine_shared_grid(t.p), dim3(32 * kCombineWarps), 0, st, t.p, sp);
+  if constexpr (kShared) return launch_combine_shared<__nv_bfloat16, kD, kTcRows>(t.p, sp, st);
   else return launch(combine_kernel<__nv_bfloat16, kD, kTcRows>, dim3(kTcBlocks, 8), dim3(32 * kCombineWarps), 0, st, t.p);
 }
 

@@ -52,6 +52,11 @@ int check(const gdn_paged_attn_args* a) {
   return GDN_OK;
 }
 
+void set_work(Params& p, int dtype, void* work) {
+  p.notes = static_cast<int4*>(work);
+  p.partials = reinterpret_cast<float*>(p.notes + blocks_of(p.d, dtype));
+}
+
 Params params_of(const gdn_paged_attn_args* a) {
   Params p = {};
   p.B = a->B;
@@ -102,8 +107,7 @@ extern "C" GDN_API int gdn_paged_attention(const gdn_paged_attn_args* a, void* s
   const int rc = check(a);
   if (rc != GDN_OK || a->B == 0 || a->n_q_rows == 0) return rc;
   Params p = params_of(a);
-  p.notes = static_cast<int4*>(a->work);
-  p.partials = reinterpret_cast<float*>(p.notes + blocks_of(p.d, a->in_dtype));
+  set_work(p, a->in_dtype, a->work);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return a->in_dtype == GDN_DTYPE_BF16 ? run_tc(p, st) : run_simt<false>(p, Nothing{}, st);
 }

@@ -28,11 +28,12 @@ size_t places(const gdn_paged_attn_args& a) { return 2 * (size_t)a.n_q_rows * a.
 
 using namespace gdnattn;
 
-// the attention's partials, and for every place its columns and its entry
+// the attention's notes and partials, for every place its columns and its entry, and the ranked rows
 extern "C" GDN_API size_t gdn_shared_attention_work_bytes(const gdn_shared_attn_args* args) {
   if (check_sizes(args) != GDN_OK) return 0;
   const size_t partials = gdn_paged_attention_work_bytes(&args->attn);
-  return partials == 0 ? 0 : partials + places(args->attn) * (args->attn.d * sizeof(float) + sizeof(int4));
+  const size_t ranks = ((size_t)args->attn.n_q_rows + 1) * sizeof(int);
+  return partials == 0 ? 0 : partials + places(args->attn) * (args->attn.d * sizeof(float) + sizeof(int4)) + ranks;
 }
 
 extern "C" GDN_API int gdn_shared_attention(const gdn_shared_attn_args* a, void* stream) {
@@ -46,9 +47,12 @@ extern "C" GDN_API int gdn_shared_attention(const gdn_shared_attn_args* a, void*
   sp.prefix_len = a->prefix_len;
   sp.lse = a->lse;
   sp.lse_row = a->lse_row_stride;
-  sp.entries = static_cast<int4*>(a->attn.work);
+  const size_t attn_bytes = gdn_paged_attention_work_bytes(&a->attn);
+  set_work(p, a->attn.in_dtype, a->attn.work);
+  sp.entries = reinterpret_cast<int4*>(static_cast<char*>(a->attn.work) + attn_bytes);
   sp.dense = reinterpret_cast<float*>(sp.entries + places(a->attn));
-  p.partials = sp.dense + places(a->attn) * p.d;
+  sp.rank_row = reinterpret_cast<int*>(sp.dense + places(a->attn) * p.d);
+  sp.count = sp.rank_row + a->attn.n_q_rows;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return a->attn.in_dtype == GDN_DTYPE_BF16 ? run_shared_tc(p, sp, st) : run_simt<true>(p, sp, st);
 }

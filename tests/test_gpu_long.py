@@ -31,6 +31,18 @@ def hy(cuda_lib):
     return hybrid
 
 
+@pytest.fixture(scope="module")
+def always(hy):
+    """The attention built for tests: it shares prefixes whatever that costs (and drops no copy unless told to)."""
+    import ctypes
+
+    from speculative_decode_gateddeltanet_gb300 import build as pkg_build
+
+    lib = ctypes.CDLL(str(pkg_build.build_attn_test_hooks()))
+    lib.gdn_shared_attention.argtypes = [ctypes.POINTER(hy.GdnSharedAttnArgs), ctypes.c_void_p]
+    return lib
+
+
 def ints(v):
     return torch.tensor(np.asarray(v, dtype=np.int32), device="cuda")
 
@@ -60,9 +72,20 @@ class Shared:
         self.work = torch.full((hy.shared_attention_work_bytes(self.args),), 255, dtype=torch.uint8, device="cuda")  # NaN
         self.args.attn.work = self.work.data_ptr()
 
-    def run(self):
-        self.hy.gdn_shared_attention(self.args)
+    def run(self, lib=None):
+        if lib is None:
+            self.hy.gdn_shared_attention(self.args)
+        else:
+            assert lib.gdn_shared_attention(self.args, torch.cuda.current_stream().cuda_stream or None) == 0
         return self
+
+    def again(self, lib):
+        self.o.fill_(7.0)
+        if self.lse is not None:
+            self.lse.fill_(7.0)
+        self.status.zero_()
+        self.work.fill_(255)
+        return self.run(lib)
 
     def check(self, n=None, status=0):
         torch.cuda.synchronize()
@@ -109,7 +132,7 @@ SHARED = [
 
 
 @pytest.mark.parametrize("groups,alone,H_q,H_kv,d,P,dtype,layout,R", SHARED, ids=range(len(SHARED)))
-def test_shared_attention_matches_the_plain_form(hy, groups, alone, H_q, H_kv, d, P, dtype, layout, R):
+def test_shared_attention_matches_the_plain_form(hy, always, groups, alone, H_q, H_kv, d, P, dtype, layout, R):
     case = long_ref.make_shared(groups=groups, alone=alone, H_q=H_q, H_kv=H_kv, d=d, P=P, dtype=dtype, layout=layout, R=R, seed=len(groups))
     s = Shared(hy, case, R).run()
     s.check()
@@ -117,6 +140,7 @@ def test_shared_attention_matches_the_plain_form(hy, groups, alone, H_q, H_kv, d
     s.run()
     torch.cuda.synchronize()
     assert torch.equal(s.o, first[0]) and torch.equal(s.lse, first[1])  # the same bits again
+    s.again(always).check()
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
@@ -127,22 +151,26 @@ def test_shared_attention_without_groups_or_log_sums(hy, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
-def test_shared_attention_with_scales_of_either_sign_and_large_scores(hy, dtype):
+def test_shared_attention_with_scales_of_either_sign_and_large_scores(hy, always, dtype):
     for scale in (-0.1, 0.0, 1.0):
         case = long_ref.make_shared(groups=[(200, [(3, 2), (60, 2)])], H_q=8, H_kv=2, d=64, P=16, dtype=dtype, R=2, scale=scale)
-        Shared(hy, case, 2).run().check()
+        s = Shared(hy, case, 2).run()
+        s.check()
+        s.again(always).check()
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("start", [[0, 3, 2], [0, 2, 9], [-1, 2, 4], [0, -(2 ** 31), 2 ** 31 - 1]])
-def test_groups_that_do_not_rise_share_nothing(hy, dtype, start):
+def test_groups_that_do_not_rise_share_nothing(hy, always, dtype, start):
     case = long_ref.make_shared(groups=[(100, [(0, 1), (5, 1)]), (60, [(1, 1), (2, 1)])], H_q=4, H_kv=2, d=64, P=16, dtype=dtype, R=1)
     case["group_start"] = np.array(start)
-    Shared(hy, case, 1).run().check(status=hy.STATUS_BAD_GROUP)
+    s = Shared(hy, case, 1).run()
+    s.check(status=hy.STATUS_BAD_GROUP)
+    s.again(always).check(status=hy.STATUS_BAD_GROUP)
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
-def test_requests_shorter_than_their_groups_prefix_read_their_own_pages(hy, dtype):
+def test_requests_shorter_than_their_groups_prefix_read_their_own_pages(hy, always, dtype):
     """A request with fewer cached tokens than the prefix takes no part in it; a negative or huge prefix is none."""
     case = long_ref.make_shared(groups=[(100, [(0, 2), (5, 2), (30, 2)]), (60, [(1, 2), (2, 2)]), (20, [(1, 1), (2, 2)])], H_q=4, H_kv=2,
                                 d=64, P=16, dtype=dtype, R=2)
@@ -151,11 +179,13 @@ def test_requests_shorter_than_their_groups_prefix_read_their_own_pages(hy, dtyp
             case["ctx"] = case["ctx"] - np.array([20, 0, 0, 40, 0, 0, 0])  # the first of two groups
         for prefix in ([100, 60, 20], [-5, 2 ** 31 - 1, -(2 ** 31)], [99, 59, 19], [16, 15, 1], [106, 62, 22]):
             case["prefix_len"] = np.array(prefix)
-            Shared(hy, case, 2).run().check()
+            s = Shared(hy, case, 2).run()
+            s.check()
+            s.again(always).check()
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
-def test_shared_attention_skips_bad_requests_alone(hy, dtype):
+def test_shared_attention_skips_bad_requests_alone(hy, always, dtype):
     case = long_ref.make_shared(groups=[(100, [(0, 2), (5, 2), (30, 2), (1, 2), (4, 1)])], alone=[(20, 2)], H_q=4, H_kv=2, d=64, P=16,
                                 dtype=dtype, R=2)
     s = Shared(hy, case, 2)
@@ -166,10 +196,11 @@ def test_shared_attention_skips_bad_requests_alone(hy, dtype):
     n = case["n"].copy()
     n[[0, 1, 3]] = 0
     s.check(n=n, status=hy.STATUS_BAD_LENGTH | 2)
+    s.again(always).check(n=n, status=hy.STATUS_BAD_LENGTH | 2)
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
-def test_shared_attention_reads_bad_pages_as_zeros(hy, dtype):
+def test_shared_attention_reads_bad_pages_as_zeros(hy, always, dtype):
     case = long_ref.make_shared(groups=[(100, [(0, 2), (5, 2)])], alone=[(40, 2)], H_q=4, H_kv=2, d=64, P=16, dtype=dtype, R=2)
     bad = case["table"][0, 1]
     case["k_cache"][bad] = 0
@@ -178,20 +209,23 @@ def test_shared_attention_reads_bad_pages_as_zeros(hy, dtype):
     for b, page in ((0, -3), (1, case["k_cache"].shape[0])):
         s.t["table"][b, 1] = page
     s.run().check(status=hy.STATUS_BAD_PAGE)
+    s.again(always).check(status=hy.STATUS_BAD_PAGE)
 
 
-def test_shared_attention_in_a_graph_follows_lengths_and_groups(hy):
+@pytest.mark.parametrize("forced", [False, True])
+def test_shared_attention_in_a_graph_follows_lengths_and_groups(hy, always, forced):
     """One captured graph serves other lengths, rows, groups and prefixes."""
     case = long_ref.make_shared(groups=[(400, [(0, 4), (50, 4), (9, 4)]), (100, [(7, 4), (8, 4)])], alone=[(30, 4)], H_q=16, H_kv=2, d=128,
                                 P=16, dtype=BF16, R=4)
-    s = Shared(hy, case, 4).run()
+    lib = always if forced else None
+    s = Shared(hy, case, 4).run(lib)
     torch.cuda.synchronize()
     stream = torch.cuda.Stream()
     with torch.cuda.stream(stream):
-        s.run()
+        s.run(lib)
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph, stream=stream):
-            s.run()
+            s.run(lib)
     for n, starts, prefix in (([4, 4, 4, 4, 4, 4], [0, 3, 5], [400, 100]), ([1, 0, 4, 2, 3, 1], [0, 3, 5], [400, 100]),
                               ([2, 2, 2, 2, 2, 2], [0, 2, 3], [384, 100]), ([4, 1, 1, 1, 1, 4], [3, 3, 5], [0, 100])):
         s.t["n"].copy_(ints(n))
@@ -203,7 +237,7 @@ def test_shared_attention_in_a_graph_follows_lengths_and_groups(hy):
         s.check(n=np.array(n))
 
 
-def test_shared_attention_with_far_pages_and_strided_rows(hy):
+def test_shared_attention_with_far_pages_and_strided_rows(hy, always):
     """Element offsets beyond 2^31, q and o as slices of wider rows, lse with a row stride."""
     case = long_ref.make_shared(groups=[(40, [(0, 2), (25, 2)])], H_q=4, H_kv=2, d=64, P=16, dtype=BF16, R=2, spare=1)
     s = Shared(hy, case, 2)
@@ -221,9 +255,35 @@ def test_shared_attention_with_far_pages_and_strided_rows(hy):
                                          row_start=s.t["start"], R=2, o=s.o, scale=case["scale"], lse=lse[:, :4], status=s.status,
                                          group_start=s.t["group_start"], prefix_len=s.t["prefix_len"])
     args.attn.work = s.work.data_ptr()
-    hy.gdn_shared_attention(args)
-    s.lse.copy_(lse[:, :4])
-    assert (lse[:, 4:] == 7.0).all()
+    for lib in (None, always):
+        if lib is None:
+            hy.gdn_shared_attention(args)
+        else:
+            s.o.fill_(7.0)
+            lse.fill_(7.0)
+            assert lib.gdn_shared_attention(args, torch.cuda.current_stream().cuda_stream or None) == 0
+        s.lse.copy_(lse[:, :4])
+        assert (lse[:, 4:] == 7.0).all()
+        s.check()
+
+
+@pytest.mark.parametrize("dtype,d,own", [(BF16, 128, 300), (BF16, 256, 20), (F32, 64, 40)])
+def test_a_wide_batch_shares_by_itself(hy, dtype, d, own):
+    """Calls in which sharing pays, with many parts a prefix, several groups, and one that does not pay among them."""
+    groups = [(2500, [(own * i // 40, 1 + i % 3) for i in range(40)]), (1700, [(i, 2) for i in range(30)]), (60, [(5, 1), (900, 2)])]
+    case = long_ref.make_shared(groups=groups, alone=[(700, 3)], H_q=16, H_kv=4, d=d, P=32, dtype=dtype, R=3)
+    s = Shared(hy, case, 3).run()
+    s.check()
+    first = s.o.clone(), s.lse.clone()
+    s.run()
+    torch.cuda.synchronize()
+    assert torch.equal(s.o, first[0]) and torch.equal(s.lse, first[1])
+    # half of the prefix's tokens moved to other pages: the table rows of requests behind the first are not asked for them
+    table = s.t["table"].clone()
+    s.t["table"][1:40, :2500 // 32] = s.t["table"][1:40, 2500 // 32, None]
+    s.again(None)
+    torch.cuda.synchronize()
+    s.t["table"].copy_(table)
     s.check()
 
 

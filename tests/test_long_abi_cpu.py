@@ -98,7 +98,7 @@ REFUSED = [
     ("gdn_shared_attention", shared_args, dict(scale=NAN), 1), ("gdn_shared_attention", shared_args, dict(work=None), 1),
     ("gdn_shared_attention", shared_args, dict(q=FAKE + 4), 3), ("gdn_shared_attention", shared_args, dict(v_token_stride=-64), 1),
     ("gdn_shared_attention", shared_args, dict(R=0, row_start=None), 1), ("gdn_shared_attention", shared_args, dict(scale=3e38), 2),
-    ("gdn_shared_attention", shared_args, dict(n_groups=-1), 1), ("gdn_shared_attention", shared_args, dict(n_groups=1025), 2),
+    ("gdn_shared_attention", shared_args, dict(n_groups=-1), 1), ("gdn_shared_attention", shared_args, dict(n_groups=513), 2),
     ("gdn_shared_attention", shared_args, dict(B=4097), 2), ("gdn_shared_attention", shared_args, dict(group_start=None), 1),
     ("gdn_shared_attention", shared_args, dict(prefix_len=None), 1), ("gdn_shared_attention", shared_args, dict(lse_row_stride=7), 1),
     ("gdn_shared_attention", shared_args, dict(reserved=1), 1), ("gdn_shared_attention", shared_args, dict(group_start=FAKE + 2), 3),

@@ -1,5 +1,4 @@
-// Eviction from the paged cache: argument checks and launches of the attention weights, the choice of tokens that leave and
-// their moves.  Simple kernels: one pass each, no tiles.
+// Eviction from the paged cache: the choice of tokens that leave, and their moves.
 #include <algorithm>
 #include <cmath>
 
@@ -31,59 +30,6 @@ __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) x += __shfl_xor_sync(kFull, x, off);
   return x;
-}
-
-// ---- weights: a warp per cached token --------------------------------------------------------------------------------------
-
-struct WeightParams {
-  Params p;  // o, v and the join's fields unused
-  float scale, keep;
-  int fresh;
-  const float* lse;
-  int64_t lse_row;
-  const int32_t *first, *position;
-  float* weight;
-  int32_t* born;
-};
-
-template <typename T>
-__global__ void __launch_bounds__(128) weight_simple(const WeightParams w) {
-  pdl_wait();
-  pdl_trigger();
-  const Params& p = w.p;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, per = p.d / 32;
-  for (int b = blockIdx.y; b < p.B; b += gridDim.y) {
-    int why = 0;
-    const Request r = request(p, b, &why);
-    if (why && blockIdx.x == 0 && threadIdx.x == 0 && p.status) atomicOr(p.status, why);
-    if (r.n <= 0) continue;
-    const int first = w.first ? max(w.first[b], 0) : 0, len = r.ctx + r.n;
-    const int start = w.fresh && w.born ? min(first, r.ctx) : first;
-    for (int64_t j64 = start + (int64_t)blockIdx.x * 4 + warp; j64 < len; j64 += (int64_t)gridDim.x * 4) {
-      const int j = (int)j64, i = (int)quotient(j, p.by_page), page = p.table[(size_t)b * p.table_stride + i], token = j - i * p.page_size;
-      if ((unsigned)page >= (unsigned)p.n_pages) {
-        if (lane == 0 && p.status) atomicOr(p.status, GDN_STATUS_BAD_PAGE);
-        continue;
-      }
-      const int slot = page * p.page_size + token;
-      if (w.fresh && w.born && j >= r.ctx && lane == 0) w.born[slot] = (w.position ? w.position[b] : r.ctx) + j - r.ctx;
-      if (j < first) continue;
-      float got = 0.f;
-      for (int h = 0; h < p.H_kv; ++h) {
-        const T* const k = static_cast<const T*>(p.k) + page * p.k_page + h * p.k_head + token * p.k_token;
-        float x[8];
-        for (int c = 0; c < per; ++c) x[c] = to_float(k[c * 32 + lane]);
-        for (int t = max(0, j - r.ctx); t < r.n; ++t)
-          for (int g = 0; g < p.G; ++g) {
-            const T* const q = static_cast<const T*>(p.q) + (int64_t)(r.row0 + t) * p.q_row + (int64_t)(h * p.G + g) * p.q_head;
-            float s = 0.f;
-            for (int c = 0; c < per; ++c) s = fmaf(x[c], to_float(q[c * 32 + lane]), s);
-            got += expf(warp_sum(s) * w.scale - w.lse[(int64_t)(r.row0 + t) * w.lse_row + h * p.G + g]);
-          }
-      }
-      if (lane == 0) w.weight[slot] = w.fresh && j >= r.ctx ? got : fmaf(w.keep, w.weight[slot], got);
-    }
-  }
 }
 
 // ---- the choice: a block per request -----------------------------------------------------------------------------------------
@@ -268,74 +214,9 @@ __global__ void __launch_bounds__(128) move_simple(const MoveParams p) {
 
 bool aligned(const void* ptr, uintptr_t n) { return reinterpret_cast<uintptr_t>(ptr) % n == 0; }
 
-// the attention's checks on what the two calls share
-gdn_paged_attn_args as_attention(const gdn_attn_weight_args* a) {
-  gdn_paged_attn_args t = {};
-  t.B = a->B;
-  t.R = a->R;
-  t.H_q = a->H_q;
-  t.H_kv = a->H_kv;
-  t.d = a->d;
-  t.page_size = a->page_size;
-  t.n_pages = a->n_pages;
-  t.max_pages = a->max_pages;
-  t.table_stride = a->table_stride;
-  t.n_q_rows = a->n_q_rows;
-  t.in_dtype = a->in_dtype;
-  t.scale = a->scale;
-  t.q = a->q;
-  t.q_row_stride = a->q_row_stride;
-  t.q_head_stride = a->q_head_stride;
-  t.k_cache = t.v_cache = a->k_cache;
-  t.k_page_stride = t.v_page_stride = a->k_page_stride;
-  t.k_head_stride = t.v_head_stride = a->k_head_stride;
-  t.k_token_stride = t.v_token_stride = a->k_token_stride;
-  t.block_table = a->block_table;
-  t.ctx_len = a->ctx_len;
-  t.n_rows = a->n_rows;
-  t.row_start = a->row_start;
-  t.o = a->work;  // nothing is written through it
-  t.work = a->work;
-  t.status = a->status;
-  return t;
-}
-
 }  // namespace gdnlong
 
 using namespace gdnlong;
-
-extern "C" GDN_API size_t gdn_attn_weight_work_bytes(const gdn_attn_weight_args* args) {
-  if (!args) return 0;
-  const gdn_paged_attn_args t = as_attention(args);
-  return gdn_paged_attention_work_bytes(&t) ? 16 : 0;
-}
-
-extern "C" GDN_API int gdn_attn_weight(const gdn_attn_weight_args* a, void* stream) {
-  if (!a) return GDN_ERR_INVALID_ARG;
-  const gdn_paged_attn_args t = as_attention(a);
-  const int rc = gdnattn::check(&t);
-  if (rc != GDN_OK) return rc;
-  if ((a->fresh != 0 && a->fresh != 1) || !std::isfinite(a->keep)) return GDN_ERR_INVALID_ARG;
-  if (a->B == 0 || a->n_q_rows == 0) return GDN_OK;
-  if (!a->lse || !a->weight || a->lse_row_stride < a->H_q) return GDN_ERR_INVALID_ARG;
-  if (!aligned(a->lse, 4) || !aligned(a->first, 4) || !aligned(a->position, 4) || !aligned(a->weight, 4) || !aligned(a->born, 4))
-    return GDN_ERR_MISALIGNED;
-  WeightParams w = {};
-  w.p = params_of(&t);
-  w.scale = a->scale;
-  w.keep = a->keep;
-  w.fresh = a->fresh;
-  w.lse = a->lse;
-  w.lse_row = a->lse_row_stride;
-  w.first = a->first;
-  w.position = a->position;
-  w.weight = a->weight;
-  w.born = a->born;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const dim3 grid(256, std::min(a->B, 1024));
-  return a->in_dtype == GDN_DTYPE_BF16 ? launch(weight_simple<__nv_bfloat16>, grid, dim3(128), 0, st, w)
-                                       : launch(weight_simple<float>, grid, dim3(128), 0, st, w);
-}
 
 extern "C" GDN_API int gdn_evict_select(const gdn_evict_args* a, void* stream) {
   if (!a) return GDN_ERR_INVALID_ARG;

@@ -1,0 +1,360 @@
+// Attention weights in bf16 on the 5th-generation tensor cores.
+//
+// One block per SM walks its units (weight_common.cuh).  For each:
+//   S = K Q^T   tcgen05.mma: 128 keys by a tile's rows, K and Q by TMA into the MMA's layout, S (32-bit) in TMEM
+//   got += sum over S's columns of 2^(log2(e) (scale s - lse))
+// Keys are S's lanes: a thread owns a key and adds up its own columns, so no number crosses a thread, and a key's sum
+// over rows and heads stays in a register until its block of keys is done.  A tile's sum, a head's and the heads' are
+// separate sums in 32 bits: one chain over a prompt's 10^5 rows and heads would lose 4e-6.
+//
+// Roles (352 threads): warps 0-3 and 4-7 take alternate tiles out of TMEM (four S buffers), warp 8 issues the products,
+// warp 9 copies K, warp 10 Q and the rows' lse.  K of a (key block, head) is loaded once and met by all its tiles; a
+// single step's few rows are one tile, and then K streams through.
+//
+// Rows past the request's, and keys past its last token, may hold anything: a column or a lane is one row or key, and
+// theirs are not counted.
+#include <cuda.h>
+
+#include <limits>
+
+#include "tc_ptx.cuh"
+#include "weight_common.cuh"
+
+namespace gdnattn {
+
+constexpr int kWeightThreads = 352, kWeightBlocks = 152, kWeightKeys = 128;
+
+template <int kD>
+struct WeightShape {
+  static constexpr int kRows = kD == 256 ? 64 : 128;  // a tile's most rows: S's columns
+  static constexpr int kChunks = kD / 64;
+  static constexpr int kKBytes = kWeightKeys * kD * 2, kQBytes = kRows * kD * 2;
+  static constexpr int kK = kD == 64 ? 6 : kD == 128 ? 3 : 2, kQ = kD == 64 ? 4 : kD == 128 ? 3 : 2;
+  static constexpr int kSmem = 1024 + kK * kKBytes + kQ * kQBytes;
+};
+static_assert(WeightShape<64>::kSmem <= 200 * 1024 && WeightShape<128>::kSmem <= 200 * 1024 && WeightShape<256>::kSmem <= 200 * 1024);
+
+__device__ __forceinline__ void tma_rows(const CUtensorMap* map, uint32_t dst, uint32_t bar, int col, int head, int row) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(col), "r"(head), "r"(row), "r"(bar)
+      : "memory");
+}
+// 4 bytes into shared memory; the lane's arrival on a barrier once its copies so far have landed
+__device__ __forceinline__ void copy4(uint32_t to, const float* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+struct WeightTcParams {
+  WeightParams w;
+  int box;    // tokens per TMA box of K
+  int width;  // columns of a product: a tile's rows up to a multiple of 16
+};
+
+template <int kD>
+__global__ void __launch_bounds__(kWeightThreads, 1)
+    weight_tc_kernel(const WeightTcParams t, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap q_map) {
+  using S = WeightShape<kD>;
+  constexpr int kKeys = kWeightKeys, kChunks = S::kChunks, kS = 4;
+  const WeightParams& w = t.w;
+  const Params& p = w.p;
+  extern __shared__ __align__(16) uint8_t raw[];
+  __shared__ __align__(8) uint64_t bars[2 * S::kK + 2 * S::kQ + 2 * kS + 5];
+  __shared__ long long scan[kWeightThreads / 32];
+  __shared__ WeightStart start;
+  __shared__ uint32_t tmem_base;
+  __shared__ int gave_up;
+  __shared__ __align__(16) float lse_s[S::kQ][S::kRows];
+  __shared__ float cross[2][kKeys];  // the second group's sums, by key block
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t base = (smem_addr(raw) + 1023) & ~1023u, k_s = base, q_s = k_s + S::kK * S::kKBytes;
+  const uint32_t b0 = smem_addr(bars);
+  auto k_full = [&](int i) { return b0 + 8 * i; };
+  auto k_empty = [&](int i) { return b0 + 8 * (S::kK + i); };
+  auto q_full = [&](int i) { return b0 + 8 * (2 * S::kK + i); };
+  auto q_empty = [&](int i) { return b0 + 8 * (2 * S::kK + S::kQ + i); };
+  constexpr int kRest = 2 * S::kK + 2 * S::kQ;
+  auto s_full = [&](int i) { return b0 + 8 * (kRest + i); };
+  auto s_empty = [&](int i) { return b0 + 8 * (kRest + kS + i); };
+  auto c_full = [&](int i) { return b0 + 8 * (kRest + 2 * kS + i); };       // cross holds a key block's sums
+  auto c_empty = [&](int i) { return b0 + 8 * (kRest + 2 * kS + 2 + i); };  // and they have been read
+  const uint32_t drained = b0 + 8 * (kRest + 2 * kS + 4);
+  if (tid == 0) {
+    gave_up = 0;
+    for (int i = 0; i < S::kK; ++i) {
+      bar_init(k_full(i), 1);
+      bar_init(k_empty(i), 1);
+    }
+    for (int i = 0; i < S::kQ; ++i) {
+      bar_init(q_full(i), 33);   // the copy's bytes, and each lane's lse
+      bar_init(q_empty(i), 5);   // the product, and the warps that read its lse
+    }
+    for (int i = 0; i < kS; ++i) {
+      bar_init(s_full(i), 1);
+      bar_init(s_empty(i), 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      bar_init(c_full(i), 4);
+      bar_init(c_empty(i), 4);
+    }
+    bar_init(drained, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 8) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&tmem_base)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (warp == 9 && lane == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&k_map) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&q_map) : "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_wait();
+  pdl_trigger();
+  const uint32_t tmem = tmem_base;
+  find_weight_start<kKeys, kWeightThreads>(w, scan, &start);
+  WeightWalk<kKeys> x;
+  const bool any = x.begin(w, start);
+  bool ok = true;
+  int sent = 0;  // copies this warp issued
+
+  if (any && warp < 8) {
+    // ---- S out of TMEM, two groups of four warps in turn; the first also writes the weights
+    const int group = warp >> 2, quarter = warp & 3, key = tid & 127;
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+    const uint64_t scale2 = pair(w.scale, w.scale), minus2 = pair(-1.f, -1.f), log2e2 = pair(1.4426950408889634f, 1.4426950408889634f);
+    float in_keys = 0.f, in_head = 0.f;  // sums over the key block's heads before this one, and over this head's tiles
+    int slot = -2;                       // of this thread's key, -2: not looked up yet
+    float old = 0.f;
+    int4 note = {0, 0, 0, 0};
+    auto look_up = [&]() {
+      const int j = x.kb * kKeys + key;
+      slot = j >= x.req.first ? weight_slot(w, x.b, x.req.ctx + x.req.n, j) : -1;
+      old = slot >= 0 && !weight_new(w, x.req, j) ? w.weight[slot] : 0.f;
+    };
+    int i = 0, f = 0;  // tiles, key blocks
+    for (; !x.done(); x.next(), ++i) {
+      if ((i & 1) == group) {
+        const int buf = i % kS, stage = i % S::kQ;
+        if (!(ok = warp_wait(q_full(stage), (i / S::kQ) & 1, &gave_up) && warp_wait(s_full(buf), (i / kS) & 1, &gave_up))) break;
+        tc_fence_after();
+        const int n_cols = x.columns(), past = x.kb * kKeys + key - x.req.ctx - x.token();
+        // a row's token t sees this key where t >= past
+        const int from = x.kb * kKeys + kKeys - 1 - x.req.ctx - x.token() > 0 ? past * w.heads : 0;
+        uint64_t sum2[2] = {0, 0};
+#pragma unroll 1
+        for (int c = 0; c < n_cols; c += 32) {
+          uint32_t s[32];
+          tmem_load(s, lanes + buf * S::kRows + c);
+          tmem_wait_load();
+          tmem_loaded(s);
+          auto term = [&](int k, float2 l) {  // columns c + k and the next
+            const float* const v = reinterpret_cast<const float*>(s) + k;
+            const uint64_t arg = mul2(fma2(pair(v[0], v[1]), scale2, mul2(pair(l.x, l.y), minus2)), log2e2);
+            const float2 y = halves(arg);
+            return make_float2(ex2(y.x), ex2(y.y));
+          };
+          if (__all_sync(kFull, c >= from && c + 32 <= n_cols)) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 4) {
+              const float4 l = *reinterpret_cast<const float4*>(&lse_s[stage][c + k]);
+              const float2 e0 = term(k, make_float2(l.x, l.y)), e1 = term(k + 2, make_float2(l.z, l.w));
+              sum2[0] = add2(sum2[0], pair(e0.x, e0.y));
+              sum2[1] = add2(sum2[1], pair(e1.x, e1.y));
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; k += 4) {
+              const float4 l = *reinterpret_cast<const float4*>(&lse_s[stage][c + k]);
+              float2 e0 = term(k, make_float2(l.x, l.y)), e1 = term(k + 2, make_float2(l.z, l.w));
+              const int at = c + k;
+              if (at < from || at >= n_cols) e0.x = 0.f;
+              if (at + 1 < from || at + 1 >= n_cols) e0.y = 0.f;
+              if (at + 2 < from || at + 2 >= n_cols) e1.x = 0.f;
+              if (at + 3 < from || at + 3 >= n_cols) e1.y = 0.f;
+              sum2[0] = add2(sum2[0], pair(e0.x, e0.y));
+              sum2[1] = add2(sum2[1], pair(e1.x, e1.y));
+            }
+          }
+        }
+        const float2 total = halves(add2(sum2[0], sum2[1]));
+        in_head += total.x + total.y;
+        tc_fence_before();
+        warp_arrive(s_empty(buf));
+        warp_arrive(q_empty(stage));
+        if (group == 0 && slot == -2) look_up();
+      }
+      if (x.head_ends()) {
+        in_keys += in_head;
+        in_head = 0.f;
+      }
+      if (!x.keys_end()) continue;
+      // the key block's sums of both groups: the second hands its own over
+      if (group == 1) {
+        if (f >= 2 && !(ok = warp_wait(c_empty(f & 1), ((f >> 1) - 1) & 1, &gave_up))) break;
+        cross[f & 1][key] = in_keys;
+        warp_arrive(c_full(f & 1));
+      } else {
+        if (slot == -2) look_up();
+        if (!(ok = warp_wait(c_full(f & 1), (f >> 1) & 1, &gave_up))) break;
+        const float got = in_keys + cross[f & 1][key];
+        warp_arrive(c_empty(f & 1));
+        const long long rest = x.rest();
+        if (x.whole && rest == 0) {
+          if (slot >= 0) w.weight[slot] = weight_new(w, x.req, x.kb * kKeys + key) ? got : fmaf(w.keep, old, got);
+        } else {
+          w.partials[(size_t)(2 * blockIdx.x + (x.whole ? 1 : 0)) * kKeys + key] = got;
+          if (x.whole) note = make_int4((int)((rest + start.per - 1) / start.per), x.b, x.kb, 0);
+        }
+        slot = -2;
+      }
+      in_keys = 0.f;
+      ++f;
+    }
+    if (tid == 0) w.notes[blockIdx.x] = note;
+  } else if (any && warp == 8) {
+    // ---- the products, issued by one thread
+    if (lane == 0) {
+      const uint32_t idesc = instruction(t.width, false);
+      const uint32_t k_lo0 = operand_lo(k_s, 16), q_lo0 = operand_lo(q_s, 16);
+      int i = 0, group = 0;
+      bool fresh = true;  // the first tile with this K
+      for (; ok && !x.done(); x.next(), ++i) {
+        const int stage = group % S::kK, q_stage = i % S::kQ, buf = i % kS;
+        ok = (!fresh || bar_wait(k_full(stage), (group / S::kK) & 1, &gave_up)) && bar_wait(q_full(q_stage), (i / S::kQ) & 1, &gave_up) &&
+             (i < kS || bar_wait(s_empty(buf), (i / kS - 1) & 1, &gave_up));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t k_lo = k_lo0 + stage * (S::kKBytes / 16), q_lo = q_lo0 + q_stage * (S::kQBytes / 16);
+#pragma unroll
+        for (int k = 0; k < kD / 16; ++k)
+          mma_ss(tmem + buf * S::kRows, k_lo + (k / 4) * (kKeys * 8) + (k % 4) * 2, q_lo + (k / 4) * (S::kRows * 8) + (k % 4) * 2, kOperandHi,
+                 idesc, k > 0);
+        tc_commit(s_full(buf));
+        tc_commit(q_empty(q_stage));
+        fresh = x.head_ends();
+        if (fresh) {
+          tc_commit(k_empty(stage));
+          ++group;
+        }
+      }
+    }
+    __syncwarp();
+  } else if (any && warp == 9) {
+    // ---- K tiles: lane (box, chunk) copies its box of 64 columns
+    const int n_box = kKeys / t.box, box = lane / kChunks, chunk = lane % kChunks;
+    const uint32_t at = (uint32_t)chunk * (kKeys * 128) + (uint32_t)box * t.box * 128;
+    bool fresh = true, new_keys = true;
+    int page = 0, token = 0, live = 0;
+    for (; ok && !x.done(); x.next()) {
+      if (fresh) {
+        if (new_keys) {
+          const int len = x.req.ctx + x.req.n, j = x.kb * kKeys + box * t.box;
+          live = min(n_box, (len - x.kb * kKeys + t.box - 1) / t.box);
+          if (box < live) {
+            const int i = (int)quotient(j, p.by_page);
+            page = p.table[(size_t)x.b * p.table_stride + i];
+            token = j - i * p.page_size;
+            if ((unsigned)page >= (unsigned)p.n_pages) page = p.n_pages;  // outside the map: zeros; its tokens take no weight
+          }
+        }
+        const int stage = sent % S::kK;
+        if (sent >= S::kK && !(ok = warp_wait(k_empty(stage), (sent / S::kK - 1) & 1, &gave_up))) break;
+        if (lane == 0) bar_expect(k_full(stage), (uint32_t)live * t.box * kD * 2);
+        __syncwarp();
+        if (box < live) tma_box(&k_map, k_s + stage * S::kKBytes + at, k_full(stage), chunk * 64, token, x.h, page);
+        ++sent;
+      }
+      fresh = x.head_ends();
+      new_keys = x.keys_end();
+    }
+  } else if (any && warp == 10) {
+    // ---- Q tiles and their rows' lse
+    const int rows = w.tokens * w.heads;
+    for (; ok && !x.done(); x.next()) {
+      const int stage = sent % S::kQ;
+      if (sent >= S::kQ && !(ok = warp_wait(q_empty(stage), (sent / S::kQ - 1) & 1, &gave_up))) break;
+      const int row0 = x.req.row0 + x.token(), head0 = x.h * p.G + x.head(), n_cols = x.columns();
+      if (lane == 0) bar_expect(q_full(stage), (uint32_t)rows * kD * 2);
+      __syncwarp();
+      if (lane < kChunks) tma_rows(&q_map, q_s + stage * S::kQBytes + lane * (S::kRows * 128), q_full(stage), lane * 64, head0, row0);
+      for (int c = lane; c < n_cols; c += 32) {
+        const int token = (int)quotient(c, w.by_heads);
+        copy4(smem_addr(&lse_s[stage][c]), w.lse + (int64_t)(row0 + token) * w.lse_row + head0 + c - token * w.heads);
+      }
+      copies_arrive(q_full(stage));
+      ++sent;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  }
+  if (!any && tid == 0) w.notes[blockIdx.x] = make_int4(0, 0, 0, 0);
+  __syncthreads();
+  if (gave_up) {
+    // products and copies that may still be in flight, with a bound again
+    const unsigned long long end = now_ns() + kWaitNs;
+    if (tid == 8 * 32) {
+      tc_commit(drained);
+      while (!bar_try(drained, 0) && now_ns() < end) {
+      }
+    }
+    if (lane == 0 && (warp == 9 || warp == 10)) {
+      const int stages = warp == 9 ? S::kK : S::kQ;
+      for (int i = max(0, sent - stages); i < sent; ++i)
+        while (!bar_try((warp == 9 ? k_full(0) : q_full(0)) + 8 * (i % stages), (i / stages) & 1) && now_ns() < end) {
+        }
+    }
+    if (tid == 0) {
+      w.notes[blockIdx.x] = make_int4(0, 0, 0, 0);
+      if (p.status) atomicOr(p.status, GDN_STATUS_TIMEOUT);
+    }
+    __syncthreads();
+  }
+  if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+// rows of q as [d][H_q][n_q_rows]
+bool make_row_map(CUtensorMap* map, const WeightParams& w) {
+  const EncodeFn encode = encoder();
+  if (!encode) return false;
+  const Params& p = w.p;
+  const cuuint64_t H_q = (cuuint64_t)p.H_kv * p.G, dims[3] = {(cuuint64_t)p.d, H_q, (cuuint64_t)p.n_q_rows};
+  // the stride of a dimension of one entry is never used, but must be a valid one
+  const cuuint64_t head = (cuuint64_t)(H_q > 1 ? p.q_head : p.d) * 2, row = p.n_q_rows > 1 ? (cuuint64_t)p.q_row * 2 : head;
+  const cuuint64_t strides[2] = {head, row};
+  const cuuint32_t box[3] = {64, (cuuint32_t)w.heads, (cuuint32_t)w.tokens}, steps[3] = {1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p.q), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int kD>
+int run(WeightTcParams& t, cudaStream_t st) {
+  using S = WeightShape<kD>;
+  if (cudaFuncSetAttribute(weight_tc_kernel<kD>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem) != cudaSuccess) return GDN_ERR_LAUNCH;
+  set_weight_tiles(t.w, S::kRows);
+  t.width = (t.w.tokens * t.w.heads + 15) / 16 * 16;
+  t.box = 16;
+  while (t.box * 2 <= kWeightKeys && t.w.p.page_size % (t.box * 2) == 0) t.box *= 2;
+  CUtensorMap k_map, q_map;
+  if (!make_map(&k_map, t.w.p, t.w.p.k, t.w.p.k_token, t.w.p.k_head, t.w.p.k_page, t.box) || !make_row_map(&q_map, t.w)) return GDN_ERR_LAUNCH;
+  const int rc = launch(weight_tc_kernel<kD>, dim3(kWeightBlocks), dim3(kWeightThreads), S::kSmem, st, t, k_map, q_map);
+  return rc != GDN_OK ? rc : launch_weight_join<kWeightKeys>(t.w, st);
+}
+
+int run_weight_tc(WeightParams& w, cudaStream_t st) {
+  w.p.n_blocks = kWeightBlocks;
+  w.partials = reinterpret_cast<float*>(w.notes + kWeightBlocks);
+  WeightTcParams t{w, 0, 0};
+  return w.p.d == 64 ? run<64>(t, st) : w.p.d == 128 ? run<128>(t, st) : run<256>(t, st);
+}
+
+}  // namespace gdnattn

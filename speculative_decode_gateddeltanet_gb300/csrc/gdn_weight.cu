@@ -43,14 +43,14 @@ __global__ void __launch_bounds__(kWsThreads, 2) weight_simt_kernel(const Weight
   float in_keys[2] = {0.f, 0.f}, in_head[2] = {0.f, 0.f};
   bool new_head = true, new_keys = true;
   if (x.begin(w, start)) {
-    for (; !x.done(); x.next()) {
+    for (; !x.done(); x.next(1)) {
       __syncthreads();  // the last unit's products are done
       if (new_keys && tid < kWsKeys) {
         const int j = x.kb * kWsKeys + tid, i = (int)quotient(j, p.by_page);
         const int page = j < x.req.ctx + x.req.n ? p.table[(size_t)x.b * p.table_stride + i] : -1;
         k_at[tid] = (unsigned)page < (unsigned)p.n_pages ? page * p.k_page + (j - i * p.page_size) * p.k_token : -1;
       }
-      const int n_cols = x.columns(), head0 = x.h * p.G + x.head(), row0 = x.req.row0 + x.token();
+      const int n_cols = x.columns(x.m), head0 = x.h * p.G + x.head(x.m), row0 = x.req.row0 + x.token(x.m);
       for (int i = tid; i < kWsRows * kChunks; i += kWsThreads) {
         const int r = i / kChunks, c = i % kChunks, token = (int)quotient(r, w.by_heads);
         const bool valid = r < n_cols;
@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(kWsThreads, 2) weight_simt_kernel(const Weight
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const int past = x.kb * kWsKeys + lane + 32 * k - x.req.ctx - x.token();  // rows from this token on see the key
+          const int past = x.kb * kWsKeys + lane + 32 * k - x.req.ctx - x.token(x.m);  // rows from this token on see the key
           float sum = 0.f;
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
@@ -105,8 +105,8 @@ __global__ void __launch_bounds__(kWsThreads, 2) weight_simt_kernel(const Weight
           in_head[k] += sum;
         }
       }
-      new_head = x.head_ends();
-      new_keys = x.keys_end();
+      new_head = x.run() == 1;
+      new_keys = x.keys_end(1);
       if (new_head) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kWsThreads, 2) weight_simt_kernel(const Weight
         float got = 0.f;
 #pragma unroll
         for (int i = 0; i < kWsThreads / 32; ++i) got += cross[i][tid];
-        const long long rest = x.rest();
+        const long long rest = x.rest(1);
         if (x.whole && rest == 0) {
           const int j = x.kb * kWsKeys + tid, slot = j >= x.req.first ? weight_slot(w, x.b, x.req.ctx + x.req.n, j) : -1;
           if (slot >= 0) w.weight[slot] = weight_new(w, x.req, j) ? got : fmaf(w.keep, w.weight[slot], got);

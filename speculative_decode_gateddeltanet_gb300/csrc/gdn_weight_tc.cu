@@ -7,8 +7,9 @@
 // over rows and heads stays in a register until its block of keys is done.  A tile's sum, a head's and the heads' are
 // separate sums in 32 bits: one chain over a prompt's 10^5 rows and heads would lose 4e-6.
 //
-// Roles (352 threads): warps 0-3 and 4-7 take alternate tiles out of TMEM (four S buffers), warp 8 issues the products,
-// warp 9 copies K, warp 10 Q and the rows' lse.  K of a (key block, head) is loaded once and met by all its tiles; a
+// Roles (512 threads): three groups of four warps take the tiles out of TMEM in turn (four S buffers), warp 12 issues the
+// products, warp 13 copies K, warp 14 Q, warp 15 the rows' lse (one warp for both took 1500 clocks a tile, more than its
+// sums).  K of a (key block, head) is loaded once and met by all its tiles; a
 // single step's few rows are one tile, and then K streams through.
 //
 // Rows past the request's, and keys past its last token, may hold anything: a column or a lane is one row or key, and
@@ -22,17 +23,21 @@
 
 namespace gdnattn {
 
-constexpr int kWeightThreads = 352, kWeightBlocks = 152, kWeightKeys = 128;
+constexpr int kGroups = 3, kWeightThreads = 128 * kGroups + 128, kWeightBlocks = 152, kWeightKeys = 128;
 
 template <int kD>
 struct WeightShape {
   static constexpr int kRows = kD == 256 ? 64 : 128;  // a tile's most rows: S's columns
   static constexpr int kChunks = kD / 64;
   static constexpr int kKBytes = kWeightKeys * kD * 2, kQBytes = kRows * kD * 2;
-  static constexpr int kK = kD == 64 ? 6 : kD == 128 ? 3 : 2, kQ = kD == 64 ? 4 : kD == 128 ? 3 : 2;
-  static constexpr int kSmem = 1024 + kK * kKBytes + kQ * kQBytes;
+  // Stages: of K at least so many, the rest is shared out by the size of a tile (run).
+  static constexpr int kLeastK = kD == 64 ? 6 : kD == 128 ? 3 : 2, kMostK = 8, kMostQ = 8;
+  static constexpr int kBytes = 216 * 1024;  // of both
+  static constexpr int kSmem = 1024 + kBytes;
 };
-static_assert(WeightShape<64>::kSmem <= 200 * 1024 && WeightShape<128>::kSmem <= 200 * 1024 && WeightShape<256>::kSmem <= 200 * 1024);
+static_assert(WeightShape<64>::kLeastK * WeightShape<64>::kKBytes + 2 * WeightShape<64>::kQBytes <= WeightShape<64>::kBytes);
+static_assert(WeightShape<128>::kLeastK * WeightShape<128>::kKBytes + 2 * WeightShape<128>::kQBytes <= WeightShape<128>::kBytes);
+static_assert(WeightShape<256>::kLeastK * WeightShape<256>::kKBytes + 2 * WeightShape<256>::kQBytes <= WeightShape<256>::kBytes);
 
 __device__ __forceinline__ void tma_rows(const CUtensorMap* map, uint32_t dst, uint32_t bar, int col, int head, int row) {
   asm volatile(
@@ -57,62 +62,70 @@ struct WeightTcParams {
   WeightParams w;
   int box;    // tokens per TMA box of K
   int width;  // columns of a product: a tile's rows up to a multiple of 16
+  int n_k, n_q;  // stages
 };
 
 template <int kD>
 __global__ void __launch_bounds__(kWeightThreads, 1)
     weight_tc_kernel(const WeightTcParams t, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap q_map) {
   using S = WeightShape<kD>;
-  constexpr int kKeys = kWeightKeys, kChunks = S::kChunks, kS = 4;
+  constexpr int kKeys = kWeightKeys, kChunks = S::kChunks, kS = 4, kL = 8;
   const WeightParams& w = t.w;
   const Params& p = w.p;
   extern __shared__ __align__(16) uint8_t raw[];
-  __shared__ __align__(8) uint64_t bars[2 * S::kK + 2 * S::kQ + 2 * kS + 5];
+  __shared__ __align__(8) uint64_t bars[2 * S::kMostK + 2 * S::kMostQ + 2 * kS + 5 + 2 * kL];
   __shared__ long long scan[kWeightThreads / 32];
   __shared__ WeightStart start;
   __shared__ uint32_t tmem_base;
   __shared__ int gave_up;
-  __shared__ __align__(16) float lse_s[S::kQ][S::kRows];
-  __shared__ float cross[2][kKeys];  // the second group's sums, by key block
+  __shared__ __align__(16) float lse_s[kL][S::kRows];
+  __shared__ float cross[2][kGroups - 1][kKeys];  // the other groups' sums, by key block
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t base = (smem_addr(raw) + 1023) & ~1023u, k_s = base, q_s = k_s + S::kK * S::kKBytes;
+  const uint32_t base = (smem_addr(raw) + 1023) & ~1023u, k_s = base, q_s = k_s + t.n_k * S::kKBytes, q_bytes = t.width * kD * 2;
   const uint32_t b0 = smem_addr(bars);
   auto k_full = [&](int i) { return b0 + 8 * i; };
-  auto k_empty = [&](int i) { return b0 + 8 * (S::kK + i); };
-  auto q_full = [&](int i) { return b0 + 8 * (2 * S::kK + i); };
-  auto q_empty = [&](int i) { return b0 + 8 * (2 * S::kK + S::kQ + i); };
-  constexpr int kRest = 2 * S::kK + 2 * S::kQ;
+  auto k_empty = [&](int i) { return b0 + 8 * (S::kMostK + i); };
+  auto q_full = [&](int i) { return b0 + 8 * (2 * S::kMostK + i); };
+  auto q_empty = [&](int i) { return b0 + 8 * (2 * S::kMostK + S::kMostQ + i); };
+  constexpr int kRest = 2 * S::kMostK + 2 * S::kMostQ;
   auto s_full = [&](int i) { return b0 + 8 * (kRest + i); };
   auto s_empty = [&](int i) { return b0 + 8 * (kRest + kS + i); };
   auto c_full = [&](int i) { return b0 + 8 * (kRest + 2 * kS + i); };       // cross holds a key block's sums
   auto c_empty = [&](int i) { return b0 + 8 * (kRest + 2 * kS + 2 + i); };  // and they have been read
   const uint32_t drained = b0 + 8 * (kRest + 2 * kS + 4);
+  // lse has a ring of its own: it is read until a tile's sums are done, some 2000 clocks after Q is free again
+  auto l_full = [&](int i) { return b0 + 8 * (kRest + 2 * kS + 5 + i); };
+  auto l_empty = [&](int i) { return b0 + 8 * (kRest + 2 * kS + 5 + kL + i); };
   if (tid == 0) {
     gave_up = 0;
-    for (int i = 0; i < S::kK; ++i) {
+    for (int i = 0; i < t.n_k; ++i) {
       bar_init(k_full(i), 1);
       bar_init(k_empty(i), 1);
     }
-    for (int i = 0; i < S::kQ; ++i) {
-      bar_init(q_full(i), 33);   // the copy's bytes, and each lane's lse
-      bar_init(q_empty(i), 5);   // the product, and the warps that read its lse
+    for (int i = 0; i < t.n_q; ++i) {
+      bar_init(q_full(i), 1);
+      bar_init(q_empty(i), 1);
+    }
+    for (int i = 0; i < kL; ++i) {
+      bar_init(l_full(i), 32);
+      bar_init(l_empty(i), 4);
     }
     for (int i = 0; i < kS; ++i) {
       bar_init(s_full(i), 1);
       bar_init(s_empty(i), 4);
     }
     for (int i = 0; i < 2; ++i) {
-      bar_init(c_full(i), 4);
+      bar_init(c_full(i), 4 * (kGroups - 1));
       bar_init(c_empty(i), 4);
     }
     bar_init(drained, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 8) {
+  if (warp == 12) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&tmem_base)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  if (warp == 9 && lane == 0) {
+  if (warp == 13 && lane == 0) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(&k_map) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(&q_map) : "memory");
   }
@@ -127,12 +140,23 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
   const bool any = x.begin(w, start);
   bool ok = true;
   int sent = 0;  // copies this warp issued
+  // a ring's stage and the parity of its round; one more step
+  struct Ring {
+    int stage, round, size;
+    __device__ void next() {
+      if (++stage == size) {
+        stage = 0;
+        ++round;
+      }
+    }
+  };
+  Ring q_ring = {0, 0, t.n_q}, k_ring = {0, 0, t.n_k};
 
-  if (any && warp < 8) {
-    // ---- S out of TMEM, two groups of four warps in turn; the first also writes the weights
+  if (any && warp < 4 * kGroups) {
+    // ---- S out of TMEM, the groups in turn; the first also writes the weights
     const int group = warp >> 2, quarter = warp & 3, key = tid & 127;
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
-    const uint64_t scale2 = pair(w.scale, w.scale), minus2 = pair(-1.f, -1.f), log2e2 = pair(1.4426950408889634f, 1.4426950408889634f);
+    const uint64_t scale2 = pair(p.scale_log2, p.scale_log2), log2e2 = pair(-1.4426950408889634f, -1.4426950408889634f);
     float in_keys = 0.f, in_head = 0.f;  // sums over the key block's heads before this one, and over this head's tiles
     int slot = -2;                       // of this thread's key, -2: not looked up yet
     float old = 0.f;
@@ -142,26 +166,24 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
       slot = j >= x.req.first ? weight_slot(w, x.b, x.req.ctx + x.req.n, j) : -1;
       old = slot >= 0 && !weight_new(w, x.req, j) ? w.weight[slot] : 0.f;
     };
-    int i = 0, f = 0;  // tiles, key blocks
-    for (; !x.done(); x.next(), ++i) {
-      if ((i & 1) == group) {
-        const int buf = i % kS, stage = i % S::kQ;
-        if (!(ok = warp_wait(q_full(stage), (i / S::kQ) & 1, &gave_up) && warp_wait(s_full(buf), (i / kS) & 1, &gave_up))) break;
+    int done = 0, turn = 0, f = 0;  // tiles so far, whose turn it is, key blocks
+    for (int run; !x.done(); x.next(run)) {
+      run = x.run();
+      int r = group - turn;  // the group's first tile of the run
+      if (r < 0) r += kGroups;
+      const int past0 = x.kb * kKeys + key - x.req.ctx;
+      for (; r < run; r += kGroups) {
+        const int i = done + r, m = x.m + r, buf = i % kS, stage = i % kL;
+        if (!(ok = warp_wait(s_full(buf), (i / kS) & 1, &gave_up) && warp_wait(l_full(stage), (i / kL) & 1, &gave_up))) break;
         tc_fence_after();
-        const int n_cols = x.columns(), past = x.kb * kKeys + key - x.req.ctx - x.token();
-        // a row's token t sees this key where t >= past
-        const int from = x.kb * kKeys + kKeys - 1 - x.req.ctx - x.token() > 0 ? past * w.heads : 0;
+        const int n_cols = x.columns(m), past = past0 - x.token(m);
+        // a row's token t sees this key where t >= past; no key of the block is hidden where the last is not
+        const int from = past - key + kKeys - 1 > 0 ? past * w.heads : 0;
         uint64_t sum2[2] = {0, 0};
-#pragma unroll 1
-        for (int c = 0; c < n_cols; c += 32) {
-          uint32_t s[32];
-          tmem_load(s, lanes + buf * S::kRows + c);
-          tmem_wait_load();
-          tmem_loaded(s);
+        auto sum_up = [&](const uint32_t (&s)[32], int c) {
           auto term = [&](int k, float2 l) {  // columns c + k and the next
             const float* const v = reinterpret_cast<const float*>(s) + k;
-            const uint64_t arg = mul2(fma2(pair(v[0], v[1]), scale2, mul2(pair(l.x, l.y), minus2)), log2e2);
-            const float2 y = halves(arg);
+            const float2 y = halves(fma2(pair(v[0], v[1]), scale2, mul2(pair(l.x, l.y), log2e2)));
             return make_float2(ex2(y.x), ex2(y.y));
           };
           if (__all_sync(kFull, c >= from && c + 32 <= n_cols)) {
@@ -186,30 +208,41 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
               sum2[1] = add2(sum2[1], pair(e1.x, e1.y));
             }
           }
+        };
+#pragma unroll 1
+        for (int c = 0; c < n_cols; c += 32) {
+          uint32_t s[32];
+          tmem_load(s, lanes + buf * S::kRows + c);
+          tmem_wait_load();
+          tmem_loaded(s);
+          sum_up(s, c);
         }
         const float2 total = halves(add2(sum2[0], sum2[1]));
         in_head += total.x + total.y;
         tc_fence_before();
         warp_arrive(s_empty(buf));
-        warp_arrive(q_empty(stage));
+        warp_arrive(l_empty(stage));
         if (group == 0 && slot == -2) look_up();
       }
-      if (x.head_ends()) {
-        in_keys += in_head;
-        in_head = 0.f;
-      }
-      if (!x.keys_end()) continue;
-      // the key block's sums of both groups: the second hands its own over
-      if (group == 1) {
+      if (!ok) break;
+      done += run;
+      turn = (turn + run) % kGroups;
+      in_keys += in_head;
+      in_head = 0.f;
+      if (!x.keys_end(run)) continue;
+      // the key block's sums of all groups: the others hand theirs over
+      if (group > 0) {
         if (f >= 2 && !(ok = warp_wait(c_empty(f & 1), ((f >> 1) - 1) & 1, &gave_up))) break;
-        cross[f & 1][key] = in_keys;
+        cross[f & 1][group - 1][key] = in_keys;
         warp_arrive(c_full(f & 1));
       } else {
         if (slot == -2) look_up();
         if (!(ok = warp_wait(c_full(f & 1), (f >> 1) & 1, &gave_up))) break;
-        const float got = in_keys + cross[f & 1][key];
+        float got = in_keys;
+#pragma unroll
+        for (int g = 0; g < kGroups - 1; ++g) got += cross[f & 1][g][key];
         warp_arrive(c_empty(f & 1));
-        const long long rest = x.rest();
+        const long long rest = x.rest(run);
         if (x.whole && rest == 0) {
           if (slot >= 0) w.weight[slot] = weight_new(w, x.req, x.kb * kKeys + key) ? got : fmaf(w.keep, old, got);
         } else {
@@ -222,78 +255,101 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
       ++f;
     }
     if (tid == 0) w.notes[blockIdx.x] = note;
-  } else if (any && warp == 8) {
+  } else if (any && warp == 12) {
     // ---- the products, issued by one thread
     if (lane == 0) {
       const uint32_t idesc = instruction(t.width, false);
       const uint32_t k_lo0 = operand_lo(k_s, 16), q_lo0 = operand_lo(q_s, 16);
-      int i = 0, group = 0;
-      bool fresh = true;  // the first tile with this K
-      for (; ok && !x.done(); x.next(), ++i) {
-        const int stage = group % S::kK, q_stage = i % S::kQ, buf = i % kS;
-        ok = (!fresh || bar_wait(k_full(stage), (group / S::kK) & 1, &gave_up)) && bar_wait(q_full(q_stage), (i / S::kQ) & 1, &gave_up) &&
-             (i < kS || bar_wait(s_empty(buf), (i / kS - 1) & 1, &gave_up));
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t k_lo = k_lo0 + stage * (S::kKBytes / 16), q_lo = q_lo0 + q_stage * (S::kQBytes / 16);
+      int i = 0;
+      for (int run; ok && !x.done(); x.next(run)) {
+        run = x.run();
+        const uint32_t k_lo = k_lo0 + k_ring.stage * (S::kKBytes / 16);
+        ok = bar_wait(k_full(k_ring.stage), k_ring.round & 1, &gave_up);
+        for (int r = 0; ok && r < run; ++r, ++i, q_ring.next()) {
+          const int buf = i % kS;
+          ok = bar_wait(q_full(q_ring.stage), q_ring.round & 1, &gave_up) && (i < kS || bar_wait(s_empty(buf), (i / kS - 1) & 1, &gave_up));
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t q_lo = q_lo0 + q_ring.stage * (q_bytes / 16), s_at = tmem + buf * S::kRows;
 #pragma unroll
-        for (int k = 0; k < kD / 16; ++k)
-          mma_ss(tmem + buf * S::kRows, k_lo + (k / 4) * (kKeys * 8) + (k % 4) * 2, q_lo + (k / 4) * (S::kRows * 8) + (k % 4) * 2, kOperandHi,
-                 idesc, k > 0);
-        tc_commit(s_full(buf));
-        tc_commit(q_empty(q_stage));
-        fresh = x.head_ends();
-        if (fresh) {
-          tc_commit(k_empty(stage));
-          ++group;
+          for (int k = 0; k < kD / 16; ++k)
+            mma_ss(s_at, k_lo + (k / 4) * (kKeys * 8) + (k % 4) * 2, q_lo + (k / 4) * (t.width * 8) + (k % 4) * 2, kOperandHi, idesc, k > 0);
+          tc_commit(s_full(buf));
+          tc_commit(q_empty(q_ring.stage));
         }
+        if (!ok) break;
+        tc_commit(k_empty(k_ring.stage));
+        k_ring.next();
       }
     }
     __syncwarp();
-  } else if (any && warp == 9) {
+  } else if (any && warp == 13) {
     // ---- K tiles: lane (box, chunk) copies its box of 64 columns
     const int n_box = kKeys / t.box, box = lane / kChunks, chunk = lane % kChunks;
     const uint32_t at = (uint32_t)chunk * (kKeys * 128) + (uint32_t)box * t.box * 128;
-    bool fresh = true, new_keys = true;
+    bool new_keys = true;
     int page = 0, token = 0, live = 0;
-    for (; ok && !x.done(); x.next()) {
-      if (fresh) {
-        if (new_keys) {
-          const int len = x.req.ctx + x.req.n, j = x.kb * kKeys + box * t.box;
-          live = min(n_box, (len - x.kb * kKeys + t.box - 1) / t.box);
-          if (box < live) {
-            const int i = (int)quotient(j, p.by_page);
-            page = p.table[(size_t)x.b * p.table_stride + i];
-            token = j - i * p.page_size;
-            if ((unsigned)page >= (unsigned)p.n_pages) page = p.n_pages;  // outside the map: zeros; its tokens take no weight
-          }
+    for (int run; ok && !x.done(); x.next(run)) {
+      run = x.run();
+      if (new_keys) {
+        const int len = x.req.ctx + x.req.n, j = x.kb * kKeys + box * t.box;
+        live = min(n_box, (len - x.kb * kKeys + t.box - 1) / t.box);
+        if (box < live) {
+          const int i = (int)quotient(j, p.by_page);
+          page = p.table[(size_t)x.b * p.table_stride + i];
+          token = j - i * p.page_size;
+          if ((unsigned)page >= (unsigned)p.n_pages) page = p.n_pages;  // outside the map: zeros; its tokens take no weight
         }
-        const int stage = sent % S::kK;
-        if (sent >= S::kK && !(ok = warp_wait(k_empty(stage), (sent / S::kK - 1) & 1, &gave_up))) break;
-        if (lane == 0) bar_expect(k_full(stage), (uint32_t)live * t.box * kD * 2);
-        __syncwarp();
-        if (box < live) tma_box(&k_map, k_s + stage * S::kKBytes + at, k_full(stage), chunk * 64, token, x.h, page);
-        ++sent;
       }
-      fresh = x.head_ends();
-      new_keys = x.keys_end();
-    }
-  } else if (any && warp == 10) {
-    // ---- Q tiles and their rows' lse
-    const int rows = w.tokens * w.heads;
-    for (; ok && !x.done(); x.next()) {
-      const int stage = sent % S::kQ;
-      if (sent >= S::kQ && !(ok = warp_wait(q_empty(stage), (sent / S::kQ - 1) & 1, &gave_up))) break;
-      const int row0 = x.req.row0 + x.token(), head0 = x.h * p.G + x.head(), n_cols = x.columns();
-      if (lane == 0) bar_expect(q_full(stage), (uint32_t)rows * kD * 2);
+      const int stage = k_ring.stage;
+      if (k_ring.round > 0 && !(ok = warp_wait(k_empty(stage), (k_ring.round - 1) & 1, &gave_up))) break;
+      if (lane == 0) bar_expect(k_full(stage), (uint32_t)live * t.box * kD * 2);
       __syncwarp();
-      if (lane < kChunks) tma_rows(&q_map, q_s + stage * S::kQBytes + lane * (S::kRows * 128), q_full(stage), lane * 64, head0, row0);
-      for (int c = lane; c < n_cols; c += 32) {
-        const int token = (int)quotient(c, w.by_heads);
-        copy4(smem_addr(&lse_s[stage][c]), w.lse + (int64_t)(row0 + token) * w.lse_row + head0 + c - token * w.heads);
-      }
-      copies_arrive(q_full(stage));
+      if (box < live) tma_box(&k_map, k_s + stage * S::kKBytes + at, k_full(stage), chunk * 64, token, x.h, page);
       ++sent;
+      k_ring.next();
+      new_keys = x.keys_end(run);
+    }
+  } else if (any && warp == 14) {
+    // ---- Q tiles: lane c copies 64 columns
+    const int rows = w.tokens * w.heads;
+    for (int run; ok && !x.done(); x.next(run)) {
+      run = x.run();
+      for (int r = 0; r < run; ++r) {
+        const int stage = q_ring.stage;
+        if (q_ring.round > 0 && !(ok = warp_wait(q_empty(stage), (q_ring.round - 1) & 1, &gave_up))) break;
+        if (lane == 0) bar_expect(q_full(stage), (uint32_t)rows * kD * 2);
+        __syncwarp();
+        if (lane < kChunks)
+          tma_rows(&q_map, q_s + stage * q_bytes + lane * (t.width * 128), q_full(stage), lane * 64, x.h * p.G + x.head(x.m + r),
+                   x.req.row0 + x.token(x.m + r));
+        ++sent;
+        q_ring.next();
+      }
+    }
+  } else if (any && warp == 15) {
+    // ---- the tiles' lse: lane c copies columns c, c + 32, ..., whose tokens and heads are the same in every tile
+    constexpr int kEach = S::kRows / 32;
+    int64_t off[kEach];
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      const int c = lane + 32 * k, token = (int)quotient(c, w.by_heads);
+      off[k] = (int64_t)token * w.lse_row + c - token * w.heads;
+    }
+    int i = 0;
+    for (int run; ok && !x.done(); x.next(run)) {
+      run = x.run();
+      for (int r = 0; r < run; ++r, ++i) {
+        const int stage = i % kL, m = x.m + r;
+        if (i >= kL && !(ok = warp_wait(l_empty(stage), (i / kL - 1) & 1, &gave_up))) break;
+        const int n_cols = x.columns(m);
+        const float* const from = w.lse + (int64_t)(x.req.row0 + x.token(m)) * w.lse_row + x.h * p.G + x.head(m);
+        const uint32_t to = smem_addr(&lse_s[stage][lane]);
+#pragma unroll
+        for (int k = 0; k < kEach; ++k)
+          if (lane + 32 * k < n_cols) copy4(to + 128 * k, from + off[k]);
+        copies_arrive(l_full(stage));
+      }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
   }
@@ -302,15 +358,15 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
   if (gave_up) {
     // products and copies that may still be in flight, with a bound again
     const unsigned long long end = now_ns() + kWaitNs;
-    if (tid == 8 * 32) {
+    if (tid == 12 * 32) {
       tc_commit(drained);
       while (!bar_try(drained, 0) && now_ns() < end) {
       }
     }
-    if (lane == 0 && (warp == 9 || warp == 10)) {
-      const int stages = warp == 9 ? S::kK : S::kQ;
+    if (lane == 0 && (warp == 13 || warp == 14)) {
+      const int stages = warp == 13 ? t.n_k : t.n_q;
       for (int i = max(0, sent - stages); i < sent; ++i)
-        while (!bar_try((warp == 9 ? k_full(0) : q_full(0)) + 8 * (i % stages), (i / stages) & 1) && now_ns() < end) {
+        while (!bar_try((warp == 13 ? k_full(0) : q_full(0)) + 8 * (i % stages), (i / stages) & 1) && now_ns() < end) {
         }
     }
     if (tid == 0) {
@@ -319,7 +375,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
     }
     __syncthreads();
   }
-  if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  if (warp == 12) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
 // rows of q as [d][H_q][n_q_rows]
@@ -342,6 +398,10 @@ int run(WeightTcParams& t, cudaStream_t st) {
   if (cudaFuncSetAttribute(weight_tc_kernel<kD>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem) != cudaSuccess) return GDN_ERR_LAUNCH;
   set_weight_tiles(t.w, S::kRows);
   t.width = (t.w.tokens * t.w.heads + 15) / 16 * 16;
+  const int q_bytes = t.width * kD * 2, left = S::kBytes - S::kLeastK * S::kKBytes;
+  t.n_q = left / q_bytes < S::kMostQ ? left / q_bytes : S::kMostQ;
+  t.n_k = (S::kBytes - t.n_q * q_bytes) / S::kKBytes;
+  if (t.n_k > S::kMostK) t.n_k = S::kMostK;
   t.box = 16;
   while (t.box * 2 <= kWeightKeys && t.w.p.page_size % (t.box * 2) == 0) t.box *= 2;
   CUtensorMap k_map, q_map;
@@ -353,7 +413,7 @@ int run(WeightTcParams& t, cudaStream_t st) {
 int run_weight_tc(WeightParams& w, cudaStream_t st) {
   w.p.n_blocks = kWeightBlocks;
   w.partials = reinterpret_cast<float*>(w.notes + kWeightBlocks);
-  WeightTcParams t{w, 0, 0};
+  WeightTcParams t{w, 0, 0, 0, 0};
   return w.p.d == 64 ? run<64>(t, st) : w.p.d == 128 ? run<128>(t, st) : run<256>(t, st);
 }
 

@@ -162,13 +162,16 @@ struct WeightWalk {
     return true;
   }
   __device__ bool done() const { return left <= 0; }
-  __device__ bool head_ends() const { return left == 1 || m + 1 == req.M; }                          // of this block
-  __device__ bool keys_end() const { return left == 1 || (m + 1 == req.M && h + 1 == w->p.H_kv); }   // of this block
-  // units of this key block behind this one
-  __device__ long long rest() const { return (long long)(w->p.H_kv - 1 - h) * (req.M - low) + req.M - 1 - m; }
-  __device__ void next() {
-    if (--left <= 0) return;
-    if (++m < req.M) return;
+  // units of this head and key block that follow each other here, this one first; walked in one step
+  __device__ int run() const { return (int)min(left, (long long)(req.M - m)); }
+  // whether the run is the block's last with its key block, and the key block's units behind it
+  __device__ bool keys_end(int run) const { return left == run || (h + 1 == w->p.H_kv && m + run == req.M); }
+  __device__ long long rest(int run) const { return (long long)(w->p.H_kv - 1 - h) * (req.M - low) + req.M - m - run; }
+  __device__ void next(int run) {
+    left -= run;
+    if (left <= 0) return;
+    m += run;
+    if (m < req.M) return;
     m = low;
     if (++h < w->p.H_kv) return;
     h = 0;
@@ -181,11 +184,11 @@ struct WeightWalk {
     }
     low = m = U::m0(*w, req, kb);
   }
-  // rows of the tile: the first token, the first of its heads, and the columns that are rows of the request
-  __device__ int token() const { return (w->parts == 1 ? m : (int)quotient(m, w->by_parts)) * w->tokens; }
-  __device__ int head() const { return w->parts == 1 ? 0 : (m - (int)quotient(m, w->by_parts) * w->parts) * w->heads; }
-  __device__ int columns() const {
-    return w->parts == 1 ? min(w->tokens, req.n - token()) * w->heads : min(w->heads, w->p.G - head());
+  // rows of tile m: the first token, the first of its heads, and the columns that are rows of the request
+  __device__ int token(int m) const { return (w->parts == 1 ? m : (int)quotient(m, w->by_parts)) * w->tokens; }
+  __device__ int head(int m) const { return w->parts == 1 ? 0 : (m - (int)quotient(m, w->by_parts) * w->parts) * w->heads; }
+  __device__ int columns(int m) const {
+    return w->parts == 1 ? min(w->tokens, req.n - token(m)) * w->heads : min(w->heads, w->p.G - head(m));
   }
 };
 

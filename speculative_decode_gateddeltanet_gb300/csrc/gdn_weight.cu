@@ -38,7 +38,7 @@ __global__ void __launch_bounds__(kWsThreads, 2) weight_simt_kernel(const Weight
   const Params& p = w.p;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   find_weight_start<kWsKeys, kWsThreads>(w, scan, &start);
-  int4 note = {0, 0, 0, 0};
+  int note = 0;
   WeightWalk<kWsKeys> x;
   float in_keys[2] = {0.f, 0.f}, in_head[2] = {0.f, 0.f};
   bool new_head = true, new_keys = true;
@@ -124,12 +124,17 @@ __global__ void __launch_bounds__(kWsThreads, 2) weight_simt_kernel(const Weight
 #pragma unroll
         for (int i = 0; i < kWsThreads / 32; ++i) got += cross[i][tid];
         const long long rest = x.rest(1);
-        if (x.whole && rest == 0) {
-          const int j = x.kb * kWsKeys + tid, slot = j >= x.req.first ? weight_slot(w, x.b, x.req.ctx + x.req.n, j) : -1;
-          if (slot >= 0) w.weight[slot] = weight_new(w, x.req, j) ? got : fmaf(w.keep, w.weight[slot], got);
+        if (!x.whole) {
+          w.partials[(size_t)(2 * blockIdx.x) * kWsKeys + tid] = got;
         } else {
-          w.partials[(size_t)(2 * blockIdx.x + (x.whole ? 1 : 0)) * kWsKeys + tid] = got;
-          if (x.whole) note = make_int4((int)((rest + start.per - 1) / start.per), x.b, x.kb, 0);
+          const int place = weight_place(w, x.req, x.b, x.kb * kWsKeys + tid);
+          if (rest == 0) {
+            add_weight(w, place, old_weight(w, place), got);
+          } else {
+            w.partials[(size_t)(2 * blockIdx.x + 1) * kWsKeys + tid] = got;
+            w.slots[blockIdx.x * kWsKeys + tid] = place;
+            note = (int)((rest + start.per - 1) / start.per);
+          }
         }
       }
     }
@@ -145,16 +150,10 @@ int run(const WeightParams& w, cudaStream_t st) {
   return rc != GDN_OK ? rc : launch_weight_join<kWsKeys>(w, st);
 }
 
-int run_weight_simt(WeightParams& w, cudaStream_t st) {
-  w.p.n_blocks = kWsBlocks;
-  w.partials = reinterpret_cast<float*>(w.notes + kWsBlocks);
+int run_weight_simt(WeightParams& w, void* work, cudaStream_t st) {
+  set_weight_work(w, kWsBlocks, kWsKeys, work);
   set_weight_tiles(w, kWsRows);
   return w.p.d == 64 ? run<64>(w, st) : w.p.d == 128 ? run<128>(w, st) : run<256>(w, st);
-}
-
-size_t weight_work_bytes(int dtype) {
-  // 152 blocks of 128 keys on the tensor cores
-  return dtype == GDN_DTYPE_BF16 ? 152 * (sizeof(int4) + 2 * 128 * sizeof(float)) : kWsBlocks * (sizeof(int4) + 2 * kWsKeys * sizeof(float));
 }
 
 // the attention's checks on what the two calls share
@@ -208,7 +207,7 @@ using namespace gdnattn;
 extern "C" GDN_API size_t gdn_attn_weight_work_bytes(const gdn_attn_weight_args* args) {
   if (!args) return 0;
   const gdn_paged_attn_args t = as_attention(args);
-  return gdn_paged_attention_work_bytes(&t) ? weight_work_bytes(args->in_dtype) : 0;
+  return gdn_paged_attention_work_bytes(&t) ? (args->in_dtype == GDN_DTYPE_BF16 ? weight_tc_work() : weight_work(kWsBlocks, kWsKeys)) : 0;
 }
 
 extern "C" GDN_API int gdn_attn_weight(const gdn_attn_weight_args* a, void* stream) {
@@ -226,7 +225,6 @@ extern "C" GDN_API int gdn_attn_weight(const gdn_attn_weight_args* a, void* stre
   w.position = a->position;
   w.weight = a->weight;
   w.born = a->born;
-  w.notes = static_cast<int4*>(a->work);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return a->in_dtype == GDN_DTYPE_BF16 ? run_weight_tc(w, st) : run_weight_simt(w, st);
+  return a->in_dtype == GDN_DTYPE_BF16 ? run_weight_tc(w, a->work, st) : run_weight_simt(w, a->work, st);
 }

@@ -12,6 +12,12 @@
 // sums).  K of a (key block, head) is loaded once and met by all its tiles; a
 // single step's few rows are one tile, and then K streams through.
 //
+// K's layout.  A page's tokens are copied whole, by one instruction: the tensor map splits a row into chunks of 64 columns
+// and the tokens into groups of eight, and takes (page, head) as one dimension, where a page is a whole number of heads
+// long.  In shared memory that is [group][chunk][8 tokens][128 bytes], which the MMA reads as well as any.  (An instruction
+// for each chunk of 16 tokens takes the issuing lane some 80 to 150 clocks; 32 of them for 64 KB took longer than HBM.)
+// Other pools are copied by group and chunk.
+//
 // Rows past the request's, and keys past its last token, may hold anything: a column or a lane is one row or key, and
 // theirs are not counted.
 #include <cuda.h>
@@ -45,6 +51,20 @@ __device__ __forceinline__ void tma_rows(const CUtensorMap* map, uint32_t dst, u
       "l"(map), "r"(col), "r"(head), "r"(row), "r"(bar)
       : "memory");
 }
+__device__ __forceinline__ void tma_page(const CUtensorMap* map, uint32_t dst, uint32_t bar, int group, int number) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(0), "r"(group), "r"(number), "r"(bar)
+      : "memory");
+}
+// mma_ss with the operands' high words apart
+__device__ __forceinline__ void mma_two(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi, uint32_t idesc, uint32_t add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %6, 0;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(add)
+      : "memory");
+}
 // 4 bytes into shared memory; the lane's arrival on a barrier once its copies so far have landed
 __device__ __forceinline__ void copy4(uint32_t to, const float* from) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
@@ -63,6 +83,8 @@ struct WeightTcParams {
   int box;    // tokens per TMA box of K
   int width;  // columns of a product: a tile's rows up to a multiple of 16
   int n_k, n_q;  // stages
+  int per_page;  // (page, head) is number page * per_page + head of the map; 0: K is copied by group and chunk
+  int outside;   // a number outside it
 };
 
 template <int kD>
@@ -158,13 +180,14 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
     const uint64_t scale2 = pair(p.scale_log2, p.scale_log2), log2e2 = pair(-1.4426950408889634f, -1.4426950408889634f);
     float in_keys = 0.f, in_head = 0.f;  // sums over the key block's heads before this one, and over this head's tiles
-    int slot = -2;                       // of this thread's key, -2: not looked up yet
+    int place = 0;  // of this thread's key's weight, and what it holds
     float old = 0.f;
-    int4 note = {0, 0, 0, 0};
+    bool known = false;
+    int note = 0;
     auto look_up = [&]() {
-      const int j = x.kb * kKeys + key;
-      slot = j >= x.req.first ? weight_slot(w, x.b, x.req.ctx + x.req.n, j) : -1;
-      old = slot >= 0 && !weight_new(w, x.req, j) ? w.weight[slot] : 0.f;
+      place = weight_place(w, x.req, x.b, x.kb * kKeys + key);
+      old = old_weight(w, place);
+      known = true;
     };
     int done = 0, turn = 0, f = 0;  // tiles so far, whose turn it is, key blocks
     for (int run; !x.done(); x.next(run)) {
@@ -222,7 +245,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
         tc_fence_before();
         warp_arrive(s_empty(buf));
         warp_arrive(l_empty(stage));
-        if (group == 0 && slot == -2) look_up();
+        if (group == 0 && !known) look_up();
       }
       if (!ok) break;
       done += run;
@@ -236,7 +259,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
         cross[f & 1][group - 1][key] = in_keys;
         warp_arrive(c_full(f & 1));
       } else {
-        if (slot == -2) look_up();
+        if (!known) look_up();
         if (!(ok = warp_wait(c_full(f & 1), (f >> 1) & 1, &gave_up))) break;
         float got = in_keys;
 #pragma unroll
@@ -244,12 +267,15 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
         warp_arrive(c_empty(f & 1));
         const long long rest = x.rest(run);
         if (x.whole && rest == 0) {
-          if (slot >= 0) w.weight[slot] = weight_new(w, x.req, x.kb * kKeys + key) ? got : fmaf(w.keep, old, got);
+          add_weight(w, place, old, got);
         } else {
           w.partials[(size_t)(2 * blockIdx.x + (x.whole ? 1 : 0)) * kKeys + key] = got;
-          if (x.whole) note = make_int4((int)((rest + start.per - 1) / start.per), x.b, x.kb, 0);
+          if (x.whole) {
+            w.slots[blockIdx.x * kKeys + key] = place;
+            note = (int)((rest + start.per - 1) / start.per);
+          }
         }
-        slot = -2;
+        known = false;
       }
       in_keys = 0.f;
       ++f;
@@ -259,6 +285,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
     // ---- the products, issued by one thread
     if (lane == 0) {
       const uint32_t idesc = instruction(t.width, false);
+      constexpr uint32_t kKeysHi = kChunks * 1024 >> 4 | 1u << 14 | 2u << 29;  // groups of eight keys kChunks * 1024 bytes apart
       const uint32_t k_lo0 = operand_lo(k_s, 16), q_lo0 = operand_lo(q_s, 16);
       int i = 0;
       for (int run; ok && !x.done(); x.next(run)) {
@@ -273,7 +300,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
           const uint32_t q_lo = q_lo0 + q_ring.stage * (q_bytes / 16), s_at = tmem + buf * S::kRows;
 #pragma unroll
           for (int k = 0; k < kD / 16; ++k)
-            mma_ss(s_at, k_lo + (k / 4) * (kKeys * 8) + (k % 4) * 2, q_lo + (k / 4) * (t.width * 8) + (k % 4) * 2, kOperandHi, idesc, k > 0);
+            mma_two(s_at, k_lo + (k / 4) * 64 + (k % 4) * 2, kKeysHi, q_lo + (k / 4) * (t.width * 8) + (k % 4) * 2, kOperandHi, idesc, k > 0);
           tc_commit(s_full(buf));
           tc_commit(q_empty(q_ring.stage));
         }
@@ -284,28 +311,46 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
     }
     __syncwarp();
   } else if (any && warp == 13) {
-    // ---- K tiles: lane (box, chunk) copies its box of 64 columns
-    const int n_box = kKeys / t.box, box = lane / kChunks, chunk = lane % kChunks;
-    const uint32_t at = (uint32_t)chunk * (kKeys * 128) + (uint32_t)box * t.box * 128;
+    // ---- K tiles: lane `box` copies its tokens' page or part of one
+    const int n_box = kKeys / t.box, box = lane;
     bool new_keys = true;
-    int page = 0, token = 0, live = 0;
+    int page = 0, token = 0, live = 0, page_b = -1, page_kb = 0, page_next = 0, token_next = 0;
+    // the page of this lane's box in a key block of the walk's request; looked up a key block ahead
+    auto page_of = [&](int kb, int* token) {
+      const int j = kb * kKeys + box * t.box, i = (int)quotient(j, p.by_page);
+      *token = j - i * p.page_size;
+      return kb < x.req.kb1 && box < n_box && j < x.req.ctx + x.req.n ? p.table[(size_t)x.b * p.table_stride + i] : -1;
+    };
     for (int run; ok && !x.done(); x.next(run)) {
       run = x.run();
       if (new_keys) {
-        const int len = x.req.ctx + x.req.n, j = x.kb * kKeys + box * t.box;
+        const int len = x.req.ctx + x.req.n;
         live = min(n_box, (len - x.kb * kKeys + t.box - 1) / t.box);
-        if (box < live) {
-          const int i = (int)quotient(j, p.by_page);
-          page = p.table[(size_t)x.b * p.table_stride + i];
-          token = j - i * p.page_size;
-          if ((unsigned)page >= (unsigned)p.n_pages) page = p.n_pages;  // outside the map: zeros; its tokens take no weight
+        if (page_b == x.b && page_kb == x.kb) {
+          page = page_next;
+          token = token_next;
+        } else {
+          page = page_of(x.kb, &token);
         }
+        page_next = page_of(x.kb + 1, &token_next);
+        page_b = x.b;
+        page_kb = x.kb + 1;
       }
       const int stage = k_ring.stage;
       if (k_ring.round > 0 && !(ok = warp_wait(k_empty(stage), (k_ring.round - 1) & 1, &gave_up))) break;
       if (lane == 0) bar_expect(k_full(stage), (uint32_t)live * t.box * kD * 2);
       __syncwarp();
-      if (box < live) tma_box(&k_map, k_s + stage * S::kKBytes + at, k_full(stage), chunk * 64, token, x.h, page);
+      if (box < live) {
+        // outside the map: zeros; such a page's tokens take no weight
+        const bool good = (unsigned)page < (unsigned)p.n_pages;
+        const uint32_t to = k_s + stage * S::kKBytes + (uint32_t)(box * t.box * kD * 2);
+        if (t.per_page > 0) {
+          tma_page(&k_map, to, k_full(stage), token / 8, good ? page * t.per_page + x.h : t.outside);
+        } else {
+          for (int i = 0; i < t.box / 8 * kChunks; ++i)
+            tma_box(&k_map, to + i * 1024, k_full(stage), i % kChunks * 64, token + i / kChunks * 8, x.h, good ? page : p.n_pages);
+        }
+      }
       ++sent;
       k_ring.next();
       new_keys = x.keys_end(run);
@@ -353,7 +398,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
   }
-  if (!any && tid == 0) w.notes[blockIdx.x] = make_int4(0, 0, 0, 0);
+  if (!any && tid == 0) w.notes[blockIdx.x] = 0;
   __syncthreads();
   if (gave_up) {
     // products and copies that may still be in flight, with a bound again
@@ -370,12 +415,34 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
         }
     }
     if (tid == 0) {
-      w.notes[blockIdx.x] = make_int4(0, 0, 0, 0);
+      w.notes[blockIdx.x] = 0;
       if (p.status) atomicOr(p.status, GDN_STATUS_TIMEOUT);
     }
     __syncthreads();
   }
   if (warp == 12) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+// K as [64][8][d / 64][page_size / 8][page and head], a page's box whole; false where a page is not a whole number of heads
+// long, or the numbers pass 32 bits.
+bool make_page_map(CUtensorMap* map, WeightTcParams& t) {
+  const EncodeFn encode = encoder();
+  const Params& p = t.w.p;
+  // the stride of a dimension of one entry is never used, but must be a valid one
+  const int64_t number = p.H_kv > 1 ? p.k_head : p.n_pages > 1 ? p.k_page : p.k_token;
+  if (!encode || number <= 0 || (p.n_pages > 1 && p.k_page % number != 0)) return false;
+  const int64_t per_page = p.n_pages > 1 ? p.k_page / number : p.H_kv;
+  if (per_page < 1 || per_page > INT32_MAX / p.n_pages - 1) return false;
+  const int64_t numbers = (p.n_pages - 1) * per_page + p.H_kv;
+  const cuuint64_t dims[5] = {64, 8, (cuuint64_t)p.d / 64, (cuuint64_t)p.page_size / 8, (cuuint64_t)numbers};
+  const cuuint64_t strides[4] = {(cuuint64_t)p.k_token * 2, 128, (cuuint64_t)p.k_token * 16, (cuuint64_t)number * 2};
+  const cuuint32_t box[5] = {64, 8, (cuuint32_t)p.d / 64, (cuuint32_t)t.box / 8, 1}, steps[5] = {1, 1, 1, 1, 1};
+  if (encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(p.k), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return false;
+  t.per_page = (int)per_page;
+  t.outside = (int)numbers;
+  return true;
 }
 
 // rows of q as [d][H_q][n_q_rows]
@@ -398,22 +465,25 @@ int run(WeightTcParams& t, cudaStream_t st) {
   if (cudaFuncSetAttribute(weight_tc_kernel<kD>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem) != cudaSuccess) return GDN_ERR_LAUNCH;
   set_weight_tiles(t.w, S::kRows);
   t.width = (t.w.tokens * t.w.heads + 15) / 16 * 16;
-  const int q_bytes = t.width * kD * 2, left = S::kBytes - S::kLeastK * S::kKBytes;
+  // a step's few rows leave K to stream through: one stage more in flight
+  const int q_bytes = t.width * kD * 2, least = S::kLeastK + (kD == 128 && t.width < S::kRows ? 1 : 0), left = S::kBytes - least * S::kKBytes;
   t.n_q = left / q_bytes < S::kMostQ ? left / q_bytes : S::kMostQ;
   t.n_k = (S::kBytes - t.n_q * q_bytes) / S::kKBytes;
   if (t.n_k > S::kMostK) t.n_k = S::kMostK;
   t.box = 16;
   while (t.box * 2 <= kWeightKeys && t.w.p.page_size % (t.box * 2) == 0) t.box *= 2;
   CUtensorMap k_map, q_map;
-  if (!make_map(&k_map, t.w.p, t.w.p.k, t.w.p.k_token, t.w.p.k_head, t.w.p.k_page, t.box) || !make_row_map(&q_map, t.w)) return GDN_ERR_LAUNCH;
+  if (!make_page_map(&k_map, t) && !make_map(&k_map, t.w.p, t.w.p.k, t.w.p.k_token, t.w.p.k_head, t.w.p.k_page, 8)) return GDN_ERR_LAUNCH;
+  if (!make_row_map(&q_map, t.w)) return GDN_ERR_LAUNCH;
   const int rc = launch(weight_tc_kernel<kD>, dim3(kWeightBlocks), dim3(kWeightThreads), S::kSmem, st, t, k_map, q_map);
   return rc != GDN_OK ? rc : launch_weight_join<kWeightKeys>(t.w, st);
 }
 
-int run_weight_tc(WeightParams& w, cudaStream_t st) {
-  w.p.n_blocks = kWeightBlocks;
-  w.partials = reinterpret_cast<float*>(w.notes + kWeightBlocks);
-  WeightTcParams t{w, 0, 0, 0, 0};
+size_t weight_tc_work() { return weight_work(kWeightBlocks, kWeightKeys); }
+
+int run_weight_tc(WeightParams& w, void* work, cudaStream_t st) {
+  set_weight_work(w, kWeightBlocks, kWeightKeys, work);
+  WeightTcParams t{w, 0, 0, 0, 0, 0, 0};
   return w.p.d == 64 ? run<64>(t, st) : w.p.d == 128 ? run<128>(t, st) : run<256>(t, st);
 }
 

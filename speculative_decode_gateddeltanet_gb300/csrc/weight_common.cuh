@@ -6,6 +6,7 @@
 //   tiles cover a token's G heads where G does not fit one).  A unit is one (key block, kv head, tile): one product and one
 //   exponential an entry.  A key block needs the tiles from its first key's row on:
 //     m0(kb) = parts * max(0, floor((kb kKeys - ctx) / tokens))
+//   A run of tiles of one key block and head costs kRun units more: its K, and tiles that the diagonal crosses.
 // Division.  All units of a call form one line, request by request, key block by key block, head by head, so that a key
 //   block's sum over heads and rows stays in one block's registers; block i takes units [i per, (i+1) per).  A request's
 //   units up to a key block are a floor sum (attn_common.cuh), so each block finds its part by itself.
@@ -27,9 +28,37 @@ struct WeightParams {
   int32_t* born;
   int tokens, heads, parts;  // of a tile: tokens * heads rows
   Div by_heads, by_parts;
-  int4* notes;      // [n_blocks] followers, request, key block
+  int* notes;       // [n_blocks] blocks that follow in a key block that a block begins and does not end
+  int* slots;       // [n_blocks][kKeys] its keys' slots, kNewSlot added for tokens that start anew, or -1
   float* partials;  // [n_blocks][2][kKeys]
 };
+
+// floor_sum where the numbers leave room: its divisions in 32 bits
+__device__ inline long long weight_floor_sum(int n, int m, int a, long long b) {
+  if (((long long)n * (a > m ? a : m) + b) >> 31) return floor_sum(n, m, a, b);
+  long long s = 0;
+  uint32_t N = n, M = m, A = a, C = (uint32_t)b;
+  while (N > 0) {
+    if (A >= M) {
+      const uint32_t q = A / M;
+      s += (long long)N * (N - 1) / 2 * q;
+      A -= q * M;
+    }
+    if (C >= M) {
+      const uint32_t q = C / M;
+      s += (long long)N * q;
+      C -= q * M;
+    }
+    const uint32_t y = A * N + C;
+    if (y < M) break;
+    N = y / M;
+    C = y - N * M;
+    const uint32_t t = M;
+    M = A;
+    A = t;
+  }
+  return s;
+}
 
 struct WeightRequest {
   int ctx, n, row0, first;
@@ -39,6 +68,8 @@ struct WeightRequest {
 
 template <int kKeys>
 struct WeightUnits {
+  // 8192 tokens at d = 64 take 243 us, with 0 282, 1 253, 4 237; at d = 128 277, with 0 299, 1 281, 4 279.
+  static constexpr int kRun = kKeys == 128 ? 2 : 0;
   __device__ static WeightRequest request(const WeightParams& w, int b, int* why = nullptr) {
     const Request r = gdnattn::request(w.p, b, why);
     WeightRequest x = {r.ctx, r.n, r.row0, 0, 0, 0, 0};
@@ -58,8 +89,8 @@ struct WeightUnits {
   // units of one head in key blocks [0, kb)
   __device__ static long long before(const WeightParams& w, const WeightRequest& r, int kb) {
     const int K1 = r.ctx / kKeys + 1;  // the first block whose first key is not a cached token's, and m0 > 0 at most from there
-    long long s = (long long)kb * r.M;
-    if (kb > K1) s -= w.parts * floor_sum(kb - K1, w.tokens, kKeys, (long long)K1 * kKeys - r.ctx);
+    long long s = (long long)kb * (r.M + kRun);
+    if (kb > K1) s -= w.parts * weight_floor_sum(kb - K1, w.tokens, kKeys, (long long)K1 * kKeys - r.ctx);
     return s;
   }
   // units of one head of the request
@@ -103,7 +134,7 @@ __device__ __forceinline__ void find_weight_start(const WeightParams& w, long lo
     total += scan[i];
   }
   const long long at = before + inc - mine;
-  const long long per = max(1ll, total >> 31 ? (total + n_blocks - 1) / n_blocks
+  const long long per = max(U::kRun + 1ll, total >> 31 ? (total + n_blocks - 1) / n_blocks
                                              : (long long)(((uint32_t)total + (uint32_t)n_blocks - 1) / (uint32_t)n_blocks));
   const long long want = per * blockIdx.x;
   if (threadIdx.x == 0) {
@@ -135,7 +166,8 @@ struct WeightWalk {
   const WeightParams* w;
   WeightRequest req;
   int b, kb, h, m, low;  // low: m0 of kb
-  long long left;        // units still to do, this one among them
+  int skip;              // the run's units before its tiles that are this block's
+  long long left;        // units still to do, these among them
   bool whole;            // the block has its key block from its first unit
 
   __device__ bool begin(const WeightParams& params, const WeightStart& s) {
@@ -155,34 +187,45 @@ struct WeightWalk {
     kb = lo;
     low = U::m0(*w, req, kb);
     const long long off = s.off - w->p.H_kv * (U::before(*w, req, lo) - base);
-    const int each = req.M - low;
+    const int each = req.M - low + U::kRun;
     h = (int)(off / each);
-    m = low + (int)(off - (long long)h * each);
-    whole = off == 0;
-    return true;
+    const int at = (int)(off - (long long)h * each);
+    m = low + max(0, at - U::kRun);
+    skip = max(0, U::kRun - at);
+    whole = h == 0 && m == low;
+    if (left <= skip) left = 0;  // its units end before the run's first tile
+    return left > 0;
   }
   __device__ bool done() const { return left <= 0; }
-  // units of this head and key block that follow each other here, this one first; walked in one step
-  __device__ int run() const { return (int)min(left, (long long)(req.M - m)); }
-  // whether the run is the block's last with its key block, and the key block's units behind it
-  __device__ bool keys_end(int run) const { return left == run || (h + 1 == w->p.H_kv && m + run == req.M); }
-  __device__ long long rest(int run) const { return (long long)(w->p.H_kv - 1 - h) * (req.M - low) + req.M - m - run; }
+  // tiles of this head and key block that follow each other here, this one first; walked in one step
+  __device__ int run() const { return (int)min(left - skip, (long long)(req.M - m)); }
+  // whether the run is the block's last with its key block
+  __device__ bool keys_end(int run) const { return left - skip - run <= U::kRun || (h + 1 == w->p.H_kv && m + run == req.M); }
+  // the key block's units behind the block's
+  __device__ long long rest(int run) const {
+    const long long behind = (long long)(w->p.H_kv - 1 - h) * (req.M - low + U::kRun) + req.M - m - run;
+    return behind > 0 ? max(0ll, behind - (left - skip - run)) : 0;
+  }
   __device__ void next(int run) {
-    left -= run;
+    left -= skip + run;
+    skip = 0;
     if (left <= 0) return;
     m += run;
     if (m < req.M) return;
+    skip = U::kRun;
     m = low;
-    if (++h < w->p.H_kv) return;
-    h = 0;
-    whole = true;
-    if (++kb == req.kb1) {
-      do {
-        req = U::request(*w, ++b);
-      } while (U::sum(*w, req) == 0);
-      kb = req.kb0;
+    if (++h == w->p.H_kv) {
+      h = 0;
+      whole = true;
+      if (++kb == req.kb1) {
+        do {
+          req = U::request(*w, ++b);
+        } while (U::sum(*w, req) == 0);
+        kb = req.kb0;
+      }
+      low = m = U::m0(*w, req, kb);
     }
-    low = m = U::m0(*w, req, kb);
+    if (left <= skip) left = 0;
   }
   // rows of tile m: the first token, the first of its heads, and the columns that are rows of the request
   __device__ int token(int m) const { return (w->parts == 1 ? m : (int)quotient(m, w->by_parts)) * w->tokens; }
@@ -204,33 +247,55 @@ __device__ __forceinline__ int weight_slot(const WeightParams& w, int b, int len
 }
 __device__ __forceinline__ bool weight_new(const WeightParams& w, const WeightRequest& r, int j) { return w.fresh && j >= r.ctx; }
 
+// The place of a key's weight: kNewSlot on top of slots of tokens that start anew, -1 for none.
+constexpr uint32_t kNewSlot = 1u << 31;
+constexpr int kNoSlot = -1;
+__device__ __forceinline__ int weight_place(const WeightParams& w, const WeightRequest& r, int b, int j) {
+  const int slot = j >= r.first ? weight_slot(w, b, r.ctx + r.n, j) : kNoSlot;  // below 2^31 - 1: a pool has fewer slots
+  return slot != kNoSlot && weight_new(w, r, j) ? (int)(slot | kNewSlot) : slot;
+}
+__device__ __forceinline__ void add_weight(const WeightParams& w, int place, float old, float got) {
+  if (place == kNoSlot) return;
+  w.weight[place & ~kNewSlot] = place < 0 ? got : fmaf(w.keep, old, got);
+}
+__device__ __forceinline__ float old_weight(const WeightParams& w, int place) { return place >= 0 ? w.weight[place] : 0.f; }
+
 // Joins the partials of the key block that block blockIdx.x begins and does not end, and notes the step's own tokens' ages.
 template <int kKeys>
 __global__ void __launch_bounds__(kKeys) weight_join_kernel(const WeightParams w) {
   pdl_wait();
   pdl_trigger();
-  const int4 note = (int)blockIdx.x < w.p.n_blocks ? w.notes[blockIdx.x] : make_int4(0, 0, 0, 0);
-  if (note.x > 0) {
-    const WeightRequest r = WeightUnits<kKeys>::request(w, note.y);
-    const int j = note.z * kKeys + threadIdx.x, slot = j >= r.first ? weight_slot(w, note.y, r.ctx + r.n, j) : -1;
-    float got = w.partials[(size_t)(2 * blockIdx.x + 1) * kKeys + threadIdx.x];
-    for (int i = 1; i <= note.x; ++i) got += w.partials[(size_t)(2 * (blockIdx.x + i)) * kKeys + threadIdx.x];
-    if (slot >= 0) w.weight[slot] = weight_new(w, r, j) ? got : fmaf(w.keep, w.weight[slot], got);
+  const int followers = w.notes[blockIdx.x], place = w.slots[blockIdx.x * kKeys + threadIdx.x];
+  float got = w.partials[(size_t)(2 * blockIdx.x + 1) * kKeys + threadIdx.x];
+  if (followers > 0) {
+    const float old = old_weight(w, place);
+    for (int i = 1; i <= followers; ++i) got += w.partials[(size_t)(2 * (blockIdx.x + i)) * kKeys + threadIdx.x];
+    add_weight(w, place, old, got);
   }
-  if (w.fresh && w.born)
-    for (int b = blockIdx.x; b < w.p.B; b += gridDim.x) {
+  if (w.fresh && w.born) {
+    // blocks b, b + B, ... share request b's tokens
+    const int shares = max(1, (int)gridDim.x / w.p.B);
+    for (int b = blockIdx.x % w.p.B, share = blockIdx.x / w.p.B; b < w.p.B && share < shares; b += gridDim.x) {
       const Request r = request(w.p, b);
       const int position = r.n > 0 && w.position ? w.position[b] : r.ctx;
-      for (int t = threadIdx.x; t < r.n; t += kKeys) {
-        const int slot = weight_slot(w, b, r.ctx + r.n, r.ctx + t);
-        if (slot >= 0) w.born[slot] = position + t;
+      for (long long t = share * kKeys + threadIdx.x; t < r.n; t += shares * kKeys) {
+        const int slot = weight_slot(w, b, r.ctx + r.n, r.ctx + (int)t);
+        if (slot >= 0) w.born[slot] = position + (int)t;
       }
     }
+  }
 }
 
-size_t weight_work_bytes(int dtype);
-int run_weight_tc(WeightParams& w, cudaStream_t st);
-int run_weight_simt(WeightParams& w, cudaStream_t st);
+// work: notes, places and partials of every block
+inline size_t weight_work(int blocks, int keys) { return (size_t)blocks * (sizeof(int) + keys * (sizeof(int) + 2 * sizeof(float))); }
+inline void set_weight_work(WeightParams& w, int blocks, int keys, void* work) {
+  w.p.n_blocks = blocks;
+  w.notes = static_cast<int*>(work);
+  w.slots = w.notes + blocks;
+  w.partials = reinterpret_cast<float*>(w.slots + (size_t)blocks * keys);
+}
+size_t weight_tc_work();
+int run_weight_tc(WeightParams& w, void* work, cudaStream_t st);
 
 // one tile's rows: as many tokens as fit `most` rows, but no more than a padded request has
 inline void set_weight_tiles(WeightParams& w, int most) {

@@ -432,6 +432,26 @@ def test_weights_with_far_pages_strided_rows_and_a_negative_scale(hy, dtype):
     w.check()
 
 
+@pytest.mark.parametrize("dtype,d,P", [(BF16, 64, 16), (BF16, 256, 48), (F32, 128, 16)])
+def test_weights_of_pools_whose_pages_are_no_whole_number_of_heads(hy, dtype, d, P):
+    case = hybrid_ref.make_attention(lens=[(300, 2), (30, 2), (5, 1)], H_q=4, H_kv=2, d=d, P=P, dtype=dtype, R=2)
+    w = Weight(hy, case, 2)
+    pages, stride = case["k_cache"].shape[0], 2 * P * d + 24
+    k = torch.full((pages * stride,), float("nan"), dtype=dtype, device="cuda").as_strided((pages, 2, P, d), (stride, P * d, d, 1))
+    k.copy_(w.k)
+    args = hy.make_attn_weight_args(**(w.tensors | dict(k_cache=k)), R=2, scale=case["scale"], fresh=True)
+    args.work = w.work.data_ptr()
+    hy.gdn_attn_weight(args)
+    w.check()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_weights_of_one_page_and_one_head(hy, dtype):
+    for H_kv, P, lens in ((1, 128, [(100, 2)]), (3, 64, [(40, 5)]), (1, 16, [(100, 2), (3, 1)])):
+        case = hybrid_ref.make_attention(lens=lens, H_q=3 * H_kv, H_kv=H_kv, d=64, P=P, dtype=dtype, spare=0)
+        Weight(hy, case).run().check()
+
+
 def test_weights_in_a_graph_follow_lengths(hy):
     case = hybrid_ref.make_attention(lens=[(400, 4), (50, 4), (1000, 4)], H_q=16, H_kv=2, d=128, P=16, dtype=BF16, R=4)
     w = Weight(hy, case, 4)

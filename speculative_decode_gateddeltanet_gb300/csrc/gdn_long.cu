@@ -1,4 +1,6 @@
 // Eviction from the paged cache: the choice of tokens that leave, and their moves.
+#include <cooperative_groups.h>
+
 #include <algorithm>
 #include <cmath>
 
@@ -32,9 +34,23 @@ __device__ __forceinline__ float warp_sum(float x) {
   return x;
 }
 
-// ---- the choice: a block per request -----------------------------------------------------------------------------------------
+// ---- the choice -----------------------------------------------------------------------------------------------------------
+//
+// One block of 1024 threads for a request, or a cluster of eight where its table row can hold more than kOneBlock tokens.
+// A warp owns consecutive tokens.  Their weights are read once, as whole numbers in the same order (kStays for those that may
+// not leave), into shared memory; the heaviest key that leaves is found digit by digit with histograms of 11, 11 and 10 bits;
+// then three passes over the keys count the equal ones, count gaps and movers, and write the lists: each warp's place in
+// them comes from the counts of the warps and blocks before it, so they are in index order whatever the timing.  Histograms
+// and counts of the cluster's blocks are read from each other's shared memory, with one cluster barrier for each.
+// Tokens beyond what shared memory holds (eight blocks: 393216) are read again in each pass.
+// Bound by latency: @@@
 
-constexpr int kSelectThreads = 1024;
+namespace cg = cooperative_groups;
+
+constexpr int kSelectThreads = 1024, kSelectWarps = kSelectThreads / 32, kOneBlock = 16384;
+constexpr int kHeld = 49152;  // keys that a block of a cluster holds
+constexpr int kBins = 2048;
+constexpr uint32_t kStays = 0xffffffffu;  // above every weight's key
 
 // weights as whole numbers in the same order; NaN as -infinity, -0 as 0
 __device__ __forceinline__ uint32_t weight_key(float x) {
@@ -43,131 +59,267 @@ __device__ __forceinline__ uint32_t weight_key(float x) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// sums over the block's threads before this one, and in all
-__device__ __forceinline__ int block_before(int x, int* part, int* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int inc = x;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int v = __shfl_up_sync(kFull, inc, off);
-    if (lane >= off) inc += v;
-  }
-  if (lane == 31) part[warp] = inc;
-  __syncthreads();
-  int before = inc - x, all = 0;
-  for (int w = 0; w < kSelectThreads / 32; ++w) {
-    if (w < warp) before += part[w];
-    all += part[w];
-  }
-  __syncthreads();
-  *total = all;
-  return before;
-}
+struct SelectShared {
+  int hist[3][kBins];
+  int warps[2][kSelectWarps];  // counts of each warp, then those before it
+  int counts[4][2];            // this block's, by exchange
+  int found[2];                // a pass's digit, and how many of that digit leave
+  int bad_page;
+};
 
-__global__ void __launch_bounds__(kSelectThreads) select_simple(const gdn_evict_args p, const Div by_page) {
-  __shared__ int part[kSelectThreads / 32], hist[256], found[2], bad_page;
+template <int kC>
+__global__ void __launch_bounds__(kSelectThreads, 1) select_kernel(const gdn_evict_args p, const Div by_page) {
+  extern __shared__ uint32_t held[];
+  __shared__ SelectShared sh;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = kC == 1 ? 0 : blockIdx.x % kC, b = blockIdx.x / kC;
+  for (int i = tid; i < 3 * kBins; i += kSelectThreads) (&sh.hist[0][0])[i] = 0;
+  if (tid == 0) sh.bad_page = 0;
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x;
-  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-    const int L = p.ctx_len[b], budget = max(p.budget[b], 0), pinned = p.pinned ? max(p.pinned[b], 0) : 0;
-    const int keep_from = p.keep_from && p.born ? p.keep_from[b] : INT32_MAX;
-    const bool bound = p.keep_from && p.born;
-    const int32_t* const pages = p.block_table + (size_t)b * p.table_stride;
-    __syncthreads();
-    if (tid == 0) bad_page = 0;
-    __syncthreads();
-    const bool bad_length = L < 0 || L > (int64_t)p.max_pages * p.page_size;
-    if (!bad_length)
-      for (int i = tid; i < (L + p.page_size - 1) / p.page_size; i += kSelectThreads)
-        if ((unsigned)pages[i] >= (unsigned)p.n_pages) bad_page = 1;
-    __syncthreads();
-    if (bad_length || bad_page) {
-      if (tid == 0) {
-        p.ctx_out[b] = L;
-        p.n_moves[b] = 0;
-        if (p.status) atomicOr(p.status, bad_length ? GDN_STATUS_BAD_LENGTH : GDN_STATUS_BAD_PAGE);
-      }
-      continue;
+  const int L = p.ctx_len[b], budget = max(p.budget[b], 0), pinned = p.pinned ? max(p.pinned[b], 0) : 0;
+  const bool bound = p.keep_from && p.born;
+  const int keep_from = bound ? p.keep_from[b] : 0;
+  const int32_t* const pages = p.block_table + (size_t)b * p.table_stride;
+  auto leave = [&](int status) {  // as it was
+    if (rank == 0 && tid == 0) {
+      p.ctx_out[b] = L;
+      p.n_moves[b] = 0;
+      if (status && p.status) atomicOr(p.status, status);
     }
-    auto slot_of = [&](int j) {
-      const int i = (int)quotient(j, by_page);
-      return pages[i] * p.page_size + j - i * p.page_size;
-    };
-    auto may_go = [&](int j, int slot) { return j >= pinned && (!bound || p.born[slot] < keep_from); };
-    int mine = 0, n_may;
-    for (int64_t j = tid; j < L; j += kSelectThreads) mine += may_go((int)j, slot_of((int)j));
-    block_before(mine, part, &n_may);
-    const int go = min(max(L - budget, 0), n_may), K = L - go;
-    // the go-th lightest key, eight bits at a time: `low` keys are lighter, and `ties` of those that equal it leave too
-    uint32_t key = 0, mask = 0;
-    int ties = go;
-    for (int shift = 24; shift >= 0 && go > 0; shift -= 8) {
-      for (int i = tid; i < 256; i += kSelectThreads) hist[i] = 0;
-      __syncthreads();
-      for (int64_t j = tid; j < L; j += kSelectThreads) {
-        const int slot = slot_of((int)j);
-        if (!may_go((int)j, slot)) continue;
-        const uint32_t k = weight_key(p.weight[slot]);
-        if ((k & mask) == key) atomicAdd(&hist[k >> shift & 255], 1);
-      }
-      __syncthreads();
-      if (tid == 0) {
-        int i = 0, left = ties;
-        while (left > hist[i]) left -= hist[i++];
-        found[0] = i;
-        found[1] = left;
-      }
-      __syncthreads();
-      key |= (uint32_t)found[0] << shift;
-      mask |= 255u << shift;
-      ties = found[1];
-    }
-    int equal = 0, n_equal;
-    for (int64_t j = tid; j < L && go > 0; j += kSelectThreads) {
-      const int slot = slot_of((int)j);
-      equal += may_go((int)j, slot) && weight_key(p.weight[slot]) == key;
-    }
-    block_before(equal, part, &n_equal);
-    int64_t done_equal = 0, gaps = 0, movers = 0;
-    // twice: the number of moves first, then the lists
-    for (int round = 0; round < 2; ++round) {
-      const int64_t moves = gaps;
-      if (round == 1 && moves > p.max_moves) break;
-      done_equal = gaps = movers = 0;
-      for (int64_t j0 = 0; j0 < L && go > 0; j0 += kSelectThreads) {
-        const int64_t j = j0 + tid;
-        const int slot = j < L ? slot_of((int)j) : 0;
-        const bool may = j < L && may_go((int)j, slot);
-        const uint32_t k = may ? weight_key(p.weight[slot]) : 0;
-        int n;
-        const int tie_at = block_before(may && k == key, part, &n);
-        const bool goes = may && (k < key || (k == key && done_equal + tie_at >= n_equal - ties));
-        done_equal += n;
-        const bool gap = goes && j < K, mover = j < L && !goes && j >= K;
-        const int gap_at = block_before(gap, part, &n);
-        if (round == 1 && gap) p.move_to[(size_t)b * p.max_moves + gaps + gap_at] = slot;
-        gaps += n;
-        const int mover_at = block_before(mover, part, &n);
-        if (round == 1 && mover) p.move_from[(size_t)b * p.max_moves + movers + mover_at] = slot;
-        movers += n;
-      }
-      if (round == 1 || moves > 0) continue;
-    }
-    const bool full = gaps > p.max_moves;
-    __syncthreads();
-    if (!full)
-      for (int64_t i = tid; i < gaps; i += kSelectThreads) {
-        const int from = p.move_from[(size_t)b * p.max_moves + i], to = p.move_to[(size_t)b * p.max_moves + i];
-        p.weight[to] = p.weight[from];
-        if (p.born) p.born[to] = p.born[from];
-      }
-    if (tid == 0) {
-      p.ctx_out[b] = full ? L : K;
-      p.n_moves[b] = full ? 0 : (int)gaps;
-      if (full && p.status) atomicOr(p.status, GDN_STATUS_MOVES_FULL);
-    }
+  };
+  // every block of the cluster reads the length before any writes the new one: they meet below, or none goes that far
+  const bool bad_length = L < 0 || L > (int64_t)p.max_pages * p.page_size;
+  auto meet = [&]() {
+    if constexpr (kC > 1) cg::this_cluster().sync();
+    else __syncthreads();
+  };
+  if (bad_length) {
+    meet();
+    return leave(GDN_STATUS_BAD_LENGTH);
   }
+  // this warp's tokens
+  const int each = (int)(((int64_t)L + kC * kSelectThreads - 1) / (kC * kSelectThreads)) * 32;
+  const int64_t first64 = ((int64_t)rank * kSelectWarps + warp) * each;
+  const int first = (int)min(first64, (int64_t)L), mine = (int)min((int64_t)each, (int64_t)L - first);
+  const bool staged = (int64_t)each * kSelectWarps <= (kC == 1 ? kOneBlock : kHeld);
+  uint32_t* const keys = held + (staged ? warp * each : 0);
+  auto slot_of = [&](int j, bool* good) {
+    const int i = (int)quotient(j, by_page), page = pages[i];
+    *good = (unsigned)page < (unsigned)p.n_pages;
+    return page * p.page_size + j - i * p.page_size;
+  };
+  auto read_key = [&](int j, int* bad) {
+    bool good;
+    const int slot = slot_of(j, &good);
+    if (!good) {
+      *bad = 1;
+      return kStays;
+    }
+    const float w = p.weight[slot];
+    const int age = bound ? p.born[slot] : -1;
+    return j >= pinned && (!bound || age < keep_from) ? weight_key(w) : kStays;
+  };
+  auto key_at = [&](int i) {
+    int bad;
+    return staged ? keys[i] : read_key(first + i, &bad);
+  };
+  int may = 0, bad = 0;
+#pragma unroll 4
+  for (int i = lane; i < mine; i += 32) {
+    const uint32_t k = read_key(first + i, &bad);
+    if (staged) keys[i] = k;
+    may += k != kStays;
+  }
+  // sums over the cluster of two numbers of each warp (in lane 0), and over the warps before this one
+  int round = 0;
+  auto exchange = [&](int x, int y, int* before_x, int* before_y, int* all_x, int* all_y) {
+    if (lane == 0) {
+      sh.warps[0][warp] = x;
+      sh.warps[1][warp] = y;
+    }
+    __syncthreads();
+    if (warp < 2) {
+      const int v = sh.warps[warp][lane];
+      int inc = v;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int u = __shfl_up_sync(kFull, inc, off);
+        if (lane >= off) inc += u;
+      }
+      sh.warps[warp][lane] = inc - v;
+      if (lane == 31) sh.counts[round][warp] = inc;
+    }
+    meet();
+    int bx = sh.warps[0][warp], by = sh.warps[1][warp], ax = 0, ay = 0;
+#pragma unroll
+    for (int r = 0; r < kC; ++r) {
+      const int* const c = kC == 1 ? sh.counts[round] : cg::this_cluster().map_shared_rank(&sh.counts[round][0], r);
+      if (r < rank) {
+        bx += c[0];
+        by += c[1];
+      }
+      ax += c[0];
+      ay += c[1];
+    }
+    ++round;
+    *before_x = bx;
+    *before_y = by;
+    *all_x = ax;
+    *all_y = ay;
+  };
+  int bx, by, n_may, n_bad;
+  exchange(__reduce_add_sync(kFull, may), __any_sync(kFull, bad), &bx, &by, &n_may, &n_bad);
+  const int go = min(max(L - budget, 0), n_may), K = L - go;
+  if (n_bad > 0 || go == 0) {
+    if (kC > 1) meet();  // no block ends while another reads its counts
+    return leave(n_bad > 0 ? GDN_STATUS_BAD_PAGE : 0);
+  }
+  // the go-th lightest key
+  uint32_t key = 0, mask = 0;
+  int ties = go;
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
+    for (int i0 = 0; i0 < mine; i0 += 32) {
+      const int i = i0 + lane;
+      const uint32_t k = i < mine ? key_at(i) : kStays;
+      const bool in = k != kStays && (k & mask) == key;
+      const unsigned any = __ballot_sync(kFull, in);
+      if (any == 0) continue;
+      const int bin = (int)(k >> shift) & (bins - 1), of_first = __shfl_sync(kFull, bin, __ffs(any) - 1);
+      // one addition where all of the warp's are alike, as in a cache of equal weights
+      if (__ballot_sync(kFull, in && bin == of_first) == any) {
+        if (lane == 0) atomicAdd(&sh.hist[pass][of_first], __popc(any));
+      } else if (in) {
+        atomicAdd(&sh.hist[pass][bin], 1);
+      }
+    }
+    meet();
+    int n[2] = {0, 0};  // bins 2 tid and 2 tid + 1, of the whole cluster
+    if (2 * tid < bins) {
+#pragma unroll
+      for (int r = 0; r < kC; ++r) {
+        const int* const h = kC == 1 ? sh.hist[pass] : cg::this_cluster().map_shared_rank(&sh.hist[pass][0], r);
+        const int2 v = *reinterpret_cast<const int2*>(h + 2 * tid);
+        n[0] += v.x;
+        n[1] += v.y;
+      }
+    }
+    int inc = n[0] + n[1];
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int u = __shfl_up_sync(kFull, inc, off);
+      if (lane >= off) inc += u;
+    }
+    if (lane == 31) sh.warps[0][warp] = inc;
+    __syncthreads();
+    if (warp == 0) {
+      const int v = sh.warps[0][lane];
+      int s = v;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int u = __shfl_up_sync(kFull, s, off);
+        if (lane >= off) s += u;
+      }
+      sh.warps[1][lane] = s - v;
+    }
+    __syncthreads();
+    const int below = sh.warps[1][warp] + inc - n[0] - n[1];
+    if (ties > below && ties <= below + n[0] + n[1]) {  // one thread
+      const bool second = ties > below + n[0];
+      sh.found[0] = 2 * tid + second;
+      sh.found[1] = ties - below - (second ? n[0] : 0);
+    }
+    __syncthreads();
+    key |= (uint32_t)sh.found[0] << shift;
+    mask |= (uint32_t)(bins - 1) << shift;
+    ties = sh.found[1];
+  }
+  // `ties` of the keys that equal it leave: the last ones
+  int equal = 0;
+  for (int i = lane; i < mine; i += 32) equal += key_at(i) == key;
+  int equal_before, n_equal, gaps_before, movers_before, n_gaps, n_movers;
+  exchange(__reduce_add_sync(kFull, equal), 0, &equal_before, &by, &n_equal, &bx);
+  // f(token, whether it leaves) for each of the warp's tokens
+  auto walk = [&](auto f) {
+    int seen = equal_before;
+    for (int i0 = 0; i0 < mine; i0 += 32) {
+      const int i = i0 + lane;
+      const uint32_t k = i < mine ? key_at(i) : kStays;
+      const unsigned same = __ballot_sync(kFull, k == key);
+      const bool leaves = k < key || (k == key && seen + __popc(same & ((1u << lane) - 1)) >= n_equal - ties);
+      seen += __popc(same);
+      f(first + i, i < mine, leaves);
+    }
+  };
+  int gaps = 0, movers = 0;
+  walk([&](int j, bool is, bool leaves) {
+    gaps += is && leaves && j < K;
+    movers += is && !leaves && j >= K;
+  });
+  exchange(__reduce_add_sync(kFull, gaps), __reduce_add_sync(kFull, movers), &gaps_before, &movers_before, &n_gaps, &n_movers);
+  if (n_gaps > p.max_moves) {
+    if (kC > 1) meet();
+    return leave(GDN_STATUS_MOVES_FULL);
+  }
+  const size_t list = (size_t)b * p.max_moves;
+  {
+    int gap = gaps_before, mover = movers_before;
+    walk([&](int j, bool is, bool leaves) {
+      const unsigned g = __ballot_sync(kFull, is && leaves && j < K), m = __ballot_sync(kFull, is && !leaves && j >= K);
+      const unsigned below = (1u << lane) - 1;
+      if ((g | m) >> lane & 1) {
+        bool good;
+        const int slot = slot_of(j, &good);
+        if (g >> lane & 1) p.move_to[list + gap + __popc(g & below)] = slot;
+        else p.move_from[list + mover + __popc(m & below)] = slot;
+      }
+      gap += __popc(g);
+      mover += __popc(m);
+    });
+  }
+  meet();  // the lists are whole
+  for (int i = rank * kSelectThreads + tid; i < n_gaps; i += kC * kSelectThreads) {
+    const int from = p.move_from[list + i], to = p.move_to[list + i];
+    const float w = p.weight[from];
+    const int age = p.born ? p.born[from] : 0;
+    p.weight[to] = w;
+    if (p.born) p.born[to] = age;
+  }
+  if (rank == 0 && tid == 0) {
+    p.ctx_out[b] = K;
+    p.n_moves[b] = n_gaps;
+  }
+}
+
+int run_select(const gdn_evict_args& a, cudaStream_t st) {
+  const Div by_page = make_div((uint32_t)a.page_size);
+  const int64_t most = (int64_t)a.max_pages * a.page_size;
+  if (most <= kOneBlock) {
+    const int smem = (int)((most + kSelectThreads - 1) / kSelectThreads * kSelectThreads * sizeof(uint32_t));
+    if (cudaFuncSetAttribute(select_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kOneBlock * (int)sizeof(uint32_t)) != cudaSuccess)
+      return GDN_ERR_LAUNCH;
+    return launch(select_kernel<1>, dim3(a.B), dim3(kSelectThreads), smem, st, a, by_page);
+  }
+  constexpr int kC = 8;
+  const int64_t each = (most + kC * kSelectThreads - 1) / (kC * kSelectThreads) * kSelectThreads;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.B * kC);
+  cfg.blockDim = dim3(kSelectThreads);
+  cfg.dynamicSmemBytes = (size_t)(each < kHeld ? each : kHeld) * sizeof(uint32_t);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kC;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (cudaFuncSetAttribute(select_kernel<kC>, cudaFuncAttributeMaxDynamicSharedMemorySize, kHeld * (int)sizeof(uint32_t)) != cudaSuccess ||
+      cudaLaunchKernelEx(&cfg, select_kernel<kC>, a, by_page) != cudaSuccess || cudaGetLastError() != cudaSuccess)
+    return GDN_ERR_LAUNCH;
+  return GDN_OK;
 }
 
 // ---- moves -----------------------------------------------------------------------------------------------------------------
@@ -229,7 +381,7 @@ extern "C" GDN_API int gdn_evict_select(const gdn_evict_args* a, void* stream) {
   const void* all[] = {a->block_table, a->ctx_len, a->budget, a->pinned, a->keep_from, a->weight, a->born, a->ctx_out, a->n_moves, a->move_from, a->move_to, a->status};
   for (const void* ptr : all)
     if (!aligned(ptr, 4)) return GDN_ERR_MISALIGNED;
-  return launch(select_simple, dim3(a->B), dim3(kSelectThreads), 0, static_cast<cudaStream_t>(stream), *a, make_div((uint32_t)a->page_size));
+  return run_select(*a, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" GDN_API int gdn_kv_move(const gdn_kv_move_args* a, void* stream) {

@@ -14,7 +14,7 @@ from pathlib import Path
 PKG = Path(__file__).resolve().parent
 ROOT = PKG.parent
 SOURCES = [PKG / "csrc" / f"{name}.cu" for name in ("gdn_spec", "gdn_accept", "gdn_pages", "gdn_attn", "gdn_attn_tc", "gdn_sample", "gdn_shared",
-                                                      "gdn_shared_tc", "gdn_weight", "gdn_weight_tc", "gdn_long")]
+                                                      "gdn_shared_tc", "gdn_weight", "gdn_weight_tc", "gdn_evict")]
 HEADERS = [ROOT / "include" / "gdnspec.h", ROOT / "include" / "gdnhybrid.h", ROOT / "include" / "gdnlong.h", *(PKG / "csrc" / name for name in ("attn_common.cuh", "attn_simt.cuh", "attn_tc.cuh", "attn_tc.h", "tc_ptx.cuh", "weight_common.cuh"))]
 LIB = PKG / "_lib" / "libgdnspec.so"
 # test-only variant: the verify/commit kernels with GDN_TEST_HOOKS (a state copy

@@ -7,7 +7,7 @@
 #include "attn_common.cuh"
 #include "gdnlong.h"
 
-namespace gdnlong {
+namespace gdnevict {
 
 using gdnattn::Div;
 using gdnattn::kFull;
@@ -43,7 +43,9 @@ __device__ __forceinline__ float warp_sum(float x) {
 // them comes from the counts of the warps and blocks before it, so they are in index order whatever the timing.  Histograms
 // and counts of the cluster's blocks are read from each other's shared memory, with one cluster barrier for each.
 // Tokens beyond what shared memory holds (eight blocks: 393216) are read again in each pass.
-// Bound by latency: @@@
+// Bound by latency: 16 requests of 1000 to 8000 tokens take 15 us (lengths 0.6, keys 2.3, a digit 1.5 each, counts 1.2, lists
+// 1.2, weights moved 0.6), 8 of 60000 to 130000 39 us, where a digit costs 4 us: a cluster barrier and eight blocks'
+// histograms.
 
 namespace cg = cooperative_groups;
 
@@ -63,7 +65,7 @@ struct SelectShared {
   int hist[3][kBins];
   int warps[2][kSelectWarps];  // counts of each warp, then those before it
   int counts[4][2];            // this block's, by exchange
-  int found[2];                // a pass's digit, and how many of that digit leave
+  int found[3];                // a pass's digit, how many of that digit leave, and whether those are all
   int bad_page;
 };
 
@@ -124,7 +126,7 @@ __global__ void __launch_bounds__(kSelectThreads, 1) select_kernel(const gdn_evi
     return staged ? keys[i] : read_key(first + i, &bad);
   };
   int may = 0, bad = 0;
-#pragma unroll 4
+#pragma unroll 8
   for (int i = lane; i < mine; i += 32) {
     const uint32_t k = read_key(first + i, &bad);
     if (staged) keys[i] = k;
@@ -177,6 +179,7 @@ __global__ void __launch_bounds__(kSelectThreads, 1) select_kernel(const gdn_evi
   // the go-th lightest key
   uint32_t key = 0, mask = 0;
   int ties = go;
+  bool found_all = false;  // all keys that equal it leave
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
@@ -229,18 +232,18 @@ __global__ void __launch_bounds__(kSelectThreads, 1) select_kernel(const gdn_evi
       const bool second = ties > below + n[0];
       sh.found[0] = 2 * tid + second;
       sh.found[1] = ties - below - (second ? n[0] : 0);
+      sh.found[2] = sh.found[1] == (second ? n[1] : n[0]);
     }
     __syncthreads();
     key |= (uint32_t)sh.found[0] << shift;
     mask |= (uint32_t)(bins - 1) << shift;
     ties = sh.found[1];
+    found_all = sh.found[2];
   }
-  // `ties` of the keys that equal it leave: the last ones
-  int equal = 0;
-  for (int i = lane; i < mine; i += 32) equal += key_at(i) == key;
-  int equal_before, n_equal, gaps_before, movers_before, n_gaps, n_movers;
-  exchange(__reduce_add_sync(kFull, equal), 0, &equal_before, &by, &n_equal, &bx);
-  // f(token, whether it leaves) for each of the warp's tokens
+  // `ties` of the keys that equal it leave, the last ones: all of them in most calls, and then one count of gaps and movers
+  // does; otherwise it is made again once the equal keys before each warp are known
+  int equal_before = 0, n_equal = ties;
+  // f(token, whether it is one, whether it leaves) for each of the warp's tokens
   auto walk = [&](auto f) {
     int seen = equal_before;
     for (int i0 = 0; i0 < mine; i0 += 32) {
@@ -251,13 +254,26 @@ __global__ void __launch_bounds__(kSelectThreads, 1) select_kernel(const gdn_evi
       seen += __popc(same);
       f(first + i, i < mine, leaves);
     }
+    return seen - equal_before;
   };
-  int gaps = 0, movers = 0;
-  walk([&](int j, bool is, bool leaves) {
-    gaps += is && leaves && j < K;
-    movers += is && !leaves && j >= K;
-  });
-  exchange(__reduce_add_sync(kFull, gaps), __reduce_add_sync(kFull, movers), &gaps_before, &movers_before, &n_gaps, &n_movers);
+  int gaps_before, movers_before, n_gaps, n_movers;
+  auto count = [&](int* equal) {
+    int gaps = 0, movers = 0;
+    *equal = walk([&](int j, bool is, bool leaves) {
+      gaps += is && leaves && j < K;
+      movers += is && !leaves && j >= K;
+    });
+    exchange(__reduce_add_sync(kFull, gaps), __reduce_add_sync(kFull, movers), &gaps_before, &movers_before, &n_gaps, &n_movers);
+  };
+  int equal, n_ties;
+  if (found_all) {
+    count(&equal);
+  } else {
+    equal = 0;
+    for (int i = lane; i < mine; i += 32) equal += key_at(i) == key;
+    exchange(__reduce_add_sync(kFull, equal), 0, &equal_before, &by, &n_equal, &n_ties);
+    count(&equal);
+  }
   if (n_gaps > p.max_moves) {
     if (kC > 1) meet();
     return leave(GDN_STATUS_MOVES_FULL);
@@ -322,53 +338,113 @@ int run_select(const gdn_evict_args& a, cudaStream_t st) {
   return GDN_OK;
 }
 
-// ---- moves -----------------------------------------------------------------------------------------------------------------
+// ---- moves ------------------------------------------------------------------------------------------------------------------
+//
+// A copy, bound by HBM, or by a chain of three reads where it is small: count and slots at once, the data, the store.  A
+// thread moves one or four 16-byte chunks, all loads in flight before the first store: sources and destinations are disjoint.
 
 struct MoveParams {
-  int B, max_moves, n_slots, chunks, H_kv;
-  Div page;
-  int page_size;
+  int max_moves, first, moves;  // this launch's moves of each request
+  int n_slots, page_size;
+  Div per_row, per_pool, per_head, page;  // chunks of K and V of a token, of one of them, of a head
+  int row_chunks, pool_chunks, head_chunks;
   const int32_t *from, *to, *n;
   uint4 *k, *v;  // strides in 16-byte chunks
   int64_t k_page, k_head, k_token, v_page, v_head, v_token;
   int32_t* status;
 };
 
-__global__ void __launch_bounds__(128) move_simple(const MoveParams p) {
+constexpr int kMoveThreads = 256;
+
+template <int kUnroll>
+__global__ void __launch_bounds__(kMoveThreads) move_kernel(const MoveParams p) {
   pdl_wait();
   pdl_trigger();
-  for (int b = blockIdx.y; b < p.B; b += gridDim.y) {
-    const int n = p.n[b];
-    if (n < 0 || n > p.max_moves) {
-      if (blockIdx.x == 0 && threadIdx.x == 0 && p.status) atomicOr(p.status, GDN_STATUS_BAD_LENGTH);
+  const int b = blockIdx.y;
+  const int n = p.n[b];
+  const uint32_t total = (uint32_t)p.moves * p.row_chunks, base = blockIdx.x * (kMoveThreads * kUnroll) + threadIdx.x;
+  if (n < 0 || n > p.max_moves) {
+    if (base == 0 && p.first == 0 && p.status) atomicOr(p.status, GDN_STATUS_BAD_LENGTH);
+    return;
+  }
+  uint4 val[kUnroll];
+  uint4* to[kUnroll];
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const uint32_t i = base + u * kMoveThreads;
+    to[u] = nullptr;
+    if (i >= total) continue;
+    const uint32_t move = quotient(i, p.per_row), in_row = i - move * p.row_chunks;
+    if (p.first + (int)move >= n) continue;
+    const size_t at = (size_t)b * p.max_moves + p.first + move;
+    const int from = p.from[at], dest = p.to[at];
+    if ((unsigned)from >= (unsigned)p.n_slots || (unsigned)dest >= (unsigned)p.n_slots) {
+      if (in_row == 0 && p.status) atomicOr(p.status, GDN_STATUS_BAD_PAGE);
       continue;
     }
-    for (int i = blockIdx.x; i < n; i += gridDim.x) {
-      const int from = p.from[(size_t)b * p.max_moves + i], to = p.to[(size_t)b * p.max_moves + i];
-      if ((unsigned)from >= (unsigned)p.n_slots || (unsigned)to >= (unsigned)p.n_slots) {
-        if (threadIdx.x == 0 && p.status) atomicOr(p.status, GDN_STATUS_BAD_PAGE);
-        continue;
-      }
-      const int from_page = (int)quotient(from, p.page), from_token = from - from_page * p.page_size;
-      const int to_page = (int)quotient(to, p.page), to_token = to - to_page * p.page_size;
-      for (int x = threadIdx.x; x < 2 * p.H_kv * p.chunks; x += 128) {
-        const bool is_v = x >= p.H_kv * p.chunks;
-        const int y = is_v ? x - p.H_kv * p.chunks : x, h = y / p.chunks, c = y - h * p.chunks;
-        uint4* const pool = is_v ? p.v : p.k;
-        const int64_t page = is_v ? p.v_page : p.k_page, head = is_v ? p.v_head : p.k_head, token = is_v ? p.v_token : p.k_token;
-        pool[to_page * page + h * head + to_token * token + c] = pool[from_page * page + h * head + from_token * token + c];
-      }
-    }
+    const uint32_t is_v = quotient(in_row, p.per_pool), in_pool = in_row - is_v * p.pool_chunks;
+    const uint32_t head = quotient(in_pool, p.per_head), c = in_pool - head * p.head_chunks;
+    uint4* const pool = (is_v ? p.v : p.k) + head * (is_v ? p.v_head : p.k_head) + c;
+    const int64_t page = is_v ? p.v_page : p.k_page, token = is_v ? p.v_token : p.k_token;
+    const int from_page = (int)quotient(from, p.page), to_page = (int)quotient(dest, p.page);
+    val[u] = __ldcs(pool + from_page * page + (from - from_page * p.page_size) * token);  // read once
+    to[u] = pool + to_page * page + (dest - to_page * p.page_size) * token;
   }
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u)
+    if (to[u]) *to[u] = val[u];
+}
+
+// One chunk a thread where they are few (16 x 64 moves of 8 heads of 128 in bf16: 2.7 us, with four 3.5; 64 x 64 6.4 and 6.7),
+// four where HBM is the bound (16 x 512 10.9 and 10.3; 15 requests of 500 to 1999 moves in f32 79.7 and 54.1: 6.3 TB/s).
+constexpr int64_t kOneEach = 1 << 20;
+
+int run_move(const gdn_kv_move_args& a, cudaStream_t st) {
+  const int per16 = a.in_dtype == GDN_DTYPE_BF16 ? 8 : 4;
+  MoveParams p = {};
+  p.max_moves = a.max_moves;
+  p.n_slots = a.n_pages * a.page_size;
+  p.page_size = a.page_size;
+  p.head_chunks = a.d / per16;
+  p.pool_chunks = a.H_kv * p.head_chunks;
+  p.row_chunks = 2 * p.pool_chunks;
+  p.per_row = make_div((uint32_t)p.row_chunks);
+  p.per_pool = make_div((uint32_t)p.pool_chunks);
+  p.per_head = make_div((uint32_t)p.head_chunks);
+  p.page = make_div((uint32_t)a.page_size);
+  p.from = a.move_from;
+  p.to = a.move_to;
+  p.n = a.n_moves;
+  p.k = static_cast<uint4*>(a.k_cache);
+  p.v = static_cast<uint4*>(a.v_cache);
+  p.k_page = a.k_page_stride / per16;
+  p.k_head = a.k_head_stride / per16;
+  p.k_token = a.k_token_stride / per16;
+  p.v_page = a.v_page_stride / per16;
+  p.v_head = a.v_head_stride / per16;
+  p.v_token = a.v_token_stride / per16;
+  p.status = a.status;
+  const int most = (INT32_MAX - 4 * kMoveThreads) / p.row_chunks;  // of one launch: chunk numbers are 32-bit
+  for (p.first = 0; p.first < a.max_moves; p.first += p.moves) {
+    p.moves = std::min(most, a.max_moves - p.first);
+    const int64_t chunks = (int64_t)p.moves * p.row_chunks;
+    auto run = [&](auto kernel, int unroll) {
+      const dim3 grid((unsigned)((chunks + kMoveThreads * unroll - 1) / (kMoveThreads * unroll)), a.B);
+      return launch(kernel, grid, dim3(kMoveThreads), 0, st, p);
+    };
+    const int rc = chunks * a.B <= kOneEach ? run(move_kernel<1>, 1) : run(move_kernel<4>, 4);
+    if (rc != GDN_OK) return rc;
+  }
+  return GDN_OK;
 }
 
 // ---- host --------------------------------------------------------------------------------------------------------------------
 
 bool aligned(const void* ptr, uintptr_t n) { return reinterpret_cast<uintptr_t>(ptr) % n == 0; }
 
-}  // namespace gdnlong
+}  // namespace gdnevict
 
-using namespace gdnlong;
+using namespace gdnevict;
 
 extern "C" GDN_API int gdn_evict_select(const gdn_evict_args* a, void* stream) {
   if (!a) return GDN_ERR_INVALID_ARG;
@@ -389,7 +465,7 @@ extern "C" GDN_API int gdn_kv_move(const gdn_kv_move_args* a, void* stream) {
   if (a->B < 0 || a->max_moves < 0 || a->H_kv < 1 || a->d < 1 || a->page_size < 1 || a->n_pages < 1 || a->reserved != 0) return GDN_ERR_INVALID_ARG;
   if (a->in_dtype != GDN_DTYPE_BF16 && a->in_dtype != GDN_DTYPE_F32) return GDN_ERR_UNSUPPORTED;
   const int size = a->in_dtype == GDN_DTYPE_BF16 ? 2 : 4, per16 = 16 / size;
-  if ((int64_t)a->d * size % 16 != 0 || (int64_t)a->H_kv * (a->d / per16) > INT32_MAX / 2 || (int64_t)a->n_pages * a->page_size > INT32_MAX ||
+  if ((int64_t)a->d * size % 16 != 0 || (int64_t)a->H_kv * (a->d / per16) > INT32_MAX / 4 || (int64_t)a->n_pages * a->page_size > INT32_MAX ||
       a->B > 65535 || (int64_t)a->B * a->max_moves > INT32_MAX)
     return GDN_ERR_UNSUPPORTED;
   if (a->B == 0 || a->max_moves == 0) return GDN_OK;
@@ -402,25 +478,5 @@ extern "C" GDN_API int gdn_kv_move(const gdn_kv_move_args* a, void* stream) {
   if (!aligned(a->k_cache, 16) || !aligned(a->v_cache, 16) || !aligned(a->move_from, 4) || !aligned(a->move_to, 4) || !aligned(a->n_moves, 4) ||
       !aligned(a->status, 4))
     return GDN_ERR_MISALIGNED;
-  MoveParams p = {};
-  p.B = a->B;
-  p.max_moves = a->max_moves;
-  p.n_slots = a->n_pages * a->page_size;
-  p.chunks = a->d / per16;
-  p.H_kv = a->H_kv;
-  p.page = make_div((uint32_t)a->page_size);
-  p.page_size = a->page_size;
-  p.from = a->move_from;
-  p.to = a->move_to;
-  p.n = a->n_moves;
-  p.k = static_cast<uint4*>(a->k_cache);
-  p.v = static_cast<uint4*>(a->v_cache);
-  p.k_page = a->k_page_stride / per16;
-  p.k_head = a->k_head_stride / per16;
-  p.k_token = a->k_token_stride / per16;
-  p.v_page = a->v_page_stride / per16;
-  p.v_head = a->v_head_stride / per16;
-  p.v_token = a->v_token_stride / per16;
-  p.status = a->status;
-  return launch(move_simple, dim3(std::min(a->max_moves, 256), std::min(a->B, 1024)), dim3(128), 0, static_cast<cudaStream_t>(stream), p);
+  return run_move(*a, static_cast<cudaStream_t>(stream));
 }

@@ -216,10 +216,10 @@ struct Lines {
     const int g = r.n > 0 ? group_of(b) : -1, L = g >= 0 ? prefix[g] : 0;
     return own(r, b, align, r.ctx < L || r.n > most ? 0 : L);
   }
-  __device__ Line group(int g) const {
+  __device__ Line group(int g, bool find = true) const {  // find: its table row too, which its units do not depend on
     if (prefix[g] == 0 || rows[starts[g + 1]] == rows[starts[g]]) return {0, 0, 0, 0, 0, 0, -1};
     const int first = rows[starts[g]];
-    return {prefix[g] - 1, rows[starts[g + 1]] - first, first, 0, 0, request_of(first), -1};
+    return {prefix[g] - 1, rows[starts[g + 1]] - first, first, 0, 0, find ? request_of(first) : 0, -1};
   }
   __device__ Line line(const Params& p, int v, int align) const { return v < B ? own(request(p, v), v, align) : group(v - B); }
   // row of q and o of a line's token
@@ -388,6 +388,7 @@ __device__ __forceinline__ Lines find_lines(const Params& p, const SharedParams&
   int* const rows = prefix + sp.n_groups;
   int why = 0, broken = 0;
   Request first = {0, 0, 0};
+  int first_g = -1;  // the group whose prefix it may meet
   const int reads = sp.n_groups > 0 && tid <= sp.n_groups;
   int x = 0, y = 0, length = 0;  // on their way with the request's
   if (reads) {
@@ -438,29 +439,39 @@ __device__ __forceinline__ Lines find_lines(const Params& p, const SharedParams&
   };
   if (lines.G > 0) {
     // rows of request b that may meet the prefix; what its own line then lacks goes to its group
-    auto counted = [&](const Request& r, int b, bool count) {
+    auto counted = [&](const Request& r, int b) {
       const int g = r.n > 0 ? lines.group_of(b) : -1;
-      if (g < 0 || prefix[g] == 0 || r.ctx < prefix[g] || r.n > lines.most) return 0;
-      if (count) {
-        const long long whole = T::sum(p, lines.own(r, b, sp.key_align, 0)), own = T::sum(p, lines.own(r, b, sp.key_align, prefix[g]));
-        atomicAdd(reinterpret_cast<unsigned long long*>(&saved[g]), (unsigned long long)(whole - own - kJoinUnits));
-      }
-      return r.n;
+      return g < 0 || prefix[g] == 0 || r.ctx < prefix[g] || r.n > lines.most ? -1 : g;
     };
     long long mine = 0, total;
-    for (int b = b0; b < b1; ++b) mine += counted(b == b0 ? first : request(p, b, &why), b, true);
+    for (int b = b0; b < b1; ++b) {
+      const Request r = b == b0 ? first : request(p, b, &why);
+      const int g = counted(r, b);
+      if (b == b0) first_g = g;
+      if (g < 0) continue;
+      mine += r.n;
+      // at most one tile, as the request's rows do not fill it
+      const Line l = lines.own(r, b, sp.key_align, prefix[g]);
+      const int whole = T::blocks(p, lines.own(r, b, sp.key_align, 0), 0), own = T::blocks(p, l, 0);
+      atomicAdd(reinterpret_cast<unsigned long long*>(&saved[g]), (unsigned long long)(long long)(whole - own - kJoinUnits));
+    }
     long long before = sums(mine, scan, &total);
     if (total > min(p.max_rows, p.n_q_rows)) {  // rows that overlap, or too many for a tile's numbers
       lines.G = 0;  // uniform
     } else {
       for (int b = b0; b < b1; ++b) {
         rows[b] = (int)before;
-        before += counted(b == b0 ? first : request(p, b), b, false);
+        if (b == b0) {
+          before += first_g >= 0 ? first.n : 0;
+        } else {
+          const Request r = request(p, b);
+          before += counted(r, b) >= 0 ? r.n : 0;
+        }
       }
       if (tid == 0) rows[p.B] = (int)total;
       __syncthreads();
       for (int g = tid; g < lines.G; g += kThreads) {
-        const long long less = saved[g] - T::sum(p, lines.group(g));
+        const long long less = saved[g] - T::sum(p, lines.group(g, false));
         if (kShareAlways) continue;
         if (less > 0) atomicAdd(&gain, (unsigned long long)(less * p.H_kv));
         else prefix[g] = 0;
@@ -475,7 +486,7 @@ __device__ __forceinline__ Lines find_lines(const Params& p, const SharedParams&
   if (blockIdx.x == gridDim.x - 1) {  // for the join; this block has the least to do
     for (int b = b0; b < b1 && lines.G > 0; ++b) {
       const int n = rows[b + 1] - rows[b], row0 = n == 0 ? 0 : b == b0 ? first.row0 : request(p, b).row0;
-      const bool shares = n > 0 && prefix[lines.group_of(b)] > 0;
+      const bool shares = n > 0 && prefix[b == b0 ? first_g : lines.group_of(b)] > 0;
       for (int t = 0; t < n; ++t) sp.rank_row[rows[b] + t] = shares ? row0 + t : -1;
     }
     if (tid == 0) *sp.count = lines.G > 0 ? rows[p.B] : 0;
@@ -483,12 +494,13 @@ __device__ __forceinline__ Lines find_lines(const Params& p, const SharedParams&
   long long mine = 0, mine_g = 0, head = 0, total, total_g = 0;
   Line l = {};
   for (int b = b0; b < b1; ++b) {
-    l = lines.own(b == b0 ? first : request(p, b), b, sp.key_align);
+    l = b == b0 ? lines.own(first, b, sp.key_align, lines.G > 0 && first_g >= 0 ? prefix[first_g] : 0)
+                : lines.own(request(p, b), b, sp.key_align);
     head = T::sum(p, l);
     mine += p.H_kv * head;
   }
   const int each_g = (lines.G + kThreads - 1) / kThreads, g0 = tid * each_g, g1 = min(lines.G, g0 + each_g);
-  for (int g = g0; g < g1; ++g) mine_g += p.H_kv * T::sum(p, lines.group(g));
+  for (int g = g0; g < g1; ++g) mine_g += p.H_kv * T::sum(p, lines.group(g, false));
   const long long mine_at = sums(mine, scan + kThreads / 32, &total);
   long long g_at = 0;
   if (lines.G > 0) g_at = sums(mine_g, scan + 2 * (kThreads / 32), &total_g) + total;
@@ -705,17 +717,18 @@ __global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const Param
   }
 }
 
-// A shared call's join.  The first kTileBlocks * n_blocks blocks take the rows of split tiles whose requests take part in no
-// prefix, the others the ranked rows, which join the parts over their request's own keys and over its prefix.  A row's parts
-// are added in one order: the first own one, those of the blocks that follow, the prefix's first and its followers.
-// kTeam warps share a row's parts: four where rows are few, and a tile is cut into many parts, one where they are many.
-// First parts and what says where the others lie are fetched at once.
-constexpr int kTileBlocks = 16;
+// A shared call's join: the rows of split tiles whose requests take part in no prefix, and the ranked rows, which join the
+// parts over their request's own keys and over its prefix.  Every block adds up the notes' rows, so that all of them share
+// both kinds of rows evenly, however few tiles are split.  A row's parts are added in one order: the first own one, those of
+// the blocks that follow, the prefix's first and its followers.  kTeam warps share a row's parts: four where rows are few,
+// and a tile is cut into many parts, one where they are many.
+constexpr int kMostBlocks = 4 * 32 * kCombineWarps;  // of an attention launch
 
 template <typename T, int kD, int kRows, int kTeam>
 __global__ void __launch_bounds__(32 * kCombineWarps) combine_shared(const Params p, const SharedParams sp) {
   constexpr int kPer = kD / 32, kBatch = 4, kRowsAtOnce = kCombineWarps / kTeam;
   __shared__ float sums[kTeam > 1 ? kTeam : 1][kTeam > 1 ? kD : 1];
+  __shared__ int tile_rows[kMostBlocks], warp_rows[kCombineWarps];  // rows of the split tiles before each block's
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, member = warp % kTeam, H_q = p.H_kv * p.G;
@@ -806,31 +819,65 @@ __global__ void __launch_bounds__(32 * kCombineWarps) combine_shared(const Param
     }
     if (sp.lse && lane == 0) sp.lse[(int64_t)row * sp.lse_row + head] = (base + log2f(sum)) * kLn2;
   };
-  // the two kinds of rows are one loop's items, so that the join is compiled once
-  const bool tiles = (int)blockIdx.x < kTileBlocks * p.n_blocks;
-  const int block = tiles ? blockIdx.x % kTileBlocks : blockIdx.x - kTileBlocks * p.n_blocks;
-  const int blocks = tiles ? kTileBlocks : gridDim.x - kTileBlocks * p.n_blocks, x_block = blockIdx.x / kTileBlocks;
-  const int4 note = tiles ? p.notes[x_block] : make_int4(0, 0, 0, 0);
-  const long long items = !tiles ? (long long)*sp.count * H_q : note.x > 0 ? note.z & 255 : 0;
+  const int count = *sp.count;
+  constexpr int kEach = kMostBlocks / (32 * kCombineWarps);
+  int mine[kEach], rows_here = 0;
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    const int x = threadIdx.x * kEach + k;
+    const int4 note = x < p.n_blocks ? p.notes[x] : make_int4(0, 0, 0, 0);
+    mine[k] = note.x > 0 ? note.z & 255 : 0;
+    rows_here += mine[k];
+  }
+  int inc = rows_here;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int v = __shfl_up_sync(kFull, inc, off);
+    if (lane >= off) inc += v;
+  }
+  if (lane == 31) warp_rows[warp] = inc;
+  __syncthreads();
+  int before = inc - rows_here, of_tiles = 0;
+#pragma unroll
+  for (int i = 0; i < kCombineWarps; ++i) {
+    if (i < warp) before += warp_rows[i];
+    of_tiles += warp_rows[i];
+  }
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    tile_rows[threadIdx.x * kEach + k] = before;
+    before += mine[k];
+  }
+  __syncthreads();
+  const long long items = of_tiles + (long long)count * H_q;
   const size_t places = (size_t)p.n_q_rows * H_q;
   // where a block gave up, a row's entry may be anything
   auto inside = [&](const int4& e) { return e.z >= 0 && e.z < p.n_blocks && (e.w & 0xffff) < p.n_blocks - e.z && (e.w >> 16 & 255) < kRows; };
-  for (long long item = (long long)block * kRowsAtOnce + warp / kTeam; item < items; item += (long long)blocks * kRowsAtOnce) {
+  // the two kinds of rows are one loop's items, so that the join is compiled once
+  for (long long item = (long long)blockIdx.x * kRowsAtOnce + warp / kTeam; item < items; item += (long long)gridDim.x * kRowsAtOnce) {
     int row, head;
     float acc[kPer], x_pre[kPer] = {};
     int4 own, pre;
-    if (tiles) {
-      const int at = note.w + (int)item, token = (int)quotient(at, p.by_G);
+    if (item < of_tiles) {
+      int x_block = 0, hi = p.n_blocks;  // tile_rows[x_block] <= item < tile_rows[hi], the last such block
+      while (hi - x_block > 1) {
+        const int mid = (x_block + hi) >> 1;
+        if (tile_rows[mid] <= item) x_block = mid;
+        else hi = mid;
+      }
+      const int4 note = p.notes[x_block];
+      const int in_tile = (int)item - tile_rows[x_block], at = note.w + in_tile, token = (int)quotient(at, p.by_G);
       row = note.y + token;
       head = (note.z >> 8) * p.G + at - token * p.G;
       const float* const first = partial(p, x_block, 1, kRows);
-      const float2 s = reinterpret_cast<const float2*>(first + (size_t)kRows * kD)[item];
-      own = make_int4(__float_as_int(s.x), __float_as_int(s.y), x_block, entry_word(note.x, (int)item));
+      const float2 s = reinterpret_cast<const float2*>(first + (size_t)kRows * kD)[in_tile];
+      own = make_int4(__float_as_int(s.x), __float_as_int(s.y), x_block, entry_word(note.x, in_tile));
       pre = make_int4(__float_as_int(-INFINITY), 0, 0, 0);
-      if (kTeam == 1 || member == 0) load(acc, first + (size_t)item * kD);
+      if (kTeam == 1 || member == 0) load(acc, first + (size_t)in_tile * kD);
     } else {
-      const int rank = item >> 31 ? (int)(item / H_q) : (int)((uint32_t)item / (uint32_t)H_q);
-      head = (int)(item - (long long)rank * H_q);
+      const long long i = item - of_tiles;
+      const int rank = i >> 31 ? (int)(i / H_q) : (int)((uint32_t)i / (uint32_t)H_q);
+      head = (int)(i - (long long)rank * H_q);
       row = sp.rank_row[rank];
       if (row < 0) continue;
       const int h = (int)quotient(head, p.by_G);
@@ -870,7 +917,8 @@ template <typename T, int kD, int kRows>
 int launch_combine_shared(const Params& p, const SharedParams& sp, cudaStream_t st) {
   const long long rows = (long long)p.n_q_rows * p.H_kv * p.G;
   const dim3 block(32 * kCombineWarps);
-  auto grid = [&](long long blocks) { return dim3((unsigned)(kTileBlocks * p.n_blocks + (sp.n_groups == 0 ? 0 : blocks < 152 * 32 ? blocks : 152 * 32))); };
+  // no row is an item twice
+  auto grid = [&](long long blocks) { return dim3((unsigned)(blocks < 152 * 16 ? blocks : 152 * 16)); };
   if (rows <= 152 * 16) return launch(combine_shared<T, kD, kRows, kCombineWarps>, grid(rows), block, 0, st, p, sp);
   return launch(combine_shared<T, kD, kRows, 1>, grid((rows + kCombineWarps - 1) / kCombineWarps), block, 0, st, p, sp);
 }

@@ -351,7 +351,7 @@ __device__ __forceinline__ void find_start(const Params& p, int min_units, long 
 
 // Words of shared memory that a shared call's lines take.
 constexpr int kMaxSharedB = 4096, kMaxGroups = 512;
-constexpr int lines_words(int B, int n_groups) { return B + 4 * n_groups + 2; }
+constexpr int lines_words(int B, int n_groups) { return B + 3 * n_groups + 2; }
 constexpr int kMaxLinesWords = lines_words(kMaxSharedB, kMaxGroups);
 
 // What a call must save by sharing, in units of one block: the join of every row's parts.  Measured (tensor cores, shared
@@ -367,7 +367,7 @@ constexpr bool kShareAlways = true;  // test builds: whatever it costs
 constexpr bool kShareAlways = false;
 #endif
 
-// find_start for the lines of a shared call.  at: lines_words of shared memory, 8-byte aligned, filled here; scan:
+// find_start for the lines of a shared call.  at: lines_words of shared memory, filled here; scan:
 // 3 * kThreads/32 words.  Where group_start does not rise within [0, B], or the counted rows pass 32 bits, no prefix is
 // shared, and what is computed is the same.
 //
@@ -382,8 +382,8 @@ __device__ __forceinline__ Lines find_lines(const Params& p, const SharedParams&
   __shared__ unsigned long long gain;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int each = (p.B + kThreads - 1) / kThreads, b0 = tid * each, b1 = min(p.B, b0 + each);
-  long long* const saved = reinterpret_cast<long long*>(at);  // [G] units of a kv head that a group's requests leave out
-  int* const starts = at + 2 * sp.n_groups;
+  int* const saved = at;  // [G] units of a kv head that a group's requests leave out
+  int* const starts = saved + sp.n_groups;
   int* const prefix = starts + sp.n_groups + 1;
   int* const rows = prefix + sp.n_groups;
   int why = 0, broken = 0;
@@ -453,7 +453,7 @@ __device__ __forceinline__ Lines find_lines(const Params& p, const SharedParams&
       // at most one tile, as the request's rows do not fill it
       const Line l = lines.own(r, b, sp.key_align, prefix[g]);
       const int whole = T::blocks(p, lines.own(r, b, sp.key_align, 0), 0), own = T::blocks(p, l, 0);
-      atomicAdd(reinterpret_cast<unsigned long long*>(&saved[g]), (unsigned long long)(long long)(whole - own - kJoinUnits));
+      atomicAdd(&saved[g], min(whole - own - kJoinUnits, 1 << 18));  // 4096 of them stay below 2^31
     }
     long long before = sums(mine, scan, &total);
     if (total > min(p.max_rows, p.n_q_rows)) {  // rows that overlap, or too many for a tile's numbers
@@ -501,9 +501,37 @@ __device__ __forceinline__ Lines find_lines(const Params& p, const SharedParams&
   }
   const int each_g = (lines.G + kThreads - 1) / kThreads, g0 = tid * each_g, g1 = min(lines.G, g0 + each_g);
   for (int g = g0; g < g1; ++g) mine_g += p.H_kv * T::sum(p, lines.group(g, false));
-  const long long mine_at = sums(mine, scan + kThreads / 32, &total);
-  long long g_at = 0;
-  if (lines.G > 0) g_at = sums(mine_g, scan + 2 * (kThreads / 32), &total_g) + total;
+  long long mine_at, g_at;
+  {
+    long long x = mine, y = mine_g;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long u = __shfl_up_sync(kFull, x, off), v = __shfl_up_sync(kFull, y, off);
+      if (lane >= off) {
+        x += u;
+        y += v;
+      }
+    }
+    long long* const part = scan + kThreads / 32;
+    if (lane == 31) {
+      part[warp] = x;
+      part[kThreads / 32 + warp] = y;
+    }
+    __syncthreads();
+    mine_at = x - mine;
+    g_at = y - mine_g;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) {
+        mine_at += part[w];
+        g_at += part[kThreads / 32 + w];
+      }
+      total += part[w];
+      total_g += part[kThreads / 32 + w];
+    }
+    g_at += total;
+  }
   total += total_g;
   const long long per = max(total >> 31 ? (total + p.n_blocks - 1) / p.n_blocks
                                         : (long long)(((uint32_t)total + (uint32_t)p.n_blocks - 1) / (uint32_t)p.n_blocks),

@@ -165,7 +165,7 @@ struct Tiles {
   __device__ static int extra(const Params& p, const Request&) { return kExtra; }
   // In a shared call (128-key blocks: requests' tiles, prefixes' tiles) 64 single tokens behind 32768 take 99.4 us with 5 and
   // 3, 106 with 3 and 3, 105 with 8 and 3; 16 requests of 4 tokens behind 8011 at d = 256 31.7 with 5 and 8, 34.0 with 5 and 5.
-  __device__ static int extra(const Params& p, const Line& l) { return kExtra == 0 ? 0 : kKeys == 64 && l.flat() ? 8 : 5 - 2 * l.flat(); }
+  __device__ static int extra(const Params& p, const Line& l) { return kExtra == 0 ? 0 : kKeys == 64 && l.flat() ? 8 : l.prefix > 0 ? 5 : kExtra; }
   // units of the tiles before m
   __device__ static long long before(const Params& p, const R& r, int m) {
     if (m == 0) return 0;

@@ -12,11 +12,8 @@
 // sums).  K of a (key block, head) is loaded once and met by all its tiles; a
 // single step's few rows are one tile, and then K streams through.
 //
-// K's layout.  A page's tokens are copied whole, by one instruction: the tensor map splits a row into chunks of 64 columns
-// and the tokens into groups of eight, and takes (page, head) as one dimension, where a page is a whole number of heads
-// long.  In shared memory that is [group][chunk][8 tokens][128 bytes], which the MMA reads as well as any.  (An instruction
-// for each chunk of 16 tokens takes the issuing lane some 80 to 150 clocks; 32 of them for 64 KB took longer than HBM.)
-// Other pools are copied by group and chunk.
+// K's pages are copied whole, by one instruction (an instruction for each chunk of 16 tokens takes the issuing lane some 80 to
+// 150 clocks; 32 of them for 64 KB took longer than HBM).
 //
 // Rows past the request's, and keys past its last token, may hold anything: a column or a lane is one row or key, and
 // theirs are not counted.
@@ -51,20 +48,6 @@ __device__ __forceinline__ void tma_rows(const CUtensorMap* map, uint32_t dst, u
       "l"(map), "r"(col), "r"(head), "r"(row), "r"(bar)
       : "memory");
 }
-__device__ __forceinline__ void tma_page(const CUtensorMap* map, uint32_t dst, uint32_t bar, int group, int number) {
-  asm volatile(
-      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(map), "r"(0), "r"(group), "r"(number), "r"(bar)
-      : "memory");
-}
-// mma_ss with the operands' high words apart
-__device__ __forceinline__ void mma_two(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi, uint32_t idesc, uint32_t add) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %6, 0;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d),
-      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(add)
-      : "memory");
-}
 // 4 bytes into shared memory; the lane's arrival on a barrier once its copies so far have landed
 __device__ __forceinline__ void copy4(uint32_t to, const float* from) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
@@ -83,8 +66,7 @@ struct WeightTcParams {
   int box;    // tokens per TMA box of K
   int width;  // columns of a product: a tile's rows up to a multiple of 16
   int n_k, n_q;  // stages
-  int per_page;  // (page, head) is number page * per_page + head of the map; 0: K is copied by group and chunk
-  int outside;   // a number outside it
+  PageMap k_pages;
 };
 
 template <int kD>
@@ -285,7 +267,6 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
     // ---- the products, issued by one thread
     if (lane == 0) {
       const uint32_t idesc = instruction(t.width, false);
-      constexpr uint32_t kKeysHi = kChunks * 1024 >> 4 | 1u << 14 | 2u << 29;  // groups of eight keys kChunks * 1024 bytes apart
       const uint32_t k_lo0 = operand_lo(k_s, 16), q_lo0 = operand_lo(q_s, 16);
       int i = 0;
       for (int run; ok && !x.done(); x.next(run)) {
@@ -300,7 +281,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
           const uint32_t q_lo = q_lo0 + q_ring.stage * (q_bytes / 16), s_at = tmem + buf * S::kRows;
 #pragma unroll
           for (int k = 0; k < kD / 16; ++k)
-            mma_two(s_at, k_lo + (k / 4) * 64 + (k % 4) * 2, kKeysHi, q_lo + (k / 4) * (t.width * 8) + (k % 4) * 2, kOperandHi, idesc, k > 0);
+            mma_two(s_at, k_lo + (k / 4) * 64 + (k % 4) * 2, page_tile_hi<kD>(), q_lo + (k / 4) * (t.width * 8) + (k % 4) * 2, kOperandHi, idesc, k > 0);
           tc_commit(s_full(buf));
           tc_commit(q_empty(q_ring.stage));
         }
@@ -341,15 +322,8 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
       if (lane == 0) bar_expect(k_full(stage), (uint32_t)live * t.box * kD * 2);
       __syncwarp();
       if (box < live) {
-        // outside the map: zeros; such a page's tokens take no weight
-        const bool good = (unsigned)page < (unsigned)p.n_pages;
-        const uint32_t to = k_s + stage * S::kKBytes + (uint32_t)(box * t.box * kD * 2);
-        if (t.per_page > 0) {
-          tma_page(&k_map, to, k_full(stage), token / 8, good ? page * t.per_page + x.h : t.outside);
-        } else {
-          for (int i = 0; i < t.box / 8 * kChunks; ++i)
-            tma_box(&k_map, to + i * 1024, k_full(stage), i % kChunks * 64, token + i / kChunks * 8, x.h, good ? page : p.n_pages);
-        }
+        // a page outside the pool: zeros; its tokens take no weight
+        copy_page<kD>(&k_map, t.k_pages, k_s + stage * S::kKBytes + (uint32_t)(box * t.box * kD * 2), k_full(stage), t.box, token, x.h, page, p.n_pages);
       }
       ++sent;
       k_ring.next();
@@ -423,28 +397,6 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
   if (warp == 12) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
-// K as [64][8][d / 64][page_size / 8][page and head], a page's box whole; false where a page is not a whole number of heads
-// long, or the numbers pass 32 bits.
-bool make_page_map(CUtensorMap* map, WeightTcParams& t) {
-  const EncodeFn encode = encoder();
-  const Params& p = t.w.p;
-  // the stride of a dimension of one entry is never used, but must be a valid one
-  const int64_t number = p.H_kv > 1 ? p.k_head : p.n_pages > 1 ? p.k_page : p.k_token;
-  if (!encode || number <= 0 || (p.n_pages > 1 && p.k_page % number != 0)) return false;
-  const int64_t per_page = p.n_pages > 1 ? p.k_page / number : p.H_kv;
-  if (per_page < 1 || per_page > INT32_MAX / p.n_pages - 1) return false;
-  const int64_t numbers = (p.n_pages - 1) * per_page + p.H_kv;
-  const cuuint64_t dims[5] = {64, 8, (cuuint64_t)p.d / 64, (cuuint64_t)p.page_size / 8, (cuuint64_t)numbers};
-  const cuuint64_t strides[4] = {(cuuint64_t)p.k_token * 2, 128, (cuuint64_t)p.k_token * 16, (cuuint64_t)number * 2};
-  const cuuint32_t box[5] = {64, 8, (cuuint32_t)p.d / 64, (cuuint32_t)t.box / 8, 1}, steps[5] = {1, 1, 1, 1, 1};
-  if (encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(p.k), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-    return false;
-  t.per_page = (int)per_page;
-  t.outside = (int)numbers;
-  return true;
-}
-
 // rows of q as [d][H_q][n_q_rows]
 bool make_row_map(CUtensorMap* map, const WeightParams& w) {
   const EncodeFn encode = encoder();
@@ -473,8 +425,8 @@ int run(WeightTcParams& t, cudaStream_t st) {
   t.box = 16;
   while (t.box * 2 <= kWeightKeys && t.w.p.page_size % (t.box * 2) == 0) t.box *= 2;
   CUtensorMap k_map, q_map;
-  if (!make_page_map(&k_map, t) && !make_map(&k_map, t.w.p, t.w.p.k, t.w.p.k_token, t.w.p.k_head, t.w.p.k_page, 8)) return GDN_ERR_LAUNCH;
-  if (!make_row_map(&q_map, t.w)) return GDN_ERR_LAUNCH;
+  if (!make_page_map(&k_map, &t.k_pages, t.w.p, t.w.p.k, t.w.p.k_token, t.w.p.k_head, t.w.p.k_page, t.box) || !make_row_map(&q_map, t.w))
+    return GDN_ERR_LAUNCH;
   const int rc = launch(weight_tc_kernel<kD>, dim3(kWeightBlocks), dim3(kWeightThreads), S::kSmem, st, t, k_map, q_map);
   return rc != GDN_OK ? rc : launch_weight_join<kWeightKeys>(t.w, st);
 }
@@ -483,7 +435,7 @@ size_t weight_tc_work() { return weight_work(kWeightBlocks, kWeightKeys); }
 
 int run_weight_tc(WeightParams& w, void* work, cudaStream_t st) {
   set_weight_work(w, kWeightBlocks, kWeightKeys, work);
-  WeightTcParams t{w, 0, 0, 0, 0, 0, 0};
+  WeightTcParams t{w, 0, 0, 0, 0, {0, 0}};
   return w.p.d == 64 ? run<64>(t, st) : w.p.d == 128 ? run<128>(t, st) : run<256>(t, st);
 }
 

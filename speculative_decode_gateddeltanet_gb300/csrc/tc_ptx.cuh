@@ -77,6 +77,12 @@ __device__ __forceinline__ void tma_box(const CUtensorMap* map, uint32_t dst, ui
       : "memory");
 }
 
+__device__ __forceinline__ void tma_page(const CUtensorMap* map, uint32_t dst, uint32_t bar, int group, int number) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(0), "r"(group), "r"(number), "r"(bar)
+      : "memory");
+}
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -91,6 +97,14 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo,
       "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d),
       "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(add)
+      : "memory");
+}
+// mma_ss with the operands' high words apart
+__device__ __forceinline__ void mma_two(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi, uint32_t idesc, uint32_t add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %6, 0;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(add)
       : "memory");
 }
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t hi, uint32_t idesc, uint32_t add) {
@@ -205,6 +219,53 @@ inline bool make_map(CUtensorMap* map, const Params& p, const void* base, int64_
   return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box_dims, steps,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// How a pool's pages are copied whole: its rows as [64][8][d / 64][page_size / 8][page and head], so that one instruction copies
+// a page's tokens of a head, or `box` of them, to [group of eight][chunk of 64][8 tokens][128 bytes].
+struct PageMap {
+  int per_page;  // (page, head) is number page * per_page + head; 0: a page is no whole number of heads long, or the numbers
+                 // pass 32 bits, and `map` is make_map's with boxes of eight tokens
+  int outside;   // a number outside the map
+};
+inline bool make_page_map(CUtensorMap* map, PageMap* m, const Params& p, const void* base, int64_t token, int64_t head, int64_t page, int box) {
+  const EncodeFn encode = encoder();
+  *m = {0, 0};
+  // the stride of a dimension of one entry is never used, but must be a valid one
+  const int64_t number = p.H_kv > 1 ? head : p.n_pages > 1 ? page : token;
+  if (encode && number > 0 && (p.n_pages == 1 || page % number == 0)) {
+    const int64_t per_page = p.n_pages > 1 ? page / number : p.H_kv;
+    if (per_page >= 1 && per_page <= INT32_MAX / p.n_pages - 1) {
+      const int64_t numbers = (p.n_pages - 1) * per_page + p.H_kv;
+      const cuuint64_t dims[5] = {64, 8, (cuuint64_t)p.d / 64, (cuuint64_t)p.page_size / 8, (cuuint64_t)numbers};
+      const cuuint64_t strides[4] = {(cuuint64_t)token * 2, 128, (cuuint64_t)token * 16, (cuuint64_t)number * 2};
+      const cuuint32_t box_dims[5] = {64, 8, (cuuint32_t)p.d / 64, (cuuint32_t)box / 8, 1}, steps[5] = {1, 1, 1, 1, 1};
+      if (encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, box_dims, steps,
+                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS) {
+        *m = {(int)per_page, (int)numbers};
+        return true;
+      }
+    }
+  }
+  return make_map(map, p, base, token, head, page, 8);
+}
+// `box` tokens of a page and head to `to`, by one lane; outside the pool: zeros
+template <int kD>
+__device__ __forceinline__ void copy_page(const CUtensorMap* map, const PageMap& m, uint32_t to, uint32_t bar, int box, int token, int head, int page,
+                                          int n_pages) {
+  const bool good = (unsigned)page < (unsigned)n_pages;
+  if (m.per_page > 0) {
+    tma_page(map, to, bar, token / 8, good ? page * m.per_page + head : m.outside);
+  } else {
+    for (int i = 0; i < box / 8 * (kD / 64); ++i)
+      tma_box(map, to + i * 1024, bar, i % (kD / 64) * 64, token + i / (kD / 64) * 8, head, good ? page : n_pages);
+  }
+}
+// the high word of such a tile's descriptor
+template <int kD>
+__host__ __device__ constexpr uint32_t page_tile_hi() {
+  return (kD / 64) * 1024 >> 4 | 1u << 14 | 2u << 29;
 }
 
 }  // namespace gdnattn

@@ -287,6 +287,25 @@ def test_a_wide_batch_shares_by_itself(hy, dtype, d, own):
     s.check()
 
 
+@pytest.mark.parametrize("d,P", [(64, 16), (128, 48), (256, 16)])
+def test_shared_attention_of_pools_whose_pages_are_no_whole_number_of_heads(hy, always, d, P):
+    case = long_ref.make_shared(groups=[(140, [(0, 2), (25, 2)])], alone=[(33, 2)], H_q=4, H_kv=2, d=d, P=P, dtype=BF16, R=2)
+    s = Shared(hy, case, 2)
+    pages, stride = case["k_cache"].shape[0], 2 * P * d + 24
+    k, v = (torch.full((pages * stride,), float("nan"), dtype=BF16, device="cuda").as_strided((pages, 2, P, d), (stride, P * d, d, 1))
+            for _ in range(2))
+    k.copy_(s.k)
+    v.copy_(s.v)
+    args = hy.make_shared_attention_args(q=s.q, k_cache=k, v_cache=v, block_table=s.t["table"], ctx_len=s.t["ctx"], n_rows=s.t["n"],
+                                         row_start=s.t["start"], R=2, o=s.o, scale=case["scale"], lse=s.lse, status=s.status,
+                                         group_start=s.t["group_start"], prefix_len=s.t["prefix_len"])
+    args.attn.work = s.work.data_ptr()
+    hy.gdn_shared_attention(args)
+    s.check()
+    s.args = args
+    s.again(always).check()
+
+
 # ---- weights -------------------------------------------------------------------
 
 

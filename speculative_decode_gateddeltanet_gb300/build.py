@@ -13,16 +13,17 @@ from pathlib import Path
 
 PKG = Path(__file__).resolve().parent
 ROOT = PKG.parent
-SOURCES = [PKG / "csrc" / f"{name}.cu" for name in ("gdn_spec", "gdn_accept", "gdn_pages", "gdn_attn", "gdn_attn_tc", "gdn_sample", "gdn_shared",
-                                                      "gdn_shared_tc", "gdn_weight", "gdn_weight_tc", "gdn_evict")]
-HEADERS = [ROOT / "include" / "gdnspec.h", ROOT / "include" / "gdnhybrid.h", ROOT / "include" / "gdnlong.h", *(PKG / "csrc" / name for name in ("attn_common.cuh", "attn_simt.cuh", "attn_tc.cuh", "attn_tc.h", "tc_ptx.cuh", "weight_common.cuh"))]
+SOURCES = [PKG / "csrc" / f"{name}.cu" for name in ("gdn_spec", "gdn_accept", "gdn_pages", "gdn_attn", "gdn_attn_tc", "gdn_sample",
+                                                     "gdn_shared", "gdn_shared_tc", "gdn_weight", "gdn_weight_tc", "gdn_evict")]
+HEADERS = [ROOT / "include" / f"{name}.h" for name in ("gdnspec", "gdnhybrid", "gdnlong")] + \
+          [PKG / "csrc" / name for name in ("attn_common.cuh", "attn_simt.cuh", "attn_tc.cuh", "attn_tc.h", "tc_ptx.cuh", "weight_common.cuh")]
 LIB = PKG / "_lib" / "libgdnspec.so"
 # test-only variant: the verify/commit kernels with GDN_TEST_HOOKS (a state copy
 # that can be declared and never issued) and a 2 ms staging-wait limit, for the
 # test that makes the bounded wait run out; never loaded by the package
 TEST_HOOKS_LIB = PKG / "_lib" / "libgdnspec_testhooks.so"
 TEST_HOOKS_FLAGS = ["-DGDN_TEST_HOOKS", "-DGDN_WAIT_LIMIT_NS=2000000ull"]
-# the same for the tensor-core attention; prefixes are shared whatever it costs
+# the same for the tensor-core attention and its weights; prefixes are shared whatever it costs
 ATTN_TEST_HOOKS_LIB = PKG / "_lib" / "libgdnhybrid_testhooks.so"
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMPILE_FLAGS = ARCH + [
@@ -82,7 +83,7 @@ def build_test_hooks(force: bool = False) -> Path:
 def build_attn_test_hooks(force: bool = False) -> Path:
     """Compile the test-only variant of the attention calls if it is missing
     or older than its sources."""
-    src = [PKG / "csrc" / f"{name}.cu" for name in ("gdn_attn", "gdn_attn_tc", "gdn_shared", "gdn_shared_tc")]
+    src = [PKG / "csrc" / f"{name}.cu" for name in ("gdn_attn", "gdn_attn_tc", "gdn_shared", "gdn_shared_tc", "gdn_weight", "gdn_weight_tc")]
     if not force and not stale(ATTN_TEST_HOOKS_LIB, src):
         return ATTN_TEST_HOOKS_LIB
     return _compile(ATTN_TEST_HOOKS_LIB, src, TEST_HOOKS_FLAGS)

@@ -61,6 +61,11 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   return r;
 }
 
+#ifdef GDN_TEST_HOOKS
+// Test builds only: the block whose first K copy is declared on its barrier but never issued (-1: none).
+__device__ int g_test_drop_block = -1;
+#endif
+
 struct WeightTcParams {
   WeightParams w;
   int box;    // tokens per TMA box of K
@@ -321,7 +326,12 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
       if (k_ring.round > 0 && !(ok = warp_wait(k_empty(stage), (k_ring.round - 1) & 1, &gave_up))) break;
       if (lane == 0) bar_expect(k_full(stage), (uint32_t)live * t.box * kD * 2);
       __syncwarp();
-      if (box < live) {
+#ifdef GDN_TEST_HOOKS
+      const bool issue = sent > 0 || (int)blockIdx.x != g_test_drop_block;
+#else
+      constexpr bool issue = true;
+#endif
+      if (issue && box < live) {
         // a page outside the pool: zeros; its tokens take no weight
         copy_page<kD>(&k_map, t.k_pages, k_s + stage * S::kKBytes + (uint32_t)(box * t.box * kD * 2), k_full(stage), t.box, token, x.h, page, p.n_pages);
       }
@@ -440,3 +450,10 @@ int run_weight_tc(WeightParams& w, void* work, cudaStream_t st) {
 }
 
 }  // namespace gdnattn
+
+#ifdef GDN_TEST_HOOKS
+// Test builds only: drop the first K copy of block `block` of later calls (-1 restores it).
+extern "C" GDN_API int gdn_test_drop_weight_copy(int block) {
+  return cudaMemcpyToSymbol(gdnattn::g_test_drop_block, &block, sizeof(int)) == cudaSuccess ? GDN_OK : GDN_ERR_LAUNCH;
+}
+#endif

@@ -40,7 +40,10 @@ def always(hy):
 
     lib = ctypes.CDLL(str(pkg_build.build_attn_test_hooks()))
     lib.gdn_shared_attention.argtypes = [ctypes.POINTER(hy.GdnSharedAttnArgs), ctypes.c_void_p]
-    return lib
+    lib.gdn_attn_weight.argtypes = [ctypes.POINTER(hy.GdnAttnWeightArgs), ctypes.c_void_p]
+    yield lib
+    lib.gdn_test_drop_shared_copy(-1)
+    lib.gdn_test_drop_weight_copy(-1)
 
 
 def ints(v):
@@ -377,6 +380,11 @@ WEIGHT = [
     ([(60, 3), (2, 2)], 128, 1, 64, 16, BF16, "heads", 3, None, 1.0, True),
     ([(700, 16), (20, 7)], 24, 2, 128, 16, BF16, "tokens", 16, None, 1.0, False),
     ([(0, 90), (2000, 33)], 5, 5, 64, 16, BF16, "heads", 0, [40, 17], 1.0, True),
+    ([(200, 3), (0, 5)], 128, 1, 256, 16, BF16, "heads", 0, None, 1.0, True),   # heads of a token over two tiles
+    ([(130, 2), (300, 1)], 144, 2, 256, 32, BF16, "tokens", 2, [3, 0], 1.0, False),
+    ([(70, 3), (0, 2)], 80, 2, 64, 16, F32, "heads", 3, None, 1.0, True),
+    ([(3, 2), (0, 0), (1, 1)], 2, 2, 128, 16, BF16, "heads", 2, [5, 0, 2 ** 31 - 1], 1.0, True),  # firsts at and past the end
+    ([(2, 40)], 6, 1, 64, 5, F32, "heads", 0, [42], 1.0, True),
 ]
 
 
@@ -731,3 +739,63 @@ def test_a_request_keeps_attending_to_the_tokens_that_stay(hy):
             del model[b][int(want["ctx_out"][b]):]
         assert int(status.item()) == 0
     assert seen_moves > 20 and seen_pages_back >= 0 and all(len(m) <= budget for m in model)
+
+
+# ---- bounded waits, streams ------------------------------------------------------
+
+
+def test_a_wait_that_runs_out_ends_the_shared_attention(hy, always):
+    """A block whose first K copy never lands gives up; rows that it had no part in are right, and the context serves the next
+    call.  No copy is in flight: it was declared on its barrier and not issued."""
+    case = long_ref.make_shared(groups=[(300, [(i, 1) for i in range(20)])], alone=[(200, 1)] * 20, H_q=16, H_kv=8, d=128, P=16,
+                                dtype=BF16, R=1)
+    s = Shared(hy, case, 1)
+    assert always.gdn_test_drop_shared_copy(0) == 0
+    s.run(always)
+    torch.cuda.synchronize()  # returns: no wait is without bound
+    assert int(s.status.item()) == 8
+    # block 0 begins with request 0's own keys
+    ref, vmax = hybrid_ref.attention(*(case[x] for x in ("q", "k_cache", "v_cache", "table", "ctx", "n", "start", "scale")))
+    bound = 2.0 ** -8 * (vmax[..., None] + np.abs(ref)) + 1e-5 * vmax[..., None]
+    assert (np.abs(s.o.double().cpu().numpy() - ref)[25:] <= bound[25:]).all()
+    assert always.gdn_test_drop_shared_copy(-1) == 0
+    s.again(always).check()
+
+
+def test_a_wait_that_runs_out_ends_the_weights(hy, always):
+    case = hybrid_ref.make_attention(lens=[(1500, 2)] * 30, H_q=16, H_kv=4, d=128, P=16, dtype=BF16, R=2)
+    w = Weight(hy, case, 2)
+    assert always.gdn_test_drop_weight_copy(3) == 0
+    assert always.gdn_attn_weight(w.args, torch.cuda.current_stream().cuda_stream or None) == 0
+    torch.cuda.synchronize()
+    assert int(w.status.item()) == 8
+    # 30 requests of 12 key blocks and 4 heads, three units each, over 152 blocks: block 3 has units of request 0 and 1 alone
+    want, _, off = w.expected()
+    slots = (case["table"][2:, :94, None] * 16 + np.arange(16)).reshape(28, -1)[:, :1500]
+    got = w.weight.double().cpu().numpy()
+    assert (np.abs(got - want)[slots] <= off[slots]).all()
+    assert always.gdn_test_drop_weight_copy(-1) == 0
+    w.weight.copy_(torch.tensor(w.weight0))
+    w.born.copy_(ints(w.born0))
+    w.status.zero_()
+    assert always.gdn_attn_weight(w.args, torch.cuda.current_stream().cuda_stream or None) == 0
+    w.check()
+
+
+def test_calls_on_two_streams_with_buffers_of_their_own(hy):
+    case = long_ref.make_shared(groups=[(900, [(5 * i, 2) for i in range(12)])], alone=[(400, 2)], H_q=16, H_kv=4, d=128, P=16, dtype=BF16, R=2)
+    attend = [Shared(hy, case, 2) for _ in range(2)]
+    weigh = [Weight(hy, case, 2, first=case["ctx"] - 3) for _ in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        for s, w, stream in zip(attend, weigh, streams):
+            hy.gdn_shared_attention(s.args, stream)
+            w.weight.record_stream(stream)
+            with torch.cuda.stream(stream):
+                w.weight.copy_(torch.tensor(w.weight0), non_blocking=False)
+            hy.gdn_attn_weight(w.args, stream)
+    torch.cuda.synchronize()
+    for s, w in zip(attend, weigh):
+        s.check()
+        w.check()

@@ -209,7 +209,7 @@ struct Lines {
     return lo;
   }
   __device__ Line own(const Request& r, int b, int align, int L) const {
-    const int k0 = L - L % align;
+    const int k0 = L & -align;  // a power of two
     return {r.ctx - k0, r.n, r.row0, k0, L - k0, b, L};
   }
   __device__ Line own(const Request& r, int b, int align) const {

@@ -48,19 +48,6 @@ __device__ __forceinline__ void tma_rows(const CUtensorMap* map, uint32_t dst, u
       "l"(map), "r"(col), "r"(head), "r"(row), "r"(bar)
       : "memory");
 }
-// 4 bytes into shared memory; the lane's arrival on a barrier once its copies so far have landed
-__device__ __forceinline__ void copy4(uint32_t to, const float* from) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
-}
-__device__ __forceinline__ void copies_arrive(uint32_t bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
 #ifdef GDN_TEST_HOOKS
 // Test builds only: the block whose first K copy is declared on its barrier but never issued (-1: none).
 __device__ int g_test_drop_block = -1;
@@ -116,7 +103,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
       bar_init(q_empty(i), 1);
     }
     for (int i = 0; i < kL; ++i) {
-      bar_init(l_full(i), 32);
+      bar_init(l_full(i), 1);
       bar_init(l_empty(i), 4);
     }
     for (int i = 0; i < kS; ++i) {
@@ -165,7 +152,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
     // ---- S out of TMEM, the groups in turn; the first also writes the weights
     const int group = warp >> 2, quarter = warp & 3, key = tid & 127;
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
-    const uint64_t scale2 = pair(p.scale_log2, p.scale_log2), log2e2 = pair(-1.4426950408889634f, -1.4426950408889634f);
+    const uint64_t scale2 = pair(p.scale_log2, p.scale_log2);
     float in_keys = 0.f, in_head = 0.f;  // sums over the key block's heads before this one, and over this head's tiles
     int place = 0;  // of this thread's key's weight, and what it holds
     float old = 0.f;
@@ -193,7 +180,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
         auto sum_up = [&](const uint32_t (&s)[32], int c) {
           auto term = [&](int k, float2 l) {  // columns c + k and the next
             const float* const v = reinterpret_cast<const float*>(s) + k;
-            const float2 y = halves(fma2(pair(v[0], v[1]), scale2, mul2(pair(l.x, l.y), log2e2)));
+            const float2 y = halves(fma2(pair(v[0], v[1]), scale2, pair(l.x, l.y)));
             return make_float2(ex2(y.x), ex2(y.y));
           };
           if (__all_sync(kFull, c >= from && c + 32 <= n_cols)) {
@@ -357,7 +344,8 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
       }
     }
   } else if (any && warp == 15) {
-    // ---- the tiles' lse: lane c copies columns c, c + 32, ..., whose tokens and heads are the same in every tile
+    // ---- the tiles' lse, in the exponent of 2 and negative: lane c takes columns c, c + 32, ..., whose tokens and heads are the
+    // same in every tile; the next tile's are on their way while a place in the ring is waited for
     constexpr int kEach = S::kRows / 32;
     int64_t off[kEach];
 #pragma unroll
@@ -365,22 +353,33 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
       const int c = lane + 32 * k, token = (int)quotient(c, w.by_heads);
       off[k] = (int64_t)token * w.lse_row + c - token * w.heads;
     }
-    int i = 0;
-    for (int run; ok && !x.done(); x.next(run)) {
-      run = x.run();
-      for (int r = 0; r < run; ++r, ++i) {
-        const int stage = i % kL, m = x.m + r;
-        if (i >= kL && !(ok = warp_wait(l_empty(stage), (i / kL - 1) & 1, &gave_up))) break;
-        const int n_cols = x.columns(m);
-        const float* const from = w.lse + (int64_t)(x.req.row0 + x.token(m)) * w.lse_row + x.h * p.G + x.head(m);
-        const uint32_t to = smem_addr(&lse_s[stage][lane]);
+    auto load = [&](float (&v)[kEach], int m) {
+      const int n_cols = x.columns(m);
+      const float* const from = w.lse + (int64_t)(x.req.row0 + x.token(m)) * w.lse_row + x.h * p.G + x.head(m);
 #pragma unroll
-        for (int k = 0; k < kEach; ++k)
-          if (lane + 32 * k < n_cols) copy4(to + 128 * k, from + off[k]);
-        copies_arrive(l_full(stage));
+      for (int k = 0; k < kEach; ++k) v[k] = lane + 32 * k < n_cols ? __ldg(from + off[k]) : 0.f;
+    };
+    float now[kEach], ahead[kEach];
+    int run = x.run(), r = 0;
+    load(now, x.m);
+    for (int i = 0; ok; ++i) {
+      if (++r == run) {
+        x.next(run);
+        run = x.run();
+        r = 0;
       }
+      const bool more = !x.done();
+      if (more) load(ahead, x.m + r);
+      const int stage = i % kL;
+      if (i >= kL && !(ok = warp_wait(l_empty(stage), (i / kL - 1) & 1, &gave_up))) break;
+#pragma unroll
+      for (int k = 0; k < kEach; ++k) {
+        lse_s[stage][lane + 32 * k] = now[k] * -1.4426950408889634f;
+        now[k] = ahead[k];
+      }
+      warp_arrive(l_full(stage));
+      if (!more) break;
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
   }
   if (!any && tid == 0) w.notes[blockIdx.x] = 0;
   __syncthreads();

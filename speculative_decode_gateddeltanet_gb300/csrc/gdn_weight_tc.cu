@@ -9,8 +9,15 @@
 //
 // Roles (512 threads): three groups of four warps take the tiles out of TMEM in turn (four S buffers), warp 12 issues the
 // products, warp 13 copies K, warp 14 Q, warp 15 the rows' lse (one warp for both took 1500 clocks a tile, more than its
-// sums).  K of a (key block, head) is loaded once and met by all its tiles; a
-// single step's few rows are one tile, and then K streams through.
+// sums).  K of a (key block, head) is loaded once and met by all its tiles; a single step's few rows are one tile, and then K
+// streams through.
+//
+// Measured.  Prompts: 8192 tokens at d = 128, 32 heads 255 us (1.08 PFLOP/s), at d = 64 230, at d = 256 (64 rows a tile) 344;
+// 1500 to 4096 tokens of two requests 82.  A tile of 128 x 128 takes 1250 clocks, where its products and its exponentials
+// take 512 each: bound by instructions (issue 62 %, exponentials 51 % of their rate).  Steps: 16 requests of 4 tokens over 1000
+// to 8000 at d = 256 19.7 us, of which 3 are HBM's wait for the first K and 9 the stream at HBM's rate; one token over 65537
+// at d = 128 40, where a unit takes 0.95 us and its 32 KB of K 0.72: without K, Q and sums it would still take 34, the roles'
+// own steps between their waits.
 //
 // K's pages are copied whole, by one instruction (an instruction for each chunk of 16 tokens takes the issuing lane some 80 to
 // 150 clocks; 32 of them for 64 KB took longer than HBM).
@@ -69,7 +76,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
   const WeightParams& w = t.w;
   const Params& p = w.p;
   extern __shared__ __align__(16) uint8_t raw[];
-  __shared__ __align__(8) uint64_t bars[2 * S::kMostK + 2 * S::kMostQ + 2 * kS + 5 + 2 * kL];
+  __shared__ __align__(8) uint64_t bars[2 * S::kMostK + 2 * S::kMostQ + kS + 5 + 3 * kL];
   __shared__ long long scan[kWeightThreads / 32];
   __shared__ WeightStart start;
   __shared__ uint32_t tmem_base;
@@ -84,14 +91,16 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
   auto q_full = [&](int i) { return b0 + 8 * (2 * S::kMostK + i); };
   auto q_empty = [&](int i) { return b0 + 8 * (2 * S::kMostK + S::kMostQ + i); };
   constexpr int kRest = 2 * S::kMostK + 2 * S::kMostQ;
-  auto s_full = [&](int i) { return b0 + 8 * (kRest + i); };
-  auto s_empty = [&](int i) { return b0 + 8 * (kRest + kS + i); };
-  auto c_full = [&](int i) { return b0 + 8 * (kRest + 2 * kS + i); };       // cross holds a key block's sums
-  auto c_empty = [&](int i) { return b0 + 8 * (kRest + 2 * kS + 2 + i); };  // and they have been read
-  const uint32_t drained = b0 + 8 * (kRest + 2 * kS + 4);
+  auto s_empty = [&](int i) { return b0 + 8 * (kRest + i); };
+  auto c_full = [&](int i) { return b0 + 8 * (kRest + kS + i); };       // cross holds a key block's sums
+  auto c_empty = [&](int i) { return b0 + 8 * (kRest + kS + 2 + i); };  // and they have been read
+  const uint32_t drained = b0 + 8 * (kRest + kS + 4);
   // lse has a ring of its own: it is read until a tile's sums are done, some 2000 clocks after Q is free again
-  auto l_full = [&](int i) { return b0 + 8 * (kRest + 2 * kS + 5 + i); };
-  auto l_empty = [&](int i) { return b0 + 8 * (kRest + 2 * kS + 5 + kL + i); };
+  auto l_empty = [&](int i) { return b0 + 8 * (kRest + kS + 5 + i); };
+  // A wait names a phase by its parity, so a waiter must know that the phase before has passed.  A group waits for every third
+  // tile: that tile i - 3 is there, by its own wait, says that tile i - kL is, as products and lse come in order.
+  auto s_full = [&](int i) { return b0 + 8 * (kRest + kS + 5 + kL + i % kL); };
+  auto l_full = [&](int i) { return b0 + 8 * (kRest + kS + 5 + 2 * kL + i % kL); };
   if (tid == 0) {
     gave_up = 0;
     for (int i = 0; i < t.n_k; ++i) {
@@ -103,13 +112,11 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
       bar_init(q_empty(i), 1);
     }
     for (int i = 0; i < kL; ++i) {
+      bar_init(s_full(i), 1);
       bar_init(l_full(i), 1);
       bar_init(l_empty(i), 4);
     }
-    for (int i = 0; i < kS; ++i) {
-      bar_init(s_full(i), 1);
-      bar_init(s_empty(i), 4);
-    }
+    for (int i = 0; i < kS; ++i) bar_init(s_empty(i), 4);
     for (int i = 0; i < 2; ++i) {
       bar_init(c_full(i), 4 * (kGroups - 1));
       bar_init(c_empty(i), 4);
@@ -171,7 +178,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
       const int past0 = x.kb * kKeys + key - x.req.ctx;
       for (; r < run; r += kGroups) {
         const int i = done + r, m = x.m + r, buf = i % kS, stage = i % kL;
-        if (!(ok = warp_wait(s_full(buf), (i / kS) & 1, &gave_up) && warp_wait(l_full(stage), (i / kL) & 1, &gave_up))) break;
+        if (!(ok = warp_wait(s_full(i), (i / kL) & 1, &gave_up) && warp_wait(l_full(i), (i / kL) & 1, &gave_up))) break;
         tc_fence_after();
         const int n_cols = x.columns(m), past = past0 - x.token(m);
         // a row's token t sees this key where t >= past; no key of the block is hidden where the last is not
@@ -274,7 +281,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
 #pragma unroll
           for (int k = 0; k < kD / 16; ++k)
             mma_two(s_at, k_lo + (k / 4) * 64 + (k % 4) * 2, page_tile_hi<kD>(), q_lo + (k / 4) * (t.width * 8) + (k % 4) * 2, kOperandHi, idesc, k > 0);
-          tc_commit(s_full(buf));
+          tc_commit(s_full(i));
           tc_commit(q_empty(q_ring.stage));
         }
         if (!ok) break;
@@ -377,7 +384,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
         lse_s[stage][lane + 32 * k] = now[k] * -1.4426950408889634f;
         now[k] = ahead[k];
       }
-      warp_arrive(l_full(stage));
+      warp_arrive(l_full(i));
       if (!more) break;
     }
   }

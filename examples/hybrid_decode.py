@@ -1,7 +1,7 @@
 """Speculative decoding of a toy hybrid: one GatedDeltaNet layer and one full-attention
 layer over a paged cache, random weights, everything decided on the device.
 
-    python examples/hybrid_decode.py [--drafts 3] [--steps 64] [--temperature 0.0]
+    python examples/hybrid_decode.py [--drafts 3] [--steps 64] [--temperature 0.0] [--budget 0]
 
 One step verifies the rows [pending, d1..dk] of every request:
 
@@ -10,6 +10,13 @@ One step verifies the rows [pending, d1..dk] of every request:
   gdn_kv_append         the rows' K and V to those slots
   gdn_paged_attention   the rows over their requests' pages
   gdn_sample_accept     the target's sampled tokens, and how many drafts they confirm
+
+With a budget the attention layer's cache keeps at most so many tokens of a request:
+
+  gdn_shared_attention  in place of gdn_paged_attention: it also gives each row's log sum of exponentials
+  gdn_attn_weight       what the accepted rows gave to each cached token
+  gdn_evict_select      the lightest tokens beyond the budget leave, but for a request's first ones and its latest
+  gdn_kv_move           K and V of the tokens that take their places
 
 The projections between them are plain matrix products.  Drafts come from a table of the last
 seen successor of each token.  No step reads anything back to the host.
@@ -51,8 +58,8 @@ class Model:
 class Decoder:
     """Caches and call arguments of B requests, each starting from one token."""
 
-    def __init__(self, model: Model, first, drafts: int, pages: int = 512, temperature=0.0, seed=0):
-        self.m, self.k, self.B, self.R = model, drafts, len(first), drafts + 1
+    def __init__(self, model: Model, first, drafts: int, pages: int = 512, temperature=0.0, seed=0, budget: int = 0):
+        self.m, self.k, self.B, self.R, self.budget = model, drafts, len(first), drafts + 1, budget
         B, R, dt = self.B, self.R, model.dtype
         self.rng = torch.Generator(device="cuda").manual_seed(seed)
         self.pending = torch.tensor(first, dtype=torch.int32, device="cuda")
@@ -92,6 +99,43 @@ class Decoder:
             row_start=self.starts, slot_map=self.slot_map, positions=self.positions, page_size=PAGE, R=R, status=self.status)
             for i in range(2)]
         self.steps = 0
+        if budget:
+            self.make_eviction(pages)
+
+    def make_eviction(self, pages):
+        """Arguments of the calls that keep the cache within the budget."""
+        B, R = self.B, self.R
+        self.text, self.count, self.keep_from = i32(B), i32(B), i32(B)  # tokens of the text, rows that count, ages that stay
+        self.lse = torch.zeros((B * R, H_Q), device="cuda")
+        self.weight, self.born = torch.zeros(pages * PAGE, device="cuda"), i32(pages * PAGE)
+        self.n_moves, self.move_from, self.move_to = i32(B), i32(B, R), i32(B, R)  # a step adds at most R tokens
+        self.most, self.pinned = i32(B, fill=self.budget), i32(B, fill=4)
+        cache = dict(k_cache=self.pool[:, 0], v_cache=self.pool[:, 1])
+        self.shared = hybrid.make_shared_attention_args(
+            q=self.qkv[:, :H_Q], **cache, block_table=self.table, ctx_len=self.ctx, n_rows=self.rows, row_start=self.starts, R=R, o=self.o2,
+            lse=self.lse, status=self.status)
+        self.shared_work = torch.empty(hybrid.shared_attention_work_bytes(self.shared), dtype=torch.uint8, device="cuda")
+        self.shared.attn.work = self.shared_work.data_ptr()
+        self.weigh = hybrid.make_attn_weight_args(
+            q=self.qkv[:, :H_Q], k_cache=self.pool[:, 0], lse=self.lse, block_table=self.table, ctx_len=self.ctx, n_rows=self.count,
+            row_start=self.starts, R=R, weight=self.weight, born=self.born, position=self.text, fresh=True, status=self.status)
+        self.weigh_work = torch.empty(hybrid.attn_weight_work_bytes(self.weigh), dtype=torch.uint8, device="cuda")
+        self.weigh.work = self.weigh_work.data_ptr()
+        self.select = hybrid.make_evict_select_args(
+            weight=self.weight, born=self.born, block_table=self.table, ctx_len=self.ctx, budget=self.most, ctx_out=self.ctx,
+            n_moves=self.n_moves, move_from=self.move_from, move_to=self.move_to, page_size=PAGE, pinned=self.pinned,
+            keep_from=self.keep_from, status=self.status)
+        self.move = hybrid.make_kv_move_args(**cache, move_from=self.move_from, move_to=self.move_to, n_moves=self.n_moves, status=self.status)
+
+    def evict(self, accept):
+        """After a step: the accepted rows' weights, and the tokens beyond the budget out of the cache."""
+        torch.add(accept, 1, out=self.count)
+        hybrid.gdn_attn_weight(self.weigh)
+        self.ctx += self.count
+        self.text += self.count
+        torch.sub(self.text, self.budget // 2, out=self.keep_from)
+        hybrid.gdn_evict_select(self.select)
+        hybrid.gdn_kv_move(self.move)
 
     def gdn_args(self, turn, x, a, b, carry):
         return gdn.make_args(x=x, g=a, beta=b, conv_w=self.m.conv, conv_state=self.window, ssm_state=self.state, slot_ids=self.slots,
@@ -122,7 +166,10 @@ class Decoder:
         hybrid.gdn_page_map(self.map[turn])
         torch.matmul(h.reshape(self.B * self.R, D), m.qkv, out=self.qkv.reshape(self.B * self.R, -1))
         hybrid.gdn_kv_append(self.append)
-        hybrid.gdn_paged_attention(self.attn)
+        if self.budget:
+            hybrid.gdn_shared_attention(self.shared)
+        else:
+            hybrid.gdn_paged_attention(self.attn)
         h = h + (self.o2.reshape(self.B, self.R, -1) @ m.o2)
         # the target's tokens, and the drafts they confirm
         logits = h @ m.out
@@ -134,7 +181,10 @@ class Decoder:
         target = self.target.clone()
         self.guess.scatter_(0, tokens[:, 0].long(), target[:, 0])
         self.pending = target.gather(1, accept.long()[:, None])[:, 0]
-        self.ctx += accept + 1
+        if self.budget:
+            self.evict(accept)
+        else:
+            self.ctx += accept + 1
         self.steps += 1
         return target, accept.clone()
 
@@ -145,8 +195,9 @@ def main():
     ap.add_argument("--steps", type=int, default=64)
     ap.add_argument("--batch", type=int, default=4)
     ap.add_argument("--temperature", type=float, default=0.0)
+    ap.add_argument("--budget", type=int, default=0, help="tokens of a request that the attention layer's cache keeps (0: all)")
     a = ap.parse_args()
-    dec = Decoder(Model(), list(range(1, a.batch + 1)), a.drafts, temperature=a.temperature)
+    dec = Decoder(Model(), list(range(1, a.batch + 1)), a.drafts, temperature=a.temperature, budget=a.budget)
     done = [dec.step() for _ in range(a.steps)]
     torch.cuda.synchronize()
     counts = torch.stack([n + 1 for _, n in done]).float()

@@ -126,7 +126,9 @@ __device__ __forceinline__ Request request(const Params& p, int b, int* why = nu
 // sum over i in [0, n) of floor((a*i + b) / m), the lattice points under a line: whole multiples of m are taken out of a
 // and b, the points under what is left are counted along the other axis.  That is Euclid's algorithm on (m, a); the
 // exchange of axes is the reciprocity law of floor sums (Graham, Knuth, Patashnik: Concrete Mathematics, section 3.5).
-__device__ inline long long floor_sum(long long n, long long m, long long a, long long b) {
+// Called, not copied into each place: a launch's first time through its code is bound by fetching it, and the kernels'
+// roles together fill the instruction cache.
+static __device__ __noinline__ long long floor_sum(long long n, long long m, long long a, long long b) {
   long long s = 0;
   while (n > 0) {
     if (a >= m) {

@@ -33,8 +33,10 @@ struct WeightParams {
   float* partials;  // [n_blocks][2][kKeys]
 };
 
-// floor_sum where the numbers leave room: its divisions in 32 bits
-__device__ inline long long weight_floor_sum(int n, int m, int a, long long b) {
+// floor_sum where the numbers leave room: its divisions in 32 bits.  (With this and floor_sum called, and the next request
+// found without them, the bf16 kernel's code is 82 KB in place of 152: 16 x 4 rows at d = 256 take 17.9 us, not 19.7, ragged
+// single steps of 128 requests 67.4, not 69.3.)
+static __device__ __noinline__ long long weight_floor_sum(int n, int m, int a, long long b) {
   if (((long long)n * (a > m ? a : m) + b) >> 31) return floor_sum(n, m, a, b);
   long long s = 0;
   uint32_t N = n, M = m, A = a, C = (uint32_t)b;
@@ -220,7 +222,7 @@ struct WeightWalk {
       if (++kb == req.kb1) {
         do {
           req = U::request(*w, ++b);
-        } while (U::sum(*w, req) == 0);
+        } while (req.kb0 == req.kb1);
         kb = req.kb0;
       }
       low = m = U::m0(*w, req, kb);

@@ -47,9 +47,11 @@ enum {
  * the table row of the first of them that has rows.  (Pages before the prefix's
  * end are usually the same pages; where a prefix ends inside a page, each
  * request's table has its own copy of that page.)  Requests outside every group,
- * with fewer cached tokens than their group's prefix, or alone in their group read
- * everything through their own table row, as do all where prefix_len is not
- * positive.
+ * with fewer cached tokens than their group's prefix, or whose rows times
+ * H_q/H_kv fill a tile (128 in bf16, 32 in f32) read everything through their own
+ * table row, as do all where prefix_len is not positive, and where by the lengths
+ * reading together would save less than joining the two parts of a row costs.
+ * Which way a request goes changes o and lse by the rounding of sums alone.
  *
  *   attn         the call as gdn_paged_attention takes it; attn.work:
  *                gdn_shared_attention_work_bytes(args) bytes, 16-byte aligned
@@ -100,8 +102,9 @@ GDN_API size_t gdn_shared_attention_work_bytes(const gdn_shared_attn_args* args)
  * Arithmetic: products of the inputs' type with 32-bit sums, exponentials and
  * weights in 32 bits, added in an order that depends on the lengths alone.  The
  * same inputs give the same bits on every call.  Supported sizes, alignments and skipped
- * requests are gdn_paged_attention's; a page outside the pool (GDN_STATUS_BAD_PAGE)
- * takes no weight.  A negative first counts as 0. */
+ * requests are gdn_paged_attention's, and q's strides are not negative; a page
+ * outside the pool (GDN_STATUS_BAD_PAGE) takes no weight.  A negative first
+ * counts as 0. */
 typedef struct gdn_attn_weight_args {
   int32_t B, R;
   int32_t H_q, H_kv, d;

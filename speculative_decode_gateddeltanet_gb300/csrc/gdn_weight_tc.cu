@@ -12,8 +12,8 @@
 // sums).  K of a (key block, head) is loaded once and met by all its tiles; a single step's few rows are one tile, and then K
 // streams through.
 //
-// Measured.  Prompts: 8192 tokens at d = 128, 32 heads 259 us (1.06 PFLOP/s), at d = 64 227, at d = 256 (64 rows a tile) 340;
-// 1500 to 4096 tokens of two requests 80.  A tile of 128 x 128 takes 1250 clocks, where its products and its exponentials
+// Measured.  Prompts: 8192 tokens at d = 128, 32 heads 258 us (1.07 PFLOP/s), at d = 64 220, at d = 256 (64 rows a tile) 338;
+// 1500 to 4096 tokens of two requests 79.  A tile of 128 x 128 takes 1250 clocks, where its products and its exponentials
 // take 512 each: bound by instructions (issue 62 %, exponentials 51 % of their rate).  Steps: 16 requests of 4 tokens over 1000
 // to 8000 at d = 256 17.9 us, of which 3 are HBM's wait for the first K and 9 the stream at HBM's rate; one token over 65537
 // at d = 128 40, where a unit takes 0.95 us and its 32 KB of K 0.72: without K, Q and sums it would still take 34, the roles'

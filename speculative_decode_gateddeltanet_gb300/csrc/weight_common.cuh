@@ -70,8 +70,9 @@ struct WeightRequest {
 
 template <int kKeys>
 struct WeightUnits {
-  // 8192 tokens at d = 64 take 243 us, with 0 282, 1 253, 4 237; at d = 128 277, with 0 299, 1 281, 4 279.
-  static constexpr int kRun = kKeys == 128 ? 2 : 0;
+  // 8192 tokens at d = 64 take 220 us, with 2 226, 1 236, 0 264; at d = 128 258, with 2 257, 1 260, 0 280; prompts of 1500 to
+  // 4096 tokens 79, with 2 80, 1 82, 0 90; single steps the same.
+  static constexpr int kRun = kKeys == 128 ? 4 : 0;
   __device__ static WeightRequest request(const WeightParams& w, int b, int* why = nullptr) {
     const Request r = gdnattn::request(w.p, b, why);
     WeightRequest x = {r.ctx, r.n, r.row0, 0, 0, 0, 0};

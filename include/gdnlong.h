@@ -73,8 +73,11 @@ typedef struct gdn_shared_attn_args {
 } gdn_shared_attn_args;
 GDN_API int gdn_shared_attention(const gdn_shared_attn_args* args, void* stream);
 
-/* Bytes of attn.work: a function of d, in_dtype, H_q and n_q_rows alone.  0 if
- * the sizes are unsupported. */
+/* Bytes of attn.work: a function of B, d, in_dtype, H_q, H_kv and n_q_rows alone
+ * (not of the groups, which may change from call to call), and no smaller for a
+ * larger B or n_q_rows.  Beside gdn_paged_attention's, 2 * H_q * (4 d + 16) bytes
+ * for each row that can take part in a prefix: n_q_rows, but at most B times the
+ * rows of a request that do not fill a tile.  0 if the sizes are unsupported. */
 GDN_API size_t gdn_shared_attention_work_bytes(const gdn_shared_attn_args* args);
 
 /* ---- attention weight of cached tokens ---------------------------------------

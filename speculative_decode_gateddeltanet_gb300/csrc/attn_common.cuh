@@ -81,9 +81,10 @@ struct SharedParams {
   float* lse;
   int64_t lse_row;
   // rows that take part in a prefix, which are ranked request by request:
-  float* dense;       // [2][n_q_rows * H_q][d]: first parts over prefixes and over own keys, unnormalised
-  int4* entries;      // [2][n_q_rows * H_q]: a first part's maximum and sum, its block, and entry_word
-  int* rank_row;      // [n_q_rows] each rank's row, or -1
+  int n_ranks;        // the most that can
+  float* dense;       // [2][n_ranks * H_q][d]: first parts over prefixes and over own keys, unnormalised
+  int4* entries;      // [2][n_ranks * H_q]: a first part's maximum and sum, its block, and entry_word
+  int* rank_row;      // [n_ranks] each rank's row, or -1
   int* count;         // ranks
 };
 
@@ -224,6 +225,8 @@ struct Lines {
     return {prefix[g] - 1, rows[starts[g + 1]] - first, first, 0, 0, find ? request_of(first) : 0, -1};
   }
   __device__ Line line(const Params& p, int v, int align) const { return v < B ? own(request(p, v), v, align) : group(v - B); }
+  // rank of a line's token, where the line's rows have parts over a prefix and over their own keys
+  __device__ int rank_of(const Line& l, int token) const { return (l.flat() ? l.row0 : rows[l.b]) + token; }
   // row of q and o of a line's token
   __device__ int row_of(const Params& p, const Line& l, int token) const {
     if (!l.flat()) return l.row0 + token;
@@ -351,6 +354,9 @@ __device__ __forceinline__ void find_start(const Params& p, int min_units, long 
   __syncthreads();
 }
 
+// The most rows of a request that takes part in a prefix: with them a tile of tile_rows is not yet full.
+__host__ __device__ constexpr int most_rows(int tile_rows, int G) { return (tile_rows - 1) / G; }
+
 // Words of shared memory that a shared call's lines take.
 constexpr int kMaxSharedB = 4096, kMaxGroups = 512;
 constexpr int lines_words(int B, int n_groups) { return B + 3 * n_groups + 2; }
@@ -419,7 +425,7 @@ __device__ __forceinline__ Lines find_lines(const Params& p, const SharedParams&
   if (tid == 0) gain = 0;
   broken = __syncthreads_or(broken);
   if (broken && blockIdx.x == 0 && tid == 0 && p.status) atomicOr(p.status, GDN_STATUS_BAD_GROUP);
-  Lines lines = {p.B, broken ? 0 : sp.n_groups, (kRows - 1) / p.G, starts, prefix, rows};
+  Lines lines = {p.B, broken ? 0 : sp.n_groups, most_rows(kRows, p.G), starts, prefix, rows};
   // exclusive sum of x over the threads, and the whole sum
   auto sums = [&](long long x, long long* part, long long* total) {
     long long inc = x;
@@ -603,9 +609,9 @@ __device__ __forceinline__ int4 note_of(const Walk<kRows, kKeys, kShared>& w, co
   return {followers_of(w, s), w.req.row0, w.h << 8 | rows, w.m * kRows};
 }
 
-// a row's place among its kv head's rows in `dense` and `entries`: a tile's rows lie together
-__device__ __forceinline__ size_t place_of(const Params& p, int row, int kv_head, int g) {
-  return ((size_t)kv_head * p.n_q_rows + row) * p.G + g;
+// a rank's place among its kv head's in `dense` and `entries`: a tile's rows lie together.  Places over prefixes come first.
+__device__ __forceinline__ size_t place_of(const Params& p, const SharedParams& sp, bool own, int rank, int kv_head, int g) {
+  return ((size_t)(own ? p.H_kv + kv_head : kv_head) * sp.n_ranks + rank) * p.G + g;
 }
 // What a first part's entry says beside its maximum, sum and block: the blocks that follow, and its row in the tile.
 __device__ __forceinline__ int entry_word(int followers, int row) { return followers | row << 16; }
@@ -880,7 +886,6 @@ __global__ void __launch_bounds__(32 * kCombineWarps) combine_shared(const Param
   }
   __syncthreads();
   const long long items = of_tiles + (long long)count * H_q;
-  const size_t places = (size_t)p.n_q_rows * H_q;
   // where a block gave up, a row's entry may be anything
   auto inside = [&](const int4& e) { return e.z >= 0 && e.z < p.n_blocks && (e.w & 0xffff) < p.n_blocks - e.z && (e.w >> 16 & 255) < kRows; };
   // the two kinds of rows are one loop's items, so that the join is compiled once
@@ -911,12 +916,12 @@ __global__ void __launch_bounds__(32 * kCombineWarps) combine_shared(const Param
       row = sp.rank_row[rank];
       if (row < 0) continue;
       const int h = (int)quotient(head, p.by_G);
-      const size_t at = place_of(p, row, h, head - h * p.G);
-      own = sp.entries[places + at];
-      pre = sp.entries[at];
+      const size_t own_at = place_of(p, sp, true, rank, h, head - h * p.G), pre_at = place_of(p, sp, false, rank, h, head - h * p.G);
+      own = sp.entries[own_at];
+      pre = sp.entries[pre_at];
       if (kTeam == 1 || member == 0) {
-        load(acc, sp.dense + (places + at) * kD);
-        load(x_pre, sp.dense + at * kD);
+        load(acc, sp.dense + own_at * kD);
+        load(x_pre, sp.dense + pre_at * kD);
       }
       if (!inside(own) || !inside(pre)) continue;  // the same for the row's warps
     }

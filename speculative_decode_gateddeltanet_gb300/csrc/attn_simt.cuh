@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kSimtThreads, kD == 256 ? 2 : 3)
         if constexpr (kShared) {
           o_row = row_at[row];
           if (first) {
-            const size_t place = (w.req.flat() ? 0 : (size_t)p.n_q_rows * p.H_kv * p.G) + place_of(p, o_row, w.h, at % p.G);
+            const size_t place = place_of(p, sp, !w.req.flat(), lines.rank_of(w.req, at / p.G), w.h, at % p.G);
             out = sp.dense + place * kD;
             out_stats = reinterpret_cast<float2*>(sp.entries + place);
             if (lane == 0) reinterpret_cast<int2*>(out_stats)[1] = make_int2(blockIdx.x, entry_word(followers_of(w, s), row));

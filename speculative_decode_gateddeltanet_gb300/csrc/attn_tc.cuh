@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         bool first = false;  // of a row that takes part in a prefix
         if constexpr (kShared) {
           if (joins(w) && w.kb0 == 0) {
-            const size_t place = (w.req.flat() ? 0 : (size_t)p.n_q_rows * p.H_kv * p.G) + place_of(p, o_row, w.h, head - w.h * p.G);
+            const size_t place = place_of(p, sp, !w.req.flat(), lines.rank_of(w.req, token), w.h, head - w.h * p.G);
             first = true;
             out = sp.dense + place * kD;
             out_stats = reinterpret_cast<float2*>(sp.entries + place);

@@ -1,4 +1,6 @@
 // gdn_shared_attention: argument checks and the launches.
+#include <algorithm>
+
 #include "attn_simt.cuh"
 #include "attn_tc.h"
 #include "gdnlong.h"
@@ -21,8 +23,14 @@ int check(const gdn_shared_attn_args* a) {
   return al(a->group_start) && al(a->prefix_len) && al(a->lse) ? GDN_OK : GDN_ERR_MISALIGNED;
 }
 
-// first parts of prefixes and of requests, one of each for a row and head
-size_t places(const gdn_paged_attn_args& a) { return 2 * (size_t)a.n_q_rows * a.H_q; }
+// The most rows that can take part in a prefix: prompts, whose rows fill tiles, do not, and need no places.
+int64_t ranks(const gdn_paged_attn_args& a) {
+  const int64_t most = most_rows(a.in_dtype == GDN_DTYPE_BF16 ? tc_rows() : kSimtRows, a.H_q / a.H_kv);
+  return std::min((int64_t)a.n_q_rows, a.B * most);
+}
+// First parts of prefixes and of requests, one of each for a rank and head.  4096 requests of 127 rows and 2^31 heads of 256
+// columns are below 2^62 bytes.
+size_t places(const gdn_paged_attn_args& a) { return 2 * (size_t)ranks(a) * a.H_q; }
 
 }  // namespace gdnattn
 
@@ -32,8 +40,7 @@ using namespace gdnattn;
 extern "C" GDN_API size_t gdn_shared_attention_work_bytes(const gdn_shared_attn_args* args) {
   if (check_sizes(args) != GDN_OK) return 0;
   const size_t partials = gdn_paged_attention_work_bytes(&args->attn);
-  const size_t ranks = ((size_t)args->attn.n_q_rows + 1) * sizeof(int);
-  return partials == 0 ? 0 : partials + places(args->attn) * (args->attn.d * sizeof(float) + sizeof(int4)) + ranks;
+  return partials == 0 ? 0 : partials + places(args->attn) * (args->attn.d * sizeof(float) + sizeof(int4)) + (ranks(args->attn) + 1) * sizeof(int);
 }
 
 extern "C" GDN_API int gdn_shared_attention(const gdn_shared_attn_args* a, void* stream) {
@@ -49,10 +56,11 @@ extern "C" GDN_API int gdn_shared_attention(const gdn_shared_attn_args* a, void*
   sp.lse_row = a->lse_row_stride;
   const size_t attn_bytes = gdn_paged_attention_work_bytes(&a->attn);
   set_work(p, a->attn.in_dtype, a->attn.work);
+  sp.n_ranks = (int)ranks(a->attn);
   sp.entries = reinterpret_cast<int4*>(static_cast<char*>(a->attn.work) + attn_bytes);
   sp.dense = reinterpret_cast<float*>(sp.entries + places(a->attn));
   sp.rank_row = reinterpret_cast<int*>(sp.dense + places(a->attn) * p.d);
-  sp.count = sp.rank_row + a->attn.n_q_rows;
+  sp.count = sp.rank_row + sp.n_ranks;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return a->attn.in_dtype == GDN_DTYPE_BF16 ? run_shared_tc(p, sp, st) : run_simt<true>(p, sp, st);
 }

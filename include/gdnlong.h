@@ -22,6 +22,25 @@
  * index in the cache (page of its table row and place in it) and its position in
  * the text differ from the first eviction on: the text's length is the cache's
  * plus the tokens that left.
+ *
+ * Pages of a shared prefix.  gdn_page_map knows none: the first held[b] entries of
+ * a table row are request b's alone to it, and go back to the ring when b's lengths
+ * need them no more.  So while several requests hold a prefix of L tokens, W = L /
+ * page_size whole pages, none of their lengths may fall below W * page_size in a
+ * call, or those pages are in the ring while others read them, once for each
+ * request that ends, and later in two requests.
+ *   A request joins: the caller writes the W pages into its table row, held[b] = W,
+ *     ctx_len[b] = L.  Where L is no multiple of page_size the next gdn_page_map
+ *     takes a page of its own for the rest, and gdn_kv_move brings the rest's tokens
+ *     there from a request that has them, before attention reads them.  (Where pages
+ *     did not suffice held_out[b] is still W: the table has no such page, nothing
+ *     may be moved, and the request joins in a later step.)
+ *   It lives: first[b] of gdn_attn_weight and pinned[b] of gdn_evict_select are L or
+ *     more, so that no call writes what others read.
+ *   It ends, and others hold the prefix: a gdn_page_map with ctx_len[b] = W *
+ *     page_size, n_rows[b] = 0 takes the pages behind it; before the next one
+ *     held[b] = ctx_len[b] = 0.
+ *   The last one ends as any request does, with ctx_len[b] = n_rows[b] = 0.
  */
 #ifndef GDNLONG_H
 #define GDNLONG_H

@@ -160,7 +160,8 @@ GDN_API int gdn_kv_append(const gdn_kv_append_args* args, void* stream);
  *
  * Supported: d in {64, 128, 256}; H_q a multiple of H_kv, H_q/H_kv <= 128;
  * page_size a multiple of 16 up to 1024 (any >= 1 for GDN_DTYPE_F32).
- * q, o, pools and work 16-byte aligned, strides multiples of 16 bytes.
+ * q, o, pools and work 16-byte aligned, strides multiples of 16 bytes (the pools'
+ * below 2^39 elements for GDN_DTYPE_BF16, where a dimension has more than one entry).
  * A request with a negative ctx_len or with more tokens than max_pages pages,
  * n_rows outside [0, R] (padded), rows outside q, or more than 2^31 - 1024
  * tokens or rows times H_q/H_kv is skipped with its bit. */

@@ -124,9 +124,9 @@ GDN_API size_t gdn_shared_attention_work_bytes(const gdn_shared_attn_args* args)
  * Arithmetic: products of the inputs' type with 32-bit sums, exponentials and
  * weights in 32 bits, added in an order that depends on the lengths alone.  The
  * same inputs give the same bits on every call.  Supported sizes, alignments and skipped
- * requests are gdn_paged_attention's, and q's strides are not negative; a page
- * outside the pool (GDN_STATUS_BAD_PAGE) takes no weight.  A negative first
- * counts as 0. */
+ * requests are gdn_paged_attention's.  q's strides are not negative, and for
+ * GDN_DTYPE_BF16 below 2^39 elements, as the pool's.  A page outside the pool
+ * (GDN_STATUS_BAD_PAGE) takes no weight.  A negative first counts as 0. */
 typedef struct gdn_attn_weight_args {
   int32_t B, R;
   int32_t H_q, H_kv, d;

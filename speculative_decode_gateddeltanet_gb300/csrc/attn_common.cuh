@@ -72,6 +72,9 @@ int check(const gdn_paged_attn_args* a);
 Params params_of(const gdn_paged_attn_args* a);
 void set_work(Params& p, int dtype, void* work);  // notes and partials, gdn_paged_attention_work_bytes
 
+// whether a tensor map of 16-bit elements can have the stride of a dimension of n entries: it has 40 bits of bytes
+inline bool map_stride(int64_t elements, int64_t n) { return n <= 1 || elements < int64_t(1) << 39; }
+
 struct Nothing {};
 
 // What a shared call has beside them.

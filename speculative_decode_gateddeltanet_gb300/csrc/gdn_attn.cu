@@ -45,6 +45,10 @@ int check(const gdn_paged_attn_args* a) {
     if (s * size % 16 != 0) return GDN_ERR_MISALIGNED;
   for (int i = 2; i < 8; ++i)  // the pools': a negative offset is a key that is not there
     if (strides[i] < 0) return GDN_ERR_INVALID_ARG;
+  if (a->in_dtype == GDN_DTYPE_BF16 &&
+      (!map_stride(a->k_token_stride, a->page_size) || !map_stride(a->k_head_stride, a->H_kv) || !map_stride(a->k_page_stride, a->n_pages) ||
+       !map_stride(a->v_token_stride, a->page_size) || !map_stride(a->v_head_stride, a->H_kv) || !map_stride(a->v_page_stride, a->n_pages)))
+    return GDN_ERR_UNSUPPORTED;
   auto al = [](const void* ptr, uintptr_t n) { return reinterpret_cast<uintptr_t>(ptr) % n == 0; };
   if (!al(a->q, 16) || !al(a->k_cache, 16) || !al(a->v_cache, 16) || !al(a->o, 16) || !al(a->work, 16) ||
       !al(a->block_table, 4) || !al(a->ctx_len, 4) || !al(a->n_rows, 4) || !al(a->row_start, 4) || !al(a->status, 4))

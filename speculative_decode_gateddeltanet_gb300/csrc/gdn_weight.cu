@@ -197,6 +197,7 @@ int check(const gdn_attn_weight_args* a) {
   if ((a->fresh != 0 && a->fresh != 1) || !std::isfinite(a->keep)) return GDN_ERR_INVALID_ARG;
   if (a->B == 0 || a->n_q_rows == 0) return GDN_OK;
   if (!a->lse || !a->weight || a->lse_row_stride < a->H_q || a->q_row_stride < 0 || a->q_head_stride < 0) return GDN_ERR_INVALID_ARG;
+  if (a->in_dtype == GDN_DTYPE_BF16 && (!map_stride(a->q_row_stride, a->n_q_rows) || !map_stride(a->q_head_stride, a->H_q))) return GDN_ERR_UNSUPPORTED;
   auto al = [](const void* ptr) { return reinterpret_cast<uintptr_t>(ptr) % 4 == 0; };
   return al(a->lse) && al(a->first) && al(a->position) && al(a->weight) && al(a->born) ? GDN_OK : GDN_ERR_MISALIGNED;
 }

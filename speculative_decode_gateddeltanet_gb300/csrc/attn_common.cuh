@@ -29,13 +29,17 @@
 
 namespace gdnattn {
 
-
 constexpr unsigned kFull = 0xffffffffu;
 // the kernels' positions and row numbers are 32-bit, and run up to a block past a request's last
 constexpr int kMaxIndex = INT32_MAX - 1023;
 
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// 16 bytes into shared memory, or zeros
+__device__ __forceinline__ void copy16(float* to, const float* from, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from), "r"(valid ? 16 : 0) : "memory");
+}
 
 // x / d for 0 <= x < 2^31 as a multiplication and a shift
 struct Div {
@@ -93,7 +97,6 @@ struct SharedParams {
 
 struct Request {
   int ctx, n, row0;
-  static constexpr bool kFlat = false;
   __device__ int flat() const { return 0; }
   __device__ int len() const { return ctx + n; }                   // its keys' end
   __device__ int last(int token) const { return ctx + token; }     // the last key that a row sees

@@ -28,11 +28,6 @@ constexpr int kSimtMinUnits = 1;  // a block's least share: 3 requests of up to 
 
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 
-// 16 bytes into shared memory, or zeros
-__device__ __forceinline__ void copy16(float* to, const float* from, bool valid) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from), "r"(valid ? 16 : 0) : "memory");
-}
-
 template <int kD>
 constexpr int simt_smem() {
   return (kSimtRows * kD + kSimtKeys * (kD + 4) + kSimtKeys * kD + kSimtRows * kSimtKeys) * (int)sizeof(float);

@@ -11,28 +11,11 @@ namespace gdnevict {
 
 using gdnattn::Div;
 using gdnattn::kFull;
-using gdnattn::kMaxIndex;
 using gdnattn::launch;
 using gdnattn::make_div;
-using gdnattn::Params;
-using gdnattn::params_of;
 using gdnattn::pdl_trigger;
 using gdnattn::pdl_wait;
 using gdnattn::quotient;
-using gdnattn::request;
-using gdnattn::Request;
-
-template <typename T>
-__device__ __forceinline__ float to_float(T x) {
-  if constexpr (sizeof(T) == 2) return __bfloat162float(x);
-  else return x;
-}
-
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) x += __shfl_xor_sync(kFull, x, off);
-  return x;
-}
 
 // ---- the choice -----------------------------------------------------------------------------------------------------------
 //
@@ -66,7 +49,6 @@ struct SelectShared {
   int warps[2][kSelectWarps];  // counts of each warp, then those before it
   int counts[4][2];            // this block's, by exchange
   int found[3];                // a pass's digit, how many of that digit leave, and whether those are all
-  int bad_page;
 };
 
 template <int kC>
@@ -75,7 +57,6 @@ __global__ void __launch_bounds__(kSelectThreads, 1) select_kernel(const gdn_evi
   __shared__ SelectShared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = kC == 1 ? 0 : blockIdx.x % kC, b = blockIdx.x / kC;
   for (int i = tid; i < 3 * kBins; i += kSelectThreads) (&sh.hist[0][0])[i] = 0;
-  if (tid == 0) sh.bad_page = 0;
   pdl_wait();
   pdl_trigger();
   const int L = p.ctx_len[b], budget = max(p.budget[b], 0), pinned = p.pinned ? max(p.pinned[b], 0) : 0;

@@ -20,10 +20,6 @@ constexpr int weight_simt_smem() {
   return (kWsKeys + kWsRows) * (kD + 4) * (int)sizeof(float);
 }
 
-__device__ __forceinline__ void copy16_or_zero(float* to, const float* from, bool valid) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from), "r"(valid ? 16 : 0) : "memory");
-}
-
 template <int kD>
 __global__ void __launch_bounds__(kWsThreads, 2) weight_simt_kernel(const WeightParams w) {
   constexpr int kPitch = kD + 4, kChunks = kD / 4;
@@ -55,9 +51,9 @@ __global__ void __launch_bounds__(kWsThreads, 2) weight_simt_kernel(const Weight
       for (int i = tid; i < kWsRows * kChunks; i += kWsThreads) {
         const int r = i / kChunks, c = i % kChunks, token = (int)quotient(r, w.by_heads);
         const bool valid = r < n_cols;
-        copy16_or_zero(qs + r * kPitch + 4 * c,
-                       static_cast<const float*>(p.q) + (valid ? (int64_t)(row0 + token) * p.q_row + (int64_t)(head0 + r - token * w.heads) * p.q_head + 4 * c : 0),
-                       valid);
+        copy16(qs + r * kPitch + 4 * c,
+               static_cast<const float*>(p.q) + (valid ? (int64_t)(row0 + token) * p.q_row + (int64_t)(head0 + r - token * w.heads) * p.q_head + 4 * c : 0),
+               valid);
       }
       if (tid < n_cols) {
         const int token = (int)quotient(tid, w.by_heads);
@@ -68,7 +64,7 @@ __global__ void __launch_bounds__(kWsThreads, 2) weight_simt_kernel(const Weight
         for (int i = tid; i < kWsKeys * kChunks; i += kWsThreads) {
           const int j = i / kChunks, c = i % kChunks;
           const int64_t off = k_at[j];
-          copy16_or_zero(ks + j * kPitch + 4 * c, static_cast<const float*>(p.k) + (off >= 0 ? off + x.h * p.k_head + 4 * c : 0), off >= 0);
+          copy16(ks + j * kPitch + 4 * c, static_cast<const float*>(p.k) + (off >= 0 ? off + x.h * p.k_head + 4 * c : 0), off >= 0);
         }
       }
       asm volatile("cp.async.wait_all;" ::: "memory");

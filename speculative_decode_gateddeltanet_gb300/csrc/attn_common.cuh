@@ -644,7 +644,7 @@ constexpr int kCombineWarps = 4;
 template <typename T, int kD, int kRows>
 __global__ void __launch_bounds__(32 * kCombineWarps) combine_kernel(const Params p) {
   constexpr int kPer = kD / 32;
-  __shared__ float sums[kCombineWarps][kD];
+  __shared__ __align__(8) float sums[kCombineWarps][kD];  // two columns at once
   pdl_wait();
   pdl_trigger();
   const int4 note = p.notes[blockIdx.x];
@@ -769,7 +769,7 @@ constexpr int kMostBlocks = 4 * 32 * kCombineWarps;  // of an attention launch
 template <typename T, int kD, int kRows, int kTeam>
 __global__ void __launch_bounds__(32 * kCombineWarps) combine_shared(const Params p, const SharedParams sp) {
   constexpr int kPer = kD / 32, kBatch = 4, kRowsAtOnce = kCombineWarps / kTeam;
-  __shared__ float sums[kTeam > 1 ? kTeam : 1][kTeam > 1 ? kD : 1];
+  __shared__ __align__(8) float sums[kTeam > 1 ? kTeam : 1][kTeam > 1 ? kD : 1];  // two columns at once
   __shared__ int tile_rows[kMostBlocks], warp_rows[kCombineWarps];  // rows of the split tiles before each block's
   pdl_wait();
   pdl_trigger();

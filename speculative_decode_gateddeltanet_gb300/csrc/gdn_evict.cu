@@ -45,11 +45,13 @@ __device__ __forceinline__ uint32_t weight_key(float x) {
 }
 
 struct SelectShared {
-  int hist[3][kBins];
+  alignas(8) int hist[3][kBins];  // read two bins at once
   int warps[2][kSelectWarps];  // counts of each warp, then those before it
   int counts[4][2];            // this block's, by exchange
   int found[3];                // a pass's digit, how many of that digit leave, and whether those are all
 };
+
+static_assert(alignof(SelectShared) >= alignof(int2) && kBins % 2 == 0);
 
 template <int kC>
 __global__ void __launch_bounds__(kSelectThreads, 1) select_kernel(const gdn_evict_args p, const Div by_page) {

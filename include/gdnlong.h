@@ -68,9 +68,12 @@ enum {
  * request's table has its own copy of that page.)  Requests outside every group,
  * with fewer cached tokens than their group's prefix, or whose rows times
  * H_q/H_kv fill a tile (128 in bf16, 32 in f32) read everything through their own
- * table row, as do all where prefix_len is not positive, and where by the lengths
- * reading together would save less than joining the two parts of a row costs.
- * Which way a request goes changes o and lse by the rounding of sums alone.
+ * table row, as do all where prefix_len is not positive, and where by an estimate
+ * from the lengths reading together saves less than joining the two parts of a row
+ * costs.  Which way a request goes changes o and lse by the rounding of sums alone.
+ * A call in which nothing is shared takes 8 to 14 % longer than
+ * gdn_paged_attention, small ones 3 us: that one serves better where neither
+ * prefixes nor lse are wanted.
  *
  *   attn         the call as gdn_paged_attention takes it; attn.work:
  *                gdn_shared_attention_work_bytes(args) bytes, 16-byte aligned
@@ -185,6 +188,11 @@ GDN_API size_t gdn_attn_weight_work_bytes(const gdn_attn_weight_args* args);
  * lies outside the pool (GDN_STATUS_BAD_PAGE), or it needs more than max_moves
  * moves (GDN_STATUS_MOVES_FULL).  Two requests must not hold the same slot at or
  * behind their pinned.
+ * Time: a table row that can hold more than 16384 tokens (max_pages * page_size)
+ * gives every request eight blocks in place of one, whatever its length.  Where
+ * requests are many and short, pass the pages that they may have, not the row's
+ * width (128 requests of 1000 to 8000 tokens: 17 us, and 146 with max_pages for
+ * 131072 tokens).
  * Supported: B <= 65535, page_size >= 1, n_pages * page_size < 2^31,
  * B * max_moves < 2^31. */
 typedef struct gdn_evict_args {
@@ -213,7 +221,10 @@ GDN_API int gdn_evict_select(const gdn_evict_args* args, void* stream);
  * move_to.  A move from or to a slot outside the pool is skipped
  * (GDN_STATUS_BAD_PAGE), a request whose n_moves is outside [0, max_moves] too
  * (GDN_STATUS_BAD_LENGTH).  Pointers and strides are multiples of 16 bytes, and
- * so is d.  Supported: B <= 65535, B * max_moves < 2^31, n_pages * page_size < 2^31. */
+ * so is d.  Supported: B <= 65535, B * max_moves < 2^31, n_pages * page_size < 2^31.
+ * Time: blocks are launched for max_moves moves of every request, and those without
+ * one end at once: lists no longer than an eviction can need cost least (10 moves of
+ * each of 16 requests, 8 heads of 128 in bf16: lists of 64 2.1 us, of 4096 17). */
 typedef struct gdn_kv_move_args {
   int32_t B, max_moves;
   int32_t H_kv, d;

@@ -23,8 +23,8 @@
  * the text differ from the first eviction on: the text's length is the cache's
  * plus the tokens that left.
  *
- * Pages of a shared prefix.  gdn_page_map knows none: the first held[b] entries of
- * a table row are request b's alone to it, and go back to the ring when b's lengths
+ * Pages of a shared prefix.  gdn_page_map knows none: to it the first held[b] entries
+ * of a table row are request b's alone, and go back to the ring when b's lengths
  * need them no more.  So while several requests hold a prefix of L tokens, W = L /
  * page_size whole pages, none of their lengths may fall below W * page_size in a
  * call, or those pages are in the ring while others read them, once for each
@@ -33,8 +33,9 @@
  *     ctx_len[b] = L.  Where L is no multiple of page_size the next gdn_page_map
  *     takes a page of its own for the rest, and gdn_kv_move brings the rest's tokens
  *     there from a request that has them, before attention reads them.  (Where pages
- *     did not suffice held_out[b] is still W: the table has no such page, nothing
- *     may be moved, and the request joins in a later step.)
+ *     did not suffice held_out[b] is still W, and the table has no such page: nothing
+ *     may be moved, ctx_len[b] goes back to W * page_size for the step's other calls,
+ *     and the request joins in a later step.)
  *   It lives: first[b] of gdn_attn_weight and pinned[b] of gdn_evict_select are L or
  *     more, so that no call writes what others read.
  *   It ends, and others hold the prefix: a gdn_page_map with ctx_len[b] = W *

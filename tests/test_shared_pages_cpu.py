@@ -47,3 +47,15 @@ def test_a_request_that_joins_takes_pages_behind_the_prefix_alone():
     table[1, :W] = table[0, :W]
     x, ring, free, held = step([40, 37], [3, W], ring, free, table)  # its prefix ends inside its third page
     assert held == [3, 3] and x["table"][1].tolist() == [0, 1, 4, 9] and in_ring(ring, free) == [5, 6, 7]
+
+
+def test_a_request_that_finds_no_page_joins_later():
+    table, ring, _ = start()
+    table[1, :] = 9
+    table[1, :W] = table[0, :W]
+    x, ring, free, held = step([40, 37], [3, W], ring, np.array([0, 0]), table)
+    assert x["status"] == 32 and held == [3, W] and x["table"][1].tolist() == [0, 1, 9, 9]  # no page of its own to fill
+    x, ring, free, held = step([W * P, 37], held, ring, free, x["table"])  # the other ends: its page is free from the next call on
+    assert x["status"] == 32 and held == [W, W] and in_ring(ring, free) == [2]
+    x, ring, free, held = step([0, 37], [0, W], ring, free, x["table"])
+    assert x["status"] == 0 and held == [0, 3] and x["table"][1].tolist() == [0, 1, 2, 9] and free[1] == 0
